@@ -277,6 +277,190 @@ qgemm_status qgemm_run_scaled(const qgemm_plan* plan, int64_t M, const void* A, 
 qgemm_status qgemm_quantize_rows(const void* A, int64_t M, int64_t K, void* Q, float* scales,
                                  void* stream);
 
+/* ---- gated feed-forward block ------------------------------------------------
+ *
+ *     C[M,N] = act(A . dequant(Wg) + bg) * (A . dequant(Wu) + bu)
+ *
+ * Both projections, the activation and the product in one kernel (one more summing
+ * pass where the library splits K, as for the plain product).  A gated plan packs the
+ * two weights into one blob whose 16-column blocks alternate, so that a lane of every
+ * kernel holds the two sums of an output; they stay in fp32 (int32 for int8
+ * activations) up to the one rounding of C.
+ */
+typedef enum {
+  QGEMM_ACT_SILU = 1,     /* x sigmoid(x) */
+  QGEMM_ACT_GELU_TANH = 2 /* 0.5 x (1 + tanh(sqrt(2 / pi) (x + 0.044715 x^3))) */
+} qgemm_act;
+
+/*
+ * Create a gated plan.  The arguments are those of qgemm_create, with N the columns of
+ * C and of each projection; the output type is QGEMM_F16 (else QGEMM_ERR_UNSUPPORTED),
+ * so the tuples are (F16, I4 | U4 | F16, F16, F32) and (I8, I8 | I2, F16, I32).  K is not
+ * split by the caller (the library splits it where qgemm_create's plans do).  The size
+ * limits hold for the 2 * roundup(N, 16) columns of both projections.
+ *   act            the activation, else QGEMM_ERR_INVALID_ARG.
+ *   packed_bytes   out: size of the blob that qgemm_pack_gated writes.
+ *   workspace_bytes out: size of the workspace of qgemm_run_gated (0 if none).
+ * Gated plans run through qgemm_pack_gated, qgemm_run_gated and qgemm_gated_backward
+ * (the plain calls return QGEMM_ERR_INVALID_ARG for them) and are destroyed by
+ * qgemm_destroy.
+ */
+qgemm_status qgemm_create_gated(qgemm_plan** out, int64_t M, int64_t N, int64_t K,
+                                qgemm_dtype a_dtype, qgemm_dtype w_dtype, qgemm_dtype out_dtype,
+                                qgemm_dtype accum_dtype, int32_t group_size, int32_t has_zeros,
+                                qgemm_act act, size_t* packed_bytes, size_t* workspace_bytes);
+
+/*
+ * Pack the canonical weights of both projections (each as in qgemm_pack_weights: w
+ * [N, K], 16-byte aligned; s and z fp16 [N, G], required iff the plan has them) into
+ * the plan's blob.  Asynchronous on `stream`.
+ */
+qgemm_status qgemm_pack_gated(const qgemm_plan* plan, const void* w_gate, const void* s_gate,
+                              const void* z_gate, const void* w_up, const void* s_up,
+                              const void* z_up, void* packed, void* stream);
+
+/*
+ * Run a gated plan on `stream` for M rows, 1 <= M <= the plan's M (the kernels are
+ * chosen for this M).
+ *   A              device, [M, K] fp16 or int8, 16-byte aligned.
+ *   packed         device, the blob of qgemm_pack_gated, 16-byte aligned.
+ *   row_scales     device, fp32 [M]; col_scales_gate / _up fp32 [N]: the scales of
+ *                  int8 activations and weights as in qgemm_run_scaled.  Required iff
+ *                  the activations are int8, else all three must be NULL.
+ *   bias_gate, bias_up  device, fp16 [N], each may be NULL (none).
+ *   preact         device, fp16 [M, 2 N] or NULL: receives the two pre-activations of each
+ *                  row (gate, then up), rounded to fp16, for qgemm_gated_backward.
+ *   C              device, fp16 [M, N]; fully overwritten.
+ *   workspace, workspace_bytes: as in qgemm_run.
+ */
+qgemm_status qgemm_run_gated(const qgemm_plan* plan, int64_t M, const void* A, const void* packed,
+                             const float* row_scales, const float* col_scales_gate,
+                             const float* col_scales_up, const void* bias_gate, const void* bias_up,
+                             void* preact, void* C, void* workspace, size_t workspace_bytes,
+                             void* stream);
+
+/*
+ * Workspace of qgemm_gated_backward for M rows; weight_grads: whether any weight or bias
+ * gradient will be asked for.  QGEMM_ERR_UNSUPPORTED for int8 activations, for weight
+ * gradients of quantised weights (which are frozen), and where an operand of the
+ * products passes the size limits of qgemm_create.
+ */
+qgemm_status qgemm_gated_backward_workspace(const qgemm_plan* plan, int64_t M, int32_t weight_grads,
+                                            size_t* workspace_bytes);
+
+/*
+ * Gradients of a gated run of M rows from the gradient of its output:
+ *   dU = dC act(g), dG = dC u act'(g);  dA = dG . Wg^T + dU . Wu^T,
+ *   dWg = dG^T . A, dWu = dU^T . A, dbg and dbu the column sums of dG and dU
+ * with g and u the pre-activations as kept (rounded to fp16) and dG, dU rounded to fp16
+ * as operands of the products, which sum in fp32.  Quantised weights enter dA as
+ * (q - z) s rounded to fp16.
+ *   A          device, fp16 [M, K] (needed for weight gradients), 16-byte aligned.
+ *   packed     device, the forward's blob (needed for dA), 16-byte aligned.
+ *   preact     device, fp16 [M, 2 N], from the forward.
+ *   dC         device, fp16 [M, N].
+ *   dA         device, fp16 [M, K], or NULL.
+ *   dw_gate, dw_up       device, fp16 [N, K], both or neither (fp16 weights only); where
+ *              dw_up follows dw_gate in memory one product computes both.
+ *   dbias_gate, dbias_up device, fp16 [N], each may be NULL (fp16 weights only).
+ *   workspace  device, >= the bytes of qgemm_gated_backward_workspace, 16-byte aligned.
+ * Every output asked for is fully overwritten; the sums' order is fixed, so results are
+ * bitwise reproducible.  Asynchronous on `stream`.
+ */
+qgemm_status qgemm_gated_backward(const qgemm_plan* plan, int64_t M, const void* A,
+                                  const void* packed, const void* preact, const void* dC, void* dA,
+                                  void* dw_gate, void* dw_up, void* dbias_gate, void* dbias_up,
+                                  void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---- paged key / value cache ---------------------------------------------------
+ *
+ * Keys and values of past tokens in fp16 pages: k and v are device arrays
+ * [n_pages, kv_heads, page_size, head_dim], contiguous, 16-byte aligned, owned by the
+ * caller.  page_size is a power of two up to 65536; head_dim a multiple of 8 up to 256
+ * (else QGEMM_ERR_UNSUPPORTED).  A token's slot is page * page_size + its place in the
+ * page.  Offsets are 64 bits wide: a cache may pass 2^32 values.
+ */
+typedef struct {
+  void* k;
+  void* v;
+  int64_t n_pages;
+  int32_t page_size;
+  int32_t kv_heads;
+  int32_t head_dim;
+} qgemm_kv_cache;
+
+/*
+ * Rotate the queries and keys of T new tokens and write the keys and values into the
+ * cache.  Head h of a token is its values h * head_dim .. of the row; of each the first
+ * rot_dim values turn by the token's angles (fp32, one rounding), the others are copied:
+ *   (a, b) -> (a c - b s, b c + a s),  c = cos[p, j], s = sin[p, j], p = positions[t],
+ * over the pairs (j, j + rot_dim / 2), or (2 j, 2 j + 1) when interleaved.
+ *   T           tokens, >= 0 (0: nothing is launched).
+ *   q_heads     query heads, a multiple of the cache's kv_heads.
+ *   q, k, v     device, fp16; row t starts t * stride values in (strides >= the row's
+ *               length, so that they may be slices of one projection's output).
+ *   cos, sin    device, fp32 [n_positions, rot_dim / 2].
+ *   rot_dim     even, 0 .. head_dim (0: cos and sin may be NULL).
+ *   positions   device, int32 [T].  A token whose position is outside [0, n_positions) is
+ *               not stored, and its queries become NaN.
+ *   slots       device, int64 [T], distinct.  A token whose slot is outside the cache
+ *               (negative in unused places of a batch) is not stored.
+ *   q_out       device, fp16 [T, q_heads, head_dim]; may be q itself when q_stride is
+ *               q_heads * head_dim.
+ * 16-byte aligned arrays with strides of whole 8 values take the widest accesses.
+ */
+qgemm_status qgemm_kv_append(const qgemm_kv_cache* cache, int64_t T, int32_t q_heads, const void* q,
+                             int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                             int64_t v_stride, const float* cos, const float* sin,
+                             int64_t n_positions, int32_t rot_dim, int32_t interleaved,
+                             const int32_t* positions, const int64_t* slots, void* q_out,
+                             void* stream);
+
+/*
+ * Workspace of qgemm_attention for these sizes (0 where no work is split).
+ */
+qgemm_status qgemm_attention_workspace(const qgemm_kv_cache* cache, int64_t T, int32_t q_heads,
+                                       int64_t B, int64_t max_q, int64_t max_len,
+                                       int64_t prefix_len, size_t* workspace_bytes);
+
+/*
+ * Causal attention of B sequences over the cache, all of which may begin with one shared
+ * prefix: out = softmax(scale q K^T) V per query and head, with scores, softmax and sums
+ * in fp32 and the probabilities rounded to fp16 as operands of the product with V.
+ * Query head h reads key / value head h / (q_heads / kv_heads).
+ *   T            rows of q: the queries of all sequences, one after the other.
+ *   q            device, fp16, row t at t * q_stride values (q_stride >= q_heads *
+ *                head_dim, a multiple of 8; q 16-byte aligned).
+ *   q_starts     device, int32 [B + 1]: sequence b has the rows q_starts[b] ..
+ *                q_starts[b + 1] - 1 (n of them; none is allowed), at most max_q.
+ *   kv_lens      device, int32 [B]: own tokens of each sequence in the cache, the n new
+ *                ones included, at most max_len.
+ *   tables       device, int32 [B, table_width]: pages of each sequence's own tokens,
+ *                in order; entries past its last page are not read.
+ *   prefix_table device, int32: pages of the prefix (NULL when prefix_len is 0).
+ *   prefix_len   tokens of the prefix, >= 0; every query sees all of them.
+ * Query i of a sequence sees own token j iff j <= kv_lens[b] - n + i.  A query that sees
+ * nothing gets zeros (and lse -inf).  Keys and values that a query does not see never
+ * enter its result, whatever they hold (NaN and infinities included).
+ *   max_q, max_len  bounds of n and kv_lens (host values, so that a captured call can be
+ *                replayed with other lengths); rows past max_q are not written, tokens past
+ *                max_len or the table not read.  A page number outside the cache reads
+ *                page 0.
+ *   out          device, fp16 [T, q_heads, head_dim], 16-byte aligned; rows of no
+ *                sequence are not written.
+ *   lse          device, fp32 [T, q_heads] or NULL: ln(sum exp(scale q k)) of each row.
+ *   workspace, workspace_bytes: as stated by qgemm_attention_workspace, 16-byte aligned.
+ * The prefix is read once for rows of all sequences where sequences have few rows each;
+ * keys are split over workgroups where rows are few, and the parts' results joined in a
+ * fixed order: results are bitwise reproducible for the same sizes.
+ */
+qgemm_status qgemm_attention(const qgemm_kv_cache* cache, int64_t T, int32_t q_heads, const void* q,
+                             int64_t q_stride, int64_t B, const int32_t* q_starts,
+                             const int32_t* kv_lens, const int32_t* tables, int64_t table_width,
+                             const int32_t* prefix_table, int64_t prefix_len, int64_t max_q,
+                             int64_t max_len, float scale, void* out, float* lse, void* workspace,
+                             size_t workspace_bytes, void* stream);
+
 /* Release a plan; NULL is a no-op.  Device buffers are the caller's. */
 void qgemm_destroy(qgemm_plan* plan);
 

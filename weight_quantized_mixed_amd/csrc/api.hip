@@ -35,6 +35,8 @@ struct qgemm_plan {
   int32_t auto_parts;  // k_parts 1: parts the library splits K into on its own (0: none) ...
   int32_t auto_min_m;  // ... for runs of at least this many rows
   size_t ws_bytes;
+  int64_t gate_n;      // gated plans: output columns (N then counts the inner columns), else 0
+  float act_c0, act_c1;  // their activation, x sigmoid(x (c0 + c1 x^2))
 };
 
 namespace {
@@ -116,7 +118,8 @@ qgemm_status fill_layout(Layout* L, int fmt, int64_t N, int64_t K, int32_t g, bo
 #define QG_GEMV_NARROW_BELOW 128
 #endif
 bool choose_gemv_narrow(const qgemm_plan* p, int64_t M, int kp) {
-  return M == 1 && (p->N + 63) / 64 * kp < QG_GEMV_NARROW_BELOW;
+  // gated plans pair the column blocks, which the 16-column workgroups cannot
+  return !p->gate_n && M == 1 && (p->N + 63) / 64 * kp < QG_GEMV_NARROW_BELOW;
 }
 
 int choose_gemv_waves(const qgemm_plan* p, int cols, int kp) {
@@ -141,7 +144,7 @@ int choose_gemv_cb(const qgemm_plan* p, int kp) {
     const int64_t waves = (wgs + 255) / 256;
     if (wgs * 10 >= waves * 256 * 6) return cb;
   }
-  return 1;
+  return p->gate_n ? 2 : 1;  // a gate / up pair of blocks stays in one workgroup
 }
 
 // LDS-staged kernel: largest tile that still gives every CU a workgroup (256 CUs).
@@ -243,13 +246,16 @@ qg_choice choose(const qgemm_plan* p, int64_t M) {
                                                           scale_mode(p->L.fmt, p->group_size))
                                         : -1;
   c.gemv_narrow = c.path == QGEMM_PATH_GEMV && choose_gemv_narrow(p, M, kp);
-  c.gemv_mfma = !c.gemv_narrow && M >= QG_GEMV_MFMA_MIN_M && M <= QG_GEMV_MFMA_MAX_M &&
+  // a gated plan too narrow for the 64-column GEMV at one row takes the matrix-core GEMVs,
+  // whose workgroups may be 32 columns
+  const bool gate_narrow = p->gate_n && M == 1 && (p->N + 63) / 64 * kp < QG_GEMV_NARROW_BELOW;
+  c.gemv_mfma = !c.gemv_narrow && (gate_narrow || M >= QG_GEMV_MFMA_MIN_M) && M <= QG_GEMV_MFMA_MAX_M &&
                 ((QG_GEMV_MFMA_FMTS >> p->L.fmt) & 1);
   const int smode = scale_mode(p->L.fmt, p->group_size);
   // two rows as well when the matrix is narrow enough for 16- or 32-column
   // workgroups, which the dot-product GEMV does not have (N = 4096: 4.8 against
   // 7.8 us at K = 4096, 8.4 against 16.0 us at K = 11008)
-  const int min_m4 = choose_gemv_cb(p, kp) < 4 ? 2 : QG_GEMV4_MFMA_MIN_M;
+  const int min_m4 = gate_narrow ? 1 : choose_gemv_cb(p, kp) < 4 ? 2 : QG_GEMV4_MFMA_MIN_M;
   c.gemv_mfma4 = (p->L.fmt == FMT_I4 || p->L.fmt == FMT_U4) && !c.gemv_narrow && smode != SC_PIECE &&
                  M >= min_m4 && M <= (smode == SC_NONE ? QG_GEMV4_MFMA_MAX_M_UNSCALED : QG_GEMV4_MFMA_MAX_M);
   c.gemv_cb = (c.gemv_mfma || c.gemv_mfma4) ? choose_gemv_cb(p, kp) : 4;
@@ -291,11 +297,17 @@ RunArgs make_args(const qgemm_plan* p, const qg_choice& ch, int64_t M, const voi
   a.waves = ch.gemv_waves;
   a.gemv_cb = ch.gemv_cb;
   a.sb_per_group = p->group_size > KB ? p->group_size / KB : p->group_size < 0 ? (int32_t)p->L.nkb : 1;
-  a.out_mode = sp.kp == 1 ? OUT_STORE : sp.two_pass ? OUT_PARTIAL : OUT_ATOMIC;
+  a.out_mode = sp.kp == 1 ? (p->gate_n ? OUT_GATE : OUT_STORE) : sp.two_pass ? OUT_PARTIAL : OUT_ATOMIC;
   a.zr = nullptr;
   a.zp = nullptr;
   a.zr_gp = 0;
   a.zr_G = 0;
+  a.gate_n = (int32_t)p->gate_n;
+  a.act_c0 = p->act_c0;
+  a.act_c1 = p->act_c1;
+  a.bias_up = nullptr;
+  a.col_scale_up = nullptr;
+  a.preact = nullptr;
   return a;
 }
 
@@ -364,10 +376,17 @@ int64_t fold_rows(const qgemm_plan* p) {
   return 0;
 }
 
+// what a gated run adds to the gate projection's bias and column scales
+struct GateIo {
+  const void* bias_up = nullptr;
+  const float* col_scales_up = nullptr;
+  void* preact = nullptr;
+};
+
 // one run: the split-K fill, the kernel chosen for M rows, the finalize pass
 qgemm_status run_impl(const qgemm_plan* plan, int64_t M, const void* A, const void* packed, const void* bias,
                       const float* row_scales, const float* col_scales, void* C, void* workspace,
-                      size_t workspace_bytes, void* stream) {
+                      size_t workspace_bytes, void* stream, const GateIo& gate = {}) {
   if (!plan || !A || !packed || !C) return QGEMM_ERR_INVALID_ARG;
   if (M < 1 || M > plan->M) return QGEMM_ERR_INVALID_ARG;
   const qg_choice ch = M == plan->M ? plan->ch : choose(plan, M);
@@ -382,10 +401,16 @@ qgemm_status run_impl(const qgemm_plan* plan, int64_t M, const void* A, const vo
   if (reinterpret_cast<uintptr_t>(bias) & (out_f16 ? 1 : 3)) return QGEMM_ERR_INVALID_ARG;
   if ((reinterpret_cast<uintptr_t>(row_scales) | reinterpret_cast<uintptr_t>(col_scales)) & 3)
     return QGEMM_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(gate.bias_up) | reinterpret_cast<uintptr_t>(gate.preact)) & 1)
+    return QGEMM_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(gate.col_scales_up) & 3) return QGEMM_ERR_INVALID_ARG;
   hipStream_t st = static_cast<hipStream_t>(stream);
   RunArgs a = make_args(plan, ch, M, A, packed, bias, C, workspace);
   a.row_scale = row_scales;
   a.col_scale = col_scales;
+  a.bias_up = gate.bias_up;
+  a.col_scale_up = gate.col_scales_up;
+  a.preact = static_cast<_Float16*>(gate.preact);
   (void)hipGetLastError();  // clear an error left by an unrelated earlier call on this thread
   hipError_t e = hipSuccess;
   if (plan->L.Kpad != plan->K) {
@@ -418,11 +443,176 @@ qgemm_status run_impl(const qgemm_plan* plan, int64_t M, const void* A, const vo
         : ch.dl_tile >= 0 ? launch_mfma_dl(plan->L.fmt, ch.dl_tile, a, st)
         : launch_mfma(plan->L.fmt, ch.tile, a, st);
   if (e == hipSuccess && (a.out_mode == OUT_PARTIAL || (a.out_mode == OUT_ATOMIC && out_f16)))
-    e = launch_finalize(a, acc_fp, st);
+    e = plan->gate_n ? launch_finalize_gate(a, acc_fp, st) : launch_finalize(a, acc_fp, st);
   return e == hipSuccess ? QGEMM_OK : QGEMM_ERR_DEVICE;
 }
 
 bool dequant_plan(const qgemm_plan* p) { return p->a_dtype == QGEMM_I8 && p->out_dtype == QGEMM_F16; }
+
+int64_t split_unit(int fmt, int32_t group_size) {
+  return scale_mode(fmt, group_size) == SC_BLOCK && group_size > kb_of(fmt) ? group_size : kgrain_of(fmt);
+}
+
+// Fills *p for a validated problem; gate_n output columns for a gated plan (N is then
+// the inner columns), else 0.
+void init_plan(qgemm_plan* p, int64_t M, int64_t N, int64_t K, qgemm_dtype a_dtype, qgemm_dtype w_dtype,
+               qgemm_dtype out_dtype, qgemm_dtype accum_dtype, int32_t group_size, int32_t has_zeros, int32_t k_parts,
+               uint32_t flags, int64_t gate_n, float act_c0, float act_c1) {
+  p->M = M;
+  p->N = N;
+  p->K = K;
+  p->a_dtype = a_dtype;
+  p->w_dtype = w_dtype;
+  p->out_dtype = out_dtype;
+  p->accum_dtype = accum_dtype;
+  p->group_size = group_size;
+  p->has_zeros = has_zeros;
+  p->k_parts = k_parts;
+  p->flags = flags;
+  p->gate_n = gate_n;
+  p->act_c0 = act_c0;
+  p->act_c1 = act_c1;
+  const int fmt = fmt_of(w_dtype), KB = kb_of(fmt);
+  fill_layout(&p->L, fmt, N, K, group_size, has_zeros != 0);
+  // split unit: whole superblocks, and whole groups when groups are whole superblocks
+  // (then K is a multiple of the group, so Kpad = K)
+  const int64_t unit = split_unit(fmt, group_size), Kpad = p->L.Kpad, n_units = Kpad / unit;
+  p->unit_kb = (int32_t)(unit / KB);
+  p->n_units = (int32_t)n_units;
+  const qg_auto au = auto_parts_of(fmt, group_size, M, N, Kpad, k_parts, n_units);
+  p->auto_parts = au.parts;
+  p->auto_min_m = au.min_m;
+  const size_t mn4 = (size_t)M * (size_t)N * 4;
+  p->two_pass = k_parts > 1 && two_pass_split(M, mn4 * (size_t)k_parts, out_dtype == QGEMM_F16, flags);
+  p->ch = choose(p, M);
+  // int32 output with atomics: none (straight into C).  With the folding, the planes
+  // of the largest run that takes it, so that runs of fewer rows never need more than
+  // the plan states
+  p->ws_bytes = run_ws_bytes(p, M, p->ch);
+  const int64_t mf = fold_rows(p);
+  if (mf > 0 && run_ws_bytes_for(p, mf, true) > p->ws_bytes) p->ws_bytes = run_ws_bytes_for(p, mf, true);
+}
+
+// Checks a problem and creates its plan.
+qgemm_status create_impl(qgemm_plan** out, int64_t M, int64_t N, int64_t K, qgemm_dtype a_dtype, qgemm_dtype w_dtype,
+                         qgemm_dtype out_dtype, qgemm_dtype accum_dtype, int32_t group_size, int32_t has_zeros,
+                         int32_t k_parts, uint32_t flags, int64_t gate_n, float act_c0, float act_c1,
+                         size_t* packed_bytes, size_t* workspace_bytes) {
+  if (!out) return QGEMM_ERR_INVALID_ARG;
+  *out = nullptr;
+  if (M < 1 || N < 1 || K < 1) return QGEMM_ERR_INVALID_ARG;
+  if (M > INT32_MAX || N > INT32_MAX || K > INT32_MAX) return QGEMM_ERR_UNSUPPORTED;
+  if (!known_dtype(a_dtype) || !known_dtype(w_dtype) || !known_dtype(out_dtype) || !known_dtype(accum_dtype))
+    return QGEMM_ERR_INVALID_ARG;
+  if (has_zeros != 0 && has_zeros != 1) return QGEMM_ERR_INVALID_ARG;
+  if (k_parts < 1) return QGEMM_ERR_INVALID_ARG;
+  if (flags & ~(QGEMM_DETERMINISTIC | QGEMM_SPLIT_AUTO)) return QGEMM_ERR_INVALID_ARG;
+  if (group_size < -1) return QGEMM_ERR_INVALID_ARG;
+
+  // legal format tuples
+  const bool fp_tuple = a_dtype == QGEMM_F16 && out_dtype == QGEMM_F16 && accum_dtype == QGEMM_F32 &&
+                        (w_dtype == QGEMM_I4 || w_dtype == QGEMM_U4 || w_dtype == QGEMM_F16);
+  // int8 activations: int32 output, or fp16 output dequantised with per-row and
+  // per-column scales (qgemm_run_scaled)
+  const bool int_tuple = a_dtype == QGEMM_I8 && (out_dtype == QGEMM_I32 || out_dtype == QGEMM_F16) &&
+                         accum_dtype == QGEMM_I32 && (w_dtype == QGEMM_I8 || w_dtype == QGEMM_I2);
+  if (!fp_tuple && !int_tuple) return QGEMM_ERR_UNSUPPORTED;
+  const int fmt = fmt_of(w_dtype);
+  const int KB = kb_of(fmt);
+  const bool scaled_fmt = fmt == FMT_I4 || fmt == FMT_U4;
+
+  // scaling and zero points
+  if (!scaled_fmt && group_size != 0) return QGEMM_ERR_UNSUPPORTED;
+  if (has_zeros && (fmt != FMT_U4 || group_size == 0)) return QGEMM_ERR_UNSUPPORTED;
+  if (group_size > 0 && (K % group_size != 0 || group_size % 32 != 0)) return QGEMM_ERR_UNSUPPORTED;
+  // K: whole canonical words (8 int4, 16 int2 values); the kernels run on K padded
+  // to whole superblocks
+  if (K % pack_factor(fmt) != 0) return QGEMM_ERR_UNSUPPORTED;
+  const int64_t Kpad = round_up(K, kgrain_of(fmt));
+  if (Kpad > INT32_MAX) return QGEMM_ERR_UNSUPPORTED;
+
+  // kernels index the blob with 32-bit uint4 offsets and the activations with
+  // 32-bit byte offsets
+  if ((N + 255) / 256 * 256 / 16 * (Kpad / KB) * 64 >= INT32_MAX) return QGEMM_ERR_UNSUPPORTED;
+  if ((uint64_t)M * (uint64_t)Kpad * (a_dtype == QGEMM_F16 ? 2u : 1u) >= ((uint64_t)1 << 32))
+    return QGEMM_ERR_UNSUPPORTED;
+
+  if (k_parts > Kpad / split_unit(fmt, group_size)) return QGEMM_ERR_INVALID_ARG;
+
+  qgemm_plan* p = new (std::nothrow) qgemm_plan();
+  if (!p) return QGEMM_ERR_NO_MEMORY;
+  init_plan(p, M, N, K, a_dtype, w_dtype, out_dtype, accum_dtype, group_size, has_zeros, k_parts, flags, gate_n, act_c0,
+            act_c1);
+  if (packed_bytes) *packed_bytes = p->L.total;
+  if (workspace_bytes) *workspace_bytes = p->ws_bytes;
+  *out = p;
+  return QGEMM_OK;
+}
+
+// The backward pass of a gated plan for M rows: its two fp16 products and the offsets of
+// what they read in the workspace.
+struct GateBackward {
+  qgemm_plan to_a;  // dA [M, K] = pre-activation gradients [M, kd] . transposed weights
+  qgemm_plan to_w;  // dW [2 N, K] = transposed gradients [2 N, mp] . A
+  int64_t kd, mp;   // reduction lengths, whole granules of the fp16 format
+  size_t rowwise, colwise, bias, blob, split, bytes;
+
+  qgemm_status init(const qgemm_plan* p, int64_t M, bool weight_grads) {
+    if (!p->gate_n || M < 1 || M > p->M) return QGEMM_ERR_INVALID_ARG;
+    // int8 activations are not differentiable; quantised weights are frozen
+    if (p->a_dtype != QGEMM_F16 || (weight_grads && p->w_dtype != QGEMM_F16)) return QGEMM_ERR_UNSUPPORTED;
+    const int64_t grain = kgrain_of(FMT_F16);
+    kd = round_up(p->N, grain);
+    mp = round_up(M, grain);
+    // the transposing passes index their grids' rows in 16 bits
+    if (kd / 32 > 65535 || mp / 32 > 65535) return QGEMM_ERR_UNSUPPORTED;
+    const int64_t most = M > 2 * p->gate_n ? M : 2 * p->gate_n;
+    const int64_t blob_k = kd > mp || !weight_grads ? kd : mp;
+    if ((uint64_t)M * kd * 2 >= (uint64_t)1 << 32 || round_up(p->K, 256) / 16 * (blob_k / 32) * 64 >= INT32_MAX ||
+        (weight_grads && (uint64_t)most * mp * 2 >= (uint64_t)1 << 32))
+      return QGEMM_ERR_UNSUPPORTED;
+    init_plan(&to_a, M, p->K, kd, QGEMM_F16, QGEMM_F16, QGEMM_F16, QGEMM_F32, 0, 0, 1, 0, 0, 0.f, 0.f);
+    if (weight_grads)
+      init_plan(&to_w, 2 * p->gate_n, p->K, mp, QGEMM_F16, QGEMM_F16, QGEMM_F16, QGEMM_F32, 0, 0, 1, 0, 0, 0.f, 0.f);
+    auto place = [this](size_t n) {
+      const size_t at = bytes;
+      bytes += (size_t)round_up((int64_t)n, 256);
+      return at;
+    };
+    bytes = 0;
+    rowwise = place((size_t)M * kd * 2);
+    colwise = place(weight_grads ? (size_t)2 * p->gate_n * mp * 2 : 0);
+    bias = place(weight_grads ? (size_t)gate_grad_row_tiles(M) * 2 * p->gate_n * 4 : 0);
+    // the products run one after the other and share the space of their weights
+    blob = place(weight_grads && to_w.L.total > to_a.L.total ? to_w.L.total : to_a.L.total);
+    split = place(weight_grads && to_w.ws_bytes > to_a.ws_bytes ? to_w.ws_bytes : to_a.ws_bytes);
+    return QGEMM_OK;
+  }
+};
+
+// the cache descriptor and a number of query heads: what both cache calls ask of them
+qgemm_status check_cache(const qgemm_kv_cache* c, int64_t T, int32_t q_heads) {
+  if (!c || !c->k || !c->v || c->n_pages < 1 || c->page_size < 1 || c->kv_heads < 1 || c->head_dim < 1)
+    return QGEMM_ERR_INVALID_ARG;
+  if (T < 0 || q_heads < 1 || q_heads % c->kv_heads != 0) return QGEMM_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(c->k) | reinterpret_cast<uintptr_t>(c->v)) & 15) return QGEMM_ERR_INVALID_ARG;
+  if ((c->page_size & (c->page_size - 1)) != 0 || c->page_size > 65536) return QGEMM_ERR_UNSUPPORTED;
+  if (c->head_dim % 8 != 0 || c->head_dim > 256) return QGEMM_ERR_UNSUPPORTED;
+  if (c->n_pages > INT32_MAX || T > INT32_MAX || q_heads > 65535) return QGEMM_ERR_UNSUPPORTED;
+  return QGEMM_OK;
+}
+
+// the sizes of an attention call, checked
+qgemm_status attention_shape(const qgemm_kv_cache* c, int64_t T, int32_t q_heads, int64_t B, int64_t max_q,
+                             int64_t max_len, int64_t prefix_len, AttnShape* s) {
+  const qgemm_status st = check_cache(c, T, q_heads);
+  if (st != QGEMM_OK) return st;
+  if (B < 1 || max_q < 1 || max_len < 0 || prefix_len < 0) return QGEMM_ERR_INVALID_ARG;
+  if (B > 65535 || max_q > INT32_MAX || max_len > INT32_MAX || prefix_len > INT32_MAX) return QGEMM_ERR_UNSUPPORTED;
+  if (max_len + prefix_len > INT32_MAX - 65536) return QGEMM_ERR_UNSUPPORTED;  // key positions are 32 bits wide
+  *s = {T, B, max_q < T ? max_q : T, max_len, prefix_len, q_heads, c->kv_heads, c->head_dim};
+  return QGEMM_OK;
+}
 
 }  // namespace
 
@@ -464,105 +654,31 @@ qgemm_status qgemm_create(qgemm_plan** out, int64_t M, int64_t N, int64_t K, qge
                           qgemm_dtype w_dtype, qgemm_dtype out_dtype, qgemm_dtype accum_dtype,
                           int32_t group_size, int32_t has_zeros, int32_t k_parts, uint32_t flags,
                           size_t* packed_bytes, size_t* workspace_bytes) {
-  if (!out) return QGEMM_ERR_INVALID_ARG;
-  *out = nullptr;
-  if (M < 1 || N < 1 || K < 1) return QGEMM_ERR_INVALID_ARG;
-  if (M > INT32_MAX || N > INT32_MAX || K > INT32_MAX) return QGEMM_ERR_UNSUPPORTED;
-  if (!known_dtype(a_dtype) || !known_dtype(w_dtype) || !known_dtype(out_dtype) || !known_dtype(accum_dtype))
-    return QGEMM_ERR_INVALID_ARG;
-  if (has_zeros != 0 && has_zeros != 1) return QGEMM_ERR_INVALID_ARG;
-  if (k_parts < 1) return QGEMM_ERR_INVALID_ARG;
-  if (flags & ~(QGEMM_DETERMINISTIC | QGEMM_SPLIT_AUTO)) return QGEMM_ERR_INVALID_ARG;
-  if (group_size < -1) return QGEMM_ERR_INVALID_ARG;
-
-  // legal format tuples
-  const bool fp_tuple = a_dtype == QGEMM_F16 && out_dtype == QGEMM_F16 && accum_dtype == QGEMM_F32 &&
-                        (w_dtype == QGEMM_I4 || w_dtype == QGEMM_U4 || w_dtype == QGEMM_F16);
-  // int8 activations: int32 output, or fp16 output dequantised with per-row and
-  // per-column scales (qgemm_run_scaled)
-  const bool int_tuple = a_dtype == QGEMM_I8 && (out_dtype == QGEMM_I32 || out_dtype == QGEMM_F16) &&
-                         accum_dtype == QGEMM_I32 && (w_dtype == QGEMM_I8 || w_dtype == QGEMM_I2);
-  if (!fp_tuple && !int_tuple) return QGEMM_ERR_UNSUPPORTED;
-  const int fmt = fmt_of(w_dtype);
-  const int KB = kb_of(fmt);
-  const bool scaled_fmt = fmt == FMT_I4 || fmt == FMT_U4;
-
-  // scaling and zero points
-  if (!scaled_fmt && group_size != 0) return QGEMM_ERR_UNSUPPORTED;
-  if (has_zeros && (fmt != FMT_U4 || group_size == 0)) return QGEMM_ERR_UNSUPPORTED;
-  if (group_size > 0 && (K % group_size != 0 || group_size % 32 != 0)) return QGEMM_ERR_UNSUPPORTED;
-  // K: whole canonical words (8 int4, 16 int2 values); the kernels run on K padded
-  // to whole superblocks
-  if (K % pack_factor(fmt) != 0) return QGEMM_ERR_UNSUPPORTED;
-  const int64_t Kpad = round_up(K, kgrain_of(fmt));
-  if (Kpad > INT32_MAX) return QGEMM_ERR_UNSUPPORTED;
-
-  // kernels index the blob with 32-bit uint4 offsets and the activations with
-  // 32-bit byte offsets
-  if ((N + 255) / 256 * 256 / 16 * (Kpad / KB) * 64 >= INT32_MAX) return QGEMM_ERR_UNSUPPORTED;
-  if ((uint64_t)M * (uint64_t)Kpad * (a_dtype == QGEMM_F16 ? 2u : 1u) >= ((uint64_t)1 << 32))
-    return QGEMM_ERR_UNSUPPORTED;
-
-  // split unit: whole superblocks, and whole groups when groups are whole superblocks
-  // (then K is a multiple of the group, so Kpad = K)
-  const int64_t unit = scale_mode(fmt, group_size) == SC_BLOCK && group_size > KB ? group_size : kgrain_of(fmt);
-  const int64_t n_units = Kpad / unit;
-  if (k_parts > n_units) return QGEMM_ERR_INVALID_ARG;
-
-  qgemm_plan* p = new (std::nothrow) qgemm_plan();
-  if (!p) return QGEMM_ERR_NO_MEMORY;
-  p->M = M;
-  p->N = N;
-  p->K = K;
-  p->a_dtype = a_dtype;
-  p->w_dtype = w_dtype;
-  p->out_dtype = out_dtype;
-  p->accum_dtype = accum_dtype;
-  p->group_size = group_size;
-  p->has_zeros = has_zeros;
-  p->k_parts = k_parts;
-  p->flags = flags;
-  fill_layout(&p->L, fmt, N, K, group_size, has_zeros != 0);
-  p->unit_kb = (int32_t)(unit / KB);
-  p->n_units = (int32_t)n_units;
-  const qg_auto au = auto_parts_of(fmt, group_size, M, N, Kpad, k_parts, n_units);
-  p->auto_parts = au.parts;
-  p->auto_min_m = au.min_m;
-  const size_t mn4 = (size_t)M * (size_t)N * 4;
-  p->two_pass = k_parts > 1 && two_pass_split(M, mn4 * (size_t)k_parts, out_dtype == QGEMM_F16, flags);
-  p->ch = choose(p, M);
-  // int32 output with atomics: none (straight into C).  With the folding, the planes
-  // of the largest run that takes it, so that runs of fewer rows never need more than
-  // the plan states
-  p->ws_bytes = run_ws_bytes(p, M, p->ch);
-  const int64_t mf = fold_rows(p);
-  if (mf > 0 && run_ws_bytes_for(p, mf, true) > p->ws_bytes) p->ws_bytes = run_ws_bytes_for(p, mf, true);
-  if (packed_bytes) *packed_bytes = p->L.total;
-  if (workspace_bytes) *workspace_bytes = p->ws_bytes;
-  *out = p;
-  return QGEMM_OK;
+  return create_impl(out, M, N, K, a_dtype, w_dtype, out_dtype, accum_dtype, group_size, has_zeros, k_parts, flags, 0,
+                     0.f, 0.f, packed_bytes, workspace_bytes);
 }
 
 qgemm_status qgemm_pack_weights(const qgemm_plan* plan, const void* w, const void* scales, const void* zeros,
                                 void* packed, void* stream) {
-  if (!plan || !w || !packed) return QGEMM_ERR_INVALID_ARG;
+  if (!plan || plan->gate_n || !w || !packed) return QGEMM_ERR_INVALID_ARG;
   if (plan->L.G && !scales) return QGEMM_ERR_INVALID_ARG;
   if (plan->L.zeros && !zeros) return QGEMM_ERR_INVALID_ARG;
   if ((reinterpret_cast<uintptr_t>(w) | reinterpret_cast<uintptr_t>(packed)) & 15) return QGEMM_ERR_INVALID_ARG;
   (void)hipGetLastError();  // clear an error left by an unrelated earlier call on this thread
-  hipError_t e = launch_pack(plan->L, w, scales, zeros, packed, static_cast<hipStream_t>(stream));
+  hipError_t e = launch_pack(plan->L, plan->N, {w, scales, zeros}, nullptr, packed,
+                             static_cast<hipStream_t>(stream));
   return e == hipSuccess ? QGEMM_OK : QGEMM_ERR_DEVICE;
 }
 
 qgemm_status qgemm_run_ex(const qgemm_plan* plan, int64_t M, const void* A, const void* packed,
                           const void* bias, void* C, void* workspace, size_t workspace_bytes, void* stream) {
-  if (!plan || dequant_plan(plan)) return QGEMM_ERR_INVALID_ARG;  // those need their scales
+  if (!plan || plan->gate_n || dequant_plan(plan)) return QGEMM_ERR_INVALID_ARG;  // those need their scales
   return run_impl(plan, M, A, packed, bias, nullptr, nullptr, C, workspace, workspace_bytes, stream);
 }
 
 qgemm_status qgemm_run_noalloc(const qgemm_plan* plan, int64_t M, const void* A, const void* packed,
                                const void* bias, void* C, void* stream) {
-  if (!plan || dequant_plan(plan)) return QGEMM_ERR_INVALID_ARG;
+  if (!plan || plan->gate_n || dequant_plan(plan)) return QGEMM_ERR_INVALID_ARG;
   if (M < 1 || M > plan->M) return QGEMM_ERR_INVALID_ARG;
   const size_t need = run_ws_bytes(plan, M, M == plan->M ? plan->ch : choose(plan, M));
   if (need > QGEMM_NOALLOC_MAX_SCRATCH) return QGEMM_ERR_UNSUPPORTED;
@@ -577,8 +693,215 @@ qgemm_status qgemm_run_noalloc(const qgemm_plan* plan, int64_t M, const void* A,
 qgemm_status qgemm_run_scaled(const qgemm_plan* plan, int64_t M, const void* A, const void* packed,
                               const float* row_scales, const float* col_scales, const void* bias, void* C,
                               void* workspace, size_t workspace_bytes, void* stream) {
-  if (!plan || !dequant_plan(plan) || !row_scales || !col_scales) return QGEMM_ERR_INVALID_ARG;
+  if (!plan || plan->gate_n || !dequant_plan(plan) || !row_scales || !col_scales) return QGEMM_ERR_INVALID_ARG;
   return run_impl(plan, M, A, packed, bias, row_scales, col_scales, C, workspace, workspace_bytes, stream);
+}
+
+// ---- gated feed-forward block
+
+qgemm_status qgemm_create_gated(qgemm_plan** out, int64_t M, int64_t N, int64_t K, qgemm_dtype a_dtype,
+                                qgemm_dtype w_dtype, qgemm_dtype out_dtype, qgemm_dtype accum_dtype,
+                                int32_t group_size, int32_t has_zeros, qgemm_act act, size_t* packed_bytes,
+                                size_t* workspace_bytes) {
+  if (!out) return QGEMM_ERR_INVALID_ARG;
+  *out = nullptr;
+  if (N < 1 || (act != QGEMM_ACT_SILU && act != QGEMM_ACT_GELU_TANH)) return QGEMM_ERR_INVALID_ARG;
+  if (N > INT32_MAX / 2 - 16) return QGEMM_ERR_UNSUPPORTED;
+  if (known_dtype(out_dtype) && out_dtype != QGEMM_F16) return QGEMM_ERR_UNSUPPORTED;
+  const float c = 1.5957691216057308f;  // 2 sqrt(2 / pi)
+  return create_impl(out, M, gate_inner(N), K, a_dtype, w_dtype, out_dtype, accum_dtype, group_size, has_zeros, 1, 0, N,
+                     act == QGEMM_ACT_SILU ? 1.f : c, act == QGEMM_ACT_SILU ? 0.f : c * 0.044715f, packed_bytes,
+                     workspace_bytes);
+}
+
+qgemm_status qgemm_pack_gated(const qgemm_plan* plan, const void* w_gate, const void* s_gate, const void* z_gate,
+                              const void* w_up, const void* s_up, const void* z_up, void* packed, void* stream) {
+  if (!plan || !plan->gate_n || !w_gate || !w_up || !packed) return QGEMM_ERR_INVALID_ARG;
+  if (plan->L.G && (!s_gate || !s_up)) return QGEMM_ERR_INVALID_ARG;
+  if (plan->L.zeros && (!z_gate || !z_up)) return QGEMM_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(w_gate) | reinterpret_cast<uintptr_t>(w_up) | reinterpret_cast<uintptr_t>(packed)) & 15)
+    return QGEMM_ERR_INVALID_ARG;
+  (void)hipGetLastError();
+  const Canonical up = {w_up, s_up, z_up};
+  hipError_t e = launch_pack(plan->L, plan->gate_n, {w_gate, s_gate, z_gate}, &up, packed, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? QGEMM_OK : QGEMM_ERR_DEVICE;
+}
+
+qgemm_status qgemm_run_gated(const qgemm_plan* plan, int64_t M, const void* A, const void* packed,
+                             const float* row_scales, const float* col_scales_gate, const float* col_scales_up,
+                             const void* bias_gate, const void* bias_up, void* preact, void* C, void* workspace,
+                             size_t workspace_bytes, void* stream) {
+  if (!plan || !plan->gate_n) return QGEMM_ERR_INVALID_ARG;
+  const bool scaled = dequant_plan(plan);
+  if (scaled && (!row_scales || !col_scales_gate || !col_scales_up)) return QGEMM_ERR_INVALID_ARG;
+  if (!scaled && (row_scales || col_scales_gate || col_scales_up)) return QGEMM_ERR_INVALID_ARG;
+  GateIo io;
+  io.bias_up = bias_up;
+  io.col_scales_up = col_scales_up;
+  io.preact = preact;
+  return run_impl(plan, M, A, packed, bias_gate, row_scales, col_scales_gate, C, workspace, workspace_bytes, stream, io);
+}
+
+qgemm_status qgemm_gated_backward_workspace(const qgemm_plan* plan, int64_t M, int32_t weight_grads,
+                                            size_t* workspace_bytes) {
+  if (!plan || !workspace_bytes) return QGEMM_ERR_INVALID_ARG;
+  GateBackward b;
+  const qgemm_status s = b.init(plan, M, weight_grads != 0);
+  if (s == QGEMM_OK) *workspace_bytes = b.bytes;
+  return s;
+}
+
+qgemm_status qgemm_gated_backward(const qgemm_plan* plan, int64_t M, const void* A, const void* packed,
+                                  const void* preact, const void* dC, void* dA, void* dw_gate, void* dw_up,
+                                  void* dbias_gate, void* dbias_up, void* workspace, size_t workspace_bytes,
+                                  void* stream) {
+  if (!plan || !preact || !dC) return QGEMM_ERR_INVALID_ARG;
+  const bool weight_grads = dw_gate || dw_up || dbias_gate || dbias_up;
+  if (!dA && !weight_grads) return QGEMM_ERR_INVALID_ARG;
+  if ((dw_gate != nullptr) != (dw_up != nullptr)) return QGEMM_ERR_INVALID_ARG;
+  if ((dA && !packed) || (dw_gate && !A)) return QGEMM_ERR_INVALID_ARG;
+  GateBackward b;
+  const qgemm_status s = b.init(plan, M, weight_grads);
+  if (s != QGEMM_OK) return s;
+  if (!workspace || workspace_bytes < b.bytes) return QGEMM_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(A) | reinterpret_cast<uintptr_t>(packed) | reinterpret_cast<uintptr_t>(workspace)) & 15)
+    return QGEMM_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(preact) | reinterpret_cast<uintptr_t>(dC) | reinterpret_cast<uintptr_t>(dA) |
+       reinterpret_cast<uintptr_t>(dw_gate) | reinterpret_cast<uintptr_t>(dw_up) |
+       reinterpret_cast<uintptr_t>(dbias_gate) | reinterpret_cast<uintptr_t>(dbias_up)) & 1)
+    return QGEMM_ERR_INVALID_ARG;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  (void)hipGetLastError();
+  char* ws = static_cast<char*>(workspace);
+  const int64_t N = plan->gate_n;
+  hipError_t e = launch_gate_grad(preact, dC, M, N, b.kd, b.mp, plan->act_c0, plan->act_c1, dA ? ws + b.rowwise : nullptr,
+                                  weight_grads ? ws + b.colwise : nullptr,
+                                  dbias_gate || dbias_up ? reinterpret_cast<float*>(ws + b.bias) : nullptr, st);
+  if (e == hipSuccess && (dbias_gate || dbias_up))
+    e = launch_bias_grad(reinterpret_cast<float*>(ws + b.bias), M, N, dbias_gate, dbias_up, st);
+  if (e == hipSuccess && dA) {
+    e = launch_transpose_blob(plan->L, N, packed, b.to_a.L, ws + b.blob, st);
+    if (e == hipSuccess &&
+        run_impl(&b.to_a, M, ws + b.rowwise, ws + b.blob, nullptr, nullptr, nullptr, dA, ws + b.split,
+                 b.to_a.ws_bytes, stream) != QGEMM_OK)
+      return QGEMM_ERR_DEVICE;
+  }
+  if (e == hipSuccess && dw_gate) {
+    e = launch_transpose_rows(A, M, plan->K, b.to_w.L, ws + b.blob, st);
+    // one product for both when the outputs lie one after the other
+    const bool joined = dw_up == static_cast<char*>(dw_gate) + (size_t)N * plan->K * 2;
+    for (int part = 0; e == hipSuccess && part < (joined ? 1 : 2); ++part)
+      if (run_impl(&b.to_w, joined ? 2 * N : N, ws + b.colwise + (size_t)part * N * b.mp * 2, ws + b.blob, nullptr,
+                   nullptr, nullptr, part ? dw_up : dw_gate, ws + b.split, b.to_w.ws_bytes, stream) != QGEMM_OK)
+        return QGEMM_ERR_DEVICE;
+  }
+  return e == hipSuccess ? QGEMM_OK : QGEMM_ERR_DEVICE;
+}
+
+// ---- paged key / value cache
+
+qgemm_status qgemm_kv_append(const qgemm_kv_cache* cache, int64_t T, int32_t q_heads, const void* q, int64_t q_stride,
+                             const void* k, int64_t k_stride, const void* v, int64_t v_stride, const float* cos,
+                             const float* sin, int64_t n_positions, int32_t rot_dim, int32_t interleaved,
+                             const int32_t* positions, const int64_t* slots, void* q_out, void* stream) {
+  const qgemm_status s = check_cache(cache, T, q_heads);
+  if (s != QGEMM_OK) return s;
+  const int64_t kv_row = (int64_t)cache->kv_heads * cache->head_dim;
+  if (rot_dim < 0 || rot_dim % 2 != 0 || rot_dim > cache->head_dim) return QGEMM_ERR_INVALID_ARG;
+  if (interleaved != 0 && interleaved != 1) return QGEMM_ERR_INVALID_ARG;
+  if (q_stride < (int64_t)q_heads * cache->head_dim || k_stride < kv_row || v_stride < kv_row)
+    return QGEMM_ERR_INVALID_ARG;
+  if (T == 0) return QGEMM_OK;
+  if (!q || !k || !v || !slots || !q_out) return QGEMM_ERR_INVALID_ARG;
+  if (rot_dim && (!cos || !sin || !positions || n_positions < 1)) return QGEMM_ERR_INVALID_ARG;
+  if (((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v) |
+        reinterpret_cast<uintptr_t>(q_out)) & 1) ||
+      ((reinterpret_cast<uintptr_t>(cos) | reinterpret_cast<uintptr_t>(sin) |
+        reinterpret_cast<uintptr_t>(positions)) & 3) ||
+      (reinterpret_cast<uintptr_t>(slots) & 7))
+    return QGEMM_ERR_INVALID_ARG;
+  AppendArgs a;
+  a.q = static_cast<const _Float16*>(q);
+  a.k = static_cast<const _Float16*>(k);
+  a.v = static_cast<const _Float16*>(v);
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.cos = cos;
+  a.sin = sin;
+  a.positions = positions;
+  a.slots = slots;
+  a.q_out = static_cast<_Float16*>(q_out);
+  a.k_cache = static_cast<_Float16*>(cache->k);
+  a.v_cache = static_cast<_Float16*>(cache->v);
+  a.n_positions = n_positions;
+  a.n_pages = cache->n_pages;
+  a.page = cache->page_size;
+  a.q_heads = q_heads;
+  a.kv_heads = cache->kv_heads;
+  a.D = cache->head_dim;
+  a.rot = rot_dim;
+  a.interleaved = interleaved;
+  (void)hipGetLastError();
+  hipError_t e = launch_kv_append(a, T, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? QGEMM_OK : QGEMM_ERR_DEVICE;
+}
+
+qgemm_status qgemm_attention_workspace(const qgemm_kv_cache* cache, int64_t T, int32_t q_heads, int64_t B,
+                                       int64_t max_q, int64_t max_len, int64_t prefix_len, size_t* workspace_bytes) {
+  if (!workspace_bytes) return QGEMM_ERR_INVALID_ARG;
+  AttnShape s;
+  const qgemm_status st = attention_shape(cache, T, q_heads, B, max_q, max_len, prefix_len, &s);
+  if (st == QGEMM_OK) *workspace_bytes = T == 0 ? 0 : attention_ws_bytes(s);
+  return st;
+}
+
+qgemm_status qgemm_attention(const qgemm_kv_cache* cache, int64_t T, int32_t q_heads, const void* q, int64_t q_stride,
+                             int64_t B, const int32_t* q_starts, const int32_t* kv_lens, const int32_t* tables,
+                             int64_t table_width, const int32_t* prefix_table, int64_t prefix_len, int64_t max_q,
+                             int64_t max_len, float scale, void* out, float* lse, void* workspace,
+                             size_t workspace_bytes, void* stream) {
+  AttnShape s;
+  const qgemm_status st = attention_shape(cache, T, q_heads, B, max_q, max_len, prefix_len, &s);
+  if (st != QGEMM_OK) return st;
+  if (table_width < 0 || q_stride < (int64_t)q_heads * cache->head_dim) return QGEMM_ERR_INVALID_ARG;
+  if (T == 0) return QGEMM_OK;
+  if (!q || !q_starts || !kv_lens || !out || (table_width && !tables) || (prefix_len && !prefix_table))
+    return QGEMM_ERR_INVALID_ARG;
+  if (q_stride % 8 != 0 || ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out)) & 15))
+    return QGEMM_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(q_starts) | reinterpret_cast<uintptr_t>(kv_lens) |
+       reinterpret_cast<uintptr_t>(tables) | reinterpret_cast<uintptr_t>(prefix_table) |
+       reinterpret_cast<uintptr_t>(lse)) & 3)
+    return QGEMM_ERR_INVALID_ARG;
+  const size_t need = attention_ws_bytes(s);
+  if (need && (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 15)))
+    return QGEMM_ERR_INVALID_ARG;
+  AttnArgs a;
+  a.q = static_cast<const _Float16*>(q);
+  a.k = static_cast<const _Float16*>(cache->k);
+  a.v = static_cast<const _Float16*>(cache->v);
+  a.out = static_cast<_Float16*>(out);
+  a.lse = lse;
+  a.q_starts = q_starts;
+  a.kv_lens = kv_lens;
+  a.tables = tables;
+  a.prefix_table = prefix_table;
+  a.q_stride = q_stride;
+  a.table_width = table_width;
+  a.prefix_len = prefix_len;
+  a.T = (int32_t)T;
+  a.q_heads = q_heads;
+  a.kv_heads = cache->kv_heads;
+  a.D = cache->head_dim;
+  a.n_pages = (int32_t)cache->n_pages;
+  a.page_shift = __builtin_ctz((unsigned)cache->page_size);
+  a.max_q = (int32_t)max_q;
+  a.max_len = (int32_t)max_len;
+  a.scale = scale;
+  (void)hipGetLastError();
+  hipError_t e = launch_attention(a, s, workspace, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? QGEMM_OK : QGEMM_ERR_DEVICE;
 }
 
 qgemm_status qgemm_quantize_rows(const void* A, int64_t M, int64_t K, void* Q, float* scales, void* stream) {

@@ -84,7 +84,9 @@ __device__ __forceinline__ T lane_value(T v, int lane) {
 // VAR (int4 only): 0 unscaled (offsets taken off exactly); 1 folded with one scale group per
 // superblock; 2 as 1 with zero points; 3 exact per-element conversion with a
 // scale group per 32-position piece (group size 32 or 64).  int2 is always folded.
-template <int FMT, int MR, int VAR>
+// GATED: the instances of gated plans (OUT_GATE), kept apart so that the plain ones keep
+// their registers.
+template <int FMT, int MR, int VAR, bool GATED>
 __global__ __launch_bounds__(64 * GEMV_MAX_WAVES) void gemv_kernel(RunArgs a) {
   constexpr bool FOLD = (FMT == FMT_I2) || ((FMT == FMT_I4 || FMT == FMT_U4) && VAR != 3);
   constexpr bool SCALED = VAR == 1 || VAR == 2;
@@ -559,6 +561,20 @@ __global__ __launch_bounds__(64 * GEMV_MAX_WAVES) void gemv_kernel(RunArgs a) {
 #pragma unroll
   for (int m = 0; m < MR; ++m) red[wave][m][lane] = tot[m];
   __syncthreads();
+  if constexpr (GATED) {
+    // lanes 0..15 and 32..47 hold gate columns, the 16 lanes after each their up columns
+    for (int idx = threadIdx.x; idx < MR * 32; idx += blockDim.x) {
+      const int m = idx >> 5, ln = (idx & 16) * 2 + (idx & 15);
+      acc_t g = 0, u = 0;
+      for (int w = 0; w < a.waves; ++w) {
+        g += red[w][m][ln];
+        u += red[w][m][ln + 16];
+      }
+      const GateCol c = gate_col(a, rb * 64 + ln);
+      if (c.in) gate_store(a, m, c, (float)g, (float)u);
+    }
+    return;
+  }
   for (int idx = threadIdx.x; idx < MR * 64; idx += blockDim.x) {
     const int m = idx >> 6, ln = idx & 63;
     acc_t s = 0;
@@ -579,17 +595,22 @@ __global__ __launch_bounds__(64 * GEMV_MAX_WAVES) void gemv_kernel(RunArgs a) {
   }
 }
 
-template <int FMT, int VAR>
-hipError_t launch_fmt(const RunArgs& a, hipStream_t st) {
+template <int FMT, int VAR, bool GATED>
+hipError_t launch_rows(const RunArgs& a, hipStream_t st) {
   dim3 grid((a.N + 63) / 64, a.k_parts), block(64 * a.waves);
   switch (a.M) {
 #define QG_CASE(R) \
-  case R: hipLaunchKernelGGL((gemv_kernel<FMT, R, VAR>), grid, block, 0, st, a); break;
+  case R: hipLaunchKernelGGL((gemv_kernel<FMT, R, VAR, GATED>), grid, block, 0, st, a); break;
     QG_CASE(1) QG_CASE(2) QG_CASE(3) QG_CASE(4) QG_CASE(5) QG_CASE(6) QG_CASE(7) QG_CASE(8)
 #undef QG_CASE
     default: return hipErrorInvalidValue;
   }
   return hipGetLastError();
+}
+
+template <int FMT, int VAR>
+hipError_t launch_fmt(const RunArgs& a, hipStream_t st) {
+  return a.out_mode == OUT_GATE ? launch_rows<FMT, VAR, true>(a, st) : launch_rows<FMT, VAR, false>(a, st);
 }
 
 }  // namespace

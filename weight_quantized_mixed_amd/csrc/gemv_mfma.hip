@@ -73,7 +73,7 @@ __device__ __forceinline__ float4v mfma(const int4v& A, const int4v& B, const fl
 }
 
 // MB row blocks of 16 (M <= 16 MB)
-template <int FMT, int MB, int CB>
+template <int FMT, int MB, int CB, bool GATED>
 __global__ __launch_bounds__(64 * GEMV_MAX_WAVES) void gemv_mfma_kernel(RunArgs a) {
   constexpr bool I2 = FMT == FMT_I2, FP = FMT == FMT_F16;
   constexpr int KB = kb_of(FMT);   // positions per superblock: 256 (int2), 64 (int8), 32 (fp16)
@@ -228,6 +228,23 @@ __global__ __launch_bounds__(64 * GEMV_MAX_WAVES) void gemv_mfma_kernel(RunArgs 
         red[wave][r][cb][i][lane] = v;
       }
   __syncthreads();
+  if constexpr (GATED) {
+    static_assert(CB >= 2, "a gate / up pair of column blocks in one workgroup");
+    // column blocks 2 cp and 2 cp + 1 are the gate and up sums of 16 output columns
+    for (int idx = threadIdx.x; idx < MB * CB / 2 * 4 * 64; idx += blockDim.x) {
+      const int r = idx / (CB / 2 * 256), cp = (idx >> 8) % (CB / 2), i = (idx >> 6) & 3, ln = idx & 63;
+      const int row = r * 16 + 4 * (ln >> 4) + i;
+      const GateCol c = gate_col(a, (rb * CB + 2 * cp) * 16 + (ln & 15));
+      if (row >= a.M || !c.in) continue;
+      acc_t g = 0, u = 0;
+      for (int w = 0; w < a.waves; ++w) {
+        g += red[w][r][2 * cp][i][ln];
+        u += red[w][r][2 * cp + 1][i][ln];
+      }
+      gate_store(a, row, c, (float)g, (float)u);
+    }
+    return;
+  }
   for (int idx = threadIdx.x; idx < MB * CB * 4 * 64; idx += blockDim.x) {
     const int r = idx / (CB * 256), cb = (idx >> 8) % CB, i = (idx >> 6) & 3, ln = idx & 63;
     const int row = r * 16 + 4 * (ln >> 4) + i, col = (rb * CB + cb) * 16 + (ln & 15);
@@ -255,13 +272,21 @@ __global__ __launch_bounds__(64 * GEMV_MAX_WAVES) void gemv_mfma_kernel(RunArgs 
 template <int FMT, int MB, int CB>
 void launch_cb(const RunArgs& a, hipStream_t st) {
   const dim3 grid((a.N + 16 * CB - 1) / (16 * CB), a.k_parts), block(64 * a.waves);
-  hipLaunchKernelGGL((gemv_mfma_kernel<FMT, MB, CB>), grid, block, 0, st, a);
+  if constexpr (CB >= 2)
+    if (a.out_mode == OUT_GATE) {
+      hipLaunchKernelGGL((gemv_mfma_kernel<FMT, MB, CB, true>), grid, block, 0, st, a);
+      return;
+    }
+  hipLaunchKernelGGL((gemv_mfma_kernel<FMT, MB, CB, false>), grid, block, 0, st, a);
 }
 
 template <int FMT, int MB>
 hipError_t launch_mb(const RunArgs& a, hipStream_t st) {
   switch (a.gemv_cb) {
-    case 1: launch_cb<FMT, MB, 1>(a, st); break;
+    case 1:
+      if (a.out_mode == OUT_GATE) return hipErrorInvalidValue;  // pairs of column blocks
+      launch_cb<FMT, MB, 1>(a, st);
+      break;
     case 2: launch_cb<FMT, MB, 2>(a, st); break;
     case 4: launch_cb<FMT, MB, 4>(a, st); break;
     default: return hipErrorInvalidValue;

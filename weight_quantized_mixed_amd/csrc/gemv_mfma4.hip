@@ -77,7 +77,7 @@ __device__ __forceinline__ float4v mfma(const uint4& A, const uint4& B, const fl
 }
 
 // VAR: 0 unscaled, 1 scaled, 2 scaled with zero points
-template <int FMT, int MB, int VAR, int CB>
+template <int FMT, int MB, int VAR, int CB, bool GATED>
 __global__ __launch_bounds__(64 * GEMV_MAX_WAVES) void gemv_mfma4_kernel(RunArgs a) {
   constexpr int KB = 128, NS = 4;  // positions and 32-position MFMA steps per superblock
   constexpr bool SCALED = VAR >= 1, ZEROS = VAR == 2;
@@ -227,6 +227,23 @@ __global__ __launch_bounds__(64 * GEMV_MAX_WAVES) void gemv_mfma4_kernel(RunArgs
 #pragma unroll
       for (int i = 0; i < 4; ++i) red[wave][r][cb][i][lane] = acc[r][cb][i];
   __syncthreads();
+  if constexpr (GATED) {
+    static_assert(CB >= 2, "a gate / up pair of column blocks in one workgroup");
+    // column blocks 2 cp and 2 cp + 1 are the gate and up sums of 16 output columns
+    for (int idx = threadIdx.x; idx < MB * CB / 2 * 4 * 64; idx += blockDim.x) {
+      const int r = idx / (CB / 2 * 256), cp = (idx >> 8) % (CB / 2), i = (idx >> 6) & 3, ln = idx & 63;
+      const int row = r * 16 + 4 * (ln >> 4) + i;
+      const GateCol c = gate_col(a, (rb * CB + 2 * cp) * 16 + (ln & 15));
+      if (row >= a.M || !c.in) continue;
+      float g = 0, u = 0;
+      for (int w = 0; w < a.waves; ++w) {
+        g += red[w][r][2 * cp][i][ln];
+        u += red[w][r][2 * cp + 1][i][ln];
+      }
+      gate_store(a, row, c, (float)g, (float)u);
+    }
+    return;
+  }
   for (int idx = threadIdx.x; idx < MB * CB * 4 * 64; idx += blockDim.x) {
     const int r = idx / (CB * 256), cb = (idx >> 8) % CB, i = (idx >> 6) & 3, ln = idx & 63;
     const int row = r * 16 + 4 * (ln >> 4) + i, col = (rb * CB + cb) * 16 + (ln & 15);
@@ -240,15 +257,23 @@ __global__ __launch_bounds__(64 * GEMV_MAX_WAVES) void gemv_mfma4_kernel(RunArgs
   }
 }
 
-template <int FMT, int MB, int CB>
-hipError_t launch_cb(const RunArgs& a, hipStream_t st) {
+template <int FMT, int MB, int CB, bool GATED>
+hipError_t launch_gated(const RunArgs& a, hipStream_t st) {
   const dim3 grid((a.N + 16 * CB - 1) / (16 * CB), a.k_parts), block(64 * a.waves);
   const int var = a.smode == SC_NONE ? 0 : a.zeros ? 2 : 1;
-  if (var == 0) hipLaunchKernelGGL((gemv_mfma4_kernel<FMT, MB, 0, CB>), grid, block, 0, st, a);
-  else if (var == 1) hipLaunchKernelGGL((gemv_mfma4_kernel<FMT, MB, 1, CB>), grid, block, 0, st, a);
-  else if (FMT == FMT_U4) hipLaunchKernelGGL((gemv_mfma4_kernel<FMT_U4, MB, 2, CB>), grid, block, 0, st, a);
+  if (var == 0) hipLaunchKernelGGL((gemv_mfma4_kernel<FMT, MB, 0, CB, GATED>), grid, block, 0, st, a);
+  else if (var == 1) hipLaunchKernelGGL((gemv_mfma4_kernel<FMT, MB, 1, CB, GATED>), grid, block, 0, st, a);
+  else if (FMT == FMT_U4) hipLaunchKernelGGL((gemv_mfma4_kernel<FMT_U4, MB, 2, CB, GATED>), grid, block, 0, st, a);
   else return hipErrorInvalidValue;
   return hipGetLastError();
+}
+
+template <int FMT, int MB, int CB>
+hipError_t launch_cb(const RunArgs& a, hipStream_t st) {
+  if constexpr (CB >= 2)
+    if (a.out_mode == OUT_GATE) return launch_gated<FMT, MB, CB, true>(a, st);
+  if (a.out_mode == OUT_GATE) return hipErrorInvalidValue;  // pairs of column blocks
+  return launch_gated<FMT, MB, CB, false>(a, st);
 }
 
 template <int FMT, int MB>

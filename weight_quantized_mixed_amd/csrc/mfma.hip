@@ -47,7 +47,7 @@ constexpr int kstep_of(int fmt, int bm) {
   return (fmt == FMT_I4 || fmt == FMT_U4 || fmt == FMT_I2) ? 1 : (bm >= 256 ? 2 : 4);
 }
 
-template <int FMT, int BM, int BN, int WM, int WN>
+template <int FMT, int BM, int BN, int WM, int WN, bool GATED>
 __global__ __launch_bounds__(WM * WN * 64) void mfma_kernel(RunArgs a) {
   using T = FmtTraits<FMT>;
   constexpr bool FP = T::FP;
@@ -252,6 +252,21 @@ __global__ __launch_bounds__(WM * WN * 64) void mfma_kernel(RunArgs a) {
   }
 
   // epilogue: lane l holds rows 4*(l/16) + r, column l%16 of each 16x16 sub-tile
+  static_assert(WTN % 2 == 0, "a wave's column blocks hold whole gate / up pairs");
+  if constexpr (GATED) {
+#pragma unroll
+    for (int j = 0; j < WTN; j += 2) {
+      const GateCol c = gate_col(a, n0 + (wn * WTN + j) * 16 + l16);
+#pragma unroll
+      for (int i = 0; i < WTM; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int row = m0 + (wm * WTM + i) * 16 + kq * 4 + r;
+          if (row < a.M && c.in) gate_store(a, row, c, (float)acc[i][j][r], (float)acc[i][j + 1][r]);
+        }
+    }
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < WTM; ++i)
 #pragma unroll
@@ -284,7 +299,9 @@ __global__ __launch_bounds__(WM * WN * 64) void mfma_kernel(RunArgs a) {
 template <int FMT, int BM, int BN, int WM, int WN>
 hipError_t launch_t(const RunArgs& a, hipStream_t st) {
   const int tiles = ((a.M + BM - 1) / BM) * ((a.N + BN - 1) / BN);
-  hipLaunchKernelGGL((mfma_kernel<FMT, BM, BN, WM, WN>), dim3(tiles * a.k_parts), dim3(WM * WN * 64), 0, st, a);
+  const dim3 grid(tiles * a.k_parts), block(WM * WN * 64);
+  if (a.out_mode == OUT_GATE) hipLaunchKernelGGL((mfma_kernel<FMT, BM, BN, WM, WN, true>), grid, block, 0, st, a);
+  else hipLaunchKernelGGL((mfma_kernel<FMT, BM, BN, WM, WN, false>), grid, block, 0, st, a);
   return hipGetLastError();
 }
 

@@ -89,7 +89,7 @@ struct BigGeo {
 // FOLD: a correction after the loop takes what the loop leaves of the weights' offset,
 // the zero points of uint4 (whose scale slot then holds (scale, zero) pairs) or the
 // offset 8 of signed int4; see nc below
-template <int FMT, bool SCALED, bool FOLD>
+template <int FMT, bool SCALED, bool FOLD, bool GATED>
 __global__ __launch_bounds__(256) void mfma_big_kernel(RunArgs a) {
   using G = BigGeo<FMT, SCALED>;
   constexpr bool FP = G::FP, PACKED = G::PACKED;
@@ -458,6 +458,21 @@ __global__ __launch_bounds__(256) void mfma_big_kernel(RunArgs a) {
         }
       }
   };
+  if constexpr (GATED) {
+    // column blocks j and j + 1 are the gate and up sums of 16 output columns
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const GateCol c = gate_col(a, n0 + wn * 128 + j * 32 + l16);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int row = m0 + wm * 128 + i * 16 + q * 4 + r;
+          if (row < a.M && c.in) gate_store(a, row, c, (float)acc[i][2 * j][r], (float)acc[i][2 * j + 1][r]);
+        }
+    }
+    return;
+  }
   // The per-column values of this lane's 8 columns (epilogue scale, bias, int8 column
   // scale) are read before any store: C is written through pointers of the types of
   // those arrays, so read between the stores each read would wait behind the stores
@@ -496,7 +511,9 @@ __global__ __launch_bounds__(256) void mfma_big_kernel(RunArgs a) {
 template <int FMT, bool SCALED, bool FOLD>
 hipError_t launch_big_t(const RunArgs& a, hipStream_t st) {
   const int tiles = ((a.M + 255) / 256) * ((a.N + 255) / 256);
-  hipLaunchKernelGGL((mfma_big_kernel<FMT, SCALED, FOLD>), dim3(tiles * a.k_parts), dim3(256), 0, st, a);
+  const dim3 grid(tiles * a.k_parts), block(256);
+  if (a.out_mode == OUT_GATE) hipLaunchKernelGGL((mfma_big_kernel<FMT, SCALED, FOLD, true>), grid, block, 0, st, a);
+  else hipLaunchKernelGGL((mfma_big_kernel<FMT, SCALED, FOLD, false>), grid, block, 0, st, a);
   return hipGetLastError();
 }
 

@@ -48,8 +48,16 @@ __device__ __forceinline__ uint4 canonical_piece(int fmt, const void* __restrict
   return r.u;
 }
 
-__global__ void pack_weights_kernel(int fmt, const void* __restrict__ w, uint4* __restrict__ out,
-                                    int64_t N, int64_t K, int64_t NB, int64_t n_pieces) {
+// column and projection behind inner column n: the weights' own, or for a gated plan
+// (up given) column 16 (n / 32) + n % 16 of the gate or the up projection
+__device__ __forceinline__ int64_t source_column(bool gated, int64_t n, bool* from_up) {
+  *from_up = gated && ((n >> 4) & 1);
+  return gated ? (n >> 5) * 16 + (n & 15) : n;
+}
+
+// N: columns of each projection
+__global__ void pack_weights_kernel(int fmt, const void* __restrict__ w_gate, const void* __restrict__ w_up,
+                                    uint4* __restrict__ out, int64_t N, int64_t K, int64_t NB, int64_t n_pieces) {
   const int KB = kb_of(fmt);
   for (int64_t p = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; p < n_pieces;
        p += (int64_t)gridDim.x * blockDim.x) {
@@ -57,7 +65,9 @@ __global__ void pack_weights_kernel(int fmt, const void* __restrict__ w, uint4* 
     const int within = (int)(p & 63);
     const int kq = within >> 4, nn = within & 15;
     const int64_t kb = sb / NB, nb = sb - kb * NB;
-    const int64_t n = nb * 16 + nn;
+    bool from_up;
+    const int64_t n = source_column(w_up != nullptr, nb * 16 + nn, &from_up);
+    const void* w = from_up ? w_up : w_gate;
     const int64_t k0 = kb * KB + (int64_t)kq * (KB / 4);
     uint4 r = make_uint4(0, 0, 0, 0);
     if (n < N) {
@@ -100,12 +110,17 @@ __global__ void pack_weights_kernel(int fmt, const void* __restrict__ w, uint4* 
 
 // rows g >= G (groups wholly past K, whose positions read zero activations) get
 // zero scales and zero points
-__global__ void pack_scales_kernel(const uint16_t* __restrict__ s, const uint16_t* __restrict__ z,
+__global__ void pack_scales_kernel(const uint16_t* __restrict__ s_gate, const uint16_t* __restrict__ z_gate,
+                                   const uint16_t* __restrict__ s_up, const uint16_t* __restrict__ z_up,
                                    void* __restrict__ out, int64_t N, int64_t Npad, int64_t G, int64_t G_store) {
   const int64_t total = G_store * Npad;
   for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < total;
        i += (int64_t)gridDim.x * blockDim.x) {
-    const int64_t g = i / Npad, n = i - g * Npad;
+    const int64_t g = i / Npad;
+    bool from_up;
+    const int64_t n = source_column(s_up != nullptr, i - g * Npad, &from_up);
+    const uint16_t* s = from_up ? s_up : s_gate;
+    const uint16_t* z = from_up ? z_up : z_gate;
     const bool in = n < N && g < G;
     const uint16_t sv = in ? s[n * G + g] : 0;
     if (z) {
@@ -126,17 +141,18 @@ int grid_for(int64_t items, int threads) {
 
 }  // namespace
 
-hipError_t launch_pack(const Layout& L, const void* w, const void* s, const void* z, void* packed,
+hipError_t launch_pack(const Layout& L, int64_t N, const Canonical& gate, const Canonical* up, void* packed,
                        hipStream_t st) {
   const int64_t n_pieces = L.nkb * L.NB * 64;
-  hipLaunchKernelGGL(pack_weights_kernel, dim3(grid_for(n_pieces, 256)), dim3(256), 0, st, L.fmt, w,
-                     static_cast<uint4*>(packed), L.N, L.K, L.NB, n_pieces);
+  hipLaunchKernelGGL(pack_weights_kernel, dim3(grid_for(n_pieces, 256)), dim3(256), 0, st, L.fmt, gate.w,
+                     up ? up->w : nullptr, static_cast<uint4*>(packed), N, L.K, L.NB, n_pieces);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || L.G == 0) return e;
   void* sdst = static_cast<char*>(packed) + L.s_offset;
   hipLaunchKernelGGL(pack_scales_kernel, dim3(grid_for(L.G_store * L.Npad, 256)), dim3(256), 0, st,
-                     static_cast<const uint16_t*>(s), L.zeros ? static_cast<const uint16_t*>(z) : nullptr,
-                     sdst, L.N, L.Npad, L.G, L.G_store);
+                     static_cast<const uint16_t*>(gate.s), L.zeros ? static_cast<const uint16_t*>(gate.z) : nullptr,
+                     up ? static_cast<const uint16_t*>(up->s) : nullptr,
+                     up && L.zeros ? static_cast<const uint16_t*>(up->z) : nullptr, sdst, N, L.Npad, L.G, L.G_store);
   return hipGetLastError();
 }
 

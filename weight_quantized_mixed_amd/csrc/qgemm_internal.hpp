@@ -39,7 +39,8 @@ enum Fmt : int { FMT_I4 = 0, FMT_U4 = 1, FMT_F16 = 2, FMT_I8 = 3, FMT_I2 = 4 };
 enum OutMode : int {
   OUT_STORE = 0,    // write C directly (k_parts == 1)
   OUT_ATOMIC = 1,   // atomic add into fp32 workspace (fp16 out) or into C (int32 out)
-  OUT_PARTIAL = 2   // write the part's partial to workspace[part][M][N] (two-pass)
+  OUT_PARTIAL = 2,  // write the part's partial to workspace[part][M][N] (two-pass)
+  OUT_GATE = 3      // gated plans, one part: C = act(gate) * up from neighbouring column blocks
 };
 
 // scale modes
@@ -79,6 +80,13 @@ struct Layout {
   bool zeros;
   size_t w_bytes, s_offset, s_bytes, total;
 };
+
+// Gated plans (C = act(A Wg + bg) * (A Wu + bu)) run both projections as one product
+// whose 16-column blocks alternate: inner column 32 b + i (i < 16) is column 16 b + i of
+// the gate projection and 32 b + 16 + i the same column of the up projection.  Every
+// compute kernel then holds the two sums of an output in one lane, in neighbouring
+// column blocks, and the block padding of N is the same for both.
+__host__ __device__ constexpr int64_t gate_inner(int64_t N) { return (N + 15) / 16 * 32; }
 
 // canonical weight values per 32-bit word (int8 / fp16 rows are plain arrays)
 constexpr int pack_factor(int fmt) { return fmt == FMT_I2 ? 16 : (fmt == FMT_I4 || fmt == FMT_U4) ? 8 : 1; }
@@ -122,6 +130,15 @@ struct RunArgs {
   const uint16_t* zp;
   int32_t zr_gp;  // groups per plane: zr_G rounded up to 32
   int32_t zr_G;   // scale groups over K
+  // gated plans (gate_n != 0): N counts the inner columns, gate_n the output's; bias and
+  // col_scale are the gate projection's, these the up projection's; act(x) =
+  // x sigmoid(x (act_c0 + act_c1 x^2)); preact, if given, receives the rounded
+  // pre-activations [M][2 gate_n] (gate | up)
+  int32_t gate_n;
+  float act_c0, act_c1;
+  const void* bias_up;
+  const float* col_scale_up;
+  _Float16* preact;
 };
 
 // bias of output column col (0 without bias): fp16 outputs add it in fp32 before
@@ -136,6 +153,55 @@ __device__ __forceinline__ int bias_i(const RunArgs& a, int col) {
 // (weight) scales and the bias applied in fp32, one rounding to fp16
 __device__ __forceinline__ _Float16 dq_out(const RunArgs& a, int row, int col, int acc) {
   return (_Float16)((float)acc * a.row_scale[row] * a.col_scale[col] + bias_f(a, col));
+}
+// One output column of a gated plan, from the inner column of its gate sum: the
+// scales that turn the two sums into pre-activations, and the biases.
+struct GateCol {
+  float sg, su, bg, bu;
+  int col;  // output column
+  bool in;
+};
+__device__ __forceinline__ GateCol gate_col(const RunArgs& a, int icol) {
+  GateCol c;
+  c.col = (icol >> 5) * 16 + (icol & 15);
+  c.in = c.col < a.gate_n;
+  c.sg = c.su = 1.f;
+  c.bg = c.bu = 0.f;
+  if (!c.in) return c;
+  if (a.epi_scale) {
+    c.sg = (float)a.epi_scale[icol];
+    c.su = (float)a.epi_scale[icol + 16];
+  } else if (a.col_scale) {
+    c.sg = a.col_scale[c.col];
+    c.su = a.col_scale_up[c.col];
+  }
+  if (a.bias) c.bg = (float)static_cast<const _Float16*>(a.bias)[c.col];
+  if (a.bias_up) c.bu = (float)static_cast<const _Float16*>(a.bias_up)[c.col];
+  return c;
+}
+// x sigmoid(t), t = x (c0 + c1 x^2): silu with (1, 0); the tanh form of gelu with
+// (2 c, 2 c 0.044715), c = sqrt(2 / pi), since (1 + tanh y) / 2 = sigmoid(2 y).  The
+// hardware exponential and reciprocal are within a few ulp in fp32.
+__device__ __forceinline__ float sigmoid_f(float t) { return __builtin_amdgcn_rcpf(1.f + __expf(-t)); }
+__device__ __forceinline__ float gate_act(const RunArgs& a, float x) {
+  return x * sigmoid_f(x * (a.act_c0 + a.act_c1 * x * x));
+}
+// stores output (row, c.col) from the two sums, in fp32 up to the one rounding of the
+// output (and one of each pre-activation, where they are kept for the backward pass)
+__device__ __forceinline__ void gate_store(const RunArgs& a, int row, const GateCol& c, float g, float u) {
+  if (a.row_scale) {
+    const float rs = a.row_scale[row];
+    g *= rs;
+    u *= rs;
+  }
+  g = g * c.sg + c.bg;
+  u = u * c.su + c.bu;
+  if (a.preact) {
+    _Float16* p = a.preact + (size_t)row * 2 * a.gate_n + c.col;
+    p[0] = (_Float16)g;
+    p[a.gate_n] = (_Float16)u;
+  }
+  static_cast<_Float16*>(a.C)[(size_t)row * a.gate_n + c.col] = (_Float16)(gate_act(a, g) * u);
 }
 // where integer split-K atomics add up: C itself, or the workspace when the
 // output is dequantised afterwards
@@ -162,7 +228,13 @@ __device__ __forceinline__ void part_units(const RunArgs& a, int part, int& u0, 
 #endif
 
 // kernel launchers (return hipSuccess or the launch error)
-hipError_t launch_pack(const Layout& L, const void* w, const void* s, const void* z, void* packed,
+// canonical arrays of a projection: words or values [N, K], scales and zero points [N, G]
+struct Canonical {
+  const void *w, *s, *z;
+};
+// up, if given, is the up projection of a gated plan of N output columns per projection
+// (L.N is then gate_inner(N))
+hipError_t launch_pack(const Layout& L, int64_t N, const Canonical& gate, const Canonical* up, void* packed,
                        hipStream_t st);
 hipError_t launch_gemv(int fmt, const RunArgs& a, hipStream_t st);
 // M = 1 with 16-column workgroups (gemv16.hip), for matrices with few 64-column blocks
@@ -180,6 +252,7 @@ enum DlTile : int {
 void dl_tile_dims(int tile, int* bm, int* bn);
 int choose_dl_tile(int fmt, int64_t M, int64_t N, int k_parts, int smode);
 hipError_t launch_mfma_dl(int fmt, int tile, const RunArgs& a, hipStream_t st);
+hipError_t launch_mfma_dl_gated(int fmt, int tile, const RunArgs& a, hipStream_t st);
 // 256 x 256 tiles of four 128 x 128 waves (mfma_big.hip) for the formats that
 // big_tile_takes; same arguments and stage layout as launch_mfma_dl's 256 x 256 tile
 bool big_tile_takes(int fmt, const RunArgs& a);
@@ -205,6 +278,51 @@ hipError_t launch_quantize_rows(const void* A, int64_t M, int64_t K, void* Q, fl
 // sums the per-part partials (or converts the atomic accumulator) into C;
 // acc_fp: fp32 accumulator (fp16 activations), else int32
 hipError_t launch_finalize(const RunArgs& a, int acc_fp, hipStream_t st);
+// the same for a gated plan: sums the parts of both projections and writes C
+hipError_t launch_finalize_gate(const RunArgs& a, int acc_fp, hipStream_t st);
+
+// passes of the gated backward (gated.hip): gradients of the pre-activations, row by row
+// (inner column order, rows of kd values) and, if colwise is given, column by column
+// (rows of mp values), with the row tiles' column sums for the bias gradients
+hipError_t launch_gate_grad(const void* preact, const void* dC, int64_t M, int64_t N, int64_t kd, int64_t mp, float c0,
+                            float c1, void* rowwise, void* colwise, float* bias_part, hipStream_t st);
+int64_t gate_grad_row_tiles(int64_t M);
+hipError_t launch_bias_grad(const float* part, int64_t M, int64_t N, void* dbg, void* dbu, hipStream_t st);
+// the transposed weights of a gated plan, and transposed fp16 rows, as fp16 blobs of layout `to`
+hipError_t launch_transpose_blob(const Layout& L, int64_t gate_n, const void* packed, const Layout& to, void* out,
+                                 hipStream_t st);
+hipError_t launch_transpose_rows(const void* X, int64_t M, int64_t K, const Layout& to, void* out, hipStream_t st);
+
+// rotation of new queries and keys, keys and values into the paged cache (kv_append.hip)
+struct AppendArgs {
+  const _Float16 *q, *k, *v;
+  int64_t q_stride, k_stride, v_stride;  // values between rows
+  const float *cos, *sin;                // [n_positions][rot / 2]
+  const int32_t* positions;
+  const int64_t* slots;
+  _Float16 *q_out, *k_cache, *v_cache;
+  int64_t n_positions, n_pages;
+  int32_t page, q_heads, kv_heads, D, rot, interleaved;
+};
+hipError_t launch_kv_append(const AppendArgs& a, int64_t T, hipStream_t st);
+
+// attention over the paged cache (attention.hip)
+struct AttnArgs {
+  const _Float16 *q, *k, *v;
+  _Float16* out;
+  float* lse;
+  const int32_t *q_starts, *kv_lens, *tables, *prefix_table;
+  int64_t q_stride, table_width, prefix_len;
+  int32_t T, q_heads, kv_heads, D, n_pages, page_shift, max_q, max_len;
+  float scale;
+};
+// sizes that the host knows, which choose the split of the work
+struct AttnShape {
+  int64_t T, B, max_q, max_len, prefix_len;
+  int32_t q_heads, kv_heads, D;
+};
+size_t attention_ws_bytes(const AttnShape& s);
+hipError_t launch_attention(const AttnArgs& a, const AttnShape& s, void* ws, hipStream_t st);
 
 // GEMV tuning: most waves per workgroup (they split the workgroup's K range)
 // and superblocks per register stage

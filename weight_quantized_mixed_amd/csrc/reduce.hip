@@ -43,6 +43,26 @@ __global__ void finalize_kernel(const void* __restrict__ ws, void* __restrict__ 
   }
 }
 
+// The same for a gated plan: output (m, n) from the parts' sums of its gate and up
+// columns (inner columns 32 (n / 16) + n % 16, and 16 further), rows of a.N inner sums.
+template <typename T>
+__global__ void finalize_gate_kernel(RunArgs a, int parts) {
+  const size_t total = (size_t)a.M * a.gate_n, mn = (size_t)a.M * a.N;
+  const size_t stride = (size_t)gridDim.x * blockDim.x;
+  for (size_t i = blockIdx.x * (size_t)blockDim.x + threadIdx.x; i < total; i += stride) {
+    const int row = (int)(i / (size_t)a.gate_n), col = (int)(i - (size_t)row * a.gate_n);
+    const int icol = (col >> 4) * 32 + (col & 15);
+    const T* w = static_cast<const T*>(a.ws) + (size_t)row * a.N + icol;
+    T g = w[0], u = w[16];
+    for (int p = 1; p < parts; ++p) {
+      g += w[(size_t)p * mn];
+      u += w[(size_t)p * mn + 16];
+    }
+    GateCol c = gate_col(a, icol);
+    gate_store(a, row, c, (float)g, (float)u);
+  }
+}
+
 // int32 C[m, n] = bias[n], rows of N elements
 __global__ void fill_bias_kernel(int* __restrict__ C, const int* __restrict__ bias, int M, int N) {
   for (int m = blockIdx.y; m < M; m += gridDim.y)
@@ -226,6 +246,13 @@ hipError_t launch_finalize(const RunArgs& a, int acc_fp, hipStream_t st) {
     hipLaunchKernelGGL(finalize_kernel<true>, dim3(grid_for(mn, 256)), dim3(256), 0, st, a.ws, a.C, mn, parts, a);
   else
     hipLaunchKernelGGL(finalize_kernel<false>, dim3(grid_for(mn, 256)), dim3(256), 0, st, a.ws, a.C, mn, parts, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_finalize_gate(const RunArgs& a, int acc_fp, hipStream_t st) {
+  const dim3 grid(grid_for((size_t)a.M * a.gate_n, 256));
+  if (acc_fp) hipLaunchKernelGGL(finalize_gate_kernel<float>, grid, dim3(256), 0, st, a, a.k_parts);
+  else hipLaunchKernelGGL(finalize_gate_kernel<int>, grid, dim3(256), 0, st, a, a.k_parts);
   return hipGetLastError();
 }
 

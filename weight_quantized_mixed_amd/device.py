@@ -29,6 +29,13 @@ def _stream(stream):
     return s.cuda_stream
 
 
+def _check(t, name, shape, dtype):
+    """A device tensor argument of this shape and type (None passes)."""
+    if t is not None and (tuple(t.shape) != tuple(shape) or t.dtype != dtype):
+        raise ValueError(f"{name}: {dtype} {tuple(shape)} expected, got {t.dtype} {tuple(t.shape)}")
+    return t
+
+
 def host_to_device(arr: np.ndarray, device="cuda") -> torch.Tensor:
     """Copy a numpy array to the device; uint32 words travel as int32 bits."""
     if arr is None:
@@ -125,3 +132,177 @@ class QGemm:
                             _ptr(col_scales), _ptr(bias), _ptr(C), _ptr(ws),
                             0 if ws is None else ws.numel(), _stream(stream))
         return C
+
+
+class QGated:
+    """One gated feed-forward plan: C = act(A . dequant(Wg) + bg) * (A . dequant(Wu) + bu), N columns each.
+
+    act: "silu" or "gelu_tanh".  int8 activations (w_dtype "i8", "i2") run through run_scaled.
+    The workspaces are kept with the object: calls that may overlap in time pass their own.
+    """
+
+    def __init__(self, M, N, K, w_dtype, group_size=0, has_zeros=False, act="silu", device="cuda"):
+        self.M, self.N, self.K, self.w_dtype = int(M), int(N), int(K), w_dtype
+        self.a_dtype = A_DTYPE[w_dtype]
+        self.device = torch.device(device)
+        self.plan, self.packed_bytes, self.ws_bytes = _q.qgemm_create_gated(
+            M, N, K, self.a_dtype, w_dtype, "f16", OUT_DTYPE[self.a_dtype][1], group_size, int(bool(has_zeros)), act)
+        self._ws = self._bws = None
+
+    close = QGemm.close
+    __del__ = close
+    workspace = QGemm.workspace
+
+    def pack(self, w_gate, w_up, s_gate=None, s_up=None, z_gate=None, z_up=None, out=None, stream=None):
+        """The blob of both projections' canonical weights (scales and zero points where the plan has them)."""
+        if out is None:
+            out = torch.empty(self.packed_bytes, dtype=torch.uint8, device=self.device)
+        _q.qgemm_pack_gated(self.plan, _ptr(w_gate), _ptr(s_gate), _ptr(z_gate), _ptr(w_up), _ptr(s_up), _ptr(z_up),
+                            _ptr(out), _stream(stream))
+        return out
+
+    def new_output(self, M=None):
+        return torch.empty((self.M if M is None else int(M), self.N), dtype=torch.float16, device=self.device)
+
+    def new_preact(self, M=None):
+        """Room for the pre-activations of M rows, which backward reads."""
+        return torch.empty((self.M if M is None else int(M), 2 * self.N), dtype=torch.float16, device=self.device)
+
+    def _run(self, A, packed, rs, csg, csu, bias_gate, bias_up, preact, C, ws, stream, M):
+        M = self.M if M is None else int(M)
+        _check(A, "A", (M, self.K), torch.float16 if self.a_dtype == "f16" else torch.int8)
+        for name, b in (("bias_gate", bias_gate), ("bias_up", bias_up)):
+            _check(b, name, (self.N,), torch.float16)
+        _check(preact, "preact", (M, 2 * self.N), torch.float16)
+        if C is None:
+            C = self.new_output(M)
+        _check(C, "C", (M, self.N), torch.float16)
+        if ws is None:
+            ws = self.workspace()
+        _q.qgemm_run_gated(self.plan, M, _ptr(A), _ptr(packed), _ptr(rs), _ptr(csg), _ptr(csu), _ptr(bias_gate),
+                           _ptr(bias_up), _ptr(preact), _ptr(C), _ptr(ws), 0 if ws is None else ws.numel(),
+                           _stream(stream))
+        return C
+
+    def run(self, A, packed, C=None, ws=None, stream=None, bias_gate=None, bias_up=None, preact=None, M=None):
+        """C for the plan's M rows (or M <= that); preact, if given, is filled for backward."""
+        return self._run(A, packed, None, None, None, bias_gate, bias_up, preact, C, ws, stream, M)
+
+    def run_scaled(self, A, packed, row_scales, col_scales_gate, col_scales_up, bias_gate=None, bias_up=None, C=None,
+                   ws=None, stream=None, M=None):
+        """C for int8 A with fp32 scales per row, and per column of each projection."""
+        _check(row_scales, "row_scales", (self.M if M is None else int(M),), torch.float32)
+        for name, s in (("col_scales_gate", col_scales_gate), ("col_scales_up", col_scales_up)):
+            _check(s, name, (self.N,), torch.float32)
+        return self._run(A, packed, row_scales, col_scales_gate, col_scales_up, bias_gate, bias_up, None, C, ws, stream, M)
+
+    def backward(self, A, packed, preact, dC, input_grad=True, weight_grads=None, bias_grads=False, ws=None,
+                 stream=None, M=None):
+        """{"dA", "dw_gate", "dw_up", "dbias_gate", "dbias_up"} of a run that filled preact (None where not asked for).
+
+        weight_grads: by default for fp16 weights (quantised ones are frozen).
+        """
+        M = self.M if M is None else int(M)
+        if weight_grads is None:
+            weight_grads = self.w_dtype == "f16"
+        half = torch.float16
+        _check(A, "A", (M, self.K), half)
+        _check(preact, "preact", (M, 2 * self.N), half)
+        _check(dC, "dC", (M, self.N), half)
+        new = lambda *shape: torch.empty(shape, dtype=half, device=self.device)  # noqa: E731
+        dA = new(M, self.K) if input_grad else None
+        dw = new(2, self.N, self.K) if weight_grads else None
+        db = new(2, self.N) if bias_grads else None
+        need = _q.qgemm_gated_backward_workspace(self.plan, M, weight_grads or bias_grads)
+        if ws is None:
+            if self._bws is None or self._bws.numel() < need:
+                self._bws = torch.empty(need, dtype=torch.uint8, device=self.device)
+            ws = self._bws
+        part = lambda t, i: None if t is None else t[i]  # noqa: E731
+        _q.qgemm_gated_backward(self.plan, M, _ptr(A), _ptr(packed), _ptr(preact), _ptr(dC), _ptr(dA),
+                                _ptr(part(dw, 0)), _ptr(part(dw, 1)), _ptr(part(db, 0)), _ptr(part(db, 1)), _ptr(ws),
+                                ws.numel(), _stream(stream))
+        return {"dA": dA, "dw_gate": part(dw, 0), "dw_up": part(dw, 1), "dbias_gate": part(db, 0),
+                "dbias_up": part(db, 1)}
+
+
+def _rows(t, width, name):
+    """(address, values between rows) of fp16 rows of at least `width` values, the last dimension contiguous."""
+    if not t.is_cuda:
+        raise ValueError("qgemm takes device tensors only")
+    if t.dtype != torch.float16 or t.dim() != 2 or t.shape[1] != width or (width > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name}: fp16 [T, {width}] with contiguous rows expected, got {t.dtype} {tuple(t.shape)}")
+    return t.data_ptr(), max(t.stride(0), width)
+
+
+class PagedKV:
+    """A paged key / value cache, k and v [n_pages, kv_heads, page_size, head_dim] in fp16 (given, or made here).
+
+    The attention workspace is kept with the object: calls that may overlap in time pass their own.
+    """
+
+    def __init__(self, n_pages, page_size, kv_heads, head_dim, device="cuda", k=None, v=None):
+        self.n_pages, self.page_size = int(n_pages), int(page_size)
+        self.kv_heads, self.head_dim = int(kv_heads), int(head_dim)
+        shape = (self.n_pages, self.kv_heads, self.page_size, self.head_dim)
+        new = lambda: torch.zeros(shape, dtype=torch.float16, device=device)  # noqa: E731
+        self.k = _check(new() if k is None else k, "k", shape, torch.float16)
+        self.v = _check(new() if v is None else v, "v", shape, torch.float16)
+        self.desc = _q.KVCacheDesc(_ptr(self.k), _ptr(self.v), self.n_pages, self.page_size, self.kv_heads, self.head_dim)
+        self._ws = None
+
+    def append(self, q, k, v, cos, sin, positions, slots, q_out=None, interleaved=False, stream=None):
+        """Rotated queries [T, q_heads, head_dim]; the rotated keys and the values go to the cache's slots.
+
+        q [T, q_heads * head_dim], k and v [T, kv_heads * head_dim]: rows may be slices of a wider array.
+        """
+        T, D = q.shape[0], self.head_dim
+        q_heads = q.shape[1] // D
+        qp, qs = _rows(q, q_heads * D, "q")
+        kp, ks = _rows(k, self.kv_heads * D, "k")
+        vp, vs = _rows(v, self.kv_heads * D, "v")
+        if k.shape[0] != T or v.shape[0] != T:
+            raise ValueError("q, k and v have a row for each token")
+        n_pos, half = cos.shape
+        _check(cos, "cos", (n_pos, half), torch.float32)
+        _check(sin, "sin", (n_pos, half), torch.float32)
+        _check(positions, "positions", (T,), torch.int32)
+        _check(slots, "slots", (T,), torch.int64)
+        if q_out is None:
+            q_out = torch.empty((T, q_heads, D), dtype=torch.float16, device=q.device)
+        _check(q_out, "q_out", (T, q_heads, D), torch.float16)
+        _q.qgemm_kv_append(self.desc, T, q_heads, qp, qs, kp, ks, vp, vs, _ptr(cos), _ptr(sin), n_pos, 2 * half,
+                           int(bool(interleaved)), _ptr(positions), _ptr(slots), _ptr(q_out), _stream(stream))
+        return q_out
+
+    def attend(self, q, q_starts, kv_lens, tables, max_q, max_len, prefix_table=None, prefix_len=0, scale=None,
+               out=None, lse=None, ws=None, stream=None):
+        """Causal attention of a ragged batch (q [T, q_heads, head_dim]) over its own pages and the shared prefix."""
+        T, q_heads, D = q.shape
+        if D != self.head_dim or q.stride(1) != D:
+            raise ValueError(f"q: [T, q_heads, {self.head_dim}] with contiguous rows expected, got {tuple(q.shape)}")
+        qp, qs = _rows(q.flatten(1) if q.is_contiguous() else q.as_strided((T, q_heads * D), (q.stride(0), q.stride(2))),
+                       q_heads * D, "q")
+        B, width = tables.shape
+        i32 = torch.int32
+        _check(q_starts, "q_starts", (B + 1,), i32)
+        _check(kv_lens, "kv_lens", (B,), i32)
+        _check(tables, "tables", (B, width), i32)
+        if prefix_len:
+            if prefix_table is None or prefix_table.numel() * self.page_size < prefix_len:
+                raise ValueError("prefix_table holds the pages of prefix_len tokens")
+            _check(prefix_table, "prefix_table", (prefix_table.numel(),), i32)
+        if out is None:
+            out = torch.empty((T, q_heads, D), dtype=torch.float16, device=q.device)
+        _check(out, "out", (T, q_heads, D), torch.float16)
+        _check(lse, "lse", (T, q_heads), torch.float32)
+        need = _q.qgemm_attention_workspace(self.desc, T, q_heads, B, max_q, max_len, prefix_len)
+        if ws is None and need:
+            if self._ws is None or self._ws.numel() < need:
+                self._ws = torch.empty(need, dtype=torch.uint8, device=q.device)
+            ws = self._ws
+        _q.qgemm_attention(self.desc, T, q_heads, qp, qs, B, _ptr(q_starts), _ptr(kv_lens), _ptr(tables), width,
+                           _ptr(prefix_table) if prefix_len else 0, prefix_len, max_q, max_len,
+                           D ** -0.5 if scale is None else scale, _ptr(out), _ptr(lse), _ptr(ws),
+                           0 if ws is None else ws.numel(), _stream(stream))
+        return out

@@ -21,11 +21,20 @@ QGEMM_OK, QGEMM_ERR_INVALID_ARG, QGEMM_ERR_UNSUPPORTED, QGEMM_ERR_NO_MEMORY, QGE
 QGEMM_DETERMINISTIC = 1
 QGEMM_SPLIT_AUTO = 2
 QGEMM_PATH_GEMV, QGEMM_PATH_MFMA = 1, 2
+ACTS = {"silu": 1, "gelu_tanh": 2}
 
 EXPORTED = ("qgemm_create", "qgemm_pack_weights", "qgemm_run", "qgemm_run_ex", "qgemm_run_noalloc",
             "qgemm_run_scaled", "qgemm_quantize_rows", "qgemm_destroy", "qgemm_plan_path",
-            "qgemm_status_string")
+            "qgemm_status_string", "qgemm_create_gated", "qgemm_pack_gated", "qgemm_run_gated",
+            "qgemm_gated_backward_workspace", "qgemm_gated_backward", "qgemm_kv_append",
+            "qgemm_attention_workspace", "qgemm_attention")
 NOALLOC_MAX_SCRATCH = 32 << 20
+
+
+class KVCacheDesc(ctypes.Structure):
+    """qgemm_kv_cache: device addresses and sizes of a paged cache."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("n_pages", ctypes.c_int64),
+                ("page_size", ctypes.c_int32), ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
 
 
 class QGemmError(RuntimeError):
@@ -77,6 +86,21 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.qgemm_plan_path.restype = c_i32
     lib.qgemm_status_string.argtypes = [c_i32]
     lib.qgemm_status_string.restype = ctypes.c_char_p
+    c_f, p_sz, p_kv = ctypes.c_float, ctypes.POINTER(c_sz), ctypes.POINTER(KVCacheDesc)
+    lib.qgemm_create_gated.argtypes = [ctypes.POINTER(c_p), c_i64, c_i64, c_i64, c_i32, c_i32, c_i32, c_i32,
+                                       c_i32, c_i32, c_i32, p_sz, p_sz]
+    lib.qgemm_pack_gated.argtypes = [c_p] * 9
+    lib.qgemm_run_gated.argtypes = [c_p, c_i64] + [c_p] * 10 + [c_sz, c_p]
+    lib.qgemm_gated_backward_workspace.argtypes = [c_p, c_i64, c_i32, p_sz]
+    lib.qgemm_gated_backward.argtypes = [c_p, c_i64] + [c_p] * 10 + [c_sz, c_p]
+    lib.qgemm_kv_append.argtypes = [p_kv, c_i64, c_i32, c_p, c_i64, c_p, c_i64, c_p, c_i64, c_p, c_p, c_i64, c_i32,
+                                    c_i32, c_p, c_p, c_p, c_p]
+    lib.qgemm_attention_workspace.argtypes = [p_kv, c_i64, c_i32, c_i64, c_i64, c_i64, c_i64, p_sz]
+    lib.qgemm_attention.argtypes = [p_kv, c_i64, c_i32, c_p, c_i64, c_i64, c_p, c_p, c_p, c_i64, c_p, c_i64, c_i64,
+                                    c_i64, c_f, c_p, c_p, c_p, c_sz, c_p]
+    for name in ("qgemm_create_gated", "qgemm_pack_gated", "qgemm_run_gated", "qgemm_gated_backward_workspace",
+                 "qgemm_gated_backward", "qgemm_kv_append", "qgemm_attention_workspace", "qgemm_attention"):
+        getattr(lib, name).restype = c_i32
     _lib = lib
     return lib
 
@@ -140,6 +164,82 @@ def qgemm_quantize_rows(A, M, K, Q, scales, stream=0):
     st = load().qgemm_quantize_rows(A or None, int(M), int(K), Q or None, scales or None, stream or None)
     if st != QGEMM_OK:
         raise QGemmError(st, "qgemm_quantize_rows")
+
+
+def qgemm_create_gated(M, N, K, a_dtype, w_dtype, out_dtype, accum_dtype, group_size=0, has_zeros=0, act="silu"):
+    """Returns (plan handle, packed_bytes, workspace_bytes); raises QGemmError."""
+    plan = ctypes.c_void_p()
+    pb, wb = ctypes.c_size_t(), ctypes.c_size_t()
+    st = load().qgemm_create_gated(ctypes.byref(plan), int(M), int(N), int(K), _dt(a_dtype), _dt(w_dtype),
+                                   _dt(out_dtype), _dt(accum_dtype), int(group_size), int(has_zeros),
+                                   ACTS[act] if isinstance(act, str) else int(act), ctypes.byref(pb),
+                                   ctypes.byref(wb))
+    if st != QGEMM_OK:
+        raise QGemmError(st, "qgemm_create_gated")
+    return plan.value, pb.value, wb.value
+
+
+def qgemm_pack_gated(plan, w_gate, s_gate, z_gate, w_up, s_up, z_up, packed, stream=0):
+    st = load().qgemm_pack_gated(plan, w_gate or None, s_gate or None, z_gate or None, w_up or None, s_up or None,
+                                 z_up or None, packed or None, stream or None)
+    if st != QGEMM_OK:
+        raise QGemmError(st, "qgemm_pack_gated")
+
+
+def qgemm_run_gated(plan, M, A, packed, row_scales, col_scales_gate, col_scales_up, bias_gate, bias_up, preact, C,
+                    workspace, workspace_bytes, stream=0):
+    st = load().qgemm_run_gated(plan, int(M), A or None, packed or None, row_scales or None, col_scales_gate or None,
+                                col_scales_up or None, bias_gate or None, bias_up or None, preact or None, C or None,
+                                workspace or None, int(workspace_bytes), stream or None)
+    if st != QGEMM_OK:
+        raise QGemmError(st, "qgemm_run_gated")
+
+
+def qgemm_gated_backward_workspace(plan, M, weight_grads) -> int:
+    n = ctypes.c_size_t()
+    st = load().qgemm_gated_backward_workspace(plan, int(M), int(bool(weight_grads)), ctypes.byref(n))
+    if st != QGEMM_OK:
+        raise QGemmError(st, "qgemm_gated_backward_workspace")
+    return n.value
+
+
+def qgemm_gated_backward(plan, M, A, packed, preact, dC, dA, dw_gate, dw_up, dbias_gate, dbias_up, workspace,
+                         workspace_bytes, stream=0):
+    st = load().qgemm_gated_backward(plan, int(M), A or None, packed or None, preact or None, dC or None, dA or None,
+                                     dw_gate or None, dw_up or None, dbias_gate or None, dbias_up or None,
+                                     workspace or None, int(workspace_bytes), stream or None)
+    if st != QGEMM_OK:
+        raise QGemmError(st, "qgemm_gated_backward")
+
+
+def qgemm_kv_append(cache, T, q_heads, q, q_stride, k, k_stride, v, v_stride, cos, sin, n_positions, rot_dim,
+                    interleaved, positions, slots, q_out, stream=0):
+    st = load().qgemm_kv_append(None if cache is None else ctypes.byref(cache), int(T), int(q_heads), q or None,
+                                int(q_stride), k or None, int(k_stride), v or None, int(v_stride), cos or None,
+                                sin or None, int(n_positions), int(rot_dim), int(interleaved), positions or None,
+                                slots or None, q_out or None, stream or None)
+    if st != QGEMM_OK:
+        raise QGemmError(st, "qgemm_kv_append")
+
+
+def qgemm_attention_workspace(cache, T, q_heads, B, max_q, max_len, prefix_len) -> int:
+    n = ctypes.c_size_t()
+    st = load().qgemm_attention_workspace(None if cache is None else ctypes.byref(cache), int(T), int(q_heads), int(B),
+                                          int(max_q), int(max_len), int(prefix_len), ctypes.byref(n))
+    if st != QGEMM_OK:
+        raise QGemmError(st, "qgemm_attention_workspace")
+    return n.value
+
+
+def qgemm_attention(cache, T, q_heads, q, q_stride, B, q_starts, kv_lens, tables, table_width, prefix_table,
+                    prefix_len, max_q, max_len, scale, out, lse, workspace, workspace_bytes, stream=0):
+    st = load().qgemm_attention(None if cache is None else ctypes.byref(cache), int(T), int(q_heads), q or None,
+                                int(q_stride), int(B), q_starts or None, kv_lens or None, tables or None,
+                                int(table_width), prefix_table or None, int(prefix_len), int(max_q), int(max_len),
+                                float(scale), out or None, lse or None, workspace or None, int(workspace_bytes),
+                                stream or None)
+    if st != QGEMM_OK:
+        raise QGemmError(st, "qgemm_attention")
 
 
 def qgemm_destroy(plan):
