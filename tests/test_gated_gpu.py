@@ -1,0 +1,229 @@
+"""GPU parity of the gated feed-forward block and its gradients with the float64
+references, over the weight formats, every kernel path of the product and ragged sizes."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import synth
+from gpu_helpers import say
+from weight_quantized_mixed_amd import qgemm as q
+from weight_quantized_mixed_amd.device import QGated, QGemm, host_to_device
+
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():  # pragma: no cover - CPU containers
+    pytest.skip("needs a GPU", allow_module_level=True)
+
+
+class GatedCase:
+    def __init__(self, M, N, K, w, g=0, zeros=False, act="silu", seed=1, bias=True):
+        self.M, self.N, self.K, self.w, self.act = M, N, K, w, act
+        self.problems = [synth.make_problem(M, N, K, w, group_size=g, has_zeros=zeros, seed=seed + 50 * i) for i in (0, 1)]
+        A = self.problems[0].A
+        self.W, self.scaled_weights = [], w in ("i4", "u4") and g != 0
+        for p in self.problems:
+            if w == "f16":
+                p.w = (p.w.astype(np.float32) / np.sqrt(K)).astype(np.float16)
+            vals = oracle.unpack_weights(p.w, w, N, K)
+            self.W.append(oracle.dequantize(vals, p.s, p.z, p.group_size, K))
+        if w in ("i4", "u4") and g == 0:
+            A = (A.astype(np.float32) * 0.02).astype(np.float16)
+        self.A = A
+        self.b = [synth.draw_bias(N, "f16", seed + i) for i in (7, 8)] if bias else [None, None]
+        self.int8 = A.dtype == np.int8
+        self.rs = synth.draw_col_scales(M, seed + 9) if self.int8 else None
+        self.cs = [synth.draw_col_scales(N, seed + i) for i in (10, 11)] if self.int8 else [None, None]
+        self.plan = QGated(M, N, K, w, g, zeros, act=act)
+        d = [[host_to_device(x) for x in (p.w, p.s, p.z)] for p in self.problems]
+        self.packed = self.plan.pack(d[0][0], d[1][0], d[0][1], d[1][1], d[0][2], d[1][2])
+        self.Ad = host_to_device(A)
+
+    def run(self, M=None, preact=None):
+        m = self.M if M is None else M
+        b = [host_to_device(x) for x in self.b]
+        if self.int8:
+            C = self.plan.run_scaled(self.Ad[:m], self.packed, host_to_device(self.rs[:m]), host_to_device(self.cs[0]),
+                                     host_to_device(self.cs[1]), b[0], b[1], M=m)
+        else:
+            C = self.plan.run(self.Ad[:m], self.packed, bias_gate=b[0], bias_up=b[1], preact=preact, M=m)
+        torch.cuda.synchronize()
+        return C.cpu().numpy().astype(np.float64)
+
+    def reference(self, M=None):
+        m = self.M if M is None else M
+        A = self.A[:m].astype(np.float64)
+        rs = None if self.rs is None else self.rs[:m]
+        C, g, u = oracle.gated_ref(A, *self.W, self.act, *self.b, rs, *self.cs)
+        e = [oracle.sum_bound(A, W, self.scaled_weights) for W in self.W]
+        if self.int8:
+            e = [x * rs[:, None].astype(np.float64) * c.astype(np.float64) for x, c in zip(e, self.cs)]
+        e = [x + 2.0**-20 * np.abs(y) for x, y in zip(e, (g, u))]
+        return C, g, u, e
+
+    def check(self, M=None):
+        C, g, u, e = self.reference(M)
+        assert_near(self.run(M), C, oracle.gated_bound(C, g, u, *e, self.act), f"C {self.w} M={M or self.M}")
+
+
+def assert_near(got, ref, bound, what):
+    assert np.isfinite(got).all(), f"{what}: not finite"
+    over = np.abs(got - ref) > bound
+    if over.any():
+        at = np.argwhere(over)[:4]
+        raise AssertionError(f"{what}: {int(over.sum())} outside the bound, first "
+                             f"{[(tuple(i), float(got[tuple(i)]), float(ref[tuple(i)]), float(bound[tuple(i)])) for i in at]}")
+
+
+FORMATS = [("i4", 128, False), ("i4", 0, False), ("i4", -1, False), ("i4", 32, False), ("u4", 128, True),
+           ("u4", -1, True), ("u4", 64, True), ("u4", 0, False), ("f16", 0, False), ("i8", 0, False), ("i2", 0, False)]
+
+
+@pytest.mark.parametrize("w,g,zeros", FORMATS)
+@pytest.mark.parametrize("M,N,K", [(1, 100, 256), (1, 4200, 512), (3, 17, 384), (8, 1000, 256), (20, 260, 512),
+                                   (33, 72, 256), (70, 500, 640), (130, 129, 256), (300, 260, 384)])
+def test_gated_formats(M, N, K, w, g, zeros):
+    say(f"case gated {w} g={g} zeros={zeros} M={M} N={N} K={K}")
+    c = GatedCase(M, N, K, w, g, zeros, act="silu" if (M + N) % 2 else "gelu_tanh", seed=M + N + K)
+    c.check()
+    if M > 2:
+        c.check(M=M // 2)
+        c.check(M=1)
+
+
+@pytest.mark.parametrize("w,g,zeros", [("i4", 128, False), ("i4", -1, False), ("i4", 0, False), ("u4", 128, True),
+                                       ("u4", 32, False), ("f16", 0, False), ("i8", 0, False), ("i2", 0, False)])
+def test_gated_largest_tiles(w, g, zeros):
+    """The 256 x 256 tiles (four and eight waves), edges in both directions."""
+    say(f"case gated large {w} g={g}")
+    GatedCase(4000, 2010, 256, w, g, zeros, seed=77).check()
+
+
+@pytest.mark.parametrize("M,w", [(128, "i4"), (40, "u4"), (20, "i4"), (12, "u4")])
+def test_gated_split_k(M, w):
+    """The library's own split of long reductions: parts of both projections joined."""
+    say(f"case gated split M={M} {w}")
+    c = GatedCase(M, 2048, 8192, w, 128, w == "u4", seed=M)
+    assert c.plan.ws_bytes > 0
+    c.check()
+    c.check(M=M - 7)
+
+
+@pytest.mark.parametrize("K", [8, 72, 136, 1000])
+def test_gated_depths_off_the_granule(K):
+    say(f"case gated K={K}")
+    for w in ("i4", "f16", "i8"):
+        GatedCase(5, 50, K, w, 0, seed=K).check()
+        GatedCase(45, 50, K, w, 0, seed=K).check()
+
+
+def test_gated_extremes_of_the_activation():
+    """Pre-activations of large magnitude: sigmoid saturates to 0 and 1 without NaN."""
+    for act in ("silu", "gelu_tanh"):
+        K, N = 64, 16
+        plan = QGated(2, N, K, "f16", act=act)
+        Wg, Wu = np.zeros((N, K), np.float16), np.zeros((N, K), np.float16)
+        Wg[:, 0] = np.linspace(-60000, 60000, N).astype(np.float16)
+        Wu[:, 1] = 1
+        A = np.zeros((2, K), np.float16)
+        A[:, 0], A[:, 1] = (1, 16), 0.5
+        C = plan.run(host_to_device(A), plan.pack(host_to_device(Wg), host_to_device(Wu))).cpu().numpy()
+        ref = oracle.gated_ref(A, Wg.T.astype(np.float64), Wu.T.astype(np.float64), act)[0]
+        with np.errstate(over="ignore"):
+            assert np.array_equal(np.isinf(C), np.isinf(ref.astype(np.float16)))
+        f = np.isfinite(C)
+        assert_near(C[f].astype(np.float64), ref[f], 2.0**-10 * np.abs(ref[f]) + 2.0**-24, act)
+
+
+TRAIN = [  # M, N, K, w, g, zeros
+    (1, 16, 64, "f16", 0, False), (5, 24, 40, "f16", 0, False), (64, 129, 72, "f16", 0, False),
+    (65, 130, 129, "f16", 0, False), (200, 320, 256, "f16", 0, False), (700, 200, 520, "f16", 0, False),
+    (33, 100, 256, "i4", 128, False), (130, 72, 384, "u4", 128, True), (65, 50, 192, "u4", 64, True),
+    (40, 40, 104, "i4", 0, False), (20, 33, 256, "i4", -1, False),
+]
+
+
+@pytest.mark.parametrize("M,N,K,w,g,zeros", TRAIN)
+def test_gated_gradients(M, N, K, w, g, zeros):
+    say(f"case gradients M={M} N={N} K={K} {w} g={g}")
+    c = GatedCase(M, N, K, w, g, zeros, act="silu" if M % 2 else "gelu_tanh", seed=M + N)
+    pre = c.plan.new_preact()
+    C, gg, uu, e = c.reference()
+    assert_near(c.run(preact=pre), C, oracle.gated_bound(C, gg, uu, *e, c.act), "C")
+    for x, ref, err in zip(np.split(pre.cpu().numpy().astype(np.float64), 2, axis=1), (gg, uu), e):
+        assert_near(x, ref, err + 2.0**-11 * np.abs(ref) + 2.0**-25, "preact")
+    dC = (synth.draw_fp16_activations(M, N, seed=M) * np.float16(0.25)).astype(np.float16)
+    learns = w == "f16"
+    out = c.plan.backward(c.Ad, c.packed, pre, host_to_device(dC), weight_grads=learns, bias_grads=learns)
+    torch.cuda.synchronize()
+    ref = oracle.gated_grads_ref(c.A, *c.W, gg, uu, dC, c.act)
+    bound = oracle.gated_grads_bound(c.A, *c.W, gg, uu, dC, c.act, *e, c.scaled_weights)
+    for name in ("dA",) + (("dw_gate", "dw_up", "dbias_gate", "dbias_up") if learns else ()):
+        got = out[name].cpu().numpy().astype(np.float64)
+        assert_near(got, ref[name], bound[name] + 2.0**-11 * np.abs(ref[name]) + 2.0**-25, name)
+    again = c.plan.backward(c.Ad, c.packed, pre, host_to_device(dC), weight_grads=learns, bias_grads=learns)
+    for name, t in out.items():  # the order of every sum is fixed
+        assert (t is None) == (again[name] is None) and (t is None or torch.equal(t, again[name]))
+
+
+def test_gradients_asked_for_one_by_one():
+    """Each output alone, separate weight gradient buffers, fewer rows than the plan's."""
+    c = GatedCase(100, 60, 96, "f16", seed=3)
+    M = 70
+    pre, dC = c.plan.new_preact(M), host_to_device(synth.draw_fp16_activations(M, 60, seed=4))
+    c.run(M=M, preact=pre)
+    full = c.plan.backward(c.Ad[:M], c.packed, pre, dC, bias_grads=True, M=M)
+    assert torch.equal(full["dA"], c.plan.backward(c.Ad[:M], c.packed, pre, dC, weight_grads=False, M=M)["dA"])
+    only = c.plan.backward(c.Ad[:M], c.packed, pre, dC, input_grad=False, M=M)
+    assert only["dA"] is None and only["dbias_up"] is None and torch.equal(full["dw_up"], only["dw_up"])
+    need = q.qgemm_gated_backward_workspace(c.plan.plan, M, 1)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    dw = [torch.empty((60, 96), dtype=torch.float16, device="cuda") for _ in range(3)]
+    q.qgemm_gated_backward(c.plan.plan, M, c.Ad.data_ptr(), 0, pre.data_ptr(), dC.data_ptr(), 0, dw[0].data_ptr(),
+                           dw[2].data_ptr(), 0, 0, ws.data_ptr(), need, torch.cuda.current_stream().cuda_stream)
+    assert torch.equal(dw[0], full["dw_gate"]) and torch.equal(dw[2], full["dw_up"])
+
+
+def test_gated_agrees_with_two_plain_products():
+    """The same blob values through the plain plans: g and u of the library itself."""
+    c = GatedCase(37, 200, 512, "i4", 128, seed=9, bias=False)
+    pre = c.plan.new_preact()
+    c.run(preact=pre)
+    for i, p in enumerate(c.problems):
+        plain = QGemm(37, 200, 512, "i4", 128)
+        y = plain.run(c.Ad, plain.pack(host_to_device(p.w), host_to_device(p.s)))
+        bound = oracle.sum_bound(c.A, c.W[i], True) * 2
+        assert_near(pre[:, 200 * i:200 * (i + 1)].cpu().numpy().astype(np.float64), y.cpu().numpy().astype(np.float64),
+                    bound + 2.0**-9 * np.abs(y.cpu().numpy().astype(np.float64)) + 2.0**-24, "preact against a plain product")
+
+
+def test_gated_on_another_stream_and_in_a_graph():
+    c = GatedCase(12, 300, 512, "u4", 128, True, seed=5)
+    base = c.run()
+    C = c.plan.new_output()
+    b = [host_to_device(x) for x in c.b]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        c.plan.run(c.Ad, c.packed, C=C, bias_gate=b[0], bias_up=b[1])
+    side.synchronize()
+    assert np.array_equal(C.cpu().numpy().astype(np.float64), base)
+    graph = torch.cuda.CUDAGraph()
+    A = c.Ad.clone()
+    with torch.cuda.graph(graph):
+        c.plan.run(A, c.packed, C=C, bias_gate=b[0], bias_up=b[1])
+    for shift in (0, 3, 5):
+        A.copy_(c.Ad.roll(shift, 0))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert np.array_equal(C.cpu().numpy().astype(np.float64), np.roll(base, shift, 0)), shift
+
+
+def test_gated_rejects_wrong_tensors():
+    c = GatedCase(4, 32, 64, "f16", seed=2)
+    for kw in (dict(A=c.Ad[:3]), dict(C=torch.empty((4, 31), dtype=torch.float16, device="cuda")),
+               dict(bias_up=torch.empty(32, device="cuda")), dict(A=c.Ad.t().contiguous().t())):
+        with pytest.raises(ValueError):
+            c.plan.run(**{"A": c.Ad, "packed": c.packed, **kw})
+    with pytest.raises(q.QGemmError):  # more rows than the plan's
+        c.plan.run(torch.zeros((5, 64), dtype=torch.float16, device="cuda"), c.packed, M=5)

@@ -599,6 +599,8 @@ qgemm_status check_cache(const qgemm_kv_cache* c, int64_t T, int32_t q_heads) {
   if ((c->page_size & (c->page_size - 1)) != 0 || c->page_size > 65536) return QGEMM_ERR_UNSUPPORTED;
   if (c->head_dim % 8 != 0 || c->head_dim > 256) return QGEMM_ERR_UNSUPPORTED;
   if (c->n_pages > INT32_MAX || T > INT32_MAX || q_heads > 65535) return QGEMM_ERR_UNSUPPORTED;
+  // one page is below 4 GiB
+  if ((uint64_t)c->page_size * c->kv_heads * c->head_dim * 2 >= (uint64_t)1 << 32) return QGEMM_ERR_UNSUPPORTED;
   return QGEMM_OK;
 }
 
@@ -611,6 +613,7 @@ qgemm_status attention_shape(const qgemm_kv_cache* c, int64_t T, int32_t q_heads
   if (B > 65535 || max_q > INT32_MAX || max_len > INT32_MAX || prefix_len > INT32_MAX) return QGEMM_ERR_UNSUPPORTED;
   if (max_len + prefix_len > INT32_MAX - 65536) return QGEMM_ERR_UNSUPPORTED;  // key positions are 32 bits wide
   *s = {T, B, max_q < T ? max_q : T, max_len, prefix_len, q_heads, c->kv_heads, c->head_dim};
+  if (T > 0 && !attention_grid_fits(*s)) return QGEMM_ERR_UNSUPPORTED;
   return QGEMM_OK;
 }
 
@@ -866,6 +869,7 @@ qgemm_status qgemm_attention(const qgemm_kv_cache* cache, int64_t T, int32_t q_h
   if (st != QGEMM_OK) return st;
   if (table_width < 0 || q_stride < (int64_t)q_heads * cache->head_dim) return QGEMM_ERR_INVALID_ARG;
   if (T == 0) return QGEMM_OK;
+  if (!(scale > 0.f) || scale > 3e38f) return QGEMM_ERR_INVALID_ARG;
   if (!q || !q_starts || !kv_lens || !out || (table_width && !tables) || (prefix_len && !prefix_table))
     return QGEMM_ERR_INVALID_ARG;
   if (q_stride % 8 != 0 || ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out)) & 15))
@@ -896,7 +900,7 @@ qgemm_status qgemm_attention(const qgemm_kv_cache* cache, int64_t T, int32_t q_h
   a.D = cache->head_dim;
   a.n_pages = (int32_t)cache->n_pages;
   a.page_shift = __builtin_ctz((unsigned)cache->page_size);
-  a.max_q = (int32_t)max_q;
+  a.max_q = (int32_t)s.max_q;
   a.max_len = (int32_t)max_len;
   a.scale = scale;
   (void)hipGetLastError();

@@ -1,86 +1,677 @@
 // Causal attention of a ragged batch over the paged cache, behind one shared prefix.
 //
 //   o = sum_j p_j v_j / sum_j p_j,  p_j = exp(s_j - m),  s_j = scale q . k_j,  m = max s_j
-// in one pass over the keys: when a block of keys raises the running maximum from m to m',
-// the sums so far shrink by exp(m - m').
+// in one pass over the keys: when a block of keys raises the running maximum, the sums so
+// far shrink by exp(old - new).  The results of parts of the keys join the same way.
 //
-// One wave per query and head.  A lane scores one key of a block of 64, the block's
-// probabilities meet in the wave, and then a lane owns head_dim / 64 places of the output.
-#include "qgemm_internal.hpp"
+// Packed rows.  All q_heads / kv_heads = G query heads of a key / value head share its
+// keys, so a row of a tile is a (query token, head of the group) pair: row r is token
+// r / G, head r % G.  A tile's rows read every key once.
+//
+// Work items (one workgroup of four waves each):
+//   prefix item    a tile of the rows of ALL sequences against a chunk of the prefix, which
+//                  every query sees whole: no mask, and the prefix is read once per tile of
+//                  up to 128 rows instead of once per sequence;
+//   sequence item  a tile of one sequence's rows against a chunk of its own tokens, or of
+//                  prefix and own tokens one after the other where the sequence's rows fill
+//                  tiles by themselves (sharing then saves nothing).
+// Both kinds run in one launch; items whose keys are split leave (m, l, o) in fp32 in the
+// workspace, which a second pass joins in slot order.
+//
+// Two tile shapes.  KEYS: few rows (up to 16): the four waves take blocks of 32 keys in
+// turn, each with LDS of its own and no barrier, and meet in LDS at the end; bound by HBM.
+// ROWS: 64 or 128 rows, each wave its own 16 or 32, all from one block of 64 keys in LDS;
+// bound by the matrix cores and the exponentials.
+//
+// The products.  S^T = K Q^T (keys x rows) and O^T = V^T P^T on 16x16x32 MFMAs: the lane
+// that holds a score column (row l % 16, keys 4 (l / 16) + i) holds exactly its operand of
+// the second product, since the order of the keys within a product is free as long as P
+// and V agree, so probabilities never leave their lane.  V^T comes from LDS by transposed
+// reads (ds_read_b64_tr_b16: lane i of 16 gets column i of a 4 x 16 block).  Keys and
+// values go from memory to LDS directly (global_load_lds_dwordx4), and so do the page
+// numbers of the block after next, so that no wait for a page number ever waits for the
+// data loads behind it.
+//
+// Precision: scores, maxima and sums in fp32, exponentials as 2^(s c - m) with c = scale
+// log2 e; probabilities round to fp16 as operands.  The maximum used may lag the true one
+// by up to 8 (probabilities up to 2^8, far inside fp16), which spares most of the
+// rescaling.
+//
+// Keys a row does not see: their scores become -inf by selection, so what K holds there
+// never matters; where a block holds such keys, V's infinities and NaN are taken out of
+// the product and added to the rows that do see them (0 times infinity would be NaN).
+#include "dl_common.hpp"
 
 namespace qg {
 namespace {
+using namespace dl;
 
-__device__ __forceinline__ float wave_max(float v) {
+typedef short short4v __attribute__((ext_vector_type(4)));
+typedef _Float16 half4v __attribute__((ext_vector_type(4)));
+
+enum TileKind : int { TILE_NONE = -1, TILE_KEYS = 0, TILE_ROWS64 = 1, TILE_ROWS128 = 2 };
+constexpr int tile_rows(int kind) { return kind == TILE_KEYS ? 16 : kind == TILE_ROWS64 ? 64 : 128; }
+
+// how the host split the work of a call
+struct AttnSplit {
+  int shared;                      // the prefix has items of its own
+  int kind_p, kind_s;
+  int p_tiles, p_splits, p_chunk;  // row tiles, parts of the keys, keys per part
+  int s_tiles, s_splits, s_chunk;
+  int p_items, s_items;
+  int slots;                       // partial results per row (0: results go out directly)
+  float* part_o;                   // [slot][T][q_heads][D]
+  float2* part_ml;                 // [slot][T][q_heads]: running maximum (log2) and sum
+};
+
+constexpr float RAISE = 8.f;  // log2 of how far the maximum used may lag
+
+__device__ __forceinline__ float exp2_f(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// over the four 16-lane rows of a wave (the lanes of one score column)
+template <typename F>
+__device__ __forceinline__ float across_rows(float v, F f) {
+  auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = f(__uint_as_float(a[0]), __uint_as_float(a[1]));
+  auto b = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return f(__uint_as_float(b[0]), __uint_as_float(b[1]));
+}
+
+// 4-byte direct global -> LDS load (lane l's value lands at lds_base + 4 l)
+__device__ __forceinline__ void dma4(const void* g, uint32_t lds_base) {
+  asm volatile("global_load_lds_dword %0, off" : : "v"(g), "{m0}"(lds_base) : "memory");
+}
+// 16-byte form (lane l's bytes land at lds_base + 16 l)
+__device__ __forceinline__ void dma16v(const void* g, uint32_t lds_base) {
+  asm volatile("global_load_lds_dwordx4 %0, off" : : "v"(g), "{m0}"(lds_base) : "memory");
+}
+// every LDS read of this wave has returned (its buffer may be loaded over)
+__device__ __forceinline__ void reads_done() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+// all but the newest N loads have landed, and no LDS read moves above
+template <int N>
+__device__ __forceinline__ void landed() {
+  wait_vmcnt<N>();
+  asm volatile("" ::: "memory");
+}
+
+// Geometry of a tile kind for head dimensions up to DP.
+template <int DP, int KIND>
+struct TileGeo {
+  static constexpr bool KEYS = KIND == TILE_KEYS;
+  static constexpr int NT = KIND == TILE_ROWS128 ? 2 : 1;  // 16-row blocks per wave
+  static constexpr int BM = tile_rows(KIND);
+  static constexpr int KT = KEYS ? 32 : 64;                // keys per block
+  static constexpr int ROWB = DP * 2, SL = ROWB / 16;      // bytes and 16-byte slots of a key
+  static constexpr int RPI = 64 / SL;                      // keys per 1 KiB load
+  static constexpr int BLOCK = KT * ROWB;                  // bytes of a block of keys (or values)
+  static constexpr int LOADS = BLOCK / 1024 / (KEYS ? 1 : 4);  // per wave
+  // KEYS: each wave one block of keys and one of values; ROWS: two of each, shared
+  static constexpr int PAGES = 2 * 256;                    // page numbers of two blocks, per wave
+  static constexpr int BUF = KEYS ? 4 * 2 * BLOCK : 2 * 2 * BLOCK;
+  static constexpr int RED = KEYS ? 4 * 16 * (DP + 4) * 4 + 4 * 16 * 8 : 0;  // the waves' results at the end
+  static constexpr int LDS = (BUF > RED ? BUF : RED) + 4 * PAGES;
+};
+
+// Position of 16-byte slot c of key r in its LDS row.  A fragment read takes 16 keys x 4
+// neighbouring slots (c = 4 t + lane / 16): the keys that share a bank range (every 64 /
+// SL-th) get their slots in different groups of four, so all 64 slots of a read differ
+// modulo 1 KiB; the transposed reads (16 keys x 2 neighbouring slots) likewise.
+template <int SL>
+__device__ __forceinline__ int slot_of(int r, int c) {
+  constexpr int RPK = 64 / SL;
+  return c ^ (((r / RPK) % (SL / 4)) << 2);
+}
+
+// what a work item covers
+struct Item {
+  int kvh, row0, rows;   // key / value head; first row of the tile, rows in all
+  int tok0, last_tok;    // query token of row 0; last query token of the item's rows
+  int key0, key1;        // keys of the part
+  int pre;               // keys [0, pre) are the prefix's
+  int lim0;              // row r sees keys below pre_lim + max(0, lim0 + r / G), ...
+  int pre_lim;           // ... with lim0 = INT_MIN / 2 for rows that see pre_lim keys
+  int slot;
+  const int32_t* own;    // pages of the keys from pre on
+};
+
+template <int DP, int KIND>
+__device__ __forceinline__ void attend_tile(const AttnArgs& a, const AttnSplit& sp, const Item& it, uint8_t* lds) {
+  using T = TileGeo<DP, KIND>;
+  constexpr bool KEYS = T::KEYS;
+  constexpr int NT = T::NT, KT = T::KT, SL = T::SL, RPI = T::RPI, LOADS = T::LOADS;
+  constexpr int NSUB = KT / 16, NK = KT / 32, ND = DP / 16, NQ = DP / 32;
+
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int g = lane >> 4, l16 = lane & 15;
+  const int G = a.q_heads / a.kv_heads, D = a.D;
+
+  // ---- rows of this wave, and the keys that they see
+  const int wrow0 = it.row0 + (KEYS ? 0 : wave * NT * 16);
+  int lim[NT];
 #pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor(v, o, 64));
-  return v;
-}
-__device__ __forceinline__ float wave_sum(float v) {
+  for (int nt = 0; nt < NT; ++nt) {
+    const int r = min(wrow0 + nt * 16 + l16, it.rows - 1);
+    lim[nt] = min(it.key1, it.pre_lim + max(0, it.lim0 + r / G));
+  }
+  // over the tile's last row (the limits grow with the row), this wave's first and last
+  auto limit_of = [&](int r) { return min(it.key1, it.pre_lim + max(0, it.lim0 + min(r, it.rows - 1) / G)); };
+  const int kend = __builtin_amdgcn_readfirstlane(limit_of(it.row0 + T::BM - 1));
+  const int wave_lo = __builtin_amdgcn_readfirstlane(limit_of(wrow0));
+  const int wave_hi = __builtin_amdgcn_readfirstlane(wrow0 < it.rows ? limit_of(wrow0 + NT * 16 - 1) : 0);
+
+  // blocks of this wave: all of them (ROWS), or every fourth (KEYS)
+  const int nblk = kend > it.key0 ? (kend - it.key0 + KT - 1) / KT : 0;
+  const int j0 = KEYS ? wave : 0, jstep = KEYS ? 4 : 1;
+  const int cnt = nblk > j0 ? (nblk - j0 + jstep - 1) / jstep : 0;
+  auto base_of = [&](int j) { return it.key0 + (j0 + j * jstep) * KT; };
+
+  float4v o[NT][ND];
+  float m[NT], l[NT];
 #pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
-  return v;
-}
+  for (int nt = 0; nt < NT; ++nt) {
+    m[nt] = -INFINITY;
+    l[nt] = 0.f;
+#pragma unroll
+    for (int d = 0; d < ND; ++d) o[nt][d] = float4v{0.f, 0.f, 0.f, 0.f};
+  }
 
-// offset of token t of sequence b's keys (prefix tokens first) in the cache arrays
-__device__ __forceinline__ int64_t token_offset(const AttnArgs& a, int b, int64_t t, int head) {
-  int64_t own = t - a.prefix_len;
-  const int32_t* table = own < 0 ? a.prefix_table : a.tables + (int64_t)b * a.table_width;
-  if (own < 0) own = t;
-  int page = table[own >> a.page_shift];
-  if ((uint32_t)page >= (uint32_t)a.n_pages) page = 0;
-  const int in_page = (int)(own & ((1 << a.page_shift) - 1));
-  return (((int64_t)page * a.kv_heads + head) << a.page_shift) * a.D + (int64_t)in_page * a.D;
-}
-
-__global__ __launch_bounds__(64) void attend_simple_kernel(AttnArgs a) {
-  const int lane = threadIdx.x, b = blockIdx.z, i = blockIdx.y, h = blockIdx.x;
-  const int start = a.q_starts[b], n = min(a.q_starts[b + 1] - start, a.max_q);
-  if (i >= n) return;
-  const int64_t row = start + i;
-  if (row < 0 || row >= a.T) return;
-  const int64_t held = min((int64_t)min(a.kv_lens[b], a.max_len), a.table_width << a.page_shift);
-  const int64_t seen = max((int64_t)0, held - n + i + 1);
-  const int64_t keys = a.prefix_len + seen;
-  const int kvh = h / (a.q_heads / a.kv_heads);
-  const _Float16* q = a.q + row * a.q_stride + (int64_t)h * a.D;
-  float m = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int64_t t0 = 0; t0 < keys; t0 += 64) {
-    const int64_t t = t0 + lane;
-    float s = -INFINITY;
-    int64_t at = 0;
-    if (t < keys) {
-      at = token_offset(a, b, t, kvh);
-      s = 0.f;
-      for (int d = 0; d < a.D; ++d) s += (float)q[d] * (float)a.k[at + d];
-      s *= a.scale;
+  if (cnt > 0) {
+    // ---- operands of the rows: lane holds row l % 16, values 32 t + 8 g .. + 7 (zero past D)
+    half8v qf[NT][NQ];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int r = min(wrow0 + nt * 16 + l16, it.rows - 1);
+      const int tok = min(it.tok0 + r / G, it.last_tok), head = it.kvh * G + r % G;
+      const _Float16* q = a.q + (int64_t)tok * a.q_stride + (int64_t)head * D;
+#pragma unroll
+      for (int t = 0; t < NQ; ++t) {
+        const int d = 32 * t + 8 * g;
+        qf[nt][t] = d < D ? *reinterpret_cast<const half8v*>(q + d) : half8v{0, 0, 0, 0, 0, 0, 0, 0};
+      }
     }
-    const float m2 = fmaxf(m, wave_max(s));
-    const float base = m2 == -INFINITY ? 0.f : m2;
-    const float keep = __expf(m - base), p = t < keys ? __expf(s - base) : 0.f;
-    l = l * keep + wave_sum(p);
-    m = m2;
-    for (int e = 0; e < 4; ++e) o[e] *= keep;
-    const int cnt = (int)min((int64_t)64, keys - t0);
-    for (int j = 0; j < cnt; ++j) {
-      const float pj = __shfl(p, j, 64);
-      const int64_t vj = __shfl(at, j, 64);
-      for (int e = 0; e < 4; ++e)
-        if (e * 64 + lane < a.D) o[e] += pj * (float)a.v[vj + e * 64 + lane];
+    const float c = a.scale * 1.4426950408889634f;
+
+    // ---- staging
+    uint8_t* const kbuf = lds + (KEYS ? wave * 2 * T::BLOCK : 0);
+    uint8_t* const pages = lds + (T::LDS - 4 * T::PAGES) + wave * T::PAGES;
+    const uint32_t kbuf_at = __builtin_amdgcn_readfirstlane(lds_off(kbuf));
+    const uint32_t pages_at = __builtin_amdgcn_readfirstlane(lds_off(pages));
+    const int page_mask = (1 << a.page_shift) - 1;
+    const uint32_t row_bytes = (uint32_t)D * 2;
+    const uint32_t page_bytes = (uint32_t)a.kv_heads * row_bytes << a.page_shift;  // below 2^32 (checked)
+    const uint32_t head_bytes = (uint32_t)it.kvh * row_bytes << a.page_shift;
+    // token of place x of block j, as its place in the prefix's or the sequence's own pages
+    auto place = [&](int j, int x, bool& own) {
+      const int t = min(base_of(j) + x, kend - 1);
+      own = t >= it.pre;
+      return own ? t - it.pre : t;
+    };
+    // page numbers of block j (one lane each) into ring slot j & 1
+    auto load_pages = [&](int j) {
+      bool own;
+      const int t = place(j, lane & (KT - 1), own);
+      const int32_t* e = (own ? it.own : a.prefix_table) + (t >> a.page_shift);
+      dma4(e, pages_at + (j & 1) * 256);
+    };
+    // byte offsets in the cache of the rows that this lane loads of block j
+    const int c_lane = lane % SL, r_lane = lane / SL;
+    auto row_of_load = [&](int i) { return (KEYS ? i : i * 4 + wave) * RPI + r_lane; };
+    int64_t off[LOADS];
+    auto find_rows = [&](int j) {
+#pragma unroll
+      for (int i = 0; i < LOADS; ++i) {
+        const int x = row_of_load(i);
+        uint32_t page = reinterpret_cast<const uint32_t*>(pages + (j & 1) * 256)[x];
+        if (page >= (uint32_t)a.n_pages) page = 0;
+        bool own;
+        const int t = place(j, x, own);
+        const int slot = slot_of<SL>(x, c_lane);
+        const uint32_t in_page = head_bytes + (uint32_t)(t & page_mask) * row_bytes + (slot * 8 < D ? slot * 16 : 0);
+        off[i] = (int64_t)((uint64_t)page * page_bytes + in_page);
+      }
+    };
+    auto load_block = [&](const _Float16* cache, uint32_t at) {
+#pragma unroll
+      for (int i = 0; i < LOADS; ++i)
+        dma16v(reinterpret_cast<const uint8_t*>(cache) + off[i], at + (KEYS ? i : i * 4 + wave) * 1024);
+    };
+
+    float4v s[NT][NSUB];
+    half8v p[NT][NK];
+    // S^T of a block: lane holds keys 16 u + 4 g + i of row l % 16
+    auto scores = [&](const uint8_t* kb) {
+#pragma unroll
+      for (int u = 0; u < NSUB; ++u) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) s[nt][u] = float4v{0.f, 0.f, 0.f, 0.f};
+        const int r = u * 16 + l16;
+#pragma unroll
+        for (int t = 0; t < NQ; ++t) {
+          const half8v kf = *reinterpret_cast<const half8v*>(kb + r * T::ROWB + slot_of<SL>(r, 4 * t + g) * 16);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) s[nt][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, qf[nt][t], s[nt][u], 0, 0, 0);
+        }
+      }
+    };
+    // probabilities of a block from its scores; keys past lim are out when masked
+    auto softmax = [&](int base, bool masked) {
+      bool raise = false;
+      float top[NT];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        if (masked) {
+          const int n = lim[nt] - base - 4 * g;
+#pragma unroll
+          for (int u = 0; u < NSUB; ++u)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[nt][u][i] = u * 16 + i < n ? s[nt][u][i] : -INFINITY;
+        }
+        float x = -INFINITY;
+#pragma unroll
+        for (int u = 0; u < NSUB; ++u)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x = fmaxf(x, s[nt][u][i]);
+        top[nt] = across_rows(x, [](float p, float q) { return fmaxf(p, q); }) * c;
+        raise |= top[nt] > m[nt] + RAISE;
+      }
+      if (__any(raise)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          // row by row, so that a row's result does not depend on the rows beside it
+          const float to = top[nt] > m[nt] + RAISE ? top[nt] : m[nt];
+          const float keep = m[nt] == to ? 1.f : exp2_f(m[nt] - to);
+          m[nt] = to;
+          l[nt] *= keep;
+#pragma unroll
+          for (int d = 0; d < ND; ++d) o[nt][d] *= keep;
+        }
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const float ref = m[nt] == -INFINITY ? 0.f : m[nt];
+        float sum = 0.f;
+#pragma unroll
+        for (int u = 0; u < NSUB; ++u)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float e = exp2_f(__builtin_fmaf(s[nt][u][i], c, -ref));
+            sum += e;
+            p[nt][u / 2][(u & 1) * 4 + i] = (_Float16)e;
+          }
+        l[nt] += sum;
+      }
+    };
+    // operand of V^T: lane holds value 16 d + l % 16 of keys 32 k + 4 g + (0..3) and + 16
+    auto v_operand = [&](const uint8_t* vb, int d, int k) {
+      half8v v;
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        const int r = k * 32 + hf * 16 + 4 * g + (l16 >> 2);
+        const int slot = slot_of<SL>(r, 2 * d + ((l16 >> 1) & 1));
+        const uint8_t* at = vb + r * T::ROWB + slot * 16 + (l16 & 1) * 8;
+        const short4v x = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (__attribute__((address_space(3))) short4v*)(__attribute__((address_space(3))) void*)at);
+        const half4v y = __builtin_bit_cast(half4v, x);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[hf * 4 + i] = y[i];
+      }
+      return v;
+    };
+    auto product = [&](const uint8_t* vb) {
+#pragma unroll
+      for (int d = 0; d < ND; ++d)
+#pragma unroll
+        for (int k = 0; k < NK; ++k) {
+          const half8v v = v_operand(vb, d, k);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) o[nt][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, p[nt][k], o[nt][d], 0, 0, 0);
+        }
+    };
+    // The same where some rows do not see some keys: finite values as above; infinities
+    // and NaN (two rare products of indicators) count for the rows that see their key.
+    auto product_masked = [&](const uint8_t* vb, int base) {
+#pragma unroll 1
+      for (int k = 0; k < NK; ++k) {
+#pragma unroll
+        for (int d = 0; d < ND; ++d) {
+          half8v v = v_operand(vb, d, k), up = {}, down = {};
+          // an exponent of all ones, plus one, carries into the sign's place
+          const uint4 w = __builtin_bit_cast(uint4, v);
+          const uint32_t carry = ((w.x & 0x7C007C00u) + 0x04000400u) | ((w.y & 0x7C007C00u) + 0x04000400u) |
+                                 ((w.z & 0x7C007C00u) + 0x04000400u) | ((w.w & 0x7C007C00u) + 0x04000400u);
+          const bool any_odd = __any((carry & 0x80008000u) != 0);
+          if (any_odd) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const _Float16 x = v[i];
+              const bool nan = x != x, above = x > (_Float16)65504.f, below = x < (_Float16)-65504.f;
+              up[i] = nan || above ? (_Float16)1.f : (_Float16)0.f;
+              down[i] = nan || below ? (_Float16)1.f : (_Float16)0.f;
+              v[i] = nan || above || below ? (_Float16)0.f : x;
+            }
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            half8v pk;
+#pragma unroll
+            for (int kk = 0; kk < NK; ++kk)
+              if (kk == k) pk = p[nt][kk];
+            o[nt][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, pk, o[nt][d], 0, 0, 0);
+            if (any_odd) {
+              half8v sees;
+              const int n = lim[nt] - base - k * 32 - 4 * g;
+#pragma unroll
+              for (int i = 0; i < 8; ++i) sees[i] = (i >> 2) * 16 + (i & 3) < n ? (_Float16)1.f : (_Float16)0.f;
+              const float4v zero = {0.f, 0.f, 0.f, 0.f};
+              const float4v nu = __builtin_amdgcn_mfma_f32_16x16x32_f16(up, sees, zero, 0, 0, 0);
+              const float4v nd = __builtin_amdgcn_mfma_f32_16x16x32_f16(down, sees, zero, 0, 0, 0);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                if (nu[i] > 0.f) o[nt][d][i] += INFINITY;
+                if (nd[i] > 0.f) o[nt][d][i] -= INFINITY;
+              }
+            }
+          }
+        }
+      }
+    };
+
+    if constexpr (KEYS) {
+      // One block of keys and one of values per wave: the next keys load from the moment
+      // the scores are done, the next values from the moment the product is.  Loads land
+      // in order, so a count of newer ones says when a block is there.
+      load_pages(0);
+      landed<0>();
+      find_rows(0);
+      reads_done();
+      load_pages(1);
+      load_block(a.k, kbuf_at);
+      load_block(a.v, kbuf_at + T::BLOCK);
+      for (int j = 0; j < cnt; ++j) {
+        const bool more = j + 1 < cnt;
+        const int base = base_of(j);
+        const bool masked = base + KT > wave_lo;
+        landed<LOADS>();  // the values may still be on their way
+        scores(kbuf);
+        if (more) find_rows(j + 1);
+        reads_done();
+        if (more) {
+          load_pages(j + 2);
+          load_block(a.k, kbuf_at);
+        }
+        softmax(base, masked);
+        if (more) landed<LOADS + 1>();
+        else landed<0>();
+        if (masked) product_masked(kbuf + T::BLOCK, base);
+        else product(kbuf + T::BLOCK);
+        reads_done();
+        if (more) load_block(a.v, kbuf_at + T::BLOCK);
+      }
+    } else {
+      // Two blocks each of keys and values for the workgroup; a wave loads a quarter.
+      load_pages(0);
+      landed<0>();
+      find_rows(0);
+      reads_done();
+      load_pages(1);
+      load_block(a.k, kbuf_at);
+      load_block(a.v, kbuf_at + T::BLOCK);
+      for (int j = 0; j < cnt; ++j) {
+        landed<0>();
+        reads_done();
+        asm volatile("s_barrier" ::: "memory");  // block j is whole, and block j - 1 no longer read
+        if (j + 1 < cnt) {
+          find_rows(j + 1);
+          reads_done();
+          load_pages(j + 2);
+          const uint32_t at = kbuf_at + ((j + 1) & 1) * 2 * T::BLOCK;
+          load_block(a.k, at);
+          load_block(a.v, at + T::BLOCK);
+        }
+        const int base = base_of(j);
+        if (base < wave_hi) {
+          const uint8_t* kb = kbuf + (j & 1) * 2 * T::BLOCK;
+          const bool masked = base + KT > wave_lo;
+          scores(kb);
+          softmax(base, masked);
+          if (masked) product_masked(kb + T::BLOCK, base);
+          else product(kb + T::BLOCK);
+        }
+      }
+    }
+    landed<0>();  // no load outlives the workgroup's LDS
+  }
+
+  // ---- results: lane holds values 16 d + 4 g + i of row l % 16
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) l[nt] = across_rows(l[nt], [](float x, float y) { return x + y; });
+  // (m, l, o) of row r: into its partial slot, or divided into the output
+  auto emit4 = [&](int r, int d0, float4v v, float mm, float ll) {
+    const int64_t th = (int64_t)(it.tok0 + r / G) * a.q_heads + it.kvh * G + r % G;
+    if (sp.slots) {
+      *reinterpret_cast<float4v*>(sp.part_o + ((int64_t)it.slot * a.T * a.q_heads + th) * D + d0) = v;
+      if (d0 == 0) sp.part_ml[(int64_t)it.slot * a.T * a.q_heads + th] = make_float2(mm, ll);
+    } else {
+      const bool none = mm == -INFINITY && ll == 0.f;  // a row that saw nothing
+      half4v h;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) h[i] = (_Float16)(none ? 0.f : v[i] / ll);
+      *reinterpret_cast<half4v*>(a.out + th * D + d0) = h;
+      if (a.lse && d0 == 0) a.lse[th] = none ? -INFINITY : (mm + __log2f(ll)) * 0.6931471805599453f;
+    }
+  };
+  if constexpr (KEYS) {
+    __syncthreads();
+    float* ro = reinterpret_cast<float*>(lds);                        // [wave][row][DP + 4]
+    float2* rml = reinterpret_cast<float2*>(ro + 4 * 16 * (DP + 4));  // [wave][row]
+#pragma unroll
+    for (int d = 0; d < ND; ++d) *reinterpret_cast<float4v*>(ro + (wave * 16 + l16) * (DP + 4) + d * 16 + 4 * g) = o[0][d];
+    if (g == 0) rml[wave * 16 + l16] = make_float2(m[0], l[0]);
+    __syncthreads();
+    for (int x = threadIdx.x; x < 16 * (DP / 4); x += 256) {
+      const int r = x / (DP / 4), d0 = x % (DP / 4) * 4;
+      if (it.row0 + r >= it.rows || d0 >= D) continue;
+      float mm = -INFINITY, ll = 0.f;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) mm = fmaxf(mm, rml[w * 16 + r].x);
+      float4v v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const float2 ml = rml[w * 16 + r];
+        if (ml.x == -INFINITY && ml.y == 0.f) continue;
+        const float f = ml.x == mm ? 1.f : exp2_f(ml.x - mm);
+        ll += f * ml.y;
+        v += f * *reinterpret_cast<const float4v*>(ro + (w * 16 + r) * (DP + 4) + d0);
+      }
+      emit4(it.row0 + r, d0, v, mm, ll);
+    }
+  } else {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int r = wrow0 + nt * 16 + l16;
+      if (r >= it.rows) continue;
+#pragma unroll
+      for (int d = 0; d < ND; ++d)
+        if (d * 16 + 4 * g < D) emit4(r, d * 16 + 4 * g, o[nt][d], m[nt], l[nt]);
     }
   }
-  _Float16* out = a.out + (row * a.q_heads + h) * a.D;
-  for (int e = 0; e < 4; ++e)
-    if (e * 64 + lane < a.D) out[e * 64 + lane] = (_Float16)(keys > 0 ? o[e] / l : 0.f);
-  if (a.lse && lane == 0) a.lse[row * a.q_heads + h] = keys > 0 ? m + __logf(l) : -INFINITY;
+}
+
+// queries of sequence b: first row of q and how many, within q and max_q
+__device__ __forceinline__ void queries_of(const AttnArgs& a, int b, int& start, int& n) {
+  start = min(max(a.q_starts[b], 0), a.T);
+  n = min(min(max(a.q_starts[b + 1], start), a.T) - start, a.max_q);
+}
+
+template <int DP, int KIND_P, int KIND_S>
+__global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void attend_kernel(AttnArgs a, AttnSplit sp) {
+  extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
+  const int G = a.q_heads / a.kv_heads;
+  int w = blockIdx.x;
+  Item it;
+  if (KIND_P != TILE_NONE && w < sp.p_items) {
+    // items of one part of the prefix and one head (the same keys) are neighbours in an XCD
+    if ((sp.p_items & 7) == 0) w = (w & 7) * (sp.p_items >> 3) + (w >> 3);
+    const int tile = w % sp.p_tiles, part = w / sp.p_tiles % sp.p_splits;
+    it.kvh = w / sp.p_tiles / sp.p_splits;
+    it.row0 = tile * tile_rows(KIND_P);
+    it.rows = a.T * G;
+    it.tok0 = 0;
+    it.last_tok = a.T - 1;
+    it.key0 = part * sp.p_chunk;
+    it.key1 = min((int)a.prefix_len, it.key0 + sp.p_chunk);
+    it.pre = it.pre_lim = (int)a.prefix_len;
+    it.lim0 = INT32_MIN / 2;
+    it.slot = part;
+    it.own = nullptr;
+    if constexpr (KIND_P != TILE_NONE) attend_tile<DP, KIND_P>(a, sp, it, lds);
+    return;
+  }
+  if (KIND_P != TILE_NONE) w -= sp.p_items;
+  if ((sp.s_items & 7) == 0) w = (w & 7) * (sp.s_items >> 3) + (w >> 3);
+  // the last tiles of a sequence see the most keys: they start first
+  const int tile = sp.s_tiles - 1 - w % sp.s_tiles, part = w / sp.s_tiles % sp.s_splits;
+  w = w / sp.s_tiles / sp.s_splits;
+  it.kvh = w % a.kv_heads;
+  const int b = w / a.kv_heads;
+  int n;
+  queries_of(a, b, it.tok0, n);
+  it.row0 = tile * tile_rows(KIND_S);
+  it.rows = n * G;
+  if (it.row0 >= it.rows) return;
+  it.last_tok = it.tok0 + n - 1;
+  const int64_t room = a.table_width << a.page_shift;
+  const int held = (int)min((int64_t)min(max(a.kv_lens[b], 0), a.max_len), room);
+  it.pre = it.pre_lim = sp.shared ? 0 : (int)a.prefix_len;
+  it.lim0 = held - n + 1;
+  it.key0 = part * sp.s_chunk;
+  it.key1 = min(it.pre + held, it.key0 + sp.s_chunk);
+  it.slot = (sp.shared ? sp.p_splits : 0) + part;
+  it.own = a.tables + (int64_t)b * a.table_width;
+  attend_tile<DP, KIND_S>(a, sp, it, lds);
+}
+
+// Joins the partial results of every row: D / 4 lanes a row, slots in order.
+__global__ __launch_bounds__(256) void attend_join_kernel(AttnArgs a, AttnSplit sp) {
+  const int per = a.D / 4, rows = 256 / per;  // lanes of a row, rows of a workgroup
+  const int lr = threadIdx.x / per, d0 = threadIdx.x % per * 4;
+  int start, n;
+  queries_of(a, blockIdx.y, start, n);
+  const int64_t x = (int64_t)blockIdx.x * rows + lr;  // row of the sequence: query * q_heads + head
+  if (lr >= rows || x >= (int64_t)n * a.q_heads) return;
+  const int64_t th = (int64_t)start * a.q_heads + x, step = (int64_t)a.T * a.q_heads;
+  float mm = -INFINITY, ll = 0.f;
+  float4v v = {0.f, 0.f, 0.f, 0.f};
+  for (int s = 0; s < sp.slots; ++s) {
+    const float2 ml = sp.part_ml[s * step + th];
+    if (ml.x == -INFINITY && ml.y == 0.f) continue;
+    const float4v p = *reinterpret_cast<const float4v*>(sp.part_o + (s * step + th) * a.D + d0);
+    const float to = fmaxf(mm, ml.x);
+    const float keep = mm == to ? 1.f : exp2_f(mm - to), f = ml.x == to ? 1.f : exp2_f(ml.x - to);
+    mm = to;
+    ll = ll * keep + ml.y * f;
+    v = v * keep + p * f;
+  }
+  const bool none = mm == -INFINITY && ll == 0.f;
+  half4v h;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) h[i] = (_Float16)(none ? 0.f : v[i] / ll);
+  *reinterpret_cast<half4v*>(a.out + th * a.D + d0) = h;
+  if (a.lse && d0 == 0) a.lse[th] = none ? -INFINITY : (mm + __log2f(ll)) * 0.6931471805599453f;
+}
+
+int64_t div_up(int64_t x, int64_t y) { return (x + y - 1) / y; }
+
+// keys per part and parts, so that about `want` items run (parts of at least min_chunk keys)
+void split_keys(int64_t keys, int64_t items, int64_t want, int64_t min_chunk, int* chunk, int* splits) {
+  int64_t s = div_up(want, items < 1 ? 1 : items);
+  const int64_t most = div_up(keys < 1 ? 1 : keys, min_chunk);
+  if (s > most) s = most;
+  if (s > 64) s = 64;
+  if (s < 1) s = 1;
+  *chunk = (int)(div_up(div_up(keys < 1 ? 1 : keys, s), 64) * 64);
+  *splits = (int)div_up(keys < 1 ? 1 : keys, *chunk);
+}
+
+int kind_for(int64_t rows) { return rows <= 16 ? TILE_KEYS : rows <= 64 ? TILE_ROWS64 : TILE_ROWS128; }
+
+AttnSplit choose_split(const AttnShape& s) {
+  AttnSplit p = {};
+  const int64_t G = s.q_heads / s.kv_heads, rows = s.max_q * G;
+  p.kind_s = kind_for(rows);
+  p.kind_p = TILE_NONE;
+  p.shared = s.prefix_len > 0 && s.B > 1 && p.kind_s != TILE_ROWS128;
+  p.s_tiles = (int)div_up(rows, tile_rows(p.kind_s));
+  const int64_t s_base = s.B * s.kv_heads * p.s_tiles;
+  if (p.shared) {
+    p.kind_p = kind_for(s.T * G);
+    p.p_tiles = (int)div_up(s.T * G, tile_rows(p.kind_p));
+    split_keys(s.prefix_len, (int64_t)p.p_tiles * s.kv_heads, 256, 128, &p.p_chunk, &p.p_splits);
+    p.p_items = p.p_tiles * p.p_splits * s.kv_heads;
+  }
+  split_keys(s.max_len + (p.shared ? 0 : s.prefix_len), s_base, 512, 128, &p.s_chunk, &p.s_splits);
+  p.s_items = (int)(s_base * p.s_splits);
+  p.slots = (p.shared ? p.p_splits : 0) + p.s_splits;
+  if (p.slots == 1) p.slots = 0;
+  return p;
+}
+
+size_t part_o_bytes(const AttnShape& s, const AttnSplit& p) {
+  return (size_t)p.slots * s.T * s.q_heads * s.D * sizeof(float);
+}
+
+template <int DP, int KIND_P, int KIND_S>
+hipError_t launch_kinds(const AttnArgs& a, const AttnSplit& p, hipStream_t st) {
+  constexpr int ls = TileGeo<DP, KIND_S>::LDS;
+  constexpr int lp = KIND_P == TILE_NONE ? 0 : TileGeo<DP, KIND_P == TILE_NONE ? KIND_S : KIND_P>::LDS;
+  constexpr int lds = ls > lp ? ls : lp;
+  static_assert(lds <= 160 * 1024, "LDS budget");
+  hipLaunchKernelGGL((attend_kernel<DP, KIND_P, KIND_S>), dim3((unsigned)(p.p_items + p.s_items)), dim3(256), lds, st, a, p);
+  return hipGetLastError();
+}
+
+template <int DP>
+hipError_t launch_dim(const AttnArgs& a, const AttnSplit& p, hipStream_t st) {
+  switch (p.kind_p * 4 + p.kind_s) {
+    case TILE_NONE * 4 + TILE_KEYS: return launch_kinds<DP, TILE_NONE, TILE_KEYS>(a, p, st);
+    case TILE_NONE * 4 + TILE_ROWS64: return launch_kinds<DP, TILE_NONE, TILE_ROWS64>(a, p, st);
+    case TILE_NONE * 4 + TILE_ROWS128: return launch_kinds<DP, TILE_NONE, TILE_ROWS128>(a, p, st);
+    case TILE_KEYS * 4 + TILE_KEYS: return launch_kinds<DP, TILE_KEYS, TILE_KEYS>(a, p, st);
+    case TILE_ROWS64 * 4 + TILE_KEYS: return launch_kinds<DP, TILE_ROWS64, TILE_KEYS>(a, p, st);
+    case TILE_ROWS64 * 4 + TILE_ROWS64: return launch_kinds<DP, TILE_ROWS64, TILE_ROWS64>(a, p, st);
+    case TILE_ROWS128 * 4 + TILE_KEYS: return launch_kinds<DP, TILE_ROWS128, TILE_KEYS>(a, p, st);
+    case TILE_ROWS128 * 4 + TILE_ROWS64: return launch_kinds<DP, TILE_ROWS128, TILE_ROWS64>(a, p, st);
+    case TILE_KEYS * 4 + TILE_ROWS64: return launch_kinds<DP, TILE_ROWS64, TILE_ROWS64>(a, p, st);  // (T below max_q)
+  }
+  return hipErrorInvalidValue;
 }
 
 }  // namespace
 
-size_t attention_ws_bytes(const AttnShape&) { return 0; }
+bool attention_grid_fits(const AttnShape& s) {
+  const int64_t G = s.q_heads / s.kv_heads, tiles = div_up(s.max_q * G, 16), all = div_up(s.T * G, 16);
+  return (s.B * tiles + all) * s.kv_heads * 64 < INT32_MAX && s.T * G < INT32_MAX / 2 &&
+         s.max_q * s.q_heads < INT32_MAX;
+}
 
-hipError_t launch_attention(const AttnArgs& a, const AttnShape& s, void*, hipStream_t st) {
-  hipLaunchKernelGGL(attend_simple_kernel, dim3(a.q_heads, (unsigned)a.max_q, (unsigned)s.B), dim3(64), 0, st, a);
+size_t attention_ws_bytes(const AttnShape& s) {
+  const AttnSplit p = choose_split(s);
+  if (!p.slots) return 0;
+  return part_o_bytes(s, p) + (size_t)p.slots * s.T * s.q_heads * sizeof(float2);
+}
+
+hipError_t launch_attention(const AttnArgs& a, const AttnShape& s, void* ws, hipStream_t st) {
+  AttnSplit p = choose_split(s);
+  if (p.slots) {
+    p.part_o = static_cast<float*>(ws);
+    p.part_ml = reinterpret_cast<float2*>(static_cast<char*>(ws) + part_o_bytes(s, p));
+  }
+  hipError_t e = s.D <= 64 ? launch_dim<64>(a, p, st) : s.D <= 128 ? launch_dim<128>(a, p, st) : launch_dim<256>(a, p, st);
+  if (e != hipSuccess || !p.slots) return e;
+  const int rows = 256 / (s.D / 4);
+  hipLaunchKernelGGL(attend_join_kernel, dim3((unsigned)div_up(s.max_q * s.q_heads, rows), (unsigned)s.B), dim3(256), 0, st,
+                     a, p);
   return hipGetLastError();
 }
 
