@@ -112,14 +112,19 @@ struct TileGeo {
   static constexpr int LDS = (BUF > RED ? BUF : RED) + 4 * PAGES;
 };
 
-// Position of 16-byte slot c of key r in its LDS row.  A fragment read takes 16 keys x 4
-// neighbouring slots (c = 4 t + lane / 16): the keys that share a bank range (every 64 /
-// SL-th) get their slots in different groups of four, so all 64 slots of a read differ
-// modulo 1 KiB; the transposed reads (16 keys x 2 neighbouring slots) likewise.
+// Position of 16-byte slot c of key r in its LDS row: c XOR f(r), f linear in the bits of
+// r.  The LDS serves the 64 lanes of a read in groups of 16, 32 or all, each of which
+// should touch every 16-byte slot of 256, 512 or 1024 bytes once.  A fragment read of K
+// takes 16 keys (lane % 16) at 4 neighbouring slots (lane / 16), a transposed read of V 16
+// keys at 2 neighbouring slots, 8 keys by half a wave; f is chosen so that both are free of
+// conflicts (checked for all keys and slots on the host; with f = 4 (r / 4), which spreads
+// the keys over 1024 bytes only, conflicts were 74 % of the LDS cycles of a prefill).
 template <int SL>
 __device__ __forceinline__ int slot_of(int r, int c) {
-  constexpr int RPK = 64 / SL;
-  return c ^ (((r / RPK) % (SL / 4)) << 2);
+  if constexpr (SL == 8) return c ^ (r & 6) ^ (((r >> 3) & 1) * 7);
+  const int f = (r ^ ((r & 1) << 3)) & 15;
+  if constexpr (SL == 16) return c ^ f;
+  return c ^ f ^ ((((r >> 3) ^ (r >> 1)) & 1) << 4);
 }
 
 // what a work item covers
@@ -237,48 +242,57 @@ __device__ __forceinline__ void attend_tile(const AttnArgs& a, const AttnSplit& 
         dma16v(reinterpret_cast<const uint8_t*>(cache) + off[i], at + (KEYS ? i : i * 4 + wave) * 1024);
     };
 
-    float4v s[NT][NSUB];
     half8v p[NT][NK];
-    // S^T of a block: lane holds keys 16 u + 4 g + i of row l % 16
-    auto scores = [&](const uint8_t* kb) {
-#pragma unroll
-      for (int u = 0; u < NSUB; ++u) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) s[nt][u] = float4v{0.f, 0.f, 0.f, 0.f};
-        const int r = u * 16 + l16;
-#pragma unroll
-        for (int t = 0; t < NQ; ++t) {
-          const half8v kf = *reinterpret_cast<const half8v*>(kb + r * T::ROWB + slot_of<SL>(r, 4 * t + g) * 16);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) s[nt][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, qf[nt][t], s[nt][u], 0, 0, 0);
-        }
-      }
+    typedef float4v Scores[NT][NSUB];
+    // operand of K: lane holds values 32 t + 8 g .. + 7 of key 16 u + l % 16
+    auto k_operand = [&](const uint8_t* kb, int u, int t) {
+      const int r = u * 16 + l16;
+      return *reinterpret_cast<const half8v*>(kb + r * T::ROWB + slot_of<SL>(r, 4 * t + g) * 16);
     };
-    // probabilities of a block from its scores; keys past lim are out when masked
-    auto softmax = [&](int base, bool masked) {
-      bool raise = false;
-      float top[NT];
+    auto score_step = [&](const half8v& kf, Scores& s, int u, int t) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+        s[nt][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, qf[nt][t], t ? s[nt][u] : float4v{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
+    };
+    // S^T of a block: lane holds keys 16 u + 4 g + i of row l % 16
+    auto scores = [&](const uint8_t* kb, Scores& s) {
+#pragma unroll
+      for (int u = 0; u < NSUB; ++u)
+#pragma unroll
+        for (int t = 0; t < NQ; ++t) score_step(k_operand(kb, u, t), s, u, t);
+    };
+    // the scores of keys that a row does not see
+    auto hide = [&](Scores& s, int base) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        if (masked) {
-          const int n = lim[nt] - base - 4 * g;
+        const int n = lim[nt] - base - 4 * g;
 #pragma unroll
-          for (int u = 0; u < NSUB; ++u)
+        for (int u = 0; u < NSUB; ++u)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) s[nt][u][i] = u * 16 + i < n ? s[nt][u][i] : -INFINITY;
-        }
+          for (int i = 0; i < 4; ++i) s[nt][u][i] = u * 16 + i < n ? s[nt][u][i] : -INFINITY;
+      }
+    };
+    // the largest score of each row of a block (log2 units)
+    auto largest = [&](const Scores& s, float (&top)[NT]) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
         float x = -INFINITY;
 #pragma unroll
         for (int u = 0; u < NSUB; ++u)
 #pragma unroll
           for (int i = 0; i < 4; ++i) x = fmaxf(x, s[nt][u][i]);
         top[nt] = across_rows(x, [](float p, float q) { return fmaxf(p, q); }) * c;
-        raise |= top[nt] > m[nt] + RAISE;
       }
-      if (__any(raise)) {
+    };
+    // raises the maxima that lag too far, row by row (a row's result does not depend on the
+    // rows beside it), with what the rows have summed so far
+    auto raise = [&](const float (&top)[NT]) {
+      bool any = false;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) any |= top[nt] > m[nt] + RAISE;
+      if (__any(any)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          // row by row, so that a row's result does not depend on the rows beside it
           const float to = top[nt] > m[nt] + RAISE ? top[nt] : m[nt];
           const float keep = m[nt] == to ? 1.f : exp2_f(m[nt] - to);
           m[nt] = to;
@@ -287,20 +301,28 @@ __device__ __forceinline__ void attend_tile(const AttnArgs& a, const AttnSplit& 
           for (int d = 0; d < ND; ++d) o[nt][d] *= keep;
         }
       }
+    };
+    // probabilities from scores, two at a time: pair x of a block (key half x / (4 NT),
+    // then row block, then pairs of its 8 keys), against ref = m or 0 where m is -inf
+    float ref[NT];
+    auto set_ref = [&] {
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const float ref = m[nt] == -INFINITY ? 0.f : m[nt];
-        float sum = 0.f;
+      for (int nt = 0; nt < NT; ++nt) ref[nt] = m[nt] == -INFINITY ? 0.f : m[nt];
+    };
+    auto exp_pair = [&](const Scores& s, int x) {
+      const int k = x / (4 * NT), nt = x / 4 % NT, y = x % 4 * 2;
 #pragma unroll
-        for (int u = 0; u < NSUB; ++u)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float e = exp2_f(__builtin_fmaf(s[nt][u][i], c, -ref));
-            sum += e;
-            p[nt][u / 2][(u & 1) * 4 + i] = (_Float16)e;
-          }
-        l[nt] += sum;
+      for (int e = 0; e < 2; ++e) {
+        const int u = 2 * k + (y + e) / 4, i = (y + e) % 4;
+        const float v = exp2_f(__builtin_fmaf(s[nt][u][i], c, -ref[nt]));
+        l[nt] += v;
+        p[nt][k][y + e] = (_Float16)v;
       }
+    };
+    auto exponentials = [&](const Scores& s) {
+      set_ref();
+#pragma unroll
+      for (int x = 0; x < NK * NT * 4; ++x) exp_pair(s, x);
     };
     // operand of V^T: lane holds value 16 d + l % 16 of keys 32 k + 4 g + (0..3) and + 16
     auto v_operand = [&](const uint8_t* vb, int d, int k) {
@@ -320,9 +342,9 @@ __device__ __forceinline__ void attend_tile(const AttnArgs& a, const AttnSplit& 
     };
     auto product = [&](const uint8_t* vb) {
 #pragma unroll
-      for (int d = 0; d < ND; ++d)
+      for (int k = 0; k < NK; ++k)
 #pragma unroll
-        for (int k = 0; k < NK; ++k) {
+        for (int d = 0; d < ND; ++d) {
           const half8v v = v_operand(vb, d, k);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) o[nt][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, p[nt][k], o[nt][d], 0, 0, 0);
@@ -393,14 +415,19 @@ __device__ __forceinline__ void attend_tile(const AttnArgs& a, const AttnSplit& 
         const int base = base_of(j);
         const bool masked = base + KT > wave_lo;
         landed<LOADS>();  // the values may still be on their way
-        scores(kbuf);
+        Scores s;
+        scores(kbuf, s);
         if (more) find_rows(j + 1);
         reads_done();
         if (more) {
           load_pages(j + 2);
           load_block(a.k, kbuf_at);
         }
-        softmax(base, masked);
+        if (masked) hide(s, base);
+        float top[NT];
+        largest(s, top);
+        raise(top);
+        exponentials(s);
         if (more) landed<LOADS + 1>();
         else landed<0>();
         if (masked) product_masked(kbuf + T::BLOCK, base);
@@ -409,34 +436,114 @@ __device__ __forceinline__ void attend_tile(const AttnArgs& a, const AttnSplit& 
         if (more) load_block(a.v, kbuf_at + T::BLOCK);
       }
     } else {
-      // Two blocks each of keys and values for the workgroup; a wave loads a quarter.
+      // Two blocks each of keys and values for the workgroup, of which a wave loads a
+      // quarter.  Keys run one block ahead of the values: while the vector units take the
+      // exponentials of block j, the matrix cores score block j + 1, and while they
+      // multiply block j with its values, its successor's maxima are found.
+      uint8_t* const vbuf = kbuf + 2 * T::BLOCK;
+      const uint32_t vbuf_at = kbuf_at + 2 * T::BLOCK;
       load_pages(0);
+      load_pages(1);
       landed<0>();
       find_rows(0);
-      reads_done();
-      load_pages(1);
       load_block(a.k, kbuf_at);
-      load_block(a.v, kbuf_at + T::BLOCK);
-      for (int j = 0; j < cnt; ++j) {
+      load_block(a.v, vbuf_at);
+      find_rows(1);
+      reads_done();
+      load_pages(2);
+      if (cnt > 1) load_block(a.k, kbuf_at + T::BLOCK);
+      // blocks that every row of the tile sees whole
+      const int whole = (max(limit_of(it.row0), it.key0) - it.key0) / KT;
+      Scores sa, sb;
+      float top[NT];
+      landed<0>();
+      asm volatile("s_barrier" ::: "memory");
+      scores(kbuf, sa);
+      if (whole < 1) hide(sa, it.key0);
+      largest(sa, top);
+      raise(top);
+      // block j and the loads behind it; LDS halves of the two parities
+      auto stage = [&](int j, int odd) {
         landed<0>();
         reads_done();
-        asm volatile("s_barrier" ::: "memory");  // block j is whole, and block j - 1 no longer read
-        if (j + 1 < cnt) {
-          find_rows(j + 1);
+        asm volatile("s_barrier" ::: "memory");  // keys j + 1 and values j are whole; keys j, values j - 1 no longer read
+        if (j + 1 < cnt) load_block(a.v, vbuf_at + (odd ^ 1) * T::BLOCK);
+        if (j + 2 < cnt) {
+          find_rows(j + 2);
           reads_done();
-          load_pages(j + 2);
-          const uint32_t at = kbuf_at + ((j + 1) & 1) * 2 * T::BLOCK;
-          load_block(a.k, at);
-          load_block(a.v, at + T::BLOCK);
+          load_pages(j + 3);
+          load_block(a.k, kbuf_at + odd * T::BLOCK);
         }
+      };
+      // A block that every row sees whole, in a fixed order of small steps (the fences keep
+      // the scheduler from hoisting all reads to the front, which spilled): each step has
+      // its MFMAs, the LDS read of the operand AHEAD steps on, and a share of the vector
+      // work that fits in their shadow: in the scores of the next block the exponentials
+      // of this one's first 32 keys, in the first half of the product those of the other
+      // 32, in its second half the next block's maxima.
+      auto whole_block = [&](int j, int odd, Scores& now, Scores& next) {
+        constexpr int AHEAD = 4, NS = NSUB * NQ, NP = NK * ND, PAIRS = NT * 4;
+        stage(j, odd);
+        const uint8_t* kb = kbuf + (odd ^ 1) * T::BLOCK;
+        const uint8_t* vb = vbuf + odd * T::BLOCK;
+        auto fence = [] { __builtin_amdgcn_sched_barrier(0); };
+        half8v f[AHEAD];
+        set_ref();
+#pragma unroll
+        for (int x = 0; x < AHEAD; ++x) f[x] = k_operand(kb, x / NQ, x % NQ);
+        fence();
+        static_for(std::make_integer_sequence<int, NS>{}, [&](auto X) {
+          constexpr int x = decltype(X)::value;
+          score_step(f[x % AHEAD], next, x / NQ, x % NQ);
+          if constexpr (x + AHEAD < NS) f[x % AHEAD] = k_operand(kb, (x + AHEAD) / NQ, (x + AHEAD) % NQ);
+          else f[x % AHEAD] = v_operand(vb, x + AHEAD - NS, 0);
+#pragma unroll
+          for (int y = x * PAIRS / NS; y < (x + 1) * PAIRS / NS; ++y) exp_pair(now, y);
+          fence();
+        });
+        static_assert(NS % AHEAD == 0 && ND >= AHEAD && NK == 2, "operand ring");
+        float part[NT];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) part[nt] = -INFINITY;
+        static_for(std::make_integer_sequence<int, NP>{}, [&](auto X) {
+          constexpr int x = decltype(X)::value, k = x / ND, d = x % ND;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            o[nt][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f[x % AHEAD], p[nt][k], o[nt][d], 0, 0, 0);
+          if constexpr (x + AHEAD < NP) f[x % AHEAD] = v_operand(vb, (x + AHEAD) % ND, (x + AHEAD) / ND);
+          if constexpr (k == 0) {
+#pragma unroll
+            for (int y = d * PAIRS / ND; y < (d + 1) * PAIRS / ND; ++y) exp_pair(now, PAIRS + y);
+          } else {
+#pragma unroll
+            for (int y = d * NSUB * NT / ND; y < (d + 1) * NSUB * NT / ND; ++y)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) part[y % NT] = fmaxf(part[y % NT], next[y % NT][y / NT][i]);
+          }
+          fence();
+        });
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) top[nt] = across_rows(part[nt], [](float x, float y) { return fmaxf(x, y); }) * c;
+        raise(top);
+      };
+      int j = 0;
+      for (; j + 2 < whole; j += 2) {  // block j + 2 is whole too
+        whole_block(j, 0, sa, sb);
+        whole_block(j + 1, 1, sb, sa);
+      }
+#pragma unroll 1
+      for (; j < cnt; ++j) {
+        stage(j, j & 1);
         const int base = base_of(j);
         if (base < wave_hi) {
-          const uint8_t* kb = kbuf + (j & 1) * 2 * T::BLOCK;
-          const bool masked = base + KT > wave_lo;
-          scores(kb);
-          softmax(base, masked);
-          if (masked) product_masked(kb + T::BLOCK, base);
-          else product(kb + T::BLOCK);
+          exponentials(sa);
+          product_masked(vbuf + (j & 1) * T::BLOCK, base);
+        }
+        if (base + KT < wave_hi) {
+          scores(kbuf + ((j & 1) ^ 1) * T::BLOCK, sa);
+          if (base + 2 * KT > wave_lo) hide(sa, base + KT);
+          largest(sa, top);
+          raise(top);
         }
       }
     }
@@ -613,18 +720,21 @@ void split_keys(int64_t keys, int64_t items, int64_t want, int64_t min_chunk, in
   *splits = (int)div_up(keys < 1 ? 1 : keys, *chunk);
 }
 
-int kind_for(int64_t rows) { return rows <= 16 ? TILE_KEYS : rows <= 64 ? TILE_ROWS64 : TILE_ROWS128; }
+// (head dimensions past 128 keep 64 rows: with 128 the accumulators of a wave spilled)
+int kind_for(int64_t rows, int D) {
+  return rows <= 16 ? TILE_KEYS : rows <= 64 || D > 128 ? TILE_ROWS64 : TILE_ROWS128;
+}
 
 AttnSplit choose_split(const AttnShape& s) {
   AttnSplit p = {};
   const int64_t G = s.q_heads / s.kv_heads, rows = s.max_q * G;
-  p.kind_s = kind_for(rows);
+  p.kind_s = kind_for(rows, s.D);
   p.kind_p = TILE_NONE;
-  p.shared = s.prefix_len > 0 && s.B > 1 && p.kind_s != TILE_ROWS128;
+  p.shared = s.prefix_len > 0 && s.B > 1 && rows <= 64;
   p.s_tiles = (int)div_up(rows, tile_rows(p.kind_s));
   const int64_t s_base = s.B * s.kv_heads * p.s_tiles;
   if (p.shared) {
-    p.kind_p = kind_for(s.T * G);
+    p.kind_p = kind_for(s.T * G, s.D);
     p.p_tiles = (int)div_up(s.T * G, tile_rows(p.kind_p));
     split_keys(s.prefix_len, (int64_t)p.p_tiles * s.kv_heads, 256, 128, &p.p_chunk, &p.p_splits);
     p.p_items = p.p_tiles * p.p_splits * s.kv_heads;
@@ -652,16 +762,17 @@ hipError_t launch_kinds(const AttnArgs& a, const AttnSplit& p, hipStream_t st) {
 
 template <int DP>
 hipError_t launch_dim(const AttnArgs& a, const AttnSplit& p, hipStream_t st) {
-  switch (p.kind_p * 4 + p.kind_s) {
-    case TILE_NONE * 4 + TILE_KEYS: return launch_kinds<DP, TILE_NONE, TILE_KEYS>(a, p, st);
-    case TILE_NONE * 4 + TILE_ROWS64: return launch_kinds<DP, TILE_NONE, TILE_ROWS64>(a, p, st);
-    case TILE_NONE * 4 + TILE_ROWS128: return launch_kinds<DP, TILE_NONE, TILE_ROWS128>(a, p, st);
-    case TILE_KEYS * 4 + TILE_KEYS: return launch_kinds<DP, TILE_KEYS, TILE_KEYS>(a, p, st);
-    case TILE_ROWS64 * 4 + TILE_KEYS: return launch_kinds<DP, TILE_ROWS64, TILE_KEYS>(a, p, st);
-    case TILE_ROWS64 * 4 + TILE_ROWS64: return launch_kinds<DP, TILE_ROWS64, TILE_ROWS64>(a, p, st);
-    case TILE_ROWS128 * 4 + TILE_KEYS: return launch_kinds<DP, TILE_ROWS128, TILE_KEYS>(a, p, st);
-    case TILE_ROWS128 * 4 + TILE_ROWS64: return launch_kinds<DP, TILE_ROWS128, TILE_ROWS64>(a, p, st);
-    case TILE_KEYS * 4 + TILE_ROWS64: return launch_kinds<DP, TILE_ROWS64, TILE_ROWS64>(a, p, st);  // (T below max_q)
+  if (p.kind_p == TILE_NONE) {
+    if (p.kind_s == TILE_KEYS) return launch_kinds<DP, TILE_NONE, TILE_KEYS>(a, p, st);
+    if (p.kind_s == TILE_ROWS64) return launch_kinds<DP, TILE_NONE, TILE_ROWS64>(a, p, st);
+    if constexpr (DP <= 128) return launch_kinds<DP, TILE_NONE, TILE_ROWS128>(a, p, st);
+  } else if (p.kind_s == TILE_KEYS) {
+    if (p.kind_p == TILE_KEYS) return launch_kinds<DP, TILE_KEYS, TILE_KEYS>(a, p, st);
+    if (p.kind_p == TILE_ROWS64) return launch_kinds<DP, TILE_ROWS64, TILE_KEYS>(a, p, st);
+    if constexpr (DP <= 128) return launch_kinds<DP, TILE_ROWS128, TILE_KEYS>(a, p, st);
+  } else {  // more than 16 rows a sequence, so more than 16 in all
+    if (p.kind_p == TILE_ROWS64) return launch_kinds<DP, TILE_ROWS64, TILE_ROWS64>(a, p, st);
+    if constexpr (DP <= 128) return launch_kinds<DP, TILE_ROWS128, TILE_ROWS64>(a, p, st);
   }
   return hipErrorInvalidValue;
 }
