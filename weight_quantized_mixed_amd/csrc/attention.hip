@@ -38,8 +38,8 @@
 // rescaling.
 //
 // Keys a row does not see: their scores become -inf by selection, so what K holds there
-// never matters; where a block holds such keys, V's infinities and NaN are taken out of
-// the product and added to the rows that do see them (0 times infinity would be NaN).
+// never matters; where a block holds such keys, V's infinities and NaN are added to the
+// rows that do see them and taken out of the product (0 times infinity would be NaN).
 #include "dl_common.hpp"
 
 namespace qg {
@@ -350,53 +350,66 @@ __device__ __forceinline__ void attend_tile(const AttnArgs& a, const AttnSplit& 
           for (int nt = 0; nt < NT; ++nt) o[nt][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, p[nt][k], o[nt][d], 0, 0, 0);
         }
     };
-    // The same where some rows do not see some keys: finite values as above; infinities
-    // and NaN (two rare products of indicators) count for the rows that see their key.
-    auto product_masked = [&](const uint8_t* vb, int base) {
+    // whether a block of values holds no infinity and no NaN
+    auto finite = [&](const uint8_t* vb) {
+      uint32_t carry = 0;  // an exponent of all ones, plus one, carries into the sign's place
+#pragma unroll
+      for (int i = 0; i < T::BLOCK / 1024; ++i) {
+        const uint4 w = *reinterpret_cast<const uint4*>(vb + i * 1024 + lane * 16);
+        carry |= ((w.x & 0x7C007C00u) + 0x04000400u) | ((w.y & 0x7C007C00u) + 0x04000400u) |
+                 ((w.z & 0x7C007C00u) + 0x04000400u) | ((w.w & 0x7C007C00u) + 0x04000400u);
+      }
+      return !__any((carry & 0x80008000u) != 0);
+    };
+    // Takes the infinities and NaN out of a block of values that some rows do not see whole
+    // (0 times one would be NaN): first each is added to the rows that see its key, then it
+    // becomes 0 in LDS.  Rare, and small rather than fast: one element at a time.
+    auto set_apart = [&](uint8_t* vb, int base) {
+      constexpr int PER = DP / 64;  // values of a key that a lane looks at
 #pragma unroll 1
-      for (int k = 0; k < NK; ++k) {
+      for (int x = 0; x < KT; ++x) {
+#pragma unroll 1
+        for (int h = 0; h < PER; ++h) {
+          const int e = lane * PER + h;
+          const uint32_t bits =
+              *reinterpret_cast<const uint16_t*>(vb + x * T::ROWB + slot_of<SL>(x, e / 8) * 16 + e % 8 * 2);
+          uint64_t bad = __ballot((bits & 0x7C00u) == 0x7C00u);
+          while (bad) {
+            const int from = __builtin_ctzll(bad);
+            bad &= bad - 1;
+            const uint32_t b16 = (uint32_t)__builtin_amdgcn_readlane((int)bits, from);
+            const float val = (float)__builtin_bit_cast(_Float16, (uint16_t)b16);
+            const int at = from * PER + h;  // place of the value: register (at / 16, at % 4) of lanes with g = at / 4 % 4
 #pragma unroll
-        for (int d = 0; d < ND; ++d) {
-          half8v v = v_operand(vb, d, k), up = {}, down = {};
-          // an exponent of all ones, plus one, carries into the sign's place
-          const uint4 w = __builtin_bit_cast(uint4, v);
-          const uint32_t carry = ((w.x & 0x7C007C00u) + 0x04000400u) | ((w.y & 0x7C007C00u) + 0x04000400u) |
-                                 ((w.z & 0x7C007C00u) + 0x04000400u) | ((w.w & 0x7C007C00u) + 0x04000400u);
-          const bool any_odd = __any((carry & 0x80008000u) != 0);
-          if (any_odd) {
+            for (int nt = 0; nt < NT; ++nt) {
+              const float add = g == (at >> 2 & 3) && base + x < lim[nt] ? val : 0.f;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const _Float16 x = v[i];
-              const bool nan = x != x, above = x > (_Float16)65504.f, below = x < (_Float16)-65504.f;
-              up[i] = nan || above ? (_Float16)1.f : (_Float16)0.f;
-              down[i] = nan || below ? (_Float16)1.f : (_Float16)0.f;
-              v[i] = nan || above || below ? (_Float16)0.f : x;
-            }
-          }
+              for (int d = 0; d < ND; ++d)
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            half8v pk;
-#pragma unroll
-            for (int kk = 0; kk < NK; ++kk)
-              if (kk == k) pk = p[nt][kk];
-            o[nt][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, pk, o[nt][d], 0, 0, 0);
-            if (any_odd) {
-              half8v sees;
-              const int n = lim[nt] - base - k * 32 - 4 * g;
-#pragma unroll
-              for (int i = 0; i < 8; ++i) sees[i] = (i >> 2) * 16 + (i & 3) < n ? (_Float16)1.f : (_Float16)0.f;
-              const float4v zero = {0.f, 0.f, 0.f, 0.f};
-              const float4v nu = __builtin_amdgcn_mfma_f32_16x16x32_f16(up, sees, zero, 0, 0, 0);
-              const float4v nd = __builtin_amdgcn_mfma_f32_16x16x32_f16(down, sees, zero, 0, 0, 0);
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                if (nu[i] > 0.f) o[nt][d][i] += INFINITY;
-                if (nd[i] > 0.f) o[nt][d][i] -= INFINITY;
-              }
+                for (int i = 0; i < 4; ++i)
+                  if (d == at >> 4 && i == (at & 3)) o[nt][d][i] += add;
             }
           }
         }
       }
+      reads_done();
+      if constexpr (!KEYS) asm volatile("s_barrier" ::: "memory");  // (no wave cleans what another still looks at)
+#pragma unroll 1
+      for (int i = KEYS ? 0 : wave; i < T::BLOCK / 1024; i += KEYS ? 1 : 4) {
+        uint4* at = reinterpret_cast<uint4*>(vb + i * 1024 + lane * 16);
+        uint4 w = *at;
+        auto clean = [](uint32_t& x) {
+          if ((x & 0x7C00u) == 0x7C00u) x &= 0xFFFF0000u;
+          if ((x & 0x7C000000u) == 0x7C000000u) x &= 0xFFFFu;
+        };
+        clean(w.x);
+        clean(w.y);
+        clean(w.z);
+        clean(w.w);
+        *at = w;
+      }
+      reads_done();
+      if constexpr (!KEYS) asm volatile("s_barrier" ::: "memory");
     };
 
     if constexpr (KEYS) {
@@ -430,8 +443,8 @@ __device__ __forceinline__ void attend_tile(const AttnArgs& a, const AttnSplit& 
         exponentials(s);
         if (more) landed<LOADS + 1>();
         else landed<0>();
-        if (masked) product_masked(kbuf + T::BLOCK, base);
-        else product(kbuf + T::BLOCK);
+        if (masked && !finite(kbuf + T::BLOCK)) set_apart(kbuf + T::BLOCK, base);
+        product(kbuf + T::BLOCK);
         reads_done();
         if (more) load_block(a.v, kbuf_at + T::BLOCK);
       }
@@ -522,22 +535,37 @@ __device__ __forceinline__ void attend_tile(const AttnArgs& a, const AttnSplit& 
           }
           fence();
         });
+        if (j + 1 < whole) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) top[nt] = across_rows(part[nt], [](float x, float y) { return fmaxf(x, y); }) * c;
+          for (int nt = 0; nt < NT; ++nt) top[nt] = across_rows(part[nt], [](float x, float y) { return fmaxf(x, y); }) * c;
+        } else {  // (past the last block: nothing is seen of what its buffer holds)
+          hide(next, base_of(j + 1));
+          largest(next, top);
+        }
         raise(top);
       };
       int j = 0;
-      for (; j + 2 < whole; j += 2) {  // block j + 2 is whole too
+      for (; j + 1 < whole; j += 2) {
         whole_block(j, 0, sa, sb);
         whole_block(j + 1, 1, sb, sa);
+      }
+      if (j < whole) {
+        whole_block(j, 0, sa, sb);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int u = 0; u < NSUB; ++u) sa[nt][u] = sb[nt][u];
+        ++j;
       }
 #pragma unroll 1
       for (; j < cnt; ++j) {
         stage(j, j & 1);
         const int base = base_of(j);
+        uint8_t* const vb = vbuf + (j & 1) * T::BLOCK;
+        if (!finite(vb)) set_apart(vb, base);  // all four waves or none
         if (base < wave_hi) {
           exponentials(sa);
-          product_masked(vbuf + (j & 1) * T::BLOCK, base);
+          product(vb);
         }
         if (base + KT < wave_hi) {
           scores(kbuf + ((j & 1) ^ 1) * T::BLOCK, sa);
