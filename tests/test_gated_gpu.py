@@ -227,3 +227,16 @@ def test_gated_rejects_wrong_tensors():
             c.plan.run(**{"A": c.Ad, "packed": c.packed, **kw})
     with pytest.raises(q.QGemmError):  # more rows than the plan's
         c.plan.run(torch.zeros((5, 64), dtype=torch.float16, device="cuda"), c.packed, M=5)
+
+
+def test_gradient_of_a_long_reduction_in_parts():
+    """dA over more than 8192 inner columns runs in ordered parts; M not a multiple of any tile."""
+    c = GatedCase(70, 4200, 256, "i4", 128, seed=21, bias=False)
+    pre = c.plan.new_preact()
+    c.run(preact=pre)
+    _, gg, uu, e = c.reference()
+    dC = (synth.draw_fp16_activations(70, 4200, seed=5) * np.float16(0.1)).astype(np.float16)
+    out = c.plan.backward(c.Ad, c.packed, pre, host_to_device(dC))
+    ref = oracle.gated_grads_ref(c.A, *c.W, gg, uu, dC, c.act)["dA"]
+    bound = oracle.gated_grads_bound(c.A, *c.W, gg, uu, dC, c.act, *e, True)["dA"]
+    assert_near(out["dA"].cpu().numpy().astype(np.float64), ref, bound + 2.0**-11 * np.abs(ref) + 2.0**-25, "dA")

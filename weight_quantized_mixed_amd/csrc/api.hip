@@ -576,7 +576,13 @@ struct GateBackward {
     if ((uint64_t)M * kd * 2 >= (uint64_t)1 << 32 || round_up(p->K, 256) / 16 * (blob_k / 32) * 64 >= INT32_MAX ||
         (weight_grads && (uint64_t)most * mp * 2 >= (uint64_t)1 << 32))
       return QGEMM_ERR_UNSUPPORTED;
-    init_plan(&to_a, M, p->K, kd, QGEMM_F16, QGEMM_F16, QGEMM_F16, QGEMM_F32, 0, 0, 1, 0, 0, 0.f, 0.f);
+    // Long reductions over few tiles: four ordered parts (measured at 22016 inner columns,
+    // K = 4096: M = 128 / 512 / 1024 63 / 123 / 187 -> 43 / 99 / 170 us; M = 1536, 96 tiles of
+    // 256 x 256, 263 -> 314 us)
+    const int64_t tiles = ((M + 255) / 256) * ((p->K + 255) / 256);
+    const int parts = kd >= 8192 && tiles <= 64 ? 4 : 1;
+    init_plan(&to_a, M, p->K, kd, QGEMM_F16, QGEMM_F16, QGEMM_F16, QGEMM_F32, 0, 0, parts,
+              parts > 1 ? QGEMM_DETERMINISTIC : 0u, 0, 0.f, 0.f);
     if (weight_grads)
       init_plan(&to_w, 2 * p->gate_n, p->K, mp, QGEMM_F16, QGEMM_F16, QGEMM_F16, QGEMM_F32, 0, 0, 1, 0, 0, 0.f, 0.f);
     auto place = [this](size_t n) {

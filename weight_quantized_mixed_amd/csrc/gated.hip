@@ -38,37 +38,47 @@ __global__ __launch_bounds__(256) void gate_grad_kernel(const _Float16* __restri
                                                         float* __restrict__ bias_part) {
   __shared__ __attribute__((aligned(16))) _Float16 t[2][GT][GPITCH];  // [gate, up][column][row]
   const int m0 = blockIdx.y * GT, n0 = blockIdx.x * GT;
-  constexpr int PER_ROW = GT / V;
-  for (int i = threadIdx.x; i < GT * PER_ROW; i += 256) {
-    const int r = i / PER_ROW, n = n0 + (i % PER_ROW) * V, m = m0 + r;
-    typedef _Float16 vec __attribute__((ext_vector_type(V)));
-    vec g = {}, u = {}, d = {};
-    if (m < M && n < N) {  // N is a multiple of V
-      const _Float16* p = preact + (size_t)m * 2 * N + n;
-      g = *reinterpret_cast<const vec*>(p);
-      u = *reinterpret_cast<const vec*>(p + N);
-      d = *reinterpret_cast<const vec*>(dC + (size_t)m * N + n);
-    }
-    vec dg, du;
+  constexpr int PER_ROW = GT / V, STEPS = GT * PER_ROW / 256, AT_ONCE = STEPS < 4 ? STEPS : 4;
+  typedef _Float16 vec __attribute__((ext_vector_type(V)));
+#pragma unroll 1
+  for (int s0 = 0; s0 < STEPS; s0 += AT_ONCE) {
+    // the loads of a few steps before their first use
+    vec g[AT_ONCE], u[AT_ONCE], d[AT_ONCE];
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-      const float x = (float)g[e], dc = (float)d[e];
-      const float s = sigmoid_f(x * (c0 + c1 * x * x));
-      // act'(x) = s + x s (1 - s) t'(x)
-      dg[e] = (_Float16)(dc * (float)u[e] * (s + x * s * (1.f - s) * (c0 + 3.f * c1 * x * x)));
-      du[e] = (_Float16)(dc * x * s);
+    for (int s = 0; s < AT_ONCE; ++s) {
+      const int i = (s0 + s) * 256 + threadIdx.x, m = m0 + i / PER_ROW, n = n0 + (i % PER_ROW) * V;
+      g[s] = u[s] = d[s] = vec{};
+      if (m < M && n < N) {  // N is a multiple of V
+        const _Float16* p = preact + (size_t)m * 2 * N + n;
+        g[s] = *reinterpret_cast<const vec*>(p);
+        u[s] = *reinterpret_cast<const vec*>(p + N);
+        d[s] = *reinterpret_cast<const vec*>(dC + (size_t)m * N + n);
+      }
     }
-    if (rowwise && m < M) {
-      const int c = (n >> 4) * 32 + (n & 15);
-      _Float16* o = rowwise + (size_t)m * kd + c;
-      if (c < kd) *reinterpret_cast<vec*>(o) = dg;
-      if (c + 16 < kd) *reinterpret_cast<vec*>(o + 16) = du;
-    }
-    if (colwise) {
+#pragma unroll
+    for (int s = 0; s < AT_ONCE; ++s) {
+      const int i = (s0 + s) * 256 + threadIdx.x, r = i / PER_ROW, m = m0 + r, n = n0 + (i % PER_ROW) * V;
+      vec dg, du;
 #pragma unroll
       for (int e = 0; e < V; ++e) {
-        t[0][n - n0 + e][r] = dg[e];
-        t[1][n - n0 + e][r] = du[e];
+        const float x = (float)g[s][e], dc = (float)d[s][e];
+        const float sg = sigmoid_f(x * (c0 + c1 * x * x));
+        // act'(x) = sg + x sg (1 - sg) t'(x)
+        dg[e] = (_Float16)(dc * (float)u[s][e] * (sg + x * sg * (1.f - sg) * (c0 + 3.f * c1 * x * x)));
+        du[e] = (_Float16)(dc * x * sg);
+      }
+      if (rowwise && m < M) {
+        const int c = (n >> 4) * 32 + (n & 15);
+        _Float16* o = rowwise + (size_t)m * kd + c;
+        if (c < kd) *reinterpret_cast<vec*>(o) = dg;
+        if (c + 16 < kd) *reinterpret_cast<vec*>(o + 16) = du;
+      }
+      if (colwise) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          t[0][n - n0 + e][r] = dg[e];
+          t[1][n - n0 + e][r] = du[e];
+        }
       }
     }
   }
@@ -81,7 +91,12 @@ __global__ __launch_bounds__(256) void gate_grad_kernel(const _Float16* __restri
   if (bias_part && threadIdx.x < 2 * GT) {
     const int p = threadIdx.x / GT, c = threadIdx.x % GT, n = n0 + c;
     float s = 0.f;
-    for (int r = 0; r < GT; ++r) s += (float)t[p][c][r];
+#pragma unroll
+    for (int r = 0; r < GT; r += 8) {
+      const half8v v = *reinterpret_cast<half8v*>(&t[p][c][r]);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s += (float)v[e];
+    }
     if (n < N) bias_part[(size_t)blockIdx.y * 2 * N + (size_t)p * N + n] = s;
   }
 }
@@ -194,13 +209,14 @@ hipError_t launch_gate_grad(const void* preact, const void* dC, int64_t M, int64
   // column tiles cover the inner columns' padding of rowwise too (kd / 2 output columns)
   const int64_t cols = rowwise && kd / 2 > N ? kd / 2 : N;
   const dim3 grid((unsigned)((cols + GT - 1) / GT), (unsigned)((M + GT - 1) / GT));
-  const bool vec = N % 8 == 0 && ((reinterpret_cast<uintptr_t>(preact) | reinterpret_cast<uintptr_t>(dC)) & 15) == 0;
+  const uintptr_t at = reinterpret_cast<uintptr_t>(preact) | reinterpret_cast<uintptr_t>(dC);
   auto go = [&](auto kernel) {
     hipLaunchKernelGGL(kernel, grid, dim3(256), 0, st, static_cast<const _Float16*>(preact),
                        static_cast<const _Float16*>(dC), (int)M, (int)N, (int)kd, mp, c0, c1,
                        static_cast<_Float16*>(rowwise), static_cast<_Float16*>(colwise), bias_part);
   };
-  if (vec) go(gate_grad_kernel<8>);
+  if (N % 8 == 0 && (at & 15) == 0) go(gate_grad_kernel<8>);
+  else if (N % 2 == 0 && (at & 3) == 0) go(gate_grad_kernel<2>);
   else go(gate_grad_kernel<1>);
   return hipGetLastError();
 }
