@@ -5,6 +5,8 @@ libqgemm kernel.  Non-GPU tensors are rejected: there is no host fallback.
 """
 from __future__ import annotations
 
+import functools
+
 import numpy as np
 import torch
 
@@ -37,9 +39,9 @@ def _stream(stream):
 
 
 def _check(t, name, shape, dtype):
-    """A device tensor argument of this shape and type (None passes)."""
-    if t is not None and (tuple(t.shape) != tuple(shape) or t.dtype != dtype):
-        raise ValueError(f"{name}: {dtype} {tuple(shape)} expected, got {t.dtype} {tuple(t.shape)}")
+    """A tensor argument of this shape (a tuple) and type (None passes)."""
+    if t is not None and (t.shape != shape or t.dtype != dtype):
+        raise ValueError(f"{name}: {dtype} {shape} expected, got {t.dtype} {tuple(t.shape)}")
     return t
 
 
@@ -233,13 +235,20 @@ class QGated:
                 "dbias_up": part(db, 1)}
 
 
-def _rows(t, width, name):
-    """(address, values between rows) of fp16 rows of at least `width` values, the last dimension contiguous."""
+def _rows(t, name, T, width):
+    """(address, values between rows) of fp16 [T, width], whose rows may be slices of wider ones."""
     if not t.is_cuda:
         raise ValueError("qgemm takes device tensors only")
-    if t.dtype != torch.float16 or t.dim() != 2 or t.shape[1] != width or (width > 1 and t.stride(1) != 1):
-        raise ValueError(f"{name}: fp16 [T, {width}] with contiguous rows expected, got {t.dtype} {tuple(t.shape)}")
-    return t.data_ptr(), max(t.stride(0), width)
+    step, one = t.stride() if t.dim() == 2 else (0, 0)
+    if t.dtype != torch.float16 or t.shape != (T, width) or (one != 1 and width > 1) or (step < width and T > 1):
+        raise ValueError(f"{name}: fp16 {(T, width)} with contiguous rows expected, got {t.dtype} {tuple(t.shape)}")
+    return t.data_ptr(), step if step > width else width
+
+
+# the workspace of an attention call depends on its sizes alone
+_attention_workspace = functools.lru_cache(maxsize=256)(
+    lambda n_pages, page_size, kv_heads, head_dim, *sizes: _q.qgemm_attention_workspace(
+        _q.KVCacheDesc(4096, 4096, n_pages, page_size, kv_heads, head_dim), *sizes))
 
 
 class PagedKV:
@@ -263,13 +272,11 @@ class PagedKV:
 
         q [T, q_heads * head_dim], k and v [T, kv_heads * head_dim]: rows may be slices of a wider array.
         """
-        T, D = q.shape[0], self.head_dim
-        q_heads = q.shape[1] // D
-        qp, qs = _rows(q, q_heads * D, "q")
-        kp, ks = _rows(k, self.kv_heads * D, "k")
-        vp, vs = _rows(v, self.kv_heads * D, "v")
-        if k.shape[0] != T or v.shape[0] != T:
-            raise ValueError("q, k and v have a row for each token")
+        (T, width), D = q.shape, self.head_dim
+        q_heads, kv_width = width // D, self.kv_heads * D
+        qp, qs = _rows(q, "q", T, q_heads * D)
+        kp, ks = _rows(k, "k", T, kv_width)
+        vp, vs = _rows(v, "v", T, kv_width)
         n_pos, half = cos.shape
         _check(cos, "cos", (n_pos, half), torch.float32)
         _check(sin, "sin", (n_pos, half), torch.float32)
@@ -286,10 +293,12 @@ class PagedKV:
                out=None, lse=None, ws=None, stream=None):
         """Causal attention of a ragged batch (q [T, q_heads, head_dim]) over its own pages and the shared prefix."""
         T, q_heads, D = q.shape
-        if D != self.head_dim or q.stride(1) != D:
-            raise ValueError(f"q: [T, q_heads, {self.head_dim}] with contiguous rows expected, got {tuple(q.shape)}")
-        qp, qs = _rows(q.flatten(1) if q.is_contiguous() else q.as_strided((T, q_heads * D), (q.stride(0), q.stride(2))),
-                       q_heads * D, "q")
+        step, per_head, one = q.stride()
+        if (D != self.head_dim or q.dtype != torch.float16 or not q.is_cuda or (one != 1 and D > 1)
+                or (per_head != D and q_heads > 1) or (step < q_heads * D and T > 1)):
+            raise ValueError(f"q: fp16 [T, q_heads, {self.head_dim}] with contiguous rows on the device expected, "
+                             f"got {q.dtype} {tuple(q.shape)}")
+        qp, qs = q.data_ptr(), max(step, q_heads * D)
         B, width = tables.shape
         i32 = torch.int32
         _check(q_starts, "q_starts", (B + 1,), i32)
@@ -303,7 +312,8 @@ class PagedKV:
             out = torch.empty((T, q_heads, D), dtype=torch.float16, device=q.device)
         _check(out, "out", (T, q_heads, D), torch.float16)
         _check(lse, "lse", (T, q_heads), torch.float32)
-        need = _q.qgemm_attention_workspace(self.desc, T, q_heads, B, max_q, max_len, prefix_len)
+        need = _attention_workspace(self.n_pages, self.page_size, self.kv_heads, D, T, q_heads, B, max_q, max_len,
+                                    prefix_len)
         if ws is None and need:
             if self._ws is None or self._ws.numel() < need:
                 self._ws = torch.empty(need, dtype=torch.uint8, device=q.device)
