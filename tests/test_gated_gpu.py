@@ -240,3 +240,22 @@ def test_gradient_of_a_long_reduction_in_parts():
     ref = oracle.gated_grads_ref(c.A, *c.W, gg, uu, dC, c.act)["dA"]
     bound = oracle.gated_grads_bound(c.A, *c.W, gg, uu, dC, c.act, *e, True)["dA"]
     assert_near(out["dA"].cpu().numpy().astype(np.float64), ref, bound + 2.0**-11 * np.abs(ref) + 2.0**-25, "dA")
+
+
+@pytest.mark.parametrize("M,N,K", [(3400, 100, 2900), (2100, 4100, 2300), (1300, 4105, 1700)])
+def test_input_gradient_from_the_forward_blob(M, N, K):
+    """fp16 weights and enough tiles: dA reads the forward's blob transposed (1, 2 and 4 parts)."""
+    say(f"case direct dA M={M} N={N} K={K}")
+    c = GatedCase(M, N, K, "f16", seed=M, bias=False)
+    pre = c.plan.new_preact()
+    c.run(preact=pre)
+    dC = (synth.draw_fp16_activations(M, N, seed=6) * np.float16(0.1)).astype(np.float16)
+    out = c.plan.backward(c.Ad, c.packed, pre, host_to_device(dC), weight_grads=False)["dA"].cpu().numpy().astype(np.float64)
+    rows = np.unique(np.concatenate([np.arange(0, M, 97), np.arange(M - 20, M)]))
+    A, (Wg, Wu) = c.A[rows].astype(np.float64), c.W
+    _, gg, uu = oracle.gated_ref(A, Wg, Wu, c.act)
+    e = [oracle.sum_bound(A, W, False) + 2.0**-20 * np.abs(x) for W, x in zip(c.W, (gg, uu))]
+    ref = oracle.gated_grads_ref(A, Wg, Wu, gg, uu, dC[rows], c.act)["dA"]
+    bound = oracle.gated_grads_bound(A, Wg, Wu, gg, uu, dC[rows], c.act, *e, False)["dA"]
+    assert_near(out[rows], ref, bound + 2.0**-11 * np.abs(ref) + 2.0**-25, "dA")
+    assert np.isfinite(out).all()

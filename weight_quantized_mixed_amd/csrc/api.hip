@@ -560,6 +560,7 @@ struct GateBackward {
   qgemm_plan to_a;  // dA [M, K] = pre-activation gradients [M, kd] . transposed weights
   qgemm_plan to_w;  // dW [2 N, K] = transposed gradients [2 N, mp] . A
   int64_t kd, mp;   // reduction lengths, whole granules of the fp16 format
+  bool direct;      // to_a reads the forward's fp16 blob transposed (256 x 256 tiles), without a copy of it
   size_t rowwise, colwise, bias, blob, split, bytes;
 
   qgemm_status init(const qgemm_plan* p, int64_t M, bool weight_grads) {
@@ -576,11 +577,20 @@ struct GateBackward {
     if ((uint64_t)M * kd * 2 >= (uint64_t)1 << 32 || round_up(p->K, 256) / 16 * (blob_k / 32) * 64 >= INT32_MAX ||
         (weight_grads && (uint64_t)most * mp * 2 >= (uint64_t)1 << 32))
       return QGEMM_ERR_UNSUPPORTED;
-    // Long reductions over few tiles: four ordered parts (measured at 22016 inner columns,
-    // K = 4096: M = 128 / 512 / 1024 63 / 123 / 187 -> 43 / 99 / 170 us; M = 1536, 96 tiles of
-    // 256 x 256, 263 -> 314 us)
+    // Long reductions over few tiles run in ordered parts.  fp16 weights: the 256 x 256
+    // tiles, which read the forward's blob as it is, wherever 1, 2 or 4 parts occupy 60 % of
+    // the CUs (the transposed copy alone takes 80 us at 22016 inner columns, K = 4096).
+    // Otherwise four parts (quantised weights there: M = 128 / 512 / 1024 63 / 123 / 187 ->
+    // 43 / 99 / 170 us; M = 1536, 96 tiles of 256 x 256, 263 -> 314 us).
     const int64_t tiles = ((M + 255) / 256) * ((p->K + 255) / 256);
-    const int parts = kd >= 8192 && tiles <= 64 ? 4 : 1;
+    int parts = kd >= 8192 && tiles <= 64 ? 4 : 1;
+    direct = false;
+    if (p->w_dtype == QGEMM_F16 && QG_BIG4)
+      for (int kp : {1, 2, 4})
+        if (!direct && (kp == 1 || kd >= 8192) && tiles * kp * 10 >= 256 * 6) {
+          direct = true;
+          parts = kp;
+        }
     init_plan(&to_a, M, p->K, kd, QGEMM_F16, QGEMM_F16, QGEMM_F16, QGEMM_F32, 0, 0, parts,
               parts > 1 ? QGEMM_DETERMINISTIC : 0u, 0, 0.f, 0.f);
     if (weight_grads)
@@ -595,9 +605,26 @@ struct GateBackward {
     colwise = place(weight_grads ? (size_t)2 * p->gate_n * mp * 2 : 0);
     bias = place(weight_grads ? (size_t)gate_grad_row_tiles(M) * 2 * p->gate_n * 4 : 0);
     // the products run one after the other and share the space of their weights
-    blob = place(weight_grads && to_w.L.total > to_a.L.total ? to_w.L.total : to_a.L.total);
+    const size_t blob_a = direct ? 0 : to_a.L.total, blob_w = weight_grads ? to_w.L.total : 0;
+    blob = place(blob_a > blob_w ? blob_a : blob_w);
     split = place(weight_grads && to_w.ws_bytes > to_a.ws_bytes ? to_w.ws_bytes : to_a.ws_bytes);
     return QGEMM_OK;
+  }
+
+  // dA from the row by row gradients in the workspace ws
+  hipError_t run_to_a(const qgemm_plan* p, int64_t M, const void* packed, void* dA, char* ws, hipStream_t st) const {
+    if (!direct) {
+      const hipError_t e = launch_transpose_blob(p->L, p->gate_n, packed, to_a.L, ws + blob, st);
+      if (e != hipSuccess) return e;
+      const qgemm_status s = run_impl(&to_a, M, ws + rowwise, ws + blob, nullptr, nullptr, nullptr, dA, ws + split,
+                                      to_a.ws_bytes, st);
+      return s == QGEMM_OK ? hipSuccess : hipErrorLaunchFailure;
+    }
+    RunArgs a = make_args(&to_a, to_a.ch, M, ws + rowwise, packed, nullptr, dA, ws + split);
+    a.NB = (int32_t)p->L.NB;
+    a.nkb = (int32_t)p->L.nkb;
+    const hipError_t e = launch_mfma_big_transposed(a, st);
+    return e == hipSuccess && a.out_mode == OUT_PARTIAL ? launch_finalize(a, 1, st) : e;
   }
 };
 
@@ -793,13 +820,7 @@ qgemm_status qgemm_gated_backward(const qgemm_plan* plan, int64_t M, const void*
                                   dbias_gate || dbias_up ? reinterpret_cast<float*>(ws + b.bias) : nullptr, st);
   if (e == hipSuccess && (dbias_gate || dbias_up))
     e = launch_bias_grad(reinterpret_cast<float*>(ws + b.bias), M, N, dbias_gate, dbias_up, st);
-  if (e == hipSuccess && dA) {
-    e = launch_transpose_blob(plan->L, N, packed, b.to_a.L, ws + b.blob, st);
-    if (e == hipSuccess &&
-        run_impl(&b.to_a, M, ws + b.rowwise, ws + b.blob, nullptr, nullptr, nullptr, dA, ws + b.split,
-                 b.to_a.ws_bytes, stream) != QGEMM_OK)
-      return QGEMM_ERR_DEVICE;
-  }
+  if (e == hipSuccess && dA) e = b.run_to_a(plan, M, packed, dA, ws, st);
   if (e == hipSuccess && dw_gate) {
     e = launch_transpose_rows(A, M, plan->K, b.to_w.L, ws + b.blob, st);
     // one product for both when the outputs lie one after the other

@@ -89,7 +89,13 @@ struct BigGeo {
 // FOLD: a correction after the loop takes what the loop leaves of the weights' offset,
 // the zero points of uint4 (whose scale slot then holds (scale, zero) pairs) or the
 // offset 8 of signed int4; see nc below
-template <int FMT, bool SCALED, bool FOLD, bool GATED>
+// TRANS (fp16): the weight operand is the transpose of the blob's matrix.  The blob's
+// positions (a.nkb superblock rows of 32) are then the output's columns and its columns
+// (a.NB blocks of 16) the reduction, 64 of them a stage: 8 superblock rows x 4 blocks, and
+// each fragment is two transposed LDS reads (lane i of 16: position i of four columns).  A
+// superblock's pieces (16 bytes: 8 positions of a column) of its odd position groups lie
+// with their columns' bit 2 flipped, which spreads the reads of half a wave over all banks.
+template <int FMT, bool SCALED, bool FOLD, bool GATED, bool TRANS = false>
 __global__ __launch_bounds__(256) void mfma_big_kernel(RunArgs a) {
   using G = BigGeo<FMT, SCALED>;
   constexpr bool FP = G::FP, PACKED = G::PACKED;
@@ -161,6 +167,10 @@ __global__ __launch_bounds__(256) void mfma_big_kernel(RunArgs a) {
       const int cb = (n0 >> 4) + o / BSB, wo = o % BSB;
       b_off[e] = BSB == 512 ? (uint32_t)(cb * 1024 + wo)
                             : (uint32_t)(cb * 1024 + (wo >> 10) * a.NB * 1024 + (wo & 1023));
+      if constexpr (TRANS) {  // slot wave + 4 e: superblock row e of the tile, block `wave` of the stage
+        const int row = min(e, a.nkb - 1 - (n0 >> 5));  // from the tile's first
+        b_off[e] = (uint32_t)(row * a.NB + wave) * 1024u + (uint32_t)(lane ^ (((lane >> 4) & 1) << 2)) * 16u;
+      }
     }
     // scales of columns n0 .. n0 + 255 (lanes past them re-read the last 16 bytes
     // into the unused rest of the slot); wave w loads lanes 16 w .. 16 w + 15
@@ -173,7 +183,7 @@ __global__ __launch_bounds__(256) void mfma_big_kernel(RunArgs a) {
     int nx_i = 0;
     const int64_t pos0 = (int64_t)s0 * SPOS;
     const uint8_t* nx_a = Ab + pos0 * ESZ;
-    const uint8_t* nx_w = Wb + (pos0 / KB) * a.NB * 1024 + (pos0 % KB) * 1024 / KB;
+    const uint8_t* nx_w = TRANS ? Wb + ((int64_t)(n0 >> 5) * a.NB + pos0 / 16) * 1024 : Wb + (pos0 / KB) * a.NB * 1024 + (pos0 % KB) * 1024 / KB;
     const uint8_t* nx_s = nullptr;
     int grp_left = 0;  // stages from the next one to the end of its scale group
     if constexpr (SCALED) {
@@ -189,7 +199,8 @@ __global__ __launch_bounds__(256) void mfma_big_kernel(RunArgs a) {
       nx_dst = nx_dst + STAGE == lds_end ? lds0 : nx_dst + STAGE;
       if (nx_i < nst - 1) {
         nx_a += SPOS * ESZ;
-        if constexpr (BSB == 512) nx_w += ((s0 + nx_i) & 1) ? (size_t)a.NB * 1024 - 512 : (size_t)512;
+        if constexpr (TRANS) nx_w += SPOS / 16 * 1024;
+        else if constexpr (BSB == 512) nx_w += ((s0 + nx_i) & 1) ? (size_t)a.NB * 1024 - 512 : (size_t)512;
         else nx_w += (size_t)2 * a.NB * 1024;
         if constexpr (SCALED) {
           if (--grp_left == 0) {
@@ -244,7 +255,19 @@ __global__ __launch_bounds__(256) void mfma_big_kernel(RunArgs a) {
       const uint8_t* lb = base + A_BYTES + (wn * 8 + j) * BSB;
       if constexpr (PACKED)
         rw[j] = *reinterpret_cast<const uint32_t*>(lb + ((q & 1) * 16 + l16) * 16 + (2 * t + (q >> 1)) * 4);
-      else
+      else if constexpr (TRANS) {
+        typedef short short4v __attribute__((ext_vector_type(4)));
+        typedef __attribute__((address_space(3))) short4v* lds4;
+        // columns 32 t + 8 q .. + 7 of the stage, positions 16 (j % 2) + l16 of superblock row j / 2
+        const int kq = (j & 1) * 2 + ((l16 >> 1) & 1), c = (q & 1) * 8 + (l16 >> 2);
+        const uint8_t* sb = base + A_BYTES + ((wn * 4 + j / 2) * 4 + 2 * t + (q >> 1)) * 1024;
+        const uint8_t* p0 = sb + (kq * 16 + (c ^ ((kq & 1) << 2))) * 16 + (l16 & 1) * 8;
+        const uint8_t* p1 = sb + (kq * 16 + ((c + 4) ^ ((kq & 1) << 2))) * 16 + (l16 & 1) * 8;
+        const short4v x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(__attribute__((address_space(3))) void*)p0);
+        const short4v y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(__attribute__((address_space(3))) void*)p1);
+        const uint2 lo = __builtin_bit_cast(uint2, x), hi = __builtin_bit_cast(uint2, y);
+        f.b[j] = make_uint4(lo.x, lo.y, hi.x, hi.y);
+      } else
         f.b[j] = *reinterpret_cast<const uint4*>(lb + t * 1024 + lane * 16);  // superblock t, piece = lane
       if constexpr (SCALED && t == 0 && scl) {
         const int col = (wn * 8 + j) * 16 + l16;
@@ -518,6 +541,12 @@ hipError_t launch_big_t(const RunArgs& a, hipStream_t st) {
 }
 
 }  // namespace
+
+hipError_t launch_mfma_big_transposed(const RunArgs& a, hipStream_t st) {
+  const int tiles = ((a.M + 255) / 256) * ((a.N + 255) / 256);
+  hipLaunchKernelGGL((mfma_big_kernel<FMT_F16, false, false, false, true>), dim3(tiles * a.k_parts), dim3(256), 0, st, a);
+  return hipGetLastError();
+}
 
 bool big_tile_takes(int fmt, const RunArgs& a) {
   // uint4 with zero points only with the group row sums that fold them out of the loop

@@ -257,6 +257,9 @@ hipError_t launch_mfma_dl_gated(int fmt, int tile, const RunArgs& a, hipStream_t
 // big_tile_takes; same arguments and stage layout as launch_mfma_dl's 256 x 256 tile
 bool big_tile_takes(int fmt, const RunArgs& a);
 hipError_t launch_mfma_big(int fmt, const RunArgs& a, hipStream_t st);
+// fp16 product against the transpose of the blob a.W (a.NB, a.nkb: that blob's), on the same
+// tiles: a.N output columns are the blob's positions, a.K its columns in whole granules
+hipError_t launch_mfma_big_transposed(const RunArgs& a, hipStream_t st);
 hipError_t launch_fill_zero(void* p, size_t bytes, hipStream_t st);
 // zr = the bf16 planes [R_hi | R_lo] of the group row sums of a.A (rows of a.K fp16
 // values, scale groups of a.group_size positions, or one group when it is negative)
