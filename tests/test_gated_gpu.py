@@ -259,3 +259,17 @@ def test_input_gradient_from_the_forward_blob(M, N, K):
     bound = oracle.gated_grads_bound(A, Wg, Wu, gg, uu, dC[rows], c.act, *e, False)["dA"]
     assert_near(out[rows], ref, bound + 2.0**-11 * np.abs(ref) + 2.0**-25, "dA")
     assert np.isfinite(out).all()
+
+
+@pytest.mark.parametrize("w,N,bias", [("i4", 2008, True), ("f16", 2008, False), ("i4", 2002, False), ("u4", 1992, True)])
+def test_gated_largest_tiles_keep_the_preactivations(w, N, bias):
+    """The 256 x 256 tiles' whole-row stores (N a multiple of 8) and element stores, with ragged edges."""
+    M, K = 4001, 128
+    c = GatedCase(M, N, K, w, 128 if w != "f16" else 0, w == "u4", act="gelu_tanh", seed=N, bias=bias)
+    pre = c.plan.new_preact()
+    pre.fill_(float("nan"))
+    got = c.run(preact=pre)
+    C, g, u, e = c.reference()
+    assert_near(got, C, oracle.gated_bound(C, g, u, *e, c.act), "C")
+    for x, ref, err in zip(np.split(pre.cpu().numpy().astype(np.float64), 2, axis=1), (g, u), e):
+        assert_near(x, ref, err + 2.0**-11 * np.abs(ref) + 2.0**-25, "preact")

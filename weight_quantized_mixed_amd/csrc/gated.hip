@@ -62,7 +62,7 @@ __global__ __launch_bounds__(256) void gate_grad_kernel(const _Float16* __restri
 #pragma unroll
       for (int e = 0; e < V; ++e) {
         const float x = (float)g[s][e], dc = (float)d[s][e];
-        const float sg = sigmoid_f(x * (c0 + c1 * x * x));
+        const float sg = gate_sigmoid(c0, c1, x);
         // act'(x) = sg + x sg (1 - sg) t'(x)
         dg[e] = (_Float16)(dc * (float)u[s][e] * (sg + x * sg * (1.f - sg) * (c0 + 3.f * c1 * x * x)));
         du[e] = (_Float16)(dc * x * sg);

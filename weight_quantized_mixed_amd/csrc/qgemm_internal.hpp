@@ -182,10 +182,12 @@ __device__ __forceinline__ GateCol gate_col(const RunArgs& a, int icol) {
 // x sigmoid(t), t = x (c0 + c1 x^2): silu with (1, 0); the tanh form of gelu with
 // (2 c, 2 c 0.044715), c = sqrt(2 / pi), since (1 + tanh y) / 2 = sigmoid(2 y).  The
 // hardware exponential and reciprocal are within a few ulp in fp32.
-__device__ __forceinline__ float sigmoid_f(float t) { return __builtin_amdgcn_rcpf(1.f + __expf(-t)); }
-__device__ __forceinline__ float gate_act(const RunArgs& a, float x) {
-  return x * sigmoid_f(x * (a.act_c0 + a.act_c1 * x * x));
+// sigmoid(x (c0 + c1 x^2)), with the constants times -log2 e taken out of the exponent
+__device__ __forceinline__ float gate_sigmoid(float c0, float c1, float x) {
+  constexpr float L = -1.4426950408889634f;
+  return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(x * (c0 * L + c1 * L * (x * x))));
 }
+__device__ __forceinline__ float gate_act(const RunArgs& a, float x) { return x * gate_sigmoid(a.act_c0, a.act_c1, x); }
 // stores output (row, c.col) from the two sums, in fp32 up to the one rounding of the
 // output (and one of each pre-activation, where they are kept for the backward pass)
 __device__ __forceinline__ void gate_store(const RunArgs& a, int row, const GateCol& c, float g, float u) {
