@@ -407,7 +407,8 @@ typedef struct {
  *               (negative in unused places of a batch) is not stored.
  *   q_out       device, fp16 [T, q_heads, head_dim]; may be q itself when q_stride is
  *               q_heads * head_dim.
- * 16-byte aligned arrays with strides of whole 8 values take the widest accesses.
+ * 16-byte aligned arrays with strides of whole 8 values take the widest accesses.  More
+ * than 65535 * 512 values a token (all heads) return QGEMM_ERR_UNSUPPORTED.
  */
 qgemm_status qgemm_kv_append(const qgemm_kv_cache* cache, int64_t T, int32_t q_heads, const void* q,
                              int64_t q_stride, const void* k, int64_t k_stride, const void* v,

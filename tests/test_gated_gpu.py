@@ -273,3 +273,19 @@ def test_gated_largest_tiles_keep_the_preactivations(w, N, bias):
     assert_near(got, C, oracle.gated_bound(C, g, u, *e, c.act), "C")
     for x, ref, err in zip(np.split(pre.cpu().numpy().astype(np.float64), 2, axis=1), (g, u), e):
         assert_near(x, ref, err + 2.0**-11 * np.abs(ref) + 2.0**-25, "preact")
+
+
+def test_gradients_of_saturated_preactivations():
+    """Pre-activations past fp16 are kept as infinities; their gradients are 0 or the other factor."""
+    for act in ("silu", "gelu_tanh"):
+        plan = QGated(1, 8, 64, "f16", act=act)
+        pre, dC = torch.zeros((1, 16), dtype=torch.float16, device="cuda"), torch.ones((1, 8), dtype=torch.float16, device="cuda")
+        pre[0, :4] = torch.tensor([float("inf"), -float("inf"), 60000.0, -60000.0])
+        pre[0, 8:] = 2.0
+        W = torch.zeros((8, 64), dtype=torch.float16, device="cuda")
+        W[:, 0] = torch.tensor([1.0, 2, 4, 8, 0, 0, 0, 0])
+        A = torch.zeros((1, 64), dtype=torch.float16, device="cuda")
+        A[0, 1] = 1
+        out = plan.backward(A, plan.pack(W, W * 0), pre, dC, bias_grads=True)
+        assert out["dbias_gate"][:4].tolist() == [2.0, 0.0, 2.0, 0.0] and out["dA"][0, 0].item() == 2.0 + 2.0 * 4
+        assert out["dbias_up"][1].item() == 0 and out["dbias_up"][3].item() == 0 and torch.isfinite(out["dw_gate"]).all()

@@ -224,7 +224,7 @@ def test_future_values_never_matter(qs, lens, prefix):
 def test_attention_results_do_not_depend_on_the_call_before():
     c = AttnCase(32, 8, 128, 16, [1] * 6, [0, 900, 30, 64, 5, 1], 3000, seed=2).upload()
     first = c.run()
-    c.cache._ws.fill_(0xFF)  # NaN in every partial result
+    c.cache._workspace.buffers[-1].fill_(0xFF)  # NaN in every partial result
     again = c.run()
     assert np.array_equal(first[0], again[0]) and np.array_equal(first[1], again[1])
 
@@ -318,3 +318,23 @@ def test_paged_kv_rejects_wrong_tensors():
     with pytest.raises(ValueError):
         c.cache.append(c.dq.flatten(1), c.dq.flatten(1), c.dq.flatten(1), *[torch.ones((4, 32), device="cuda")] * 2,
                        torch.zeros(1, dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int64, device="cuda"))
+
+
+def test_an_outgrown_workspace_stays_with_its_graph():
+    """A graph replays a call whose workspace a later, larger call has outgrown."""
+    c = AttnCase(8, 2, 128, 16, [1, 1], [400, 300], 600, seed=12).upload()
+    base, _ = c.run()
+    out = torch.empty_like(c.dq)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        c.cache.attend(c.dq, c.dstarts, c.dlens, c.dtables, 1, 400, c.dprefix, 600, out=out)
+    n = len(c.cache._workspace.buffers)
+    c.run(max_q=60, max_len=20000)
+    assert len(c.cache._workspace.buffers) > n
+    junk = [torch.full((1 << 20,), 0xFF, dtype=torch.uint8, device="cuda") for _ in range(8)]
+    for _ in range(3):
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert np.array_equal(out.cpu().numpy().astype(np.float64), base)
+    assert all((j == 0xFF).all() for j in junk)

@@ -846,6 +846,8 @@ qgemm_status qgemm_kv_append(const qgemm_kv_cache* cache, int64_t T, int32_t q_h
   if (interleaved != 0 && interleaved != 1) return QGEMM_ERR_INVALID_ARG;
   if (q_stride < (int64_t)q_heads * cache->head_dim || k_stride < kv_row || v_stride < kv_row)
     return QGEMM_ERR_INVALID_ARG;
+  // a token's pairs fit the grid's second dimension, one a thread
+  if (((int64_t)q_heads + 2 * cache->kv_heads) * cache->head_dim / 2 > (int64_t)65535 * 256) return QGEMM_ERR_UNSUPPORTED;
   if (T == 0) return QGEMM_OK;
   if (!q || !k || !v || !slots || !q_out) return QGEMM_ERR_INVALID_ARG;
   if (rot_dim && (!cos || !sin || !positions || n_positions < 1)) return QGEMM_ERR_INVALID_ARG;

@@ -61,7 +61,11 @@ __global__ __launch_bounds__(256) void gate_grad_kernel(const _Float16* __restri
       vec dg, du;
 #pragma unroll
       for (int e = 0; e < V; ++e) {
-        const float x = (float)g[s][e], dc = (float)d[s][e];
+        float x = (float)g[s][e];
+        const float dc = (float)d[s][e];
+        // a pre-activation past fp16 was kept as infinity: the largest value instead (where
+        // act' is 0 or 1 already), since infinity times 0 below would be NaN
+        if (fabsf(x) == INFINITY) x = copysignf(65504.f, x);
         const float sg = gate_sigmoid(c0, c1, x);
         // act'(x) = sg + x sg (1 - sg) t'(x)
         dg[e] = (_Float16)(dc * (float)u[s][e] * (sg + x * sg * (1.f - sg) * (c0 + 3.f * c1 * x * x)));

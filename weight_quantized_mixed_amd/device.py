@@ -143,6 +143,22 @@ class QGemm:
         return C
 
 
+class _Workspace:
+    """Device scratch that grows with the calls that use it.  Outgrown buffers are kept: a
+    captured graph may still replay a call that was given one."""
+
+    def __init__(self, device):
+        self.device, self.buffers = device, []
+
+    def of(self, need):
+        if not need:
+            return None
+        if not self.buffers or self.buffers[-1].numel() < need:
+            grown = max(need, 2 * self.buffers[-1].numel()) if self.buffers else need
+            self.buffers.append(torch.empty(grown, dtype=torch.uint8, device=self.device))
+        return self.buffers[-1]
+
+
 class QGated:
     """One gated feed-forward plan: C = act(A . dequant(Wg) + bg) * (A . dequant(Wu) + bu), N columns each.
 
@@ -156,7 +172,7 @@ class QGated:
         self.device = torch.device(device)
         self.plan, self.packed_bytes, self.ws_bytes = _q.qgemm_create_gated(
             M, N, K, self.a_dtype, w_dtype, "f16", OUT_DTYPE[self.a_dtype][1], group_size, int(bool(has_zeros)), act)
-        self._ws = self._bws = None
+        self._ws, self._backward_ws = None, _Workspace(self.device)
 
     close = QGemm.close
     __del__ = close
@@ -224,9 +240,7 @@ class QGated:
         db = new(2, self.N) if bias_grads else None
         need = _q.qgemm_gated_backward_workspace(self.plan, M, weight_grads or bias_grads)
         if ws is None:
-            if self._bws is None or self._bws.numel() < need:
-                self._bws = torch.empty(need, dtype=torch.uint8, device=self.device)
-            ws = self._bws
+            ws = self._backward_ws.of(need)
         part = lambda t, i: None if t is None else t[i]  # noqa: E731
         _q.qgemm_gated_backward(self.plan, M, _ptr(A), _ptr(packed), _ptr(preact), _ptr(dC), _ptr(dA),
                                 _ptr(part(dw, 0)), _ptr(part(dw, 1)), _ptr(part(db, 0)), _ptr(part(db, 1)), _ptr(ws),
@@ -265,7 +279,7 @@ class PagedKV:
         self.k = _check(new() if k is None else k, "k", shape, torch.float16)
         self.v = _check(new() if v is None else v, "v", shape, torch.float16)
         self.desc = _q.KVCacheDesc(_ptr(self.k), _ptr(self.v), self.n_pages, self.page_size, self.kv_heads, self.head_dim)
-        self._ws = None
+        self._workspace = _Workspace(self.k.device)
 
     def append(self, q, k, v, cos, sin, positions, slots, q_out=None, interleaved=False, stream=None):
         """Rotated queries [T, q_heads, head_dim]; the rotated keys and the values go to the cache's slots.
@@ -314,10 +328,8 @@ class PagedKV:
         _check(lse, "lse", (T, q_heads), torch.float32)
         need = _attention_workspace(self.n_pages, self.page_size, self.kv_heads, D, T, q_heads, B, max_q, max_len,
                                     prefix_len)
-        if ws is None and need:
-            if self._ws is None or self._ws.numel() < need:
-                self._ws = torch.empty(need, dtype=torch.uint8, device=q.device)
-            ws = self._ws
+        if ws is None:
+            ws = self._workspace.of(need)
         _q.qgemm_attention(self.desc, T, q_heads, qp, qs, B, _ptr(q_starts), _ptr(kv_lens), _ptr(tables), width,
                            _ptr(prefix_table) if prefix_len else 0, prefix_len, max_q, max_len,
                            D ** -0.5 if scale is None else scale, _ptr(out), _ptr(lse), _ptr(ws),
