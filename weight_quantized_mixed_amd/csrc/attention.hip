@@ -581,17 +581,22 @@ __device__ __forceinline__ void attend_tile(const AttnArgs& a, const AttnSplit& 
   // ---- results: lane holds values 16 d + 4 g + i of row l % 16
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) l[nt] = across_rows(l[nt], [](float x, float y) { return x + y; });
-  // (m, l, o) of row r: into its partial slot, or divided into the output
-  auto emit4 = [&](int r, int d0, float4v v, float mm, float ll) {
-    const int64_t th = (int64_t)(it.tok0 + r / G) * a.q_heads + it.kvh * G + r % G;
+  // number of row r among all (query, head) pairs
+  auto pair_of = [&](int r) {
+    const int i = r / G;
+    return (int64_t)(it.tok0 + i) * a.q_heads + it.kvh * G + (r - i * G);
+  };
+  // (m, l, o) of a pair: into its partial slot, or divided into the output
+  const int64_t slot0 = (int64_t)it.slot * a.T * a.q_heads;
+  auto emit4 = [&](int64_t th, int d0, float4v v, float mm, float ll, float inv) {
     if (sp.slots) {
-      *reinterpret_cast<float4v*>(sp.part_o + ((int64_t)it.slot * a.T * a.q_heads + th) * D + d0) = v;
-      if (d0 == 0) sp.part_ml[(int64_t)it.slot * a.T * a.q_heads + th] = make_float2(mm, ll);
+      *reinterpret_cast<float4v*>(sp.part_o + (slot0 + th) * D + d0) = v;
+      if (d0 == 0) sp.part_ml[slot0 + th] = make_float2(mm, ll);
     } else {
       const bool none = mm == -INFINITY && ll == 0.f;  // a row that saw nothing
       half4v h;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) h[i] = (_Float16)(none ? 0.f : v[i] / ll);
+      for (int i = 0; i < 4; ++i) h[i] = (_Float16)(none ? 0.f : v[i] * inv);
       *reinterpret_cast<half4v*>(a.out + th * D + d0) = h;
       if (a.lse && d0 == 0) a.lse[th] = none ? -INFINITY : (mm + __log2f(ll)) * 0.6931471805599453f;
     }
@@ -619,16 +624,18 @@ __device__ __forceinline__ void attend_tile(const AttnArgs& a, const AttnSplit& 
         ll += f * ml.y;
         v += f * *reinterpret_cast<const float4v*>(ro + (w * 16 + r) * (DP + 4) + d0);
       }
-      emit4(it.row0 + r, d0, v, mm, ll);
+      emit4(pair_of(it.row0 + r), d0, v, mm, ll, 1.f / ll);
     }
   } else {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int r = wrow0 + nt * 16 + l16;
       if (r >= it.rows) continue;
+      const int64_t th = pair_of(r);
+      const float inv = 1.f / l[nt];
 #pragma unroll
       for (int d = 0; d < ND; ++d)
-        if (d * 16 + 4 * g < D) emit4(r, d * 16 + 4 * g, o[nt][d], m[nt], l[nt]);
+        if (d * 16 + 4 * g < D) emit4(th, d * 16 + 4 * g, o[nt][d], m[nt], l[nt], inv);
     }
   }
 }
