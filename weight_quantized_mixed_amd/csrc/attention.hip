@@ -172,12 +172,11 @@ __device__ __forceinline__ void attend_tile(const AttnArgs& a, const AttnSplit& 
   auto base_of = [&](int j) { return it.key0 + (j0 + j * jstep) * KT; };
 
   float4v o[NT][ND];
-  float m[NT];
-  float4v l4[NT];  // sums of the rounded probabilities (four copies)
+  float m[NT], l[NT];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     m[nt] = -INFINITY;
-    l4[nt] = float4v{0.f, 0.f, 0.f, 0.f};
+    l[nt] = 0.f;
 #pragma unroll
     for (int d = 0; d < ND; ++d) o[nt][d] = float4v{0.f, 0.f, 0.f, 0.f};
   }
@@ -297,7 +296,7 @@ __device__ __forceinline__ void attend_tile(const AttnArgs& a, const AttnSplit& 
           const float to = top[nt] > m[nt] + RAISE ? top[nt] : m[nt];
           const float keep = m[nt] == to ? 1.f : exp2_f(m[nt] - to);
           m[nt] = to;
-          l4[nt] *= keep;
+          l[nt] *= keep;
 #pragma unroll
           for (int d = 0; d < ND; ++d) o[nt][d] *= keep;
         }
@@ -316,6 +315,7 @@ __device__ __forceinline__ void attend_tile(const AttnArgs& a, const AttnSplit& 
       for (int e = 0; e < 2; ++e) {
         const int u = 2 * k + (y + e) / 4, i = (y + e) % 4;
         const float v = exp2_f(__builtin_fmaf(s[nt][u][i], c, -ref[nt]));
+        l[nt] += v;
         p[nt][k][y + e] = (_Float16)v;
       }
     };
@@ -340,15 +340,7 @@ __device__ __forceinline__ void attend_tile(const AttnArgs& a, const AttnSplit& 
       }
       return v;
     };
-    // the sums of a block's probabilities: one more row of V that is 1 everywhere
-    const half8v one = {1, 1, 1, 1, 1, 1, 1, 1};
-    auto sum_up = [&](int k) {
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) l4[nt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(one, p[nt][k], l4[nt], 0, 0, 0);
-    };
     auto product = [&](const uint8_t* vb) {
-#pragma unroll
-      for (int k = 0; k < NK; ++k) sum_up(k);
 #pragma unroll
       for (int k = 0; k < NK; ++k)
 #pragma unroll
@@ -528,7 +520,6 @@ __device__ __forceinline__ void attend_tile(const AttnArgs& a, const AttnSplit& 
         for (int nt = 0; nt < NT; ++nt) part[nt] = -INFINITY;
         static_for(std::make_integer_sequence<int, NP>{}, [&](auto X) {
           constexpr int x = decltype(X)::value, k = x / ND, d = x % ND;
-          if constexpr (d == 0) sum_up(k);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
             o[nt][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f[x % AHEAD], p[nt][k], o[nt][d], 0, 0, 0);
@@ -588,9 +579,8 @@ __device__ __forceinline__ void attend_tile(const AttnArgs& a, const AttnSplit& 
   }
 
   // ---- results: lane holds values 16 d + 4 g + i of row l % 16
-  float l[NT];
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) l[nt] = l4[nt][0];
+  for (int nt = 0; nt < NT; ++nt) l[nt] = across_rows(l[nt], [](float x, float y) { return x + y; });
   // number of row r among all (query, head) pairs
   auto pair_of = [&](int r) {
     const int i = r / G;
