@@ -9,7 +9,8 @@
 // blockIdx.x is the token, which makes its position, slot and row addresses scalar; the
 // threads of a workgroup walk the token's heads in order, so consecutive threads touch
 // consecutive memory on both sides.  The angles of a token are read by all its heads from
-// cache.  Rotation in fp32, one rounding to fp16.
+// cache.  Rotation in fp32, one rounding to fp16.  8190 tokens of 32 + 32 + 32 heads of 128
+// (405 MB): 78 us, 5.2 TB/s (a 2 GiB copy reaches 4.9); 48 tokens: 3.0 us, the launch.
 #include "qgemm_internal.hpp"
 
 namespace qg {
