@@ -289,3 +289,15 @@ def test_gradients_of_saturated_preactivations():
         out = plan.backward(A, plan.pack(W, W * 0), pre, dC, bias_grads=True)
         assert out["dbias_gate"][:4].tolist() == [2.0, 0.0, 2.0, 0.0] and out["dA"][0, 0].item() == 2.0 + 2.0 * 4
         assert out["dbias_up"][1].item() == 0 and out["dbias_up"][3].item() == 0 and torch.isfinite(out["dw_gate"]).all()
+
+
+@pytest.mark.parametrize("w,g,zeros", [("i4", 32, False), ("i4", 96, False), ("u4", 32, True), ("u4", 64, False),
+                                       ("u4", 160, True)])
+@pytest.mark.parametrize("M,N,K", [(1, 2900, 480), (2, 70, 960), (5, 2900, 480), (16, 33, 1440), (17, 129, 960),
+                                   (32, 2900, 480)])
+def test_gated_groups_of_part_superblocks(M, N, K, w, g, zeros):
+    """Groups that end inside a superblock on the matrix-core GEMVs: a scale for each step,
+    and a last superblock that K ends inside of."""
+    K = K // g * g
+    say(f"case gated groups {w} g={g} M={M} N={N} K={K}")
+    GatedCase(M, N, K, w, g, zeros, act="silu" if M % 2 else "gelu_tanh", seed=M + g).check()

@@ -260,10 +260,20 @@ qg_choice choose(const qgemm_plan* p, int64_t M) {
   // two rows as well when the matrix is narrow enough for 16- or 32-column
   // workgroups, which the dot-product GEMV does not have (N = 4096: 4.8 against
   // 7.8 us at K = 4096, 8.4 against 16.0 us at K = 11008)
-  const int min_m4 = gate_narrow ? 1 : choose_gemv_cb(p, kp) < 4 ? 2 : QG_GEMV4_MFMA_MIN_M;
-  c.gemv_mfma4 = (p->L.fmt == FMT_I4 || p->L.fmt == FMT_U4) && !c.gemv_narrow && smode != SC_PIECE &&
+  // Gated plans whose groups are not whole superblocks (32, 64, ...) take it too, with a
+  // scale per step, at N = 11008, K = 4096, int4 / uint4 with zero points, groups of 64, M =
+  // 3 / 8 / 32: 22.7 / 37.9 / 48.9 and 46.0 / 86.8 / 60.9 us (dot products, LDS-staged
+  // tiles) against 20.0 / 19.9 / 31.1 and 21.6 / 21.7 / 34.3 us; with zero points, or in
+  // narrow matrices, from one row (N = 11008, uint4 28.2 -> 21 us; N = 4096, K = 2048 int4
+  // 6.3 -> 5.1 us; int4 at N = 11008 stays with 16.8 / 19.8 us at one and two rows).
+  const bool steps = p->gate_n && smode == SC_PIECE;
+  const int min_m4 = gate_narrow || (steps && (p->has_zeros || choose_gemv_cb(p, kp) < 4)) ? 1
+                     : choose_gemv_cb(p, kp) < 4 ? 2
+                                                 : QG_GEMV4_MFMA_MIN_M;
+  c.gemv_mfma4 = (p->L.fmt == FMT_I4 || p->L.fmt == FMT_U4) && !c.gemv_narrow && (smode != SC_PIECE || steps) &&
                  M >= min_m4 && M <= (smode == SC_NONE ? QG_GEMV4_MFMA_MAX_M_UNSCALED : QG_GEMV4_MFMA_MAX_M);
   c.gemv_cb = (c.gemv_mfma || c.gemv_mfma4) ? choose_gemv_cb(p, kp) : 4;
+  if (c.gemv_mfma4 && steps) c.gemv_cb = 2;  // a scale per step and column: registers for two blocks
   c.gemv_waves = choose_gemv_waves(p, c.gemv_narrow ? 16 : (c.gemv_mfma || c.gemv_mfma4) ? 16 * c.gemv_cb : 64, kp);
   return c;
 }

@@ -29,8 +29,9 @@
 // 1024 + b offsets in the operands (and removing them once per superblock) would
 // make T about a thousand times larger than the true sum, and its fp32 rounding
 // alone exceeds a 1e-2 error at K = 16384 without scales.
-// Groups of whole superblocks (or one group over K) only; 32- and 64-position
-// groups take the dot-product GEMV.
+// Groups of whole superblocks (or one group over K); other multiples of 32 in gated plans
+// only, which fold after every MFMA step (its 32 positions lie in one group) with the
+// step's own scale.
 #include "qgemm_internal.hpp"
 
 namespace qg {
@@ -76,11 +77,12 @@ __device__ __forceinline__ float4v mfma(const uint4& A, const uint4& B, const fl
   return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8v, A), __builtin_bit_cast(half8v, B), C, 0, 0, 0);
 }
 
-// VAR: 0 unscaled, 1 scaled, 2 scaled with zero points
+// VAR: 0 unscaled, 1 scaled, 2 scaled with zero points; 3, 4: as 1, 2 with a scale per step
 template <int FMT, int MB, int VAR, int CB, bool GATED>
 __global__ __launch_bounds__(64 * GEMV_MAX_WAVES) void gemv_mfma4_kernel(RunArgs a) {
   constexpr int KB = 128, NS = 4;  // positions and 32-position MFMA steps per superblock
-  constexpr bool SCALED = VAR >= 1, ZEROS = VAR == 2;
+  constexpr bool SCALED = VAR >= 1, ZEROS = VAR == 2 || VAR == 4, STEPS = VAR >= 3;
+  constexpr int NSC = STEPS ? NS : 1;  // scales of a column per superblock
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -105,7 +107,7 @@ __global__ __launch_bounds__(64 * GEMV_MAX_WAVES) void gemv_mfma4_kernel(RunArgs
   struct Stage {
     uint4 av[MB][NS];  // A operand of each row block and step
     uint4 wq[CB];       // piece (lane / 16, lane % 16) of each column block, as stored
-    uint32_t sc[CB];    // raw scale (| zero << 16) of each column block
+    uint32_t sc[CB][NSC];  // raw scale (| zero << 16) of each column block (and step)
   };
   auto load = [&](Stage& s, int j) {
     const uint32_t kb = (uint32_t)row_of(min(j, cnt - 1));
@@ -116,12 +118,18 @@ __global__ __launch_bounds__(64 * GEMV_MAX_WAVES) void gemv_mfma4_kernel(RunArgs
 #pragma unroll
     for (int cb = 0; cb < CB; ++cb) s.wq[cb] = stream_load16(Wq + kb * sbq_stride + cb * 64);
     if constexpr (SCALED) {
-      const uint32_t grp = a.sb_per_group == 1 ? kb : kb / (uint32_t)a.sb_per_group;
 #pragma unroll
-      for (int cb = 0; cb < CB; ++cb) {
-        const uint32_t col = (uint32_t)((rb * CB + cb) * 16 + n16);
-        if constexpr (ZEROS) s.sc[cb] = static_cast<const uint32_t*>(a.S)[grp * (uint32_t)a.Npad + col];
-        else s.sc[cb] = static_cast<const uint16_t*>(a.S)[grp * (uint32_t)a.Npad + col];
+      for (int t = 0; t < NSC; ++t) {
+        const uint32_t p = kb * KB + 32 * t;
+        const uint32_t grp = STEPS ? (a.g_shift >= 0 ? p >> a.g_shift : p / (uint32_t)a.group_size)
+                             : a.sb_per_group == 1 ? kb
+                                                   : kb / (uint32_t)a.sb_per_group;
+#pragma unroll
+        for (int cb = 0; cb < CB; ++cb) {
+          const uint32_t col = (uint32_t)((rb * CB + cb) * 16 + n16);
+          if constexpr (ZEROS) s.sc[cb][t] = static_cast<const uint32_t*>(a.S)[grp * (uint32_t)a.Npad + col];
+          else s.sc[cb][t] = static_cast<const uint16_t*>(a.S)[grp * (uint32_t)a.Npad + col];
+        }
       }
     }
   };
@@ -148,14 +156,26 @@ __global__ __launch_bounds__(64 * GEMV_MAX_WAVES) void gemv_mfma4_kernel(RunArgs
 #pragma unroll
       for (int t = 0; t < NS; ++t) w[cb][t] = x[t];
     }
-    // scaled: per-superblock sums T (and row sums S with zero points); unscaled:
+    // scaled: sums T per superblock or step (and row sums S with zero points); unscaled:
     // straight into acc
+    auto fold = [&](int cb, int t, const float4v (&T)[MB][CB], const float4v (&S)[MB]) {
+      const float sc = (float)__builtin_bit_cast(_Float16, (uint16_t)(s.sc[cb][t] & 0xFFFFu));
+      const float z = ZEROS ? (float)__builtin_bit_cast(_Float16, (uint16_t)(s.sc[cb][t] >> 16)) : 0.f;
+#pragma unroll
+      for (int r = 0; r < MB; ++r)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if constexpr (ZEROS) acc[r][cb][i] += sc * (T[r][cb][i] - z * S[r][i]);
+          else acc[r][cb][i] += sc * T[r][cb][i];
+        }
+    };
+    const float4v NONE = {0.f, 0.f, 0.f, 0.f};
     float4v T[MB][CB], S[MB];
 #pragma unroll
     for (int r = 0; r < MB; ++r) {
-      S[r] = float4v{0.f, 0.f, 0.f, 0.f};
+      S[r] = NONE;
 #pragma unroll
-      for (int cb = 0; cb < CB; ++cb) T[r][cb] = float4v{0.f, 0.f, 0.f, 0.f};
+      for (int cb = 0; cb < CB; ++cb) T[r][cb] = NONE;
     }
 #pragma unroll
     for (int t = 0; t < NS; ++t) {
@@ -165,28 +185,22 @@ __global__ __launch_bounds__(64 * GEMV_MAX_WAVES) void gemv_mfma4_kernel(RunArgs
         const uint4 B = make_uint4(code(wd), code(wd >> 4), code(wd >> 8), code(wd >> 12));
 #pragma unroll
         for (int r = 0; r < MB; ++r) {
-          if constexpr (SCALED) T[r][cb] = mfma(s.av[r][t], B, T[r][cb]);
+          if constexpr (SCALED) T[r][cb] = mfma(s.av[r][t], B, STEPS ? NONE : T[r][cb]);
           else acc[r][cb] = mfma(s.av[r][t], B, acc[r][cb]);
         }
       }
       if constexpr (ZEROS) {
 #pragma unroll
-        for (int r = 0; r < MB; ++r) S[r] = mfma(s.av[r][t], ONES, S[r]);
+        for (int r = 0; r < MB; ++r) S[r] = mfma(s.av[r][t], ONES, STEPS ? NONE : S[r]);
+      }
+      if constexpr (STEPS) {
+#pragma unroll
+        for (int cb = 0; cb < CB; ++cb) fold(cb, t, T, S);
       }
     }
-    if constexpr (SCALED) {
+    if constexpr (SCALED && !STEPS) {
 #pragma unroll
-      for (int cb = 0; cb < CB; ++cb) {
-        const float sc = (float)__builtin_bit_cast(_Float16, (uint16_t)(s.sc[cb] & 0xFFFFu));
-        const float z = ZEROS ? (float)__builtin_bit_cast(_Float16, (uint16_t)(s.sc[cb] >> 16)) : 0.f;
-#pragma unroll
-        for (int r = 0; r < MB; ++r)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            if constexpr (ZEROS) acc[r][cb][i] += sc * (T[r][cb][i] - z * S[r][i]);
-            else acc[r][cb][i] += sc * T[r][cb][i];
-          }
-      }
+      for (int cb = 0; cb < CB; ++cb) fold(cb, 0, T, S);
     }
   };
 
@@ -260,10 +274,15 @@ __global__ __launch_bounds__(64 * GEMV_MAX_WAVES) void gemv_mfma4_kernel(RunArgs
 template <int FMT, int MB, int CB, bool GATED>
 hipError_t launch_gated(const RunArgs& a, hipStream_t st) {
   const dim3 grid((a.N + 16 * CB - 1) / (16 * CB), a.k_parts), block(64 * a.waves);
-  const int var = a.smode == SC_NONE ? 0 : a.zeros ? 2 : 1;
+  const int var = a.smode == SC_NONE ? 0 : (a.zeros ? 2 : 1) + (a.smode == SC_PIECE ? 2 : 0);
+  if constexpr (GATED && CB == 2) {
+    if (var == 3) hipLaunchKernelGGL((gemv_mfma4_kernel<FMT, MB, 3, CB, true>), grid, block, 0, st, a);
+    else if (var == 4 && FMT == FMT_U4) hipLaunchKernelGGL((gemv_mfma4_kernel<FMT_U4, MB, 4, CB, true>), grid, block, 0, st, a);
+    if (var >= 3) return var == 4 && FMT != FMT_U4 ? hipErrorInvalidValue : hipGetLastError();
+  }
   if (var == 0) hipLaunchKernelGGL((gemv_mfma4_kernel<FMT, MB, 0, CB, GATED>), grid, block, 0, st, a);
   else if (var == 1) hipLaunchKernelGGL((gemv_mfma4_kernel<FMT, MB, 1, CB, GATED>), grid, block, 0, st, a);
-  else if (FMT == FMT_U4) hipLaunchKernelGGL((gemv_mfma4_kernel<FMT_U4, MB, 2, CB, GATED>), grid, block, 0, st, a);
+  else if (FMT == FMT_U4 && var == 2) hipLaunchKernelGGL((gemv_mfma4_kernel<FMT_U4, MB, 2, CB, GATED>), grid, block, 0, st, a);
   else return hipErrorInvalidValue;
   return hipGetLastError();
 }
@@ -289,7 +308,7 @@ hipError_t launch_mb(const RunArgs& a, hipStream_t st) {
 }  // namespace
 
 hipError_t launch_gemv_mfma4(int fmt, const RunArgs& a, hipStream_t st) {
-  if (a.M < 1 || a.M > 32 || a.smode == SC_PIECE) return hipErrorInvalidValue;
+  if (a.M < 1 || a.M > 32) return hipErrorInvalidValue;
   if (fmt == FMT_I4) return a.M <= 16 ? launch_mb<FMT_I4, 1>(a, st) : launch_mb<FMT_I4, 2>(a, st);
   if (fmt == FMT_U4) return a.M <= 16 ? launch_mb<FMT_U4, 1>(a, st) : launch_mb<FMT_U4, 2>(a, st);
   return hipErrorInvalidValue;
