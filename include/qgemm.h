@@ -300,7 +300,9 @@ typedef enum {
  * limits hold for the 2 * roundup(N, 16) columns of both projections.
  *   act            the activation, else QGEMM_ERR_INVALID_ARG.
  *   packed_bytes   out: size of the blob that qgemm_pack_gated writes.
- *   workspace_bytes out: size of the workspace of qgemm_run_gated (0 if none).
+ *   workspace_bytes out: size of the workspace of qgemm_run_gated (0 if none).  Runs of more
+ *                  than 128 rows whose groups are not multiples of 128 keep the weights there
+ *                  as fp16 (4 K N bytes and their padding).
  * Gated plans run through qgemm_pack_gated, qgemm_run_gated and qgemm_gated_backward
  * (the plain calls return QGEMM_ERR_INVALID_ARG for them) and are destroyed by
  * qgemm_destroy.

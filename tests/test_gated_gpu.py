@@ -294,10 +294,10 @@ def test_gradients_of_saturated_preactivations():
 @pytest.mark.parametrize("w,g,zeros", [("i4", 32, False), ("i4", 96, False), ("u4", 32, True), ("u4", 64, False),
                                        ("u4", 160, True)])
 @pytest.mark.parametrize("M,N,K", [(1, 2900, 480), (2, 70, 960), (5, 2900, 480), (16, 33, 1440), (17, 129, 960),
-                                   (32, 2900, 480)])
+                                   (32, 2900, 480), (300, 129, 1440)])
 def test_gated_groups_of_part_superblocks(M, N, K, w, g, zeros):
-    """Groups that end inside a superblock on the matrix-core GEMVs: a scale for each step,
-    and a last superblock that K ends inside of."""
+    """Groups that end inside a superblock on the matrix-core GEMVs (a scale for each step)
+    and on expanded weights, with a last superblock that K ends inside of."""
     K = K // g * g
     say(f"case gated groups {w} g={g} M={M} N={N} K={K}")
     GatedCase(M, N, K, w, g, zeros, act="silu" if M % 2 else "gelu_tanh", seed=M + g).check()

@@ -376,8 +376,33 @@ size_t run_ws_bytes_for(const qgemm_plan* p, int64_t M, bool fold) {
   if (!fold) return split_pad_bytes(p, M);
   return zp_offset(p, M) + (size_t)p->L.Npad * (size_t)zr_gp_of(p) * 2 * sizeof(uint16_t);
 }
+// Gated runs of more than 128 rows whose groups are not whole superblocks (32, 64, ...): one pass
+// writes the weights as an fp16 blob into the workspace and the fp16 tiles run on it, since
+// the direct-load tiles hold one scale per column and stage.  N = 11008, K = 4096, groups of
+// 64, int4 / uint4 with zero points on the LDS-staged tiles against so: M = 128 76 / 85 us
+// against 100, M = 192 177 / 228 against 113, M = 512 267 / 344 against 151, M = 2048 626 /
+// 689 against 356; N = 1506, K = 1536, M = 256 20.0 / 24.2 against 15.8 us.
+#ifndef QG_EXPAND_MIN_M
+#define QG_EXPAND_MIN_M 129
+#endif
+Layout expanded_layout(const qgemm_plan* p) {
+  Layout L;
+  fill_layout(&L, FMT_F16, p->N, p->L.Kpad, 0, false);
+  return L;
+}
+bool expands(const qgemm_plan* p, int64_t M) {
+  if (!p->gate_n || scale_mode(p->L.fmt, p->group_size) != SC_PIECE || M < QG_EXPAND_MIN_M) return false;
+  if (split_of(p, M).kp != 1) return false;
+  const Layout L = expanded_layout(p);
+  return L.NB * L.nkb * 64 < INT32_MAX;  // the kernels index the blob's pieces in 32 bits
+}
+size_t expanded_offset(const qgemm_plan* p, int64_t M) { return (size_t)round_up((int64_t)split_pad_bytes(p, M), 256); }
+
 // the workspace of a run of M rows with the kernels chosen for M
-size_t run_ws_bytes(const qgemm_plan* p, int64_t M, const qg_choice& ch) { return run_ws_bytes_for(p, M, zero_fold(p, ch)); }
+size_t run_ws_bytes(const qgemm_plan* p, int64_t M, const qg_choice& ch) {
+  if (expands(p, M)) return expanded_offset(p, M) + expanded_layout(p).total;
+  return run_ws_bytes_for(p, M, zero_fold(p, ch));
+}
 // The most rows of a run of this plan that takes the 256 x 256 tiles with the folding
 // (0: none).  The tile choice depends on the rows only through the number of 256-row
 // tiles (above 128 rows), so one run per tile count is checked, from the plan's down.
@@ -397,6 +422,10 @@ struct GateIo {
   const float* col_scales_up = nullptr;
   void* preact = nullptr;
 };
+
+void init_plan(qgemm_plan* p, int64_t M, int64_t N, int64_t K, qgemm_dtype a_dtype, qgemm_dtype w_dtype,
+               qgemm_dtype out_dtype, qgemm_dtype accum_dtype, int32_t group_size, int32_t has_zeros, int32_t k_parts,
+               uint32_t flags, int64_t gate_n, float act_c0, float act_c1);
 
 // one run: the split-K fill, the kernel chosen for M rows, the finalize pass
 qgemm_status run_impl(const qgemm_plan* plan, int64_t M, const void* A, const void* packed, const void* bias,
@@ -435,6 +464,15 @@ qgemm_status run_impl(const qgemm_plan* plan, int64_t M, const void* A, const vo
     e = launch_pad_rows(A, Ap, M, plan->K, plan->L.Kpad, (int)a_esz(plan), st);
     a.A = Ap;
     a.K = (int32_t)plan->L.Kpad;
+  }
+  if (e == hipSuccess && expands(plan, M)) {
+    qgemm_plan wide;
+    init_plan(&wide, M, plan->N, plan->L.Kpad, QGEMM_F16, QGEMM_F16, QGEMM_F16, QGEMM_F32, 0, 0, 1, 0, plan->gate_n,
+              plan->act_c0, plan->act_c1);
+    char* blob = static_cast<char*>(workspace) + expanded_offset(plan, M);
+    e = launch_expand_blob(plan->L, packed, wide.L, blob, st);
+    if (e != hipSuccess) return QGEMM_ERR_DEVICE;
+    return run_impl(&wide, M, a.A, blob, bias, nullptr, nullptr, C, nullptr, 0, stream, gate);
   }
   if (e == hipSuccess && fold) {
     uint16_t* zr = reinterpret_cast<uint16_t*>(static_cast<char*>(workspace) + zr_offset(plan, M));

@@ -296,6 +296,8 @@ hipError_t launch_bias_grad(const float* part, int64_t M, int64_t N, void* dbg, 
 // the transposed weights of a gated plan, and transposed fp16 rows, as fp16 blobs of layout `to`
 hipError_t launch_transpose_blob(const Layout& L, int64_t gate_n, const void* packed, const Layout& to, void* out,
                                  hipStream_t st);
+// the weights of an int4 / uint4 blob with scales as an fp16 blob of layout `to` (same columns)
+hipError_t launch_expand_blob(const Layout& L, const void* packed, const Layout& to, void* out, hipStream_t st);
 hipError_t launch_transpose_rows(const void* X, int64_t M, int64_t K, const Layout& to, void* out, hipStream_t st);
 
 // rotation of new queries and keys, keys and values into the paged cache (kv_append.hip)
