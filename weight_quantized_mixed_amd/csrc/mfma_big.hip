@@ -483,12 +483,18 @@ __global__ __launch_bounds__(256) void mfma_big_kernel(RunArgs a) {
   };
   // fp16 outputs of a wave (128 rows x 16 CB columns, CB 4 or 8) through LDS: accumulators
   // go into 16 KiB of the wave's own of the idle ring (128 columns: 64 rows at a time),
-  // value(i, c, r) for row 16 i + 4 q + r and column 16 c + l16, and leave as 16-byte stores
-  // of whole rows.  (Two-byte stores from the accumulators, 32 contiguous bytes a row, are
-  // 256 instructions a wave.)  16-byte chunks are swizzled by the row so that the writes
+  // value(i, c, r) for row 16 i + 4 q + r and column 16 c + l16, and leave as stores of
+  // whole rows, 16 bytes each or, where N or a pointer does not allow it, 4 or 2.  (Two-byte
+  // stores from the accumulators, 32 contiguous bytes a row, are 256 instructions a wave:
+  // gated, M = 2048, K = 4096, fp16 with N = 11006 346 -> 314 us, int4 with N = 11005 379 ->
+  // 353 us.)  16-byte chunks are swizzled by the row so that the writes
   // meet no bank conflicts.  dst: the wave's first row and column, rows `pitch` values
-  // apart; cols: columns that exist (a multiple of 8, with 16-byte aligned rows).
-  auto rows_out = [&](auto CBC, auto&& value, _Float16* dst, size_t pitch, int cols) {
+  // apart; cols: columns that exist; v: halves a store (row_width).
+  auto row_width = [](size_t n, const void* p, const void* p2) {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(p) | reinterpret_cast<uintptr_t>(p2);
+    return n % 8 == 0 && (at & 15) == 0 ? 8 : n % 2 == 0 && (at & 3) == 0 ? 2 : 1;
+  };
+  auto rows_out = [&](auto CBC, auto&& value, _Float16* dst, size_t pitch, int cols, int v) {
     constexpr int CB = decltype(CBC)::value, CH = 2 * CB, IB = 32 / CB;  // chunks per row, row blocks at a time
     uint8_t* const mine = lds + wave * 16384;
     auto at = [&](int row, int chunk) { return mine + row * (CH * 16) + (chunk ^ ((row >> 2 & 3) * 2)) * 16; };
@@ -503,12 +509,32 @@ __global__ __launch_bounds__(256) void mfma_big_kernel(RunArgs a) {
           for (int r = 0; r < 4; ++r)
             *reinterpret_cast<_Float16*>(at(i * 16 + q * 4 + r, 2 * c + (l16 >> 3)) + (l16 & 7) * 2) = value(i0 + i, c, r);
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      if (v == 8) {
 #pragma unroll 4
-      for (int k = 0; k < 16; ++k) {
-        const int row = k * (64 / CH) + lane / CH, chunk = lane % CH;
-        if (i0 * 16 + row < rows && chunk * 8 < cols) {
-          const uint4 v = *reinterpret_cast<const uint4*>(at(row, chunk));
-          *reinterpret_cast<uint4*>(dst + (size_t)(i0 * 16 + row) * pitch + chunk * 8) = v;
+        for (int k = 0; k < 16; ++k) {
+          const int row = k * (64 / CH) + lane / CH, chunk = lane % CH;
+          if (i0 * 16 + row < rows && chunk * 8 < cols) {
+            const uint4 x = *reinterpret_cast<const uint4*>(at(row, chunk));
+            *reinterpret_cast<uint4*>(dst + (size_t)(i0 * 16 + row) * pitch + chunk * 8) = x;
+          }
+        }
+      } else if (v == 2) {
+#pragma unroll 4
+        for (int k = 0; k < 64; ++k) {
+          const int row = k * (16 / CH) + lane / (4 * CH), c = lane % (4 * CH) * 2;
+          if (i0 * 16 + row < rows && c < cols) {
+            const uint32_t x = *reinterpret_cast<const uint32_t*>(at(row, c >> 3) + (c & 7) * 2);
+            *reinterpret_cast<uint32_t*>(dst + (size_t)(i0 * 16 + row) * pitch + c) = x;
+          }
+        }
+      } else {
+#pragma unroll 4
+        for (int k = 0; k < 128; ++k) {
+          const int row = k / (CH / 8), c = k % (CH / 8) * 64 + lane;
+          if (i0 * 16 + row < rows && c < cols) {
+            const uint16_t x = *reinterpret_cast<const uint16_t*>(at(row, c >> 3) + (c & 7) * 2);
+            *reinterpret_cast<uint16_t*>(dst + (size_t)(i0 * 16 + row) * pitch + c) = x;
+          }
         }
       }
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
@@ -521,48 +547,35 @@ __global__ __launch_bounds__(256) void mfma_big_kernel(RunArgs a) {
   if constexpr (GATED) {
     // column blocks j and j + 1 are the gate and up sums of 16 output columns
     const size_t N = a.gate_n;
-    if (N % 8 == 0 && ((reinterpret_cast<uintptr_t>(a.C) | reinterpret_cast<uintptr_t>(a.preact)) & 15) == 0) {
-      float sg[4], su[4], bg[4], bu[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const GateCol c = gate_col(a, n0 + wn * 128 + j * 32 + l16);
-        sg[j] = c.sg;
-        su[j] = c.su;
-        bg[j] = c.bg;
-        bu[j] = c.bu;
-      }
-      __syncthreads();  // every wave is done with the ring
-      const int col0 = (n0 + wn * 128) / 2, cols = a.gate_n - col0;
-      const size_t row0 = (size_t)(m0 + wm * 128);
-      // between two outputs: keeps the compiler from holding every pre-activation of the
-      // first for the second (256 values, which spilled), since it cannot tell the scales alike
-      auto forget = [&] {
-#pragma unroll
-        for (int c = 0; c < 4; ++c) asm volatile("" : "+v"(sg[c]), "+v"(su[c]), "+v"(bg[c]), "+v"(bu[c]));
-      };
-      auto gate = [&](int i, int c, int r) { return acc[i][2 * c][r] * sg[c] + bg[c]; };
-      auto up = [&](int i, int c, int r) { return acc[i][2 * c + 1][r] * su[c] + bu[c]; };
-      if (a.preact) {
-        _Float16* p = a.preact + row0 * 2 * N + col0;
-        rows_out(C4{}, [&](int i, int c, int r) { return (_Float16)gate(i, c, r); }, p, 2 * N, cols);
-        rows_out(C4{}, [&](int i, int c, int r) { return (_Float16)up(i, c, r); }, p + N, 2 * N, cols);
-        forget();
-      }
-      rows_out(C4{}, [&](int i, int c, int r) { return (_Float16)(gate_act(a, gate(i, c, r)) * up(i, c, r)); },
-               static_cast<_Float16*>(a.C) + row0 * N + col0, N, cols);
-      return;
-    }
+    const int v = row_width(N, a.C, a.preact);
+    float sg[4], su[4], bg[4], bu[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const GateCol c = gate_col(a, n0 + wn * 128 + j * 32 + l16);
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int row = m0 + wm * 128 + i * 16 + q * 4 + r;
-          if (row < a.M && c.in) gate_store(a, row, c, (float)acc[i][2 * j][r], (float)acc[i][2 * j + 1][r]);
-        }
+      sg[j] = c.sg;
+      su[j] = c.su;
+      bg[j] = c.bg;
+      bu[j] = c.bu;
     }
+    __syncthreads();  // every wave is done with the ring
+    const int col0 = (n0 + wn * 128) / 2, cols = a.gate_n - col0;
+    const size_t row0 = (size_t)(m0 + wm * 128);
+    // between two outputs: keeps the compiler from holding every pre-activation of the
+    // first for the second (256 values, which spilled), since it cannot tell the scales alike
+    auto forget = [&] {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) asm volatile("" : "+v"(sg[c]), "+v"(su[c]), "+v"(bg[c]), "+v"(bu[c]));
+    };
+    auto gate = [&](int i, int c, int r) { return acc[i][2 * c][r] * sg[c] + bg[c]; };
+    auto up = [&](int i, int c, int r) { return acc[i][2 * c + 1][r] * su[c] + bu[c]; };
+    if (a.preact) {
+      _Float16* p = a.preact + row0 * 2 * N + col0;
+      rows_out(C4{}, [&](int i, int c, int r) { return (_Float16)gate(i, c, r); }, p, 2 * N, cols, v);
+      rows_out(C4{}, [&](int i, int c, int r) { return (_Float16)up(i, c, r); }, p + N, 2 * N, cols, v);
+      forget();
+    }
+    rows_out(C4{}, [&](int i, int c, int r) { return (_Float16)(gate_act(a, gate(i, c, r)) * up(i, c, r)); },
+             static_cast<_Float16*>(a.C) + row0 * N + col0, N, cols, v);
     return;
   }
   // The per-column values of this lane's 8 columns (epilogue scale, bias, int8 column
@@ -582,14 +595,11 @@ __global__ __launch_bounds__(256) void mfma_big_kernel(RunArgs a) {
   }
   if (a.out_mode == OUT_STORE) {
     if constexpr (FP) {
-      if (a.N % 8 == 0 && (reinterpret_cast<uintptr_t>(a.C) & 15) == 0) {
-        __syncthreads();  // every wave is done with the ring
-        const int col0 = n0 + wn * 128;
-        rows_out(C8{}, [&](int i, int c, int r) { return (_Float16)(acc[i][c][r] * es[c] + bf[c]); },
-                 static_cast<_Float16*>(a.C) + (size_t)(m0 + wm * 128) * a.N + col0, (size_t)a.N, a.N - col0);
-      } else {
-        each([&](int, int j, size_t o, float v) { static_cast<_Float16*>(a.C)[o] = (_Float16)(v * es[j] + bf[j]); });
-      }
+      __syncthreads();  // every wave is done with the ring
+      const int col0 = n0 + wn * 128;
+      rows_out(C8{}, [&](int i, int c, int r) { return (_Float16)(acc[i][c][r] * es[c] + bf[c]); },
+               static_cast<_Float16*>(a.C) + (size_t)(m0 + wm * 128) * a.N + col0, (size_t)a.N, a.N - col0,
+               row_width(a.N, a.C, nullptr));
     } else if (a.row_scale)
       each([&](int row, int j, size_t o, int v) {  // as dq_out, with the column values above
         static_cast<_Float16*>(a.C)[o] = (_Float16)((float)v * a.row_scale[row] * cs[j] + bf[j]);
