@@ -248,7 +248,7 @@ qg_choice choose(const qgemm_plan* p, int64_t M) {
   c.path = M <= 8 ? QGEMM_PATH_GEMV : QGEMM_PATH_MFMA;
   c.tile = choose_tile(p, M, kp);
   c.dl_tile = c.path == QGEMM_PATH_MFMA ? choose_dl_tile(p->L.fmt, M, p->N, kp,
-                                                          scale_mode(p->L.fmt, p->group_size))
+                                                          scale_mode(p->L.fmt, p->group_size), p->gate_n != 0)
                                         : -1;
   c.gemv_narrow = c.path == QGEMM_PATH_GEMV && choose_gemv_narrow(p, M, kp);
   // a gated plan too narrow for the 64-column GEMV at one row takes the matrix-core GEMVs,

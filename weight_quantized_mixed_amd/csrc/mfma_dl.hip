@@ -11,7 +11,7 @@ void dl_tile_dims(int tile, int* bm, int* bn) {
   *bn = dims[tile][1];
 }
 
-int choose_dl_tile(int fmt, int64_t M, int64_t N, int k_parts, int smode) {
+int choose_dl_tile(int fmt, int64_t M, int64_t N, int k_parts, int smode, bool gated) {
   const bool packed = fmt == FMT_I4 || fmt == FMT_U4 || fmt == FMT_I2;
   if (packed && smode == SC_PIECE) return -1;  // one scale slot per stage holds one group per column
   const int cap = M <= 32 ? 32 : M <= 64 ? 64 : M <= 128 ? 128 : 256;
@@ -19,6 +19,26 @@ int choose_dl_tile(int fmt, int64_t M, int64_t N, int k_parts, int smode) {
 #ifdef QG_FORCE_DL_TILE
   if (QG_FORCE_DL_TILE >= 0) return QG_FORCE_DL_TILE;
 #endif
+  // Gated fp16 of 129 to 256 rows: the tile whose waves of 256 workgroups, each at the cost
+  // measured for a wave of it, are soonest done.  (The rule below jumps from one wave of
+  // large tiles that fill a little under 60 % of the CUs to three of the smallest: N = 6306,
+  // K = 2620, M = 186 67 us, so 35 us; N = 2900, K = 2560, M = 186 43 and 21 us.)
+  if (gated && fmt == FMT_F16 && M > 128 && M <= 256) {
+    static const struct { int tile, cost; } waves_of[] = {{DL_128x256, 170}, {DL_64x256, 145}, {DL_64x128, 100},
+                                                         {DL_32x128, 88},  {DL_32x64, 68}};
+    int best = -1;
+    int64_t least = 0;
+    for (const auto& w : waves_of) {
+      int bm, bn;
+      dl_tile_dims(w.tile, &bm, &bn);
+      const int64_t t = (((M + bm - 1) / bm) * ((N + bn - 1) / bn) * k_parts + 255) / 256 * w.cost;
+      if (best < 0 || t < least) {
+        best = w.tile;
+        least = t;
+      }
+    }
+    return best;
+  }
   // The largest tile whose last wave of workgroups still occupies at least 60% of
   // the 256 CUs: larger tiles re-read less of A and B, idle CUs cost in proportion.
   int pick = -1;

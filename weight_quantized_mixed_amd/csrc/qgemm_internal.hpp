@@ -252,7 +252,7 @@ enum DlTile : int {
   DL_32x64 = 0, DL_32x128, DL_32x256, DL_64x128, DL_64x256, DL_128x256, DL_256x256, DL_128x128, DL_NUM
 };
 void dl_tile_dims(int tile, int* bm, int* bn);
-int choose_dl_tile(int fmt, int64_t M, int64_t N, int k_parts, int smode);
+int choose_dl_tile(int fmt, int64_t M, int64_t N, int k_parts, int smode, bool gated);
 hipError_t launch_mfma_dl(int fmt, int tile, const RunArgs& a, hipStream_t st);
 hipError_t launch_mfma_dl_gated(int fmt, int tile, const RunArgs& a, hipStream_t st);
 // 256 x 256 tiles of four 128 x 128 waves (mfma_big.hip) for the formats that
