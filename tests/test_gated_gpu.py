@@ -301,3 +301,38 @@ def test_gated_groups_of_part_superblocks(M, N, K, w, g, zeros):
     K = K // g * g
     say(f"case gated groups {w} g={g} M={M} N={N} K={K}")
     GatedCase(M, N, K, w, g, zeros, act="silu" if M % 2 else "gelu_tanh", seed=M + g).check()
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
+def test_gradients_of_infinite_up_preactivations(act):
+    """Kept infinities of either projection stand for +-65504, beside saturated gates and
+    gradients of 0; NaN stays in its own row and column."""
+    gates, ups = (-np.inf, np.inf, 1.5, 0.0, -3.0, 60000.0, -60000.0), (np.inf, -np.inf, 2.0)
+    N, K, rng = len(gates) * len(ups) + 3, 64, np.random.default_rng(4)  # 24 columns: whole rows of 16 bytes
+    g, u = np.zeros((4, N), np.float16), np.ones((4, N), np.float16)
+    g[:, :N - 3], u[:, :N - 3] = np.repeat(gates, len(ups)), np.tile(ups, len(gates))
+    dC = np.full((4, N), 2.0**-6, np.float16)
+    dC[1] = 0.0
+    dC[2, ::2] = 0.0
+    u[3] = 0.5
+    u[3, -1] = np.nan
+    A = rng.standard_normal((4, K)).astype(np.float16)
+    W = [(rng.standard_normal((N, K)) / 8).astype(np.float16) for _ in range(2)]
+    plan = QGated(4, N, K, "f16", act=act)
+    out = plan.backward(host_to_device(A), plan.pack(*[host_to_device(w) for w in W]), host_to_device(np.concatenate([g, u], 1)),
+                        host_to_device(dC), bias_grads=True)
+    got = {k: t.cpu().numpy().astype(np.float64) for k, t in out.items()}
+    assert np.isnan(got["dA"][3]).all() and np.isnan(got["dw_gate"][-1]).all() and np.isnan(got["dbias_gate"][-1])
+    u[3, -1] = 0
+    ref, mag = ({}, {})
+    for to, f in ((ref, lambda x: x), (mag, np.abs)):  # the sums, and the sums of magnitudes
+        r = oracle.gated_grads_ref(A, *[w.T.astype(np.float64) for w in W], np.clip(g.astype(np.float64), -65504, 65504),
+                                   np.clip(u.astype(np.float64), -65504, 65504), dC, act)
+        dG, dU, w = f(r["dG"]), f(r["dU"]), [f(x.astype(np.float64)) for x in W]
+        to.update(dA=dG @ w[0] + dU @ w[1], dw_gate=dG.T @ f(A.astype(np.float64)), dw_up=dU.T @ f(A.astype(np.float64)),
+                  dbias_gate=dG.sum(0), dbias_up=dU.sum(0))
+    own = {"dA": np.s_[:3], "dw_gate": np.s_[:-1], "dbias_gate": np.s_[:-1], "dw_up": np.s_[:], "dbias_up": np.s_[:]}
+    for name, x in got.items():  # operands to 2^-11 (or half a subnormal, times at most |A|, |W| < 8), fp32 sums, the output
+        x, r, m = x[own[name]], ref[name][own[name]], mag[name][own[name]]
+        assert_near(x, r, (2.0**-11 + 2.0**-19) * m + 2 * N * 8 * 2.0**-25 + 2.0**-11 * np.abs(r) + 2.0**-25, name)
+    assert (got["dA"][1] == 0).all()

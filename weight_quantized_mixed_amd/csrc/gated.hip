@@ -25,6 +25,14 @@ typedef _Float16 half8v __attribute__((ext_vector_type(8)));
 
 __device__ __forceinline__ _Float16 as_half(uint32_t x) { return __builtin_bit_cast(_Float16, (uint16_t)x); }
 
+// A pre-activation past fp16 was kept as infinity: the largest value instead, since infinity
+// times 0 (a saturated gate's act', or a dC of 0) would be NaN.  A gate there has act' 0 or 1
+// already; an up projection's share in dG is the one of 65504.  NaN stays.
+__device__ __forceinline__ float kept(_Float16 h) {
+  const float x = (float)h;
+  return fabsf(x) == INFINITY ? copysignf(65504.f, x) : x;
+}
+
 // ---- gradients of the pre-activations: tiles of 64 rows x 64 output columns
 constexpr int GT = 64;
 constexpr int GPITCH = GT + 8;  // halves per LDS row (16-byte aligned rows, banks shifted by 4)
@@ -66,14 +74,10 @@ __global__ __launch_bounds__(256) void gate_grad_kernel(const _Float16* __restri
       vec dg, du;
 #pragma unroll
       for (int e = 0; e < V; ++e) {
-        float x = (float)g[s][e];
-        const float dc = (float)d[s][e];
-        // a pre-activation past fp16 was kept as infinity: the largest value instead (where
-        // act' is 0 or 1 already), since infinity times 0 below would be NaN
-        if (fabsf(x) == INFINITY) x = copysignf(65504.f, x);
+        const float x = kept(g[s][e]), dc = (float)d[s][e];
         const float sg = gate_sigmoid(c0, c1, x);
         // act'(x) = sg + x sg (1 - sg) t'(x)
-        dg[e] = (_Float16)(dc * (float)u[s][e] * (sg + x * sg * (1.f - sg) * (c0 + 3.f * c1 * x * x)));
+        dg[e] = (_Float16)(dc * kept(u[s][e]) * (sg + x * sg * (1.f - sg) * (c0 + 3.f * c1 * x * x)));
         du[e] = (_Float16)(dc * x * sg);
       }
       if (rowwise && m < M) {
