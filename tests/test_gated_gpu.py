@@ -336,3 +336,30 @@ def test_gradients_of_infinite_up_preactivations(act):
         x, r, m = x[own[name]], ref[name][own[name]], mag[name][own[name]]
         assert_near(x, r, (2.0**-11 + 2.0**-19) * m + 2 * N * 8 * 2.0**-25 + 2.0**-11 * np.abs(r) + 2.0**-25, name)
     assert (got["dA"][1] == 0).all()
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
+@pytest.mark.parametrize("M,N", [(2048, 64), (700, 130), (333, 37)])  # 8, 2 and 1 values an access
+def test_bias_gradients_sum_what_fp16_cannot_hold(M, N, act):
+    """Columns of terms that fp16 would round to 0, and of terms past fp16 that cancel: the sums
+    are fp32 and only the result is rounded."""
+    rng = np.random.default_rng(M)
+    g = rng.uniform(0, 1, (M, N)).astype(np.float16)
+    u = rng.uniform(0.1, 0.3, (M, N)).astype(np.float16)
+    dC = (rng.integers(1, 3, (M, N)) * 2.0**-24).astype(np.float16)
+    pairs = M // 2 * 2
+    g[:, ::3], u[:, ::3], dC[:, ::3] = 300.0, 280.0, 0.0  # the second of two rows takes back the first
+    dC[:pairs:2, ::3] = rng.integers(400, 1000, (pairs // 2, len(range(0, N, 3))))
+    dC[1:pairs:2, ::3] = -dC[:pairs:2, ::3]
+    dC[0, ::3] += 8
+    plan = QGated(M, N, 64, "f16", act=act)
+    A = torch.zeros((M, 64), dtype=torch.float16, device="cuda")
+    packed = plan.pack(*[torch.zeros((N, 64), dtype=torch.float16, device="cuda") for _ in range(2)])
+    out = plan.backward(A, packed, host_to_device(np.concatenate([g, u], 1)), host_to_device(dC), input_grad=False, bias_grads=True)
+    h, dh = oracle.activation(g.astype(np.float64), act)
+    for name, terms in (("dbias_gate", dC.astype(np.float64) * u * dh), ("dbias_up", dC.astype(np.float64) * h)):
+        ref = terms.sum(0)
+        # act and act' are sums of two products whose sigmoid is within 2^-19; fp32 sums; the output's rounding
+        bound = 2.0**-18 * 2 * np.abs(terms).sum(0) + 2.0**-11 * np.abs(ref) + 2.0**-25
+        assert (np.abs(ref) > 2 * bound)[1::3].all() and (np.abs(terms).max() > 65504)
+        assert_near(out[name].cpu().numpy().astype(np.float64), ref, bound, name)

@@ -39,9 +39,9 @@ constexpr int GPITCH = GT + 8;  // halves per LDS row (16-byte aligned rows, ban
 
 // rows [m][2 N] of preact and [m][N] of dC -> rowwise [m][kd] (inner order, zero past the
 // last inner column) and, if colwise is given, [2 N][mp] (gate rows, then up rows; zero
-// for m in [M, mp)) and bias_part [row tile][2 N], the sums of the rounded values over
-// the tile's rows in fp32.  V: values per access (8 or 2 where N and the pointers
-// allow it).
+// for m in [M, mp)) and bias_part [row tile][2 N], the sums over the tile's rows in fp32, of
+// the values before their rounding (rounded, those below 2^-25 would be lost one by one).
+// V: values per access (8 or 2 where N and the pointers allow it).
 template <int V>
 __global__ __launch_bounds__(256) void gate_grad_kernel(const _Float16* __restrict__ preact,
                                                         const _Float16* __restrict__ dC, int M, int N, int kd,
@@ -49,9 +49,14 @@ __global__ __launch_bounds__(256) void gate_grad_kernel(const _Float16* __restri
                                                         _Float16* __restrict__ rowwise,
                                                         _Float16* __restrict__ colwise,
                                                         float* __restrict__ bias_part) {
-  __shared__ __attribute__((aligned(16))) _Float16 t[2][GT][GPITCH];  // [gate, up][column][row]
-  const int m0 = blockIdx.y * GT, n0 = blockIdx.x * GT;
   constexpr int PER_ROW = GT / V, STEPS = GT * PER_ROW / 256, AT_ONCE = STEPS < 4 ? STEPS : 4;
+  __shared__ __attribute__((aligned(16))) union {
+    _Float16 t[2][GT][GPITCH];          // [gate, up][column][row]
+    float sums[256 / PER_ROW][2][GT];   // then the column sums of the threads' rows
+  } lds;
+  auto& t = lds.t;
+  const int m0 = blockIdx.y * GT, n0 = blockIdx.x * GT;
+  float sum[2][V] = {};  // a thread's rows lie in the same V columns
   typedef _Float16 vec __attribute__((ext_vector_type(V)));
 #pragma unroll 1
   for (int s0 = 0; s0 < STEPS; s0 += AT_ONCE) {
@@ -77,8 +82,11 @@ __global__ __launch_bounds__(256) void gate_grad_kernel(const _Float16* __restri
         const float x = kept(g[s][e]), dc = (float)d[s][e];
         const float sg = gate_sigmoid(c0, c1, x);
         // act'(x) = sg + x sg (1 - sg) t'(x)
-        dg[e] = (_Float16)(dc * kept(u[s][e]) * (sg + x * sg * (1.f - sg) * (c0 + 3.f * c1 * x * x)));
-        du[e] = (_Float16)(dc * x * sg);
+        const float gx = dc * kept(u[s][e]) * (sg + x * sg * (1.f - sg) * (c0 + 3.f * c1 * x * x)), ux = dc * x * sg;
+        sum[0][e] += gx;
+        sum[1][e] += ux;
+        dg[e] = (_Float16)gx;
+        du[e] = (_Float16)ux;
       }
       if (rowwise && m < M) {
         const int c = (n >> 4) * 32 + (n & 15);
@@ -101,16 +109,18 @@ __global__ __launch_bounds__(256) void gate_grad_kernel(const _Float16* __restri
     const int p = i / (GT * GT / 8), c = (i / (GT / 8)) % GT, m = (i % (GT / 8)) * 8, n = n0 + c;
     if (n < N) *reinterpret_cast<half8v*>(colwise + ((size_t)p * N + n) * mp + m0 + m) = *reinterpret_cast<half8v*>(&t[p][c][m]);
   }
-  if (bias_part && threadIdx.x < 2 * GT) {
-    const int p = threadIdx.x / GT, c = threadIdx.x % GT, n = n0 + c;
+  if (!bias_part) return;
+  __syncthreads();
+#pragma unroll
+  for (int p = 0; p < 2; ++p)
+#pragma unroll
+    for (int e = 0; e < V; ++e) lds.sums[threadIdx.x / PER_ROW][p][threadIdx.x % PER_ROW * V + e] = sum[p][e];
+  __syncthreads();
+  if (threadIdx.x < 2 * GT) {
+    const int p = threadIdx.x / GT, c = threadIdx.x % GT;
     float s = 0.f;
-#pragma unroll
-    for (int r = 0; r < GT; r += 8) {
-      const half8v v = *reinterpret_cast<half8v*>(&t[p][c][r]);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) s += (float)v[e];
-    }
-    if (n < N) bias_part[(size_t)blockIdx.y * 2 * N + (size_t)p * N + n] = s;
+    for (int r = 0; r < 256 / PER_ROW; ++r) s += lds.sums[r][p][c];
+    if (n0 + c < N) bias_part[(size_t)blockIdx.y * 2 * N + (size_t)p * N + n0 + c] = s;
   }
 }
 
