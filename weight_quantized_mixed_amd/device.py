@@ -2,6 +2,10 @@
 
 PyTorch provides device memory and the stream; every computation is a
 libqgemm kernel.  Non-GPU tensors are rejected: there is no host fallback.
+
+Every call runs on the current stream, or on `stream`: outputs and workspaces made by
+the call then come from that stream's memory.  Tensors passed in are the caller's to keep
+until the call's work is done.
 """
 from __future__ import annotations
 
@@ -38,6 +42,17 @@ def _stream(stream):
     return _raw_stream(torch.cuda.current_device())
 
 
+def _empty(shape, dtype, device, stream=None):
+    """A new tensor for work on `stream` (None: the current one).  It comes from that stream's own memory, since a
+    block just freed on the current stream may still be in use there, and when freed it waits for both."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(t.device))
+    return t
+
+
 def _check(t, name, shape, dtype):
     """A tensor argument of this shape (a tuple) and type (None passes)."""
     if t is not None and (t.shape != shape or t.dtype != dtype):
@@ -59,11 +74,32 @@ def quantize_rows(A, Q=None, scales=None, stream=None):
     """Per-row symmetric int8 codes and fp32 scales of fp16 A [M, K] (one kernel)."""
     M, K = A.shape
     if Q is None:
-        Q = torch.empty((M, K), dtype=torch.int8, device=A.device)
+        Q = _empty((M, K), torch.int8, A.device, stream)
     if scales is None:
-        scales = torch.empty(M, dtype=torch.float32, device=A.device)
+        scales = _empty((M,), torch.float32, A.device, stream)
     _q.qgemm_quantize_rows(_ptr(A), M, K, _ptr(Q), _ptr(scales), _stream(stream))
     return Q, scales
+
+
+class _Workspace:
+    """Device scratch that grows with the calls that use it.  Outgrown buffers are kept: a
+    captured graph may still replay a call that was given one."""
+
+    def __init__(self, device):
+        self.device, self.buffers, self.streams = device, [], set()
+
+    def of(self, need, stream=None):
+        if not need:
+            return None
+        if not self.buffers or self.buffers[-1].numel() < need:
+            grown = max(need, 2 * self.buffers[-1].numel()) if self.buffers else need
+            self.buffers.append(_empty(grown, torch.uint8, self.device, stream))
+            self.streams = set()
+        at = _stream(stream)
+        if at not in self.streams:  # freed with its object, the buffer waits for every stream that used it
+            self.buffers[-1].record_stream(torch.cuda.current_stream() if stream is None else stream)
+            self.streams.add(at)
+        return self.buffers[-1]
 
 
 class QGemm:
@@ -90,7 +126,7 @@ class QGemm:
             M, N, K, self.a_dtype, w_dtype, self.out_dtype, self.accum_dtype, group_size,
             int(bool(has_zeros)), k_parts, flags)
         self.path = _q.qgemm_plan_path(self.plan)
-        self._ws = None
+        self._ws = _Workspace(self.device)
 
     def close(self):
         plan = getattr(self, "plan", None)
@@ -104,25 +140,23 @@ class QGemm:
 
     def pack(self, w, s=None, z=None, out=None, stream=None):
         if out is None:
-            out = torch.empty(self.packed_bytes, dtype=torch.uint8, device=self.device)
+            out = _empty((self.packed_bytes,), torch.uint8, self.device, stream)
         _q.qgemm_pack_weights(self.plan, _ptr(w), _ptr(s), _ptr(z), _ptr(out), _stream(stream))
         return out
 
-    def workspace(self):
-        if self.ws_bytes and self._ws is None:
-            self._ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=self.device)
-        return self._ws
+    def workspace(self, stream=None):
+        return self._ws.of(self.ws_bytes, stream)
 
-    def new_output(self, M=None):
+    def new_output(self, M=None, stream=None):
         dt = torch.float16 if self.out_dtype == "f16" else torch.int32
-        return torch.empty((self.M if M is None else int(M), self.N), dtype=dt, device=self.device)
+        return _empty((self.M if M is None else int(M), self.N), dt, self.device, stream)
 
     def run(self, A, packed, C=None, ws=None, stream=None, bias=None, M=None):
         """C = A . dequant(W) (+ bias[N]) for the plan's M rows, or M <= that."""
         if C is None:
-            C = self.new_output(M)
+            C = self.new_output(M, stream)
         if ws is None:
-            ws = self.workspace()
+            ws = self.workspace(stream)
         wsb = 0 if ws is None else ws.numel()
         if bias is None and M is None:
             _q.qgemm_run(self.plan, _ptr(A), _ptr(packed), _ptr(C), _ptr(ws), wsb, _stream(stream))
@@ -134,29 +168,13 @@ class QGemm:
     def run_scaled(self, A, packed, row_scales, col_scales, bias=None, C=None, ws=None, stream=None, M=None):
         """fp16 C = acc . row_scales[m] . col_scales[n] (+ bias) for int8 A (dequant_output plans)."""
         if C is None:
-            C = self.new_output(M)
+            C = self.new_output(M, stream)
         if ws is None:
-            ws = self.workspace()
+            ws = self.workspace(stream)
         _q.qgemm_run_scaled(self.plan, self.M if M is None else M, _ptr(A), _ptr(packed), _ptr(row_scales),
                             _ptr(col_scales), _ptr(bias), _ptr(C), _ptr(ws),
                             0 if ws is None else ws.numel(), _stream(stream))
         return C
-
-
-class _Workspace:
-    """Device scratch that grows with the calls that use it.  Outgrown buffers are kept: a
-    captured graph may still replay a call that was given one."""
-
-    def __init__(self, device):
-        self.device, self.buffers = device, []
-
-    def of(self, need):
-        if not need:
-            return None
-        if not self.buffers or self.buffers[-1].numel() < need:
-            grown = max(need, 2 * self.buffers[-1].numel()) if self.buffers else need
-            self.buffers.append(torch.empty(grown, dtype=torch.uint8, device=self.device))
-        return self.buffers[-1]
 
 
 class QGated:
@@ -172,7 +190,7 @@ class QGated:
         self.device = torch.device(device)
         self.plan, self.packed_bytes, self.ws_bytes = _q.qgemm_create_gated(
             M, N, K, self.a_dtype, w_dtype, "f16", OUT_DTYPE[self.a_dtype][1], group_size, int(bool(has_zeros)), act)
-        self._ws, self._backward_ws = None, _Workspace(self.device)
+        self._ws, self._backward_ws = _Workspace(self.device), _Workspace(self.device)
 
     close = QGemm.close
     __del__ = close
@@ -181,17 +199,17 @@ class QGated:
     def pack(self, w_gate, w_up, s_gate=None, s_up=None, z_gate=None, z_up=None, out=None, stream=None):
         """The blob of both projections' canonical weights (scales and zero points where the plan has them)."""
         if out is None:
-            out = torch.empty(self.packed_bytes, dtype=torch.uint8, device=self.device)
+            out = _empty((self.packed_bytes,), torch.uint8, self.device, stream)
         _q.qgemm_pack_gated(self.plan, _ptr(w_gate), _ptr(s_gate), _ptr(z_gate), _ptr(w_up), _ptr(s_up), _ptr(z_up),
                             _ptr(out), _stream(stream))
         return out
 
-    def new_output(self, M=None):
-        return torch.empty((self.M if M is None else int(M), self.N), dtype=torch.float16, device=self.device)
+    def new_output(self, M=None, stream=None):
+        return _empty((self.M if M is None else int(M), self.N), torch.float16, self.device, stream)
 
-    def new_preact(self, M=None):
+    def new_preact(self, M=None, stream=None):
         """Room for the pre-activations of M rows, which backward reads."""
-        return torch.empty((self.M if M is None else int(M), 2 * self.N), dtype=torch.float16, device=self.device)
+        return _empty((self.M if M is None else int(M), 2 * self.N), torch.float16, self.device, stream)
 
     def _run(self, A, packed, rs, csg, csu, bias_gate, bias_up, preact, C, ws, stream, M):
         M = self.M if M is None else int(M)
@@ -200,10 +218,10 @@ class QGated:
             _check(b, name, (self.N,), torch.float16)
         _check(preact, "preact", (M, 2 * self.N), torch.float16)
         if C is None:
-            C = self.new_output(M)
+            C = self.new_output(M, stream)
         _check(C, "C", (M, self.N), torch.float16)
         if ws is None:
-            ws = self.workspace()
+            ws = self.workspace(stream)
         _q.qgemm_run_gated(self.plan, M, _ptr(A), _ptr(packed), _ptr(rs), _ptr(csg), _ptr(csu), _ptr(bias_gate),
                            _ptr(bias_up), _ptr(preact), _ptr(C), _ptr(ws), 0 if ws is None else ws.numel(),
                            _stream(stream))
@@ -234,13 +252,13 @@ class QGated:
         _check(A, "A", (M, self.K), half)
         _check(preact, "preact", (M, 2 * self.N), half)
         _check(dC, "dC", (M, self.N), half)
-        new = lambda *shape: torch.empty(shape, dtype=half, device=self.device)  # noqa: E731
+        new = lambda *shape: _empty(shape, half, self.device, stream)  # noqa: E731
         dA = new(M, self.K) if input_grad else None
         dw = new(2, self.N, self.K) if weight_grads else None
         db = new(2, self.N) if bias_grads else None
         need = _q.qgemm_gated_backward_workspace(self.plan, M, weight_grads or bias_grads)
         if ws is None:
-            ws = self._backward_ws.of(need)
+            ws = self._backward_ws.of(need, stream)
         part = lambda t, i: None if t is None else t[i]  # noqa: E731
         _q.qgemm_gated_backward(self.plan, M, _ptr(A), _ptr(packed), _ptr(preact), _ptr(dC), _ptr(dA),
                                 _ptr(part(dw, 0)), _ptr(part(dw, 1)), _ptr(part(db, 0)), _ptr(part(db, 1)), _ptr(ws),
@@ -297,7 +315,7 @@ class PagedKV:
         _check(positions, "positions", (T,), torch.int32)
         _check(slots, "slots", (T,), torch.int64)
         if q_out is None:
-            q_out = torch.empty((T, q_heads, D), dtype=torch.float16, device=q.device)
+            q_out = _empty((T, q_heads, D), torch.float16, q.device, stream)
         _check(q_out, "q_out", (T, q_heads, D), torch.float16)
         _q.qgemm_kv_append(self.desc, T, q_heads, qp, qs, kp, ks, vp, vs, _ptr(cos), _ptr(sin), n_pos, 2 * half,
                            int(bool(interleaved)), _ptr(positions), _ptr(slots), _ptr(q_out), _stream(stream))
@@ -323,13 +341,13 @@ class PagedKV:
                 raise ValueError("prefix_table holds the pages of prefix_len tokens")
             _check(prefix_table, "prefix_table", (prefix_table.numel(),), i32)
         if out is None:
-            out = torch.empty((T, q_heads, D), dtype=torch.float16, device=q.device)
+            out = _empty((T, q_heads, D), torch.float16, q.device, stream)
         _check(out, "out", (T, q_heads, D), torch.float16)
         _check(lse, "lse", (T, q_heads), torch.float32)
         need = _attention_workspace(self.n_pages, self.page_size, self.kv_heads, D, T, q_heads, B, max_q, max_len,
                                     prefix_len)
         if ws is None:
-            ws = self._workspace.of(need)
+            ws = self._workspace.of(need, stream)
         _q.qgemm_attention(self.desc, T, q_heads, qp, qs, B, _ptr(q_starts), _ptr(kv_lens), _ptr(tables), width,
                            _ptr(prefix_table) if prefix_len else 0, prefix_len, max_q, max_len,
                            D ** -0.5 if scale is None else scale, _ptr(out), _ptr(lse), _ptr(ws),
