@@ -338,3 +338,26 @@ def test_an_outgrown_workspace_stays_with_its_graph():
         torch.cuda.synchronize()
         assert np.array_equal(out.cpu().numpy().astype(np.float64), base)
     assert all((j == 0xFF).all() for j in junk)
+
+
+@pytest.mark.parametrize("hq,hkv,D,qs,lens,prefix,max_q,max_len,width", [
+    (8, 2, 128, [5, 2], [40, 30], 0, 3, 40, 9), (8, 2, 128, [5, 2], [140, 100], 70, 5, 77, 9), (4, 1, 64, [1, 1], [140, 100], 70, 1, 140, 5),
+    (4, 2, 128, [100, 150], [130, 190], 0, 70, 190, 12), (4, 2, 128, [100, 150], [130, 190], 33, 150, 100, 12),
+    (2, 2, 256, [90], [400], 0, 60, 300, 15), (8, 1, 128, [6], [6], 0, 2, 6, 1)])
+def test_rows_and_tokens_past_the_bounds_are_left_out(hq, hkv, D, qs, lens, prefix, max_q, max_len, width):
+    """More queries, tokens or pages than max_q, max_len and the table's width: the rows within
+    max_q see the tokens that they would see, as far as those are read; other rows stay as they were."""
+    say(f"case bounds q={qs} lens={lens} max_q={max_q} max_len={max_len} width={width}")
+    c = AttnCase(hq, hkv, D, 16, qs, lens, prefix, seed=13).upload()
+    c.dtables = dev(c.tables[:, :width])
+    out = torch.full((sum(qs), hq, D), 3.0, dtype=torch.float16, device="cuda")
+    got, lse = c.run(max_q=max_q, max_len=max_len, out=out)
+    for b, (n, L) in enumerate(zip(qs, lens)):
+        m, held, r0 = min(n, max_q), min(L, max_len, width * 16), c.starts[b]
+        seen = np.concatenate([np.ones((m, prefix), bool), np.arange(held)[None] <= (L - n + np.arange(m))[:, None]], axis=1)
+        for h in range(hq):
+            kt, vt = (np.concatenate([c.tokens[0][i][:, h // (hq // hkv)], c.tokens[b + 1][i][:held, h // (hq // hkv)]]) for i in (0, 1))
+            ref, ref_lse, bound = oracle.attention_ref(c.q[r0:r0 + m, h], kt, vt, seen, D ** -0.5)
+            assert_near(got[r0:r0 + m, h], ref, bound, f"sequence {b} head {h}")
+            assert (np.abs(lse[r0:r0 + m, h] - ref_lse) <= 1e-4 + 1e-5 * np.abs(ref_lse)).all()
+        assert (got[r0 + m:c.starts[b + 1]] == 3.0).all()

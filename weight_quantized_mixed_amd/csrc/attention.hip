@@ -141,7 +141,7 @@ struct Item {
   int tok0, last_tok;    // query token of row 0; last query token of the item's rows
   int key0, key1;        // keys of the part
   int pre;               // keys [0, pre) are the prefix's
-  int lim0;              // row r sees keys below pre_lim + max(0, lim0 + r / G), ...
+  int lim0;              // row r sees keys below pre_lim + max(0, lim0 + r / G) and key1, ...
   int pre_lim;           // ... with lim0 = INT_MIN / 2 for rows that see pre_lim keys
   int slot;
   const int32_t* own;    // pages of the keys from pre on
@@ -159,16 +159,15 @@ __device__ __forceinline__ void attend_tile(const AttnArgs& a, const AttnSplit& 
   const int g = lane >> 4, l16 = lane & 15;
   const int G = a.q_heads / a.kv_heads, D = a.D;
 
-  // ---- rows of this wave, and the keys that they see
+  // ---- rows of this wave, and the keys that they see (the smaller of the two bounds before
+  // pre_lim is added: the lengths that a call holds may pass the ones it states)
   const int wrow0 = it.row0 + (KEYS ? 0 : wave * NT * 16);
+  const int cap = it.key1 - it.pre_lim;
+  auto limit_of = [&](int r) { return it.pre_lim + min(cap, max(0, it.lim0 + min(r, it.rows - 1) / G)); };
   int lim[NT];
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    const int r = min(wrow0 + nt * 16 + l16, it.rows - 1);
-    lim[nt] = min(it.key1, it.pre_lim + max(0, it.lim0 + r / G));
-  }
+  for (int nt = 0; nt < NT; ++nt) lim[nt] = limit_of(wrow0 + nt * 16 + l16);
   // over the tile's last row (the limits grow with the row), this wave's first and last
-  auto limit_of = [&](int r) { return min(it.key1, it.pre_lim + max(0, it.lim0 + min(r, it.rows - 1) / G)); };
   const int kend = __builtin_amdgcn_readfirstlane(limit_of(it.row0 + T::BM - 1));
   const int wave_lo = __builtin_amdgcn_readfirstlane(limit_of(wrow0));
   const int wave_hi = __builtin_amdgcn_readfirstlane(wrow0 < it.rows ? limit_of(wrow0 + NT * 16 - 1) : 0);
@@ -648,10 +647,12 @@ __device__ __forceinline__ void attend_tile(const AttnArgs& a, const AttnSplit& 
   }
 }
 
-// queries of sequence b: first row of q and how many, within q and max_q
-__device__ __forceinline__ void queries_of(const AttnArgs& a, int b, int& start, int& n) {
+// queries of sequence b: first row of q, how many within q, and n of them within max_q
+__device__ __forceinline__ int queries_of(const AttnArgs& a, int b, int& start, int& n) {
   start = min(max(a.q_starts[b], 0), a.T);
-  n = min(min(max(a.q_starts[b + 1], start), a.T) - start, a.max_q);
+  const int all = min(max(a.q_starts[b + 1], start), a.T) - start;
+  n = min(all, a.max_q);
+  return all;
 }
 
 template <int DP, int KIND_P, int KIND_S>
@@ -705,15 +706,15 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void attend_kernel(AttnArgs
   const int part = group / a.kv_heads % sp.s_splits;
   const int b = group / a.kv_heads / sp.s_splits;
   int n;
-  queries_of(a, b, it.tok0, n);
+  const int all = queries_of(a, b, it.tok0, n);
   it.row0 = tile * tile_rows(KIND_S);
   it.rows = n * G;
   if (it.row0 >= it.rows) return;
   it.last_tok = it.tok0 + n - 1;
   const int64_t room = a.table_width << a.page_shift;
-  const int held = (int)min((int64_t)min(max(a.kv_lens[b], 0), a.max_len), room);
+  const int len = max(a.kv_lens[b], 0), held = (int)min((int64_t)min(len, a.max_len), room);
   it.pre = it.pre_lim = sp.shared ? 0 : (int)a.prefix_len;
-  it.lim0 = held - n + 1;
+  it.lim0 = len - all + 1;  // from the true lengths, also where rows or tokens past the call's bounds are left out
   it.key0 = part * sp.s_chunk;
   it.key1 = min(it.pre + held, it.key0 + sp.s_chunk);
   it.slot = (sp.shared ? sp.p_splits : 0) + part;
