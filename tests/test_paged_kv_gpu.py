@@ -361,3 +361,21 @@ def test_rows_and_tokens_past_the_bounds_are_left_out(hq, hkv, D, qs, lens, pref
             assert_near(got[r0:r0 + m, h], ref, bound, f"sequence {b} head {h}")
             assert (np.abs(lse[r0:r0 + m, h] - ref_lse) <= 1e-4 + 1e-5 * np.abs(ref_lse)).all()
         assert (got[r0 + m:c.starts[b + 1]] == 3.0).all()
+
+
+def test_a_single_token_cut_from_any_array():
+    """One row of a wider array whose row length is odd: its step to a next row does not exist."""
+    rng = np.random.default_rng(15)
+    hq, hkv, D, page = 4, 2, 64, 16
+    wide = dev(halves(rng, 5, (hq + 2 * hkv) * D + 3))
+    row = wide[:1, :(hq + 2 * hkv) * D]
+    table = dev(np.cos(rng.uniform(-3, 3, (9, 32))).astype(np.float32))
+    pos, slot = dev(np.array([4], np.int32)), torch.tensor([20], device="cuda")
+    got, want = PagedKV(4, page, hkv, D), PagedKV(4, page, hkv, D)
+    results = []
+    for cache, x in ((got, row), (want, row.clone(memory_format=torch.contiguous_format))):
+        q0, k, v = x.split([hq * D, hkv * D, hkv * D], dim=1)
+        cache.append(q0, k, v, table, table, pos, slot)
+        pages = [dev(np.array(a, np.int32)) for a in ([0, 1], [21], [[0, 1]])]
+        results.append(cache.attend(q0.view(1, hq, D), *pages, 1, 21))
+    assert torch.equal(*results) and torch.equal(got.k, want.k) and torch.equal(got.v, want.v)

@@ -268,13 +268,16 @@ class QGated:
 
 
 def _rows(t, name, T, width):
-    """(address, values between rows) of fp16 [T, width], whose rows may be slices of wider ones."""
+    """(address, values between rows) of fp16 [T, width], whose rows may be slices of wider ones.
+
+    The step of a single row says nothing, whatever the tensor that it was cut from.
+    """
     if not t.is_cuda:
         raise ValueError("qgemm takes device tensors only")
     step, one = t.stride() if t.dim() == 2 else (0, 0)
     if t.dtype != torch.float16 or t.shape != (T, width) or (one != 1 and width > 1) or (step < width and T > 1):
         raise ValueError(f"{name}: fp16 {(T, width)} with contiguous rows expected, got {t.dtype} {tuple(t.shape)}")
-    return t.data_ptr(), step if step > width else width
+    return t.data_ptr(), step if T > 1 else width
 
 
 # the workspace of an attention call depends on its sizes alone
@@ -330,7 +333,7 @@ class PagedKV:
                 or (per_head != D and q_heads > 1) or (step < q_heads * D and T > 1)):
             raise ValueError(f"q: fp16 [T, q_heads, {self.head_dim}] with contiguous rows on the device expected, "
                              f"got {q.dtype} {tuple(q.shape)}")
-        qp, qs = q.data_ptr(), max(step, q_heads * D)
+        qp, qs = q.data_ptr(), step if T > 1 else q_heads * D
         B, width = tables.shape
         i32 = torch.int32
         _check(q_starts, "q_starts", (B + 1,), i32)
