@@ -431,7 +431,8 @@ qgemm_status qgemm_attention_workspace(const qgemm_kv_cache* cache, int64_t T, i
  * prefix: out = softmax(scale q K^T) V per query and head (scale positive and finite), with scores, softmax and sums
  * in fp32 and the probabilities rounded to fp16 as operands of the product with V.
  * Query head h reads key / value head h / (q_heads / kv_heads).
- *   T            rows of q: the queries of all sequences, one after the other.
+ *   T            rows of q: the queries of all sequences, one after the other.  With 0 of them
+ *                nothing is launched, and B and max_q may be 0 (else they are at least 1).
  *   q            device, fp16, row t at t * q_stride values (q_stride >= q_heads *
  *                head_dim, a multiple of 8; q 16-byte aligned).
  *   q_starts     device, int32 [B + 1]: sequence b has the rows q_starts[b] ..

@@ -217,6 +217,15 @@ def test_attention_refuses_bad_arguments():
     assert q.load().qgemm_attention_workspace(ctypes.byref(cache()), 4, 8, 2, 1, 10, 0, None) == BAD
 
 
+def test_attention_of_an_empty_batch():
+    ok = dict(T=0, hq=8, q=0, qs=1024, B=0, starts=0, lens=0, tables=0, width=0, pt=0, pl=0, mq=0, ml=0, scale=0.1, out=0,
+              lse=0, ws=0, wsb=0)
+    assert status(q.qgemm_attention, cache(), *ok.values()) == q.QGEMM_OK
+    assert q.qgemm_attention_workspace(cache(), 0, 8, 0, 0, 0, 0) == 0
+    for kw in (dict(B=-1), dict(mq=-1), dict(T=1), dict(T=1, B=1), dict(T=1, mq=1)):
+        assert status(q.qgemm_attention, cache(), *{**ok, **kw}.values()) == BAD, kw
+
+
 def test_workspace_holds_the_parts():
     assert q.qgemm_attention_workspace(cache(), 0, 8, 1, 1, 10, 0) == 0
     assert q.qgemm_attention_workspace(cache(), 1, 8, 1, 1, 60, 0) == 0          # one part: written directly

@@ -379,3 +379,10 @@ def test_a_single_token_cut_from_any_array():
         pages = [dev(np.array(a, np.int32)) for a in ([0, 1], [21], [[0, 1]])]
         results.append(cache.attend(q0.view(1, hq, D), *pages, 1, 21))
     assert torch.equal(*results) and torch.equal(got.k, want.k) and torch.equal(got.v, want.v)
+
+
+@pytest.mark.parametrize("B", [0, 3])
+def test_attention_of_an_empty_batch(B):
+    c = AttnCase(4, 2, 64, 16, [1], [40], seed=3).upload()
+    starts, lens = (torch.zeros(n, dtype=torch.int32, device="cuda") for n in (B + 1, B))
+    assert c.cache.attend(c.dq[:0], starts, lens, torch.zeros((B, 2), dtype=torch.int32, device="cuda"), 0, 0).shape == (0, 4, 64)

@@ -695,7 +695,8 @@ qgemm_status attention_shape(const qgemm_kv_cache* c, int64_t T, int32_t q_heads
                              int64_t max_len, int64_t prefix_len, AttnShape* s) {
   const qgemm_status st = check_cache(c, T, q_heads);
   if (st != QGEMM_OK) return st;
-  if (B < 1 || max_q < 1 || max_len < 0 || prefix_len < 0) return QGEMM_ERR_INVALID_ARG;
+  const int64_t least = T > 0 ? 1 : 0;  // a batch without queries may be without sequences too
+  if (B < least || max_q < least || max_len < 0 || prefix_len < 0) return QGEMM_ERR_INVALID_ARG;
   if (B > 65535 || max_q > INT32_MAX || max_len > INT32_MAX || prefix_len > INT32_MAX) return QGEMM_ERR_UNSUPPORTED;
   if (max_len + prefix_len > INT32_MAX - 65536) return QGEMM_ERR_UNSUPPORTED;  // key positions are 32 bits wide
   *s = {T, B, max_q < T ? max_q : T, max_len, prefix_len, q_heads, c->kv_heads, c->head_dim};
