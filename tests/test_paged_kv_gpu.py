@@ -386,3 +386,25 @@ def test_attention_of_an_empty_batch(B):
     c = AttnCase(4, 2, 64, 16, [1], [40], seed=3).upload()
     starts, lens = (torch.zeros(n, dtype=torch.int32, device="cuda") for n in (B + 1, B))
     assert c.cache.attend(c.dq[:0], starts, lens, torch.zeros((B, 2), dtype=torch.int32, device="cuda"), 0, 0).shape == (0, 4, 64)
+
+
+def test_append_of_more_tokens_than_one_launch_holds():
+    """2^24 + 5 rows (a launch ends below 2^32 threads of 256 a token): the last ones are turned and stored too."""
+    T, D = 2**24 + 5, 8
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randint(-2000, 2000, (T, 3 * D), generator=gen, device="cuda", dtype=torch.int16).half()
+    qt, kt, vt = x.split([D] * 3, dim=1)
+    cos, sin = torch.tensor([[0.0], [1.0]], device="cuda"), torch.tensor([[1.0], [0.0]], device="cuda")
+    pos = (torch.arange(T, device="cuda", dtype=torch.int32) & 1) ^ 1  # every other token: a quarter turn of pair (0, 1)
+    slots = torch.full((T,), -1, dtype=torch.int64, device="cuda")
+    kept = torch.tensor([0, 2**23 - 1, 2**23, 2**24 - 1, 2**24, T - 1], device="cuda")
+    slots[kept] = torch.arange(6, device="cuda")
+    cache = PagedKV(1, 8, 1, D)
+    out = cache.append(qt, kt, vt, cos, sin, pos, slots, interleaved=True)[:, 0]
+    turned = qt.clone()
+    turned[1::2, 0], turned[1::2, 1] = -qt[1::2, 1], qt[1::2, 0]
+    assert torch.equal(out, turned)
+    k = kt[kept].clone()
+    odd = (kept & 1).bool()
+    k[odd, 0], k[odd, 1] = -kt[kept][odd, 1], kt[kept][odd, 0]
+    assert torch.equal(cache.k[0, 0, :6], k) and torch.equal(cache.v[0, 0, :6], vt[kept])

@@ -108,9 +108,21 @@ hipError_t launch_kv_append(const AppendArgs& a, int64_t T, hipStream_t st) {
   auto fits = [&](int v) {
     return counts % v == 0 && (halves & (2 * v - 1)) == 0 && (floats & ((v > 4 ? 16 : 4 * v) - 1)) == 0;
   };
+  // a launch holds fewer than 2^32 threads along its first dimension, the tokens'
+  constexpr int64_t MOST = (int64_t)1 << 23;
   auto go = [&](auto kernel, int v) {
     const int items = (a.q_heads + 2 * a.kv_heads) * (a.D / 2 / v);
-    hipLaunchKernelGGL(kernel, dim3((unsigned)T, (unsigned)((items + 255) / 256)), dim3(256), 0, st, a);
+    for (int64_t t0 = 0; t0 < T; t0 += MOST) {
+      AppendArgs b = a;
+      b.q += t0 * a.q_stride;
+      b.k += t0 * a.k_stride;
+      b.v += t0 * a.v_stride;
+      b.q_out += t0 * a.q_heads * a.D;
+      if (b.positions) b.positions += t0;
+      b.slots += t0;
+      const unsigned n = (unsigned)(T - t0 < MOST ? T - t0 : MOST);
+      hipLaunchKernelGGL(kernel, dim3(n, (unsigned)((items + 255) / 256)), dim3(256), 0, st, b);
+    }
   };
   const bool il = a.interleaved != 0;
   if (fits(8)) il ? go(kv_append_kernel<8, true>, 8) : go(kv_append_kernel<8, false>, 8);
