@@ -454,6 +454,8 @@ qgemm_status qgemm_attention_workspace(const qgemm_kv_cache* cache, int64_t T, i
  *                sequence are not written.
  *   lse          device, fp32 [T, q_heads] or NULL: ln(sum exp(scale q k)) of each row.
  *   workspace, workspace_bytes: as stated by qgemm_attention_workspace, 16-byte aligned.
+ * More than 65535 sequences, 2^31 - 65537 tokens of one sequence and the prefix, or work of
+ * 2^24 workgroups return QGEMM_ERR_UNSUPPORTED.
  * The prefix is read once for rows of all sequences where sequences have few rows each;
  * keys are split over workgroups where rows are few, and the parts' results joined in a
  * fixed order: results are bitwise reproducible for the same sizes.

@@ -226,6 +226,14 @@ def test_attention_of_an_empty_batch():
         assert status(q.qgemm_attention, cache(), *{**ok, **kw}.values()) == BAD, kw
 
 
+def test_attention_items_fit_a_launch():
+    """65535 sequences of one token and 300 heads are more workgroups of 256 than one launch holds (2^32 threads)."""
+    wide = cache(kv_heads=300, head_dim=8)
+    assert status(q.qgemm_attention_workspace, wide, 65535, 300, 65535, 1, 40, 0) == UNS
+    assert status(q.qgemm_attention, wide, 65535, 300, P, 2400, 65535, P, P, P, 3, 0, 0, 1, 40, 1.0, P, 0, P, 1 << 40) == UNS
+    assert status(q.qgemm_attention_workspace, wide, 50000, 300, 50000, 1, 40, 0) == q.QGEMM_OK
+
+
 def test_workspace_holds_the_parts():
     assert q.qgemm_attention_workspace(cache(), 0, 8, 1, 1, 10, 0) == 0
     assert q.qgemm_attention_workspace(cache(), 1, 8, 1, 1, 60, 0) == 0          # one part: written directly

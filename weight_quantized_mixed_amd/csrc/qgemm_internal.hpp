@@ -328,7 +328,7 @@ struct AttnShape {
   int64_t T, B, max_q, max_len, prefix_len;
   int32_t q_heads, kv_heads, D;
 };
-bool attention_grid_fits(const AttnShape& s);  // item counts and row numbers in 32 bits
+bool attention_grid_fits(const AttnShape& s);  // row numbers in 32 bits, work items in a launch
 size_t attention_ws_bytes(const AttnShape& s);
 hipError_t launch_attention(const AttnArgs& a, const AttnShape& s, void* ws, hipStream_t st);
 
