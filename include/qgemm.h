@@ -428,8 +428,9 @@ qgemm_status qgemm_attention_workspace(const qgemm_kv_cache* cache, int64_t T, i
 
 /*
  * Causal attention of B sequences over the cache, all of which may begin with one shared
- * prefix: out = softmax(scale q K^T) V per query and head (scale positive and finite), with scores, softmax and sums
- * in fp32 and the probabilities rounded to fp16 as operands of the product with V.
+ * prefix: out = softmax(scale q K^T) V per query and head (scale positive and scale log2 e
+ * finite in fp32), with scores, softmax and sums in fp32 and the probabilities rounded to fp16
+ * as operands of the product with V.
  * Query head h reads key / value head h / (q_heads / kv_heads).
  *   T            rows of q: the queries of all sequences, one after the other.  With 0 of them
  *                nothing is launched, and B and max_q may be 0 (else they are at least 1).

@@ -226,6 +226,12 @@ def test_attention_of_an_empty_batch():
         assert status(q.qgemm_attention, cache(), *{**ok, **kw}.values()) == BAD, kw
 
 
+def test_attention_scale_stays_finite_in_powers_of_two():
+    args = [4, 8, P, 1024, 2, P, P, P, 3, 0, 0, 1, 40]
+    for scale in (2.4e38, 3e38, 3.4e38):
+        assert status(q.qgemm_attention, cache(), *args, scale, P, 0, P, 1 << 40) == BAD, scale
+
+
 def test_attention_items_fit_a_launch():
     """65535 sequences of one token and 300 heads are more workgroups of 256 than one launch holds (2^32 threads)."""
     wide = cache(kv_heads=300, head_dim=8)

@@ -408,3 +408,10 @@ def test_append_of_more_tokens_than_one_launch_holds():
     odd = (kept & 1).bool()
     k[odd, 0], k[odd, 1] = -kt[kept][odd, 1], kt[kept][odd, 0]
     assert torch.equal(cache.k[0, 0, :6], k) and torch.equal(cache.v[0, 0, :6], vt[kept])
+
+
+def test_attention_at_the_largest_scale():
+    """Scores of 0 stay 0 at the largest scale that is taken: the mean of the values."""
+    c = AttnCase(4, 2, 64, 16, [1, 3], [40, 7], 20, seed=16)
+    c.q[:] = 0
+    c.upload().check(scale=2.3e38)

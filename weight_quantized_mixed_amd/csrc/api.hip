@@ -952,7 +952,8 @@ qgemm_status qgemm_attention(const qgemm_kv_cache* cache, int64_t T, int32_t q_h
   if (st != QGEMM_OK) return st;
   if (table_width < 0 || q_stride < (int64_t)q_heads * cache->head_dim) return QGEMM_ERR_INVALID_ARG;
   if (T == 0) return QGEMM_OK;
-  if (!(scale > 0.f) || scale > 3e38f) return QGEMM_ERR_INVALID_ARG;
+  // scores are scaled by scale log2 e: an infinite one would make NaN of a score of 0
+  if (!(scale > 0.f) || !(scale * 1.4426950408889634f <= 3.402823466e38f)) return QGEMM_ERR_INVALID_ARG;
   if (!q || !q_starts || !kv_lens || !out || (table_width && !tables) || (prefix_len && !prefix_table))
     return QGEMM_ERR_INVALID_ARG;
   if (q_stride % 8 != 0 || ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out)) & 15))
