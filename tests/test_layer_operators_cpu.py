@@ -246,3 +246,24 @@ def test_workspace_holds_the_parts():
     n = q.qgemm_attention_workspace(cache(), 1, 8, 1, 1, 2000, 0)
     parts = n // (8 * 128 * 4 + 8 * 8)
     assert parts > 1 and n == parts * (8 * 128 * 4 + 8 * 8)                       # (o, m, l) of each
+
+
+def test_gated_tensors_of_other_sizes_are_refused_before_any_address():
+    """A blob of a smaller plan, or weights and tables of another shape, would be read past their end."""
+    torch = pytest.importorskip("torch")
+    from weight_quantized_mixed_amd.device import QGated
+    plan = QGated(4, 32, 256, "u4", 64, True, device="cpu")
+    w, t = torch.zeros((32, 32), dtype=torch.int32), torch.ones((32, 4), dtype=torch.float16)
+    ok = dict(w_gate=w, w_up=w, s_gate=t, s_up=t, z_gate=t, z_up=t)
+    for kw in (dict(w_gate=w[:31]), dict(w_up=w[:, :31]), dict(w_up=torch.zeros((33, 32), dtype=torch.int32)), dict(s_gate=t[:, :2]),
+               dict(s_up=t.float()), dict(z_gate=t[:31]), dict(z_up=t.t())):
+        with pytest.raises(ValueError, match=next(iter(kw)) + ":"):
+            plan.pack(**{**ok, **kw})
+    small = torch.zeros(plan.packed_bytes - 1, dtype=torch.uint8)
+    with pytest.raises(ValueError, match="out: "):
+        plan.pack(**ok, out=small)
+    A, row = torch.zeros((4, 256), dtype=torch.float16), torch.zeros((4, 32), dtype=torch.float16)
+    with pytest.raises(ValueError, match="packed: "):
+        plan.run(A, small)
+    with pytest.raises(ValueError, match="packed: "):
+        plan.backward(A, small, torch.zeros((4, 64), dtype=torch.float16), row)

@@ -17,6 +17,7 @@ import torch
 from . import qgemm as _q
 
 A_DTYPE = {"i4": "f16", "u4": "f16", "f16": "f16", "i8": "i8", "i2": "i8"}
+WEIGHT_BITS = {"i4": 4, "u4": 4, "f16": 16, "i8": 8, "i2": 2}
 OUT_DTYPE = {"f16": ("f16", "f32"), "i8": ("i32", "i32")}
 
 
@@ -57,6 +58,14 @@ def _check(t, name, shape, dtype):
     """A tensor argument of this shape (a tuple) and type (None passes)."""
     if t is not None and (t.shape != shape or t.dtype != dtype):
         raise ValueError(f"{name}: {dtype} {shape} expected, got {t.dtype} {tuple(t.shape)}")
+    return t
+
+
+def _check_bytes(t, name, need, exact=False):
+    """A tensor argument of this many bytes (or more of them), whatever its type (None passes)."""
+    held = need if t is None else t.numel() * t.element_size()
+    if held < need or (exact and held > need):
+        raise ValueError(f"{name}: {need} bytes expected, got {held}")
     return t
 
 
@@ -190,6 +199,8 @@ class QGated:
         self.device = torch.device(device)
         self.plan, self.packed_bytes, self.ws_bytes = _q.qgemm_create_gated(
             M, N, K, self.a_dtype, w_dtype, "f16", OUT_DTYPE[self.a_dtype][1], group_size, int(bool(has_zeros)), act)
+        self.groups = 0 if group_size == 0 else 1 if group_size < 0 else self.K // group_size
+        self.has_zeros = bool(has_zeros)
         self._ws, self._backward_ws = _Workspace(self.device), _Workspace(self.device)
 
     close = QGemm.close
@@ -198,8 +209,14 @@ class QGated:
 
     def pack(self, w_gate, w_up, s_gate=None, s_up=None, z_gate=None, z_up=None, out=None, stream=None):
         """The blob of both projections' canonical weights (scales and zero points where the plan has them)."""
+        for name, w in (("w_gate", w_gate), ("w_up", w_up)):
+            _check_bytes(w, name, self.N * self.K * WEIGHT_BITS[self.w_dtype] // 8, exact=True)
+        tables = (("s_gate", s_gate), ("s_up", s_up)) if self.groups else ()
+        for name, t in tables + ((("z_gate", z_gate), ("z_up", z_up)) if self.has_zeros else ()):
+            _check(t, name, (self.N, self.groups), torch.float16)
         if out is None:
             out = _empty((self.packed_bytes,), torch.uint8, self.device, stream)
+        _check_bytes(out, "out", self.packed_bytes)
         _q.qgemm_pack_gated(self.plan, _ptr(w_gate), _ptr(s_gate), _ptr(z_gate), _ptr(w_up), _ptr(s_up), _ptr(z_up),
                             _ptr(out), _stream(stream))
         return out
@@ -217,6 +234,7 @@ class QGated:
         for name, b in (("bias_gate", bias_gate), ("bias_up", bias_up)):
             _check(b, name, (self.N,), torch.float16)
         _check(preact, "preact", (M, 2 * self.N), torch.float16)
+        _check_bytes(packed, "packed", self.packed_bytes)
         if C is None:
             C = self.new_output(M, stream)
         _check(C, "C", (M, self.N), torch.float16)
@@ -251,6 +269,7 @@ class QGated:
         half = torch.float16
         _check(A, "A", (M, self.K), half)
         _check(preact, "preact", (M, 2 * self.N), half)
+        _check_bytes(packed, "packed", self.packed_bytes)
         _check(dC, "dC", (M, self.N), half)
         new = lambda *shape: _empty(shape, half, self.device, stream)  # noqa: E731
         dA = new(M, self.K) if input_grad else None
