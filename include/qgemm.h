@@ -354,9 +354,12 @@ qgemm_status qgemm_gated_backward_workspace(const qgemm_plan* plan, int64_t M, i
  * Gradients of a gated run of M rows from the gradient of its output:
  *   dU = dC act(g), dG = dC u act'(g);  dA = dG . Wg^T + dU . Wu^T,
  *   dWg = dG^T . A, dWu = dU^T . A, dbg and dbu the column sums of dG and dU
- * with g and u the pre-activations as kept (rounded to fp16) and dG, dU rounded to fp16
- * as operands of the products, which sum in fp32.  Quantised weights enter dA as
- * (q - z) s rounded to fp16.
+ * with g and u the pre-activations as kept (rounded to fp16; a kept infinity stands for
+ * 65504 of its sign) and dG, dU rounded to fp16 as operands of the products, which sum in
+ * fp32.  A row of them (for dA) or a column (for dW) whose largest value lies past fp16 or
+ * below 2^-6 is scaled by a power of two for that, so that it neither overflows nor
+ * vanishes; the sums are scaled back before they are rounded.  Bias gradients sum the
+ * unrounded values.  Quantised weights enter dA as (q - z) s rounded to fp16.
  *   A          device, fp16 [M, K] (needed for weight gradients), 16-byte aligned.
  *   packed     device, the forward's blob (needed for dA), 16-byte aligned.
  *   preact     device, fp16 [M, 2 N], from the forward.

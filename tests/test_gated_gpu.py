@@ -363,3 +363,80 @@ def test_bias_gradients_sum_what_fp16_cannot_hold(M, N, act):
         bound = 2.0**-18 * 2 * np.abs(terms).sum(0) + 2.0**-11 * np.abs(ref) + 2.0**-25
         assert (np.abs(ref) > 2 * bound)[1::3].all() and (np.abs(terms).max() > 65504)
         assert_near(out[name].cpu().numpy().astype(np.float64), ref, bound, name)
+
+
+RANGES = [  # M, N, K, w: the products of every path that takes gradients as fp16 operands
+    (1, 1, 70, "f16"), (1, 40, 96, "f16"), (1, 40, 8300, "f16"), (5, 70, 200, "f16"), (20, 33, 136, "f16"), (40, 130, 129, "f16"),
+    (100, 72, 200, "f16"), (200, 260, 520, "f16"), (700, 60, 1300, "f16"), (700, 60, 2000, "f16"), (1300, 60, 2100, "f16"),
+    (1300, 100, 5000, "f16"), (3400, 100, 2900, "f16"), (2100, 4100, 2300, "f16"), (33, 100, 256, "i4"), (70, 4200, 256, "i4"),
+]
+
+
+@pytest.mark.parametrize("M,N,K,w", RANGES)
+@pytest.mark.parametrize("large", [True, False])
+def test_gradients_past_the_range_of_fp16(M, N, K, w, large):
+    """Rows and columns whose dG and dU lie past 65504, or far below 2^-14, beside ordinary
+    ones, and weights and activations that bring the results back: dA and dW keep 11 bits."""
+    say(f"case gradient range M={M} N={N} K={K} {w} large={large}")
+    rng = np.random.default_rng(M + N)
+    lift = rng.integers(0, 13, (M, 1)) if large else rng.integers(-22, -2, (M, 1))
+    half = lambda x: x.astype(np.float16)  # noqa: E731
+    dC = half(rng.standard_normal((M, N)) * 2.0**lift)
+    g = half(rng.standard_normal((M, N)))
+    u = half(rng.standard_normal((M, N)) * 2.0 ** (rng.integers(0, 9, N) if large else rng.integers(-8, 1, N)))
+    A = half(rng.standard_normal((M, K)) * 2.0 ** (-14 if large else 8))
+    if w == "f16":
+        plan = QGated(M, N, K, w)
+        W = [half(rng.standard_normal((N, K)) * 2.0 ** (-14 if large else 7)) for _ in range(2)]
+        packed, W = plan.pack(*[host_to_device(x) for x in W]), [x.astype(np.float64) for x in W]
+    else:
+        plan = QGated(M, N, K, w, 128)
+        p = [synth.make_problem(1, N, K, w, group_size=128, seed=N + i) for i in (0, 1)]
+        for x in p:
+            x.s = np.full_like(x.s, 2.0**-17 if large else 2.0**4)
+        packed = plan.pack(*[host_to_device(x.w) for x in p], *[host_to_device(x.s) for x in p])
+        W = [oracle.dequantize(oracle.unpack_weights(x.w, w, N, K), x.s, None, 128, K).T for x in p]
+    out = plan.backward(host_to_device(A), packed, host_to_device(np.concatenate([g, u], 1)), host_to_device(dC))
+    got = {k: t.cpu().numpy().astype(np.float64) for k, t in out.items() if t is not None}
+
+    h, dh = oracle.activation(g.astype(np.float64), "silu")
+    dG, dU = dC.astype(np.float64) * u * dh, dC.astype(np.float64) * h
+    if M >= 20:  # (a few rows may draw ordinary ones only)
+        assert max(np.abs(dG).max(), np.abs(dU).max()) > 65504 if large else (np.abs(dG).max(1) < 2.0**-14).any()
+
+    def check(x, others, result, what):
+        """x [rows, terms] of the gradients, others [terms, K]: rows of `result`, each term to 2^-12 (and the
+        activation's 2^-17), or half the smallest step of the row's scale."""
+        pick = np.unique(np.linspace(0, x.shape[0] - 1, 120).astype(int)) if x.shape[0] * K > 300000 else np.arange(x.shape[0])
+        x, y = x[pick], result[pick]
+        top = np.abs(x).max(1, keepdims=True)
+        step = np.where((top >= 2.0**-6) & (top <= 65504), 1.0, 2.0 ** (np.floor(np.log2(np.where(top > 0, top, 1))) - 13))
+        ref = x @ others
+        bound = (6 * (2.0**-11 if w != "f16" else 2.0**-12) * np.sqrt(x**2 @ others**2) + 2.0**-17 * (np.abs(x) @ np.abs(others))
+                 + 6 * 2.0**-25 * step * np.sqrt((others**2).sum(0)) + 2.0**-11 * np.abs(ref) + 2.0**-25)
+        assert np.abs(ref).max() < 60000
+        assert_near(y, ref, bound, what)
+
+    check(np.concatenate([dG, dU], 1), np.concatenate(W), got["dA"], "dA")
+    if w == "f16":
+        check(dG.T, A.astype(np.float64), got["dw_gate"], "dw_gate")
+        check(dU.T, A.astype(np.float64), got["dw_up"], "dw_up")
+
+
+def test_gradients_of_rows_without_any():
+    """Rows of zero gradients among tiny, infinite and ordinary ones: each row is its own."""
+    rng = np.random.default_rng(8)
+    M, N, K = 6, 40, 72
+    plan = QGated(M, N, K, "f16")
+    W = [host_to_device((rng.standard_normal((N, K)) / 8).astype(np.float16)) for _ in range(2)]
+    packed, A = plan.pack(*W), host_to_device(rng.standard_normal((M, K)).astype(np.float16))
+    pre = host_to_device(rng.standard_normal((M, 2 * N)).astype(np.float16))
+    dC = rng.standard_normal((M, N)).astype(np.float16)
+    dC[1], dC[2], dC[4] = 0, dC[2] * np.float16(2.0**-14), np.float16(20000)
+    out = plan.backward(A, packed, pre, host_to_device(dC), weight_grads=False)["dA"]
+    bad = dC.copy()
+    bad[3, 5] = np.inf
+    with_inf = plan.backward(A, packed, pre, host_to_device(bad), weight_grads=False)["dA"]
+    assert (out[1] == 0).all() and torch.isfinite(out).all()
+    keep = [0, 1, 2, 4, 5]
+    assert torch.equal(with_inf[keep], out[keep]) and not torch.isfinite(with_inf[3]).any()

@@ -610,6 +610,7 @@ struct GateBackward {
   int64_t kd, mp;   // reduction lengths, whole granules of the fp16 format
   bool direct;      // to_a reads the forward's fp16 blob transposed (256 x 256 tiles), without a copy of it
   size_t rowwise, colwise, bias, blob, split, bytes;
+  size_t row_scale, row_top, col_scale, col_top;  // of the gradients' rows and columns
 
   qgemm_status init(const qgemm_plan* p, int64_t M, bool weight_grads) {
     if (!p->gate_n || M < 1 || M > p->M) return QGEMM_ERR_INVALID_ARG;
@@ -652,6 +653,10 @@ struct GateBackward {
     rowwise = place((size_t)M * kd * 2);
     colwise = place(weight_grads ? (size_t)2 * p->gate_n * mp * 2 : 0);
     bias = place(weight_grads ? (size_t)gate_grad_row_tiles(M) * 2 * p->gate_n * 4 : 0);
+    row_scale = place((size_t)M * 4);
+    row_top = place((size_t)M * gate_grad_col_tiles(p->gate_n) * 4);
+    col_scale = place(weight_grads ? (size_t)2 * p->gate_n * 4 : 0);
+    col_top = place(weight_grads ? (size_t)gate_grad_row_tiles(M) * p->gate_n * 4 : 0);
     // the products run one after the other and share the space of their weights
     const size_t blob_a = direct ? 0 : to_a.L.total, blob_w = weight_grads ? to_w.L.total : 0;
     blob = place(blob_a > blob_w ? blob_a : blob_w);
@@ -664,13 +669,14 @@ struct GateBackward {
     if (!direct) {
       const hipError_t e = launch_transpose_blob(p->L, p->gate_n, packed, to_a.L, ws + blob, st);
       if (e != hipSuccess) return e;
-      const qgemm_status s = run_impl(&to_a, M, ws + rowwise, ws + blob, nullptr, nullptr, nullptr, dA, ws + split,
-                                      to_a.ws_bytes, st);
+      const qgemm_status s = run_impl(&to_a, M, ws + rowwise, ws + blob, nullptr, reinterpret_cast<float*>(ws + row_scale),
+                                      nullptr, dA, ws + split, to_a.ws_bytes, st);
       return s == QGEMM_OK ? hipSuccess : hipErrorLaunchFailure;
     }
     RunArgs a = make_args(&to_a, to_a.ch, M, ws + rowwise, packed, nullptr, dA, ws + split);
     a.NB = (int32_t)p->L.NB;
     a.nkb = (int32_t)p->L.nkb;
+    a.row_scale = reinterpret_cast<const float*>(ws + row_scale);
     const hipError_t e = launch_mfma_big_transposed(a, st);
     return e == hipSuccess && a.out_mode == OUT_PARTIAL ? launch_finalize(a, 1, st) : e;
   }
@@ -864,11 +870,25 @@ qgemm_status qgemm_gated_backward(const qgemm_plan* plan, int64_t M, const void*
   (void)hipGetLastError();
   char* ws = static_cast<char*>(workspace);
   const int64_t N = plan->gate_n;
-  hipError_t e = launch_gate_grad(preact, dC, M, N, b.kd, b.mp, plan->act_c0, plan->act_c1, dA ? ws + b.rowwise : nullptr,
-                                  weight_grads ? ws + b.colwise : nullptr,
-                                  dbias_gate || dbias_up ? reinterpret_cast<float*>(ws + b.bias) : nullptr, st);
-  if (e == hipSuccess && (dbias_gate || dbias_up))
-    e = launch_bias_grad(reinterpret_cast<float*>(ws + b.bias), M, N, dbias_gate, dbias_up, st);
+  GateGradArgs ga;
+  ga.preact = static_cast<const _Float16*>(preact);
+  ga.dC = static_cast<const _Float16*>(dC);
+  ga.rowwise = dA ? reinterpret_cast<_Float16*>(ws + b.rowwise) : nullptr;
+  ga.colwise = weight_grads ? reinterpret_cast<_Float16*>(ws + b.colwise) : nullptr;
+  ga.row_scale = reinterpret_cast<float*>(ws + b.row_scale);
+  ga.col_scale = reinterpret_cast<float*>(ws + b.col_scale);
+  ga.row_top = reinterpret_cast<float*>(ws + b.row_top);
+  ga.col_top = reinterpret_cast<uint32_t*>(ws + b.col_top);
+  ga.dbias_gate = static_cast<_Float16*>(dbias_gate);
+  ga.dbias_up = static_cast<_Float16*>(dbias_up);
+  ga.bias_part = dbias_gate || dbias_up ? reinterpret_cast<float*>(ws + b.bias) : nullptr;
+  ga.mp = b.mp;
+  ga.M = (int32_t)M;
+  ga.N = (int32_t)N;
+  ga.kd = (int32_t)b.kd;
+  ga.c0 = plan->act_c0;
+  ga.c1 = plan->act_c1;
+  hipError_t e = launch_gate_grad(ga, st);
   if (e == hipSuccess && dA) e = b.run_to_a(plan, M, packed, dA, ws, st);
   if (e == hipSuccess && dw_gate) {
     e = launch_transpose_rows(A, M, plan->K, b.to_w.L, ws + b.blob, st);
@@ -876,7 +896,8 @@ qgemm_status qgemm_gated_backward(const qgemm_plan* plan, int64_t M, const void*
     const bool joined = dw_up == static_cast<char*>(dw_gate) + (size_t)N * plan->K * 2;
     for (int part = 0; e == hipSuccess && part < (joined ? 1 : 2); ++part)
       if (run_impl(&b.to_w, joined ? 2 * N : N, ws + b.colwise + (size_t)part * N * b.mp * 2, ws + b.blob, nullptr,
-                   nullptr, nullptr, part ? dw_up : dw_gate, ws + b.split, b.to_w.ws_bytes, stream) != QGEMM_OK)
+                   reinterpret_cast<float*>(ws + b.col_scale) + part * N, nullptr, part ? dw_up : dw_gate, ws + b.split,
+                   b.to_w.ws_bytes, stream) != QGEMM_OK)
         return QGEMM_ERR_DEVICE;
   }
   return e == hipSuccess ? QGEMM_OK : QGEMM_ERR_DEVICE;

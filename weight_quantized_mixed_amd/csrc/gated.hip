@@ -6,11 +6,14 @@
 // reduction), so this file holds the passes that bring their operands into that form:
 // the gradients of the pre-activations, once per row (operand of dA) and once per
 // column (operand of dW), and the transposed weights and activations in the packed
-// superblocks of the fp16 format.  All of them read and write each value once and are
+// superblocks of the fp16 format.  The gradients of the pre-activations are rounded to fp16
+// for that, the operand type of the matrix cores at their full rate (split into two halves they
+// would double the products), each sum's terms at a common scale where fp16's range asks for
+// one.  All of the passes read and write each value once and are
 // bound by HBM; the transposes go through LDS so that both sides are contiguous (N = 11008,
-// K = 4096: gradients of the pre-activations both ways at M = 2048 57 us for 315 MB, row by
-// row at M = 1024 24 us for 113 MB; the transposed int4 weights 47 us for 225 MB; X of 2048
-// rows 7 us).
+// K = 4096: gradients of the pre-activations both ways at M = 2048 60 us for 318 MB and 5 us to
+// check their range, row by row at M = 1024 25 us for 113 MB and 5 us; the transposed int4
+// weights 48 us for 225 MB; X of 2048 rows 8 us).
 //
 // dA runs as one product over the inner columns of the gated plan (gate and up blocks of
 // 16 alternate), so its weight operand is the transpose of the forward's blob, whatever
@@ -37,27 +40,80 @@ __device__ __forceinline__ float kept(_Float16 h) {
 constexpr int GT = 64;
 constexpr int GPITCH = GT + 8;  // halves per LDS row (16-byte aligned rows, banks shifted by 4)
 
+// A sum's terms (a row of dG and dU for dA, a column of one of them for dW) are fp16 operands,
+// 11 bits of any term from 2^-14 on.  Where the largest term is past fp16 or below 2^-6
+// (from there up, 22016 terms lose below 2^-25 what the rounding of the largest alone loses),
+// all of them are taken times 2^-e, which brings the largest to 2^13 .. 2^14, and the
+// product's fp32 sum times 2^e.  Ordinary rows and columns have e = 0.
+// top: the largest term, cut to the upper half of its bits (65280 then stands for all up to
+// 65536).
+constexpr float TOP_MOST = 65280.f, TOP_LEAST = 0x1p-6f;
+__device__ __forceinline__ int range_shift(float top) {
+  if (!(top > 0.f) || top == INFINITY || (top >= TOP_LEAST && top < TOP_MOST)) return 0;
+  return max(ilogbf(top) - 13, -64);
+}
+// two magnitudes' upper halves in a word, and their maxima (the bits order like the values)
+__device__ __forceinline__ uint32_t upper_halves(float lo, float hi) {
+  return __float_as_uint(hi) & 0xFFFF0000u | __float_as_uint(lo) >> 16;
+}
+__device__ __forceinline__ uint32_t larger_halves(uint32_t x, uint32_t y) {
+  typedef uint16_t ushort2v __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(ushort2v, x), __builtin_bit_cast(ushort2v, y)));
+}
+
+// dG and dU of V outputs in fp32
+template <int V>
+struct GateGrads {
+  float g[V], u[V];
+};
+template <int V, typename VEC>
+__device__ __forceinline__ GateGrads<V> gate_grads(const GateGradArgs& a, const VEC& g, const VEC& u, const VEC& d) {
+  GateGrads<V> r;
+#pragma unroll
+  for (int e = 0; e < V; ++e) {
+    const float x = kept(g[e]), dc = (float)d[e];
+    const float sg = gate_sigmoid(a.c0, a.c1, x);
+    // act'(x) = sg + x sg (1 - sg) t'(x)
+    r.g[e] = dc * kept(u[e]) * (sg + x * sg * (1.f - sg) * (a.c0 + 3.f * a.c1 * x * x));
+    r.u[e] = dc * x * sg;
+  }
+  return r;
+}
+
+// [gate, up][column][row] of a tile; the threads' shares of the columns' maxima (both
+// projections' in a word) or of their sums
+template <int V>
+union GradTile {
+  _Float16 t[2][GT][GPITCH];
+  uint32_t top[256 / (GT / V)][GT];
+  float sum[256 / (GT / V)][2][GT];
+};
+
+// an LDS tile to its places in colwise
+template <int V>
+__device__ __forceinline__ void store_columns(const GateGradArgs& a, const GradTile<V>& lds, int m0, int n0) {
+  for (int i = threadIdx.x; i < 2 * GT * (GT / 8); i += 256) {
+    const int p = i / (GT * GT / 8), c = (i / (GT / 8)) % GT, m = (i % (GT / 8)) * 8, n = n0 + c;
+    if (n < a.N)
+      *reinterpret_cast<half8v*>(a.colwise + ((size_t)p * a.N + n) * a.mp + m0 + m) =
+          *reinterpret_cast<const half8v*>(&lds.t[p][c][m]);
+  }
+}
+
 // rows [m][2 N] of preact and [m][N] of dC -> rowwise [m][kd] (inner order, zero past the
 // last inner column) and, if colwise is given, [2 N][mp] (gate rows, then up rows; zero
-// for m in [M, mp)) and bias_part [row tile][2 N], the sums over the tile's rows in fp32, of
+// for m in [M, mp)), all unscaled, with the largest magnitudes of the tile's rows and
+// columns, and bias_part [row tile][2 N], the sums over the tile's rows in fp32, of
 // the values before their rounding (rounded, those below 2^-25 would be lost one by one).
 // V: values per access (8 or 2 where N and the pointers allow it).
 template <int V>
-__global__ __launch_bounds__(256) void gate_grad_kernel(const _Float16* __restrict__ preact,
-                                                        const _Float16* __restrict__ dC, int M, int N, int kd,
-                                                        int64_t mp, float c0, float c1,
-                                                        _Float16* __restrict__ rowwise,
-                                                        _Float16* __restrict__ colwise,
-                                                        float* __restrict__ bias_part) {
+__global__ __launch_bounds__(256) void gate_grad_kernel(GateGradArgs a) {
   constexpr int PER_ROW = GT / V, STEPS = GT * PER_ROW / 256, AT_ONCE = STEPS < 4 ? STEPS : 4;
-  __shared__ __attribute__((aligned(16))) union {
-    _Float16 t[2][GT][GPITCH];          // [gate, up][column][row]
-    float sums[256 / PER_ROW][2][GT];   // then the column sums of the threads' rows
-  } lds;
-  auto& t = lds.t;
-  const int m0 = blockIdx.y * GT, n0 = blockIdx.x * GT;
-  float sum[2][V] = {};  // a thread's rows lie in the same V columns
   typedef _Float16 vec __attribute__((ext_vector_type(V)));
+  __shared__ __attribute__((aligned(16))) GradTile<V> lds;
+  const int m0 = blockIdx.y * GT, n0 = blockIdx.x * GT, N = a.N;
+  // a thread's rows lie in the same V columns
+  float sum[2][V] = {}, top[2][V] = {};
 #pragma unroll 1
   for (int s0 = 0; s0 < STEPS; s0 += AT_ONCE) {
     // the loads of a few steps before their first use
@@ -66,73 +122,167 @@ __global__ __launch_bounds__(256) void gate_grad_kernel(const _Float16* __restri
     for (int s = 0; s < AT_ONCE; ++s) {
       const int i = (s0 + s) * 256 + threadIdx.x, m = m0 + i / PER_ROW, n = n0 + (i % PER_ROW) * V;
       g[s] = u[s] = d[s] = vec{};
-      if (m < M && n < N) {  // N is a multiple of V
-        const _Float16* p = preact + (size_t)m * 2 * N + n;
+      if (m < a.M && n < N) {  // N is a multiple of V
+        const _Float16* p = a.preact + (size_t)m * 2 * N + n;
         g[s] = *reinterpret_cast<const vec*>(p);
         u[s] = *reinterpret_cast<const vec*>(p + N);
-        d[s] = *reinterpret_cast<const vec*>(dC + (size_t)m * N + n);
+        d[s] = *reinterpret_cast<const vec*>(a.dC + (size_t)m * N + n);
       }
     }
 #pragma unroll
     for (int s = 0; s < AT_ONCE; ++s) {
       const int i = (s0 + s) * 256 + threadIdx.x, r = i / PER_ROW, m = m0 + r, n = n0 + (i % PER_ROW) * V;
+      const GateGrads<V> x = gate_grads<V>(a, g[s], u[s], d[s]);
       vec dg, du;
+      float most = 0.f;
 #pragma unroll
       for (int e = 0; e < V; ++e) {
-        const float x = kept(g[s][e]), dc = (float)d[s][e];
-        const float sg = gate_sigmoid(c0, c1, x);
-        // act'(x) = sg + x sg (1 - sg) t'(x)
-        const float gx = dc * kept(u[s][e]) * (sg + x * sg * (1.f - sg) * (c0 + 3.f * c1 * x * x)), ux = dc * x * sg;
-        sum[0][e] += gx;
-        sum[1][e] += ux;
-        dg[e] = (_Float16)gx;
-        du[e] = (_Float16)ux;
+        sum[0][e] += x.g[e];
+        sum[1][e] += x.u[e];
+        top[0][e] = fmaxf(top[0][e], fabsf(x.g[e]));
+        top[1][e] = fmaxf(top[1][e], fabsf(x.u[e]));
+        most = fmaxf(most, fmaxf(fabsf(x.g[e]), fabsf(x.u[e])));
+        dg[e] = (_Float16)x.g[e];
+        du[e] = (_Float16)x.u[e];
       }
-      if (rowwise && m < M) {
-        const int c = (n >> 4) * 32 + (n & 15);
-        _Float16* o = rowwise + (size_t)m * kd + c;
-        if (c < kd) *reinterpret_cast<vec*>(o) = dg;
-        if (c + 16 < kd) *reinterpret_cast<vec*>(o + 16) = du;
+      if (a.rowwise) {
+        if (m < a.M) {
+          const int c = (n >> 4) * 32 + (n & 15);
+          _Float16* o = a.rowwise + (size_t)m * a.kd + c;
+          if (c < a.kd) *reinterpret_cast<vec*>(o) = dg;
+          if (c + 16 < a.kd) *reinterpret_cast<vec*>(o + 16) = du;
+        }
+#pragma unroll
+        for (int o = PER_ROW / 2; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor(most, o, 64));
+        if (i % PER_ROW == 0 && m < a.M) a.row_top[(size_t)m * gridDim.x + blockIdx.x] = most;
       }
-      if (colwise) {
+      if (a.colwise) {
 #pragma unroll
         for (int e = 0; e < V; ++e) {
-          t[0][n - n0 + e][r] = dg[e];
-          t[1][n - n0 + e][r] = du[e];
+          lds.t[0][n - n0 + e][r] = dg[e];
+          lds.t[1][n - n0 + e][r] = du[e];
         }
       }
     }
   }
-  if (!colwise) return;
+  if (!a.colwise) return;
   __syncthreads();
-  for (int i = threadIdx.x; i < 2 * GT * (GT / 8); i += 256) {
-    const int p = i / (GT * GT / 8), c = (i / (GT / 8)) % GT, m = (i % (GT / 8)) * 8, n = n0 + c;
-    if (n < N) *reinterpret_cast<half8v*>(colwise + ((size_t)p * N + n) * mp + m0 + m) = *reinterpret_cast<half8v*>(&t[p][c][m]);
+  store_columns<V>(a, lds, m0, n0);
+  // over the threads of a column, in order
+  const int own_row = threadIdx.x / PER_ROW, own_col = threadIdx.x % PER_ROW * V;
+  __syncthreads();
+#pragma unroll
+  for (int e = 0; e < V; ++e) lds.top[own_row][own_col + e] = upper_halves(top[0][e], top[1][e]);
+  __syncthreads();
+  if (threadIdx.x < GT && n0 + (int)threadIdx.x < N) {
+    uint32_t x = 0;
+#pragma unroll 8
+    for (int r = 0; r < 256 / PER_ROW; ++r) x = larger_halves(x, lds.top[r][threadIdx.x]);
+    a.col_top[(size_t)blockIdx.y * N + n0 + threadIdx.x] = x;
   }
-  if (!bias_part) return;
+  if (!a.bias_part) return;
   __syncthreads();
 #pragma unroll
   for (int p = 0; p < 2; ++p)
 #pragma unroll
-    for (int e = 0; e < V; ++e) lds.sums[threadIdx.x / PER_ROW][p][threadIdx.x % PER_ROW * V + e] = sum[p][e];
+    for (int e = 0; e < V; ++e) lds.sum[own_row][p][own_col + e] = sum[p][e];
   __syncthreads();
-  if (threadIdx.x < 2 * GT) {
-    const int p = threadIdx.x / GT, c = threadIdx.x % GT;
-    float s = 0.f;
-    for (int r = 0; r < 256 / PER_ROW; ++r) s += lds.sums[r][p][c];
-    if (n0 + c < N) bias_part[(size_t)blockIdx.y * 2 * N + (size_t)p * N + n0 + c] = s;
+  const int p = threadIdx.x / GT, c = threadIdx.x % GT;
+  if (p < 2 && n0 + c < N) {
+    float x = 0.f;
+    for (int r = 0; r < 256 / PER_ROW; ++r) x += lds.sum[r][p][c];
+    a.bias_part[(size_t)blockIdx.y * 2 * N + (size_t)p * N + n0 + c] = x;
   }
 }
 
-// column sums of the tiles' sums, in tile order
-__global__ void bias_grad_kernel(const float* __restrict__ part, int tiles, int N, _Float16* __restrict__ dbg,
-                                 _Float16* __restrict__ dbu) {
-  const int n = blockIdx.x * blockDim.x + threadIdx.x;
-  if (n >= 2 * N) return;
-  float s = 0.f;
-  for (int t = 0; t < tiles; ++t) s += part[(size_t)t * 2 * N + n];
-  _Float16* out = n < N ? dbg : dbu;
-  if (out) out[n < N ? n : n - N] = (_Float16)s;
+// What is left when every tile is done: the scales of rows and columns from their tiles'
+// largest magnitudes, the rows and columns whose scale is not 1 over again, scaled, and the
+// bias gradients, the tiles' sums in tile order.  The first row_blocks workgroups take a row a
+// wave, the next col_blocks a strip of 64 columns, the others 256 bias gradients.  Ordinary
+// gradients leave it at reading the magnitudes, one or two in 64 of the values.
+template <int V>
+__global__ __launch_bounds__(256) void gate_grad_range_kernel(GateGradArgs a, int row_blocks, int col_blocks, int col_tiles,
+                                                              int row_tiles) {
+  constexpr int PER_ROW = GT / V;
+  typedef _Float16 vec __attribute__((ext_vector_type(V)));
+  __shared__ __attribute__((aligned(16))) GradTile<V> lds;
+  __shared__ float factor[2][GT];
+  const int N = a.N;
+  if ((int)blockIdx.x < row_blocks) {
+    const int lane = threadIdx.x & 63, m = blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (m >= a.M) return;
+    float top = 0.f;
+    for (int i = lane; i < col_tiles; i += 64) top = fmaxf(top, a.row_top[(size_t)m * col_tiles + i]);
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
+    const int e = range_shift(__uint_as_float(__float_as_uint(top) & 0xFFFF0000u));
+    if (lane == 0) a.row_scale[m] = ldexpf(1.f, e);
+    if (e == 0) return;
+    const float f = ldexpf(1.f, -e);
+    for (int n = lane * V; n < N; n += 64 * V) {
+      const _Float16* p = a.preact + (size_t)m * 2 * N + n;
+      const GateGrads<V> x = gate_grads<V>(a, *reinterpret_cast<const vec*>(p), *reinterpret_cast<const vec*>(p + N),
+                                           *reinterpret_cast<const vec*>(a.dC + (size_t)m * N + n));
+      vec dg, du;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        dg[i] = (_Float16)(x.g[i] * f);
+        du[i] = (_Float16)(x.u[i] * f);
+      }
+      _Float16* o = a.rowwise + (size_t)m * a.kd + (n >> 4) * 32 + (n & 15);
+      *reinterpret_cast<vec*>(o) = dg;
+      *reinterpret_cast<vec*>(o + 16) = du;
+    }
+    return;
+  }
+  if ((int)blockIdx.x >= row_blocks + col_blocks) {
+    const int n = ((int)blockIdx.x - row_blocks - col_blocks) * 256 + threadIdx.x;
+    _Float16* out = n < N ? a.dbias_gate : a.dbias_up;
+    if (n >= 2 * N || !out) return;
+    float s = 0.f;
+#pragma unroll 8
+    for (int t = 0; t < row_tiles; ++t) s += a.bias_part[(size_t)t * 2 * N + n];
+    out[n < N ? n : n - N] = (_Float16)s;
+    return;
+  }
+  const int n0 = ((int)blockIdx.x - row_blocks) * GT, n = n0 + threadIdx.x % GT;
+  uint32_t top = 0;  // a quarter of the tiles a wave
+  if (n < N) {
+#pragma unroll 8
+    for (int t = threadIdx.x / GT; t < row_tiles; t += 4) top = larger_halves(top, a.col_top[(size_t)t * N + n]);
+  }
+  lds.top[threadIdx.x / GT][threadIdx.x % GT] = top;
+  __syncthreads();
+  int e = 0;
+  if (threadIdx.x < 2 * GT) {
+    const int p = threadIdx.x / GT, c = threadIdx.x % GT;
+    for (int w = 0; w < 4; ++w) top = larger_halves(top, lds.top[w][c]);
+    e = range_shift(__uint_as_float(p ? top & 0xFFFF0000u : top << 16));
+    factor[p][c] = ldexpf(1.f, -e);
+    if (n < N) a.col_scale[(size_t)p * N + n] = ldexpf(1.f, e);
+  }
+  if (!__syncthreads_or(e != 0)) return;
+  for (int m0 = 0; m0 < a.M; m0 += GT) {
+    for (int i = threadIdx.x; i < GT * PER_ROW; i += 256) {
+      const int r = i / PER_ROW, m = m0 + r, n = n0 + (i % PER_ROW) * V;
+      vec g = {}, u = {}, d = {};
+      if (m < a.M && n < N) {
+        const _Float16* p = a.preact + (size_t)m * 2 * N + n;
+        g = *reinterpret_cast<const vec*>(p);
+        u = *reinterpret_cast<const vec*>(p + N);
+        d = *reinterpret_cast<const vec*>(a.dC + (size_t)m * N + n);
+      }
+      const GateGrads<V> x = gate_grads<V>(a, g, u, d);
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        lds.t[0][n - n0 + j][r] = (_Float16)(x.g[j] * factor[0][n - n0 + j]);
+        lds.t[1][n - n0 + j][r] = (_Float16)(x.u[j] * factor[1][n - n0 + j]);
+      }
+    }
+    __syncthreads();
+    store_columns<V>(a, lds, m0, n0);
+    __syncthreads();
+  }
 }
 
 // ---- transposed operands: tiles of 32 reduction positions x 128 columns through LDS
@@ -266,30 +416,25 @@ __global__ __launch_bounds__(256) void transpose_rows_kernel(const _Float16* __r
 
 }  // namespace
 
-hipError_t launch_gate_grad(const void* preact, const void* dC, int64_t M, int64_t N, int64_t kd, int64_t mp, float c0,
-                            float c1, void* rowwise, void* colwise, float* bias_part, hipStream_t st) {
-  // column tiles cover the inner columns' padding of rowwise too (kd / 2 output columns)
-  const int64_t cols = rowwise && kd / 2 > N ? kd / 2 : N;
-  const dim3 grid((unsigned)((cols + GT - 1) / GT), (unsigned)((M + GT - 1) / GT));
-  const uintptr_t at = reinterpret_cast<uintptr_t>(preact) | reinterpret_cast<uintptr_t>(dC);
-  auto go = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, grid, dim3(256), 0, st, static_cast<const _Float16*>(preact),
-                       static_cast<const _Float16*>(dC), (int)M, (int)N, (int)kd, mp, c0, c1,
-                       static_cast<_Float16*>(rowwise), static_cast<_Float16*>(colwise), bias_part);
+hipError_t launch_gate_grad(const GateGradArgs& a, hipStream_t st) {
+  const int64_t cols = gate_grad_col_tiles(a.N), rows = gate_grad_row_tiles(a.M);
+  const int row_blocks = a.rowwise ? (a.M + 3) / 4 : 0, col_blocks = a.colwise ? (a.N + GT - 1) / GT : 0;
+  const int bias_blocks = a.bias_part ? (2 * a.N + 255) / 256 : 0;
+  auto go = [&](auto first, auto second) {
+    hipLaunchKernelGGL(first, dim3((unsigned)cols, (unsigned)rows), dim3(256), 0, st, a);
+    hipLaunchKernelGGL(second, dim3((unsigned)(row_blocks + col_blocks + bias_blocks)), dim3(256), 0, st, a, row_blocks,
+                       col_blocks, (int)cols, (int)rows);
   };
-  if (N % 8 == 0 && (at & 15) == 0) go(gate_grad_kernel<8>);
-  else if (N % 2 == 0 && (at & 3) == 0) go(gate_grad_kernel<2>);
-  else go(gate_grad_kernel<1>);
-  return hipGetLastError();
-}
-
-hipError_t launch_bias_grad(const float* part, int64_t M, int64_t N, void* dbg, void* dbu, hipStream_t st) {
-  hipLaunchKernelGGL(bias_grad_kernel, dim3((unsigned)((2 * N + 255) / 256)), dim3(256), 0, st, part,
-                     (int)((M + GT - 1) / GT), (int)N, static_cast<_Float16*>(dbg), static_cast<_Float16*>(dbu));
+  const uintptr_t at = reinterpret_cast<uintptr_t>(a.preact) | reinterpret_cast<uintptr_t>(a.dC);
+  if (a.N % 8 == 0 && (at & 15) == 0) go(gate_grad_kernel<8>, gate_grad_range_kernel<8>);
+  else if (a.N % 2 == 0 && (at & 3) == 0) go(gate_grad_kernel<2>, gate_grad_range_kernel<2>);
+  else go(gate_grad_kernel<1>, gate_grad_range_kernel<1>);
   return hipGetLastError();
 }
 
 int64_t gate_grad_row_tiles(int64_t M) { return (M + GT - 1) / GT; }
+// the inner columns' padding of rowwise too (whole granules of 64 inner columns, 32 of the output)
+int64_t gate_grad_col_tiles(int64_t N) { return ((gate_inner(N) + 63) / 64 * 32 + GT - 1) / GT; }
 
 hipError_t launch_transpose_blob(const Layout& L, int64_t gate_n, const void* packed, const Layout& to, void* out,
                                  hipStream_t st) {

@@ -583,6 +583,8 @@ __global__ __launch_bounds__(64 * GEMV_MAX_WAVES) void gemv_kernel(RunArgs a) {
     if (col >= a.N) continue;
     const size_t o = (size_t)m * a.N + col;
     if (a.out_mode == OUT_STORE) {
+      if constexpr (FMT == FMT_F16)
+        if (a.row_scale) s *= a.row_scale[m];
       if constexpr (FP) static_cast<_Float16*>(a.C)[o] = (_Float16)(s + bias_f(a, col));
       else if (a.row_scale) static_cast<_Float16*>(a.C)[o] = dq_out(a, m, col, s);
       else static_cast<int*>(a.C)[o] = s + bias_i(a, col);

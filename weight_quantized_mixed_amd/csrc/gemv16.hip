@@ -166,6 +166,8 @@ __global__ __launch_bounds__(64 * GEMV_MAX_WAVES) void gemv16_kernel(RunArgs a) 
       for (int q = 0; q < 4; ++q) s += red[w][q * 16 + threadIdx.x];
     if (col < a.N) {
       if (a.out_mode == OUT_STORE) {
+        if constexpr (FMT == FMT_F16)
+          if (a.row_scale) s *= a.row_scale[0];
         if constexpr (FP) static_cast<_Float16*>(a.C)[col] = (_Float16)(s + bias_f(a, col));
         else if (a.row_scale) static_cast<_Float16*>(a.C)[col] = dq_out(a, 0, col, s);
         else static_cast<int*>(a.C)[col] = s + bias_i(a, col);

@@ -253,6 +253,7 @@ __global__ __launch_bounds__(64 * GEMV_MAX_WAVES) void gemv_mfma_kernel(RunArgs 
     for (int w = 0; w < a.waves; ++w) s += red[w][r][cb][i][ln];
     const size_t o = (size_t)row * a.N + col;
     if constexpr (FP) {
+      if (a.out_mode == OUT_STORE && a.row_scale) s *= a.row_scale[row];
       if (a.out_mode == OUT_STORE) static_cast<_Float16*>(a.C)[o] = (_Float16)(s + bias_f(a, col));
       else if (a.out_mode == OUT_ATOMIC) unsafeAtomicAdd(static_cast<float*>(a.ws) + o, s);
       else static_cast<float*>(a.ws)[(size_t)part * a.M * a.N + o] = s;

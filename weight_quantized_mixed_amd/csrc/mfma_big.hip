@@ -95,7 +95,8 @@ struct BigGeo {
 // each fragment is two transposed LDS reads (lane i of 16: position i of four columns).  A
 // superblock's pieces (16 bytes: 8 positions of a column) of its odd position groups lie
 // with their columns' bit 2 flipped, which spreads the reads of half a wave over all banks.
-template <int FMT, bool SCALED, bool FOLD, bool GATED, bool TRANS = false>
+// ROWS (fp16): the sums of a row times a.row_scale[row], as in the gradient products.
+template <int FMT, bool SCALED, bool FOLD, bool GATED, bool TRANS = false, bool ROWS = TRANS>
 __global__ __launch_bounds__(256) void mfma_big_kernel(RunArgs a) {
   using G = BigGeo<FMT, SCALED>;
   constexpr bool FP = G::FP, PACKED = G::PACKED;
@@ -597,6 +598,17 @@ __global__ __launch_bounds__(256) void mfma_big_kernel(RunArgs a) {
     if constexpr (FP) {
       __syncthreads();  // every wave is done with the ring
       const int col0 = n0 + wn * 128;
+      if constexpr (ROWS) {  // (these products have no bias)
+        float rs[8][4];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) rs[i][r] = a.row_scale[min(m0 + wm * 128 + i * 16 + q * 4 + r, a.M - 1)];
+        rows_out(C8{}, [&](int i, int c, int r) { return (_Float16)(acc[i][c][r] * rs[i][r]); },
+                 static_cast<_Float16*>(a.C) + (size_t)(m0 + wm * 128) * a.N + col0, (size_t)a.N, a.N - col0,
+                 row_width(a.N, a.C, nullptr));
+        return;
+      }
       rows_out(C8{}, [&](int i, int c, int r) { return (_Float16)(acc[i][c][r] * es[c] + bf[c]); },
                static_cast<_Float16*>(a.C) + (size_t)(m0 + wm * 128) * a.N + col0, (size_t)a.N, a.N - col0,
                row_width(a.N, a.C, nullptr));
@@ -621,6 +633,11 @@ template <int FMT, bool SCALED, bool FOLD>
 hipError_t launch_big_t(const RunArgs& a, hipStream_t st) {
   const int tiles = ((a.M + 255) / 256) * ((a.N + 255) / 256);
   const dim3 grid(tiles * a.k_parts), block(256);
+  if constexpr (FMT == FMT_F16)
+    if (a.row_scale) {
+      hipLaunchKernelGGL((mfma_big_kernel<FMT, SCALED, FOLD, false, false, true>), grid, block, 0, st, a);
+      return hipGetLastError();
+    }
   if (a.out_mode == OUT_GATE) hipLaunchKernelGGL((mfma_big_kernel<FMT, SCALED, FOLD, true>), grid, block, 0, st, a);
   else hipLaunchKernelGGL((mfma_big_kernel<FMT, SCALED, FOLD, false>), grid, block, 0, st, a);
   return hipGetLastError();

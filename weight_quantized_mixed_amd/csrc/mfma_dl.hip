@@ -71,6 +71,7 @@ hipError_t launch_mfma_dl(int fmt, int tile, const RunArgs& a0, hipStream_t st) 
   // at 16384^3: fp16 6.66 -> 6.41 ms, int4 6.34 -> 5.82 ms); the others keep
   // eight waves of 128 x 64, which measured faster for them
   if (tile == DL_256x256 && QG_BIG4 && big_tile_takes(fmt, a)) return launch_mfma_big(fmt, a, st);
+  if (fmt == FMT_F16 && a.row_scale) return launch_mfma_dl_rows(tile, a, st);
   return a.out_mode == OUT_GATE ? launch_mfma_dl_gated(fmt, tile, a, st) : launch_any_tile<false>(fmt, tile, a, st);
 }
 

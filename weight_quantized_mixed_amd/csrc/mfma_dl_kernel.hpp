@@ -147,7 +147,8 @@ __device__ __forceinline__ void wait_loads(int n) {
   }
 }
 
-template <int FMT, class G, bool SCALED, bool ZEROS, bool GATED>
+// ROWS: the sums of a row times a.row_scale[row] (fp16 weights)
+template <int FMT, class G, bool SCALED, bool ZEROS, bool GATED, bool ROWS>
 __global__ __launch_bounds__(G::NWT * 64) void mfma_dl_kernel(RunArgs a) {
   constexpr bool FP = G::FP, PACKED = G::PACKED;
   constexpr bool I4 = (FMT == FMT_I4 || FMT == FMT_U4);
@@ -183,6 +184,18 @@ __global__ __launch_bounds__(G::NWT * 64) void mfma_dl_kernel(RunArgs a) {
   const int gsz = min(tiles_m - first_m, GROUP_M);
   const int in_group = w - group * GROUP_M * tiles_n;
   const int m0 = (first_m + in_group % gsz) * BM, n0 = (in_group / gsz) * BN;
+
+  // the rows' scales, on their way while the products run
+  float rsv[WTM][4];
+  if constexpr (ROWS) {
+#pragma unroll
+    for (int i = 0; i < WTM; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int row = m0 + (wm * WTM + i) * 16 + q * 4 + r;
+        rsv[i][r] = a.out_mode == OUT_STORE && row < a.M ? a.row_scale[row] : 1.f;
+      }
+  }
 
   // ---- stages of this k-part
   // stages per split unit (a unit is a whole number of stages)
@@ -752,6 +765,7 @@ __global__ __launch_bounds__(G::NWT * 64) void mfma_dl_kernel(RunArgs a) {
         const size_t o = (size_t)row * a.N + col;
         auto v = acc[i][j][r];
         if constexpr (FP) v *= es;
+        if constexpr (ROWS) v *= rsv[i][r];
         if (a.out_mode == OUT_STORE) {
           if constexpr (FP) static_cast<_Float16*>(a.C)[o] = (_Float16)(v + bf);
           else if (a.row_scale)  // as dq_out, with the column values above
@@ -845,13 +859,13 @@ QG_DL_TILE(DL_256x256, 256, 256, 256x256)
 QG_DL_TILE(DL_128x128, 128, 128, 128x128)
 #undef QG_DL_TILE
 
-template <int FMT, int T, bool SCALED, bool ZEROS, bool GATED>
+template <int FMT, int T, bool SCALED, bool ZEROS, bool GATED, bool ROWS = false>
 hipError_t launch_t(const RunArgs& a, hipStream_t st) {
   using G = typename TileGeo<FMT, SCALED, T>::type;
   static_assert((size_t)G::STAGE * G::NSTAGE <= 160 * 1024, "LDS budget");
   const int tiles = ((a.M + G::BM - 1) / G::BM) * ((a.N + G::BN - 1) / G::BN);
-  hipLaunchKernelGGL((mfma_dl_kernel<FMT, G, SCALED, ZEROS, GATED>), dim3(tiles * a.k_parts), dim3(G::NWT * 64), 0, st,
-                     a);
+  hipLaunchKernelGGL((mfma_dl_kernel<FMT, G, SCALED, ZEROS, GATED, ROWS>), dim3(tiles * a.k_parts), dim3(G::NWT * 64), 0,
+                     st, a);
   return hipGetLastError();
 }
 

@@ -113,7 +113,8 @@ struct RunArgs {
   int32_t gemv_cb;      // matrix-core GEMV: 16-column blocks per workgroup (1, 2 or 4)
   const void* bias;     // [N] of the output type, or null
   // int8 activations with fp16 output: C = fp16(acc * row_scale[m] * col_scale[n]
-  // (+ bias)); null for int32 output
+  // (+ bias)); null for int32 output.  fp16 weights: C = fp16(acc * row_scale[m] (+ bias))
+  // where row_scale is given (the gradient products)
   const float* row_scale;
   const float* col_scale;
   // int4 / uint4 with one scale group over K and no zero points on the matrix-core
@@ -255,6 +256,7 @@ void dl_tile_dims(int tile, int* bm, int* bn);
 int choose_dl_tile(int fmt, int64_t M, int64_t N, int k_parts, int smode, bool gated);
 hipError_t launch_mfma_dl(int fmt, int tile, const RunArgs& a, hipStream_t st);
 hipError_t launch_mfma_dl_gated(int fmt, int tile, const RunArgs& a, hipStream_t st);
+hipError_t launch_mfma_dl_rows(int tile, const RunArgs& a, hipStream_t st);  // fp16 weights with a.row_scale
 // 256 x 256 tiles of four 128 x 128 waves (mfma_big.hip) for the formats that
 // big_tile_takes; same arguments and stage layout as launch_mfma_dl's 256 x 256 tile
 bool big_tile_takes(int fmt, const RunArgs& a);
@@ -286,13 +288,24 @@ hipError_t launch_finalize(const RunArgs& a, int acc_fp, hipStream_t st);
 // the same for a gated plan: sums the parts of both projections and writes C
 hipError_t launch_finalize_gate(const RunArgs& a, int acc_fp, hipStream_t st);
 
-// passes of the gated backward (gated.hip): gradients of the pre-activations, row by row
-// (inner column order, rows of kd values) and, if colwise is given, column by column
-// (rows of mp values), with the row tiles' column sums for the bias gradients
-hipError_t launch_gate_grad(const void* preact, const void* dC, int64_t M, int64_t N, int64_t kd, int64_t mp, float c0,
-                            float c1, void* rowwise, void* colwise, float* bias_part, hipStream_t st);
+// Passes of the gated backward (gated.hip): gradients of the pre-activations of M rows and
+// N columns, row by row (inner column order, rows of kd values, times 1 / row_scale) if
+// rowwise is given, and column by column (gate, then up: 2 N rows of mp values, times 1 /
+// col_scale) if colwise is, with the bias gradients (each may be null) if bias_part is.
+// row_top, col_top and bias_part are scratch: [M][gate_grad_col_tiles(N)],
+// [gate_grad_row_tiles(M)][N] and [gate_grad_row_tiles(M)][2 N].
+struct GateGradArgs {
+  const _Float16 *preact, *dC;
+  _Float16 *rowwise, *colwise, *dbias_gate, *dbias_up;
+  float *row_scale, *col_scale, *row_top, *bias_part;
+  uint32_t* col_top;
+  int64_t mp;
+  int32_t M, N, kd;
+  float c0, c1;  // the activation's
+};
+hipError_t launch_gate_grad(const GateGradArgs& a, hipStream_t st);
 int64_t gate_grad_row_tiles(int64_t M);
-hipError_t launch_bias_grad(const float* part, int64_t M, int64_t N, void* dbg, void* dbu, hipStream_t st);
+int64_t gate_grad_col_tiles(int64_t N);
 // the transposed weights of a gated plan, and transposed fp16 rows, as fp16 blobs of layout `to`
 hipError_t launch_transpose_blob(const Layout& L, int64_t gate_n, const void* packed, const Layout& to, void* out,
                                  hipStream_t st);

@@ -43,6 +43,21 @@ __global__ void finalize_kernel(const void* __restrict__ ws, void* __restrict__ 
   }
 }
 
+// The same for fp16 weights with a scale per row, one row a workgroup (1024 columns of it)
+__global__ __launch_bounds__(256) void finalize_rows_kernel(const float* __restrict__ ws, _Float16* __restrict__ C, int N,
+                                                            size_t mn, int parts, const float* __restrict__ row_scale) {
+  const int blocks = (N + 1023) / 1024, row = blockIdx.x / blocks, c0 = (blockIdx.x - row * blocks) * 1024 + threadIdx.x;
+  const float f = row_scale[row];
+  const size_t o = (size_t)row * N;
+  float s[4] = {};
+  for (int p = 0; p < parts; ++p)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) s[k] += ws[(size_t)p * mn + o + min(c0 + k * 256, N - 1)];
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    if (c0 + k * 256 < N) C[o + c0 + k * 256] = (_Float16)(s[k] * f);
+}
+
 // The same for a gated plan: output (m, n) from the parts' sums of its gate and up
 // columns (inner columns 32 (n / 16) + n % 16, and 16 further), rows of a.N inner sums.
 template <typename T>
@@ -242,7 +257,10 @@ hipError_t launch_zero_planes(const RunArgs& a, uint16_t* zp, hipStream_t st) {
 hipError_t launch_finalize(const RunArgs& a, int acc_fp, hipStream_t st) {
   const size_t mn = (size_t)a.M * a.N;
   const int parts = a.out_mode == OUT_PARTIAL ? a.k_parts : 1;
-  if (acc_fp)
+  if (acc_fp && a.row_scale)
+    hipLaunchKernelGGL(finalize_rows_kernel, dim3((unsigned)a.M * (unsigned)((a.N + 1023) / 1024)), dim3(256), 0, st,
+                       static_cast<const float*>(a.ws), static_cast<_Float16*>(a.C), a.N, mn, parts, a.row_scale);
+  else if (acc_fp)
     hipLaunchKernelGGL(finalize_kernel<true>, dim3(grid_for(mn, 256)), dim3(256), 0, st, a.ws, a.C, mn, parts, a);
   else
     hipLaunchKernelGGL(finalize_kernel<false>, dim3(grid_for(mn, 256)), dim3(256), 0, st, a.ws, a.C, mn, parts, a);
