@@ -844,12 +844,12 @@ hipError_t launch_dim(const AttnArgs& a, const AttnSplit& p, hipStream_t st) {
 
 bool attention_grid_fits(const AttnShape& s) {
   const int64_t G = s.q_heads / s.kv_heads, tiles = div_up(s.max_q * G, 16), all = div_up(s.T * G, 16);
-  if ((s.B * tiles + all) * s.kv_heads * 64 >= INT32_MAX || s.T * G >= INT32_MAX / 2 ||
-      s.max_q * s.q_heads >= INT32_MAX)
-    return false;
+  const int64_t most = (s.B * tiles + all) * s.kv_heads * 64;  // items, with every part that there can be
+  if (most >= INT32_MAX || s.T * G >= INT32_MAX / 2 || s.max_q * s.q_heads >= INT32_MAX) return false;
   // a launch holds fewer than 2^32 threads along a dimension, 256 a workgroup here
-  const AttnSplit p = choose_split(s);
   constexpr int64_t MOST = (int64_t)1 << 24;
+  if (most < MOST) return true;
+  const AttnSplit p = choose_split(s);
   return (int64_t)p.p_items + p.s_items < MOST && (!p.slots || div_up(s.max_q * s.q_heads, 4) < MOST);
 }
 

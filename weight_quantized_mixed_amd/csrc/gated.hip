@@ -54,7 +54,7 @@ __device__ __forceinline__ int range_shift(float top) {
 }
 // two magnitudes' upper halves in a word, and their maxima (the bits order like the values)
 __device__ __forceinline__ uint32_t upper_halves(float lo, float hi) {
-  return __float_as_uint(hi) & 0xFFFF0000u | __float_as_uint(lo) >> 16;
+  return (__float_as_uint(hi) & 0xFFFF0000u) | (__float_as_uint(lo) >> 16);
 }
 __device__ __forceinline__ uint32_t larger_halves(uint32_t x, uint32_t y) {
   typedef uint16_t ushort2v __attribute__((ext_vector_type(2)));

@@ -97,14 +97,16 @@ class _Workspace:
     def __init__(self, device):
         self.device, self.buffers, self.streams = device, [], set()
 
-    def of(self, need, stream=None):
+    def of(self, need, stream=None, at=None):
+        """A buffer of `need` bytes for work on `stream` (None: the current one), whose handle `at` the caller may know."""
         if not need:
             return None
         if not self.buffers or self.buffers[-1].numel() < need:
             grown = max(need, 2 * self.buffers[-1].numel()) if self.buffers else need
             self.buffers.append(_empty(grown, torch.uint8, self.device, stream))
             self.streams = set()
-        at = _stream(stream)
+        if at is None:
+            at = _stream(stream)
         if at not in self.streams:  # freed with its object, the buffer waits for every stream that used it
             self.buffers[-1].record_stream(torch.cuda.current_stream() if stream is None else stream)
             self.streams.add(at)
@@ -368,10 +370,11 @@ class PagedKV:
         _check(lse, "lse", (T, q_heads), torch.float32)
         need = _attention_workspace(self.n_pages, self.page_size, self.kv_heads, D, T, q_heads, B, max_q, max_len,
                                     prefix_len)
+        at = _stream(stream)
         if ws is None:
-            ws = self._workspace.of(need, stream)
+            ws = self._workspace.of(need, stream, at)
         _q.qgemm_attention(self.desc, T, q_heads, qp, qs, B, _ptr(q_starts), _ptr(kv_lens), _ptr(tables), width,
                            _ptr(prefix_table) if prefix_len else 0, prefix_len, max_q, max_len,
                            D ** -0.5 if scale is None else scale, _ptr(out), _ptr(lse), _ptr(ws),
-                           0 if ws is None else ws.numel(), _stream(stream))
+                           0 if ws is None else ws.numel(), at)
         return out
