@@ -440,3 +440,90 @@ def test_gradients_of_rows_without_any():
     assert (out[1] == 0).all() and torch.isfinite(out).all()
     keep = [0, 1, 2, 4, 5]
     assert torch.equal(with_inf[keep], out[keep]) and not torch.isfinite(with_inf[3]).any()
+
+
+@pytest.mark.parametrize("M,N,K,w,g,zeros", [(300, 130, 480, "u4", 32, True), (257, 77, 320, "i4", 64, False), (129, 64, 96, "i4", 96, False),
+                                             (700, 200, 416, "u4", 32, False)])
+def test_expanded_weights_keep_the_preactivations(M, N, K, w, g, zeros):
+    """Groups that are not whole superblocks above 128 rows: the pre-activations kept by the
+    product on the expanded weights, and the gradient through the blob."""
+    say(f"case expanded training M={M} N={N} K={K} {w} g={g}")
+    c = GatedCase(M, N, K, w, g, zeros, act="silu" if M % 2 else "gelu_tanh", seed=M + g)
+    assert c.plan.ws_bytes >= 4 * N * K  # the weights as fp16
+    pre = c.plan.new_preact()
+    pre.fill_(float("nan"))
+    C, gg, uu, e = c.reference()
+    assert_near(c.run(preact=pre), C, oracle.gated_bound(C, gg, uu, *e, c.act), "C")
+    for x, ref, err in zip(np.split(pre.cpu().numpy().astype(np.float64), 2, axis=1), (gg, uu), e):
+        assert_near(x, ref, err + 2.0**-11 * np.abs(ref) + 2.0**-25, "preact")
+    dC = (synth.draw_fp16_activations(M, N, seed=M) * np.float16(0.25)).astype(np.float16)
+    out = c.plan.backward(c.Ad, c.packed, pre, host_to_device(dC))["dA"].cpu().numpy().astype(np.float64)
+    ref = oracle.gated_grads_ref(c.A, *c.W, gg, uu, dC, c.act)["dA"]
+    bound = oracle.gated_grads_bound(c.A, *c.W, gg, uu, dC, c.act, *e, True)["dA"]
+    assert_near(out, ref, bound + 2.0**-11 * np.abs(ref) + 2.0**-25, "dA")
+
+
+@pytest.mark.parametrize("w,g,zeros", [("i4", 64, False), ("u4", 64, True), ("i4", 32, False), ("u4", 32, True), ("i4", -1, False),
+                                       ("u4", -1, True)])
+@pytest.mark.parametrize("M,fewer", [(40, (33, 32, 9)), (200, (199, 129, 40, 5))])
+def test_gated_split_k_of_other_groups(M, fewer, w, g, zeros):
+    """The library's own split where groups are not whole superblocks (no expansion then) or one
+    over K (its scale taken by the parts): parts of both projections joined, and runs of fewer rows."""
+    say(f"case gated split M={M} {w} g={g}")
+    c = GatedCase(M, 2100, 8192, w, g, zeros, seed=M + abs(g))
+    assert c.plan.ws_bytes > 0
+    for m in (M,) + fewer:
+        c.check(M=m)
+
+
+@pytest.mark.parametrize("M,N", [(186, 1300), (130, 1500), (256, 2600), (186, 3001), (200, 5440), (256, 6306), (129, 10001), (200, 12010), (256, 17000)])
+@pytest.mark.parametrize("w,g,K", [("f16", 0, 72), ("i4", 32, 96)])
+def test_gated_tiles_of_a_mid_sized_batch(M, N, w, g, K):
+    """fp16 (and expanded) weights at 129 to 256 rows: widths on both sides of each change of tile."""
+    say(f"case gated mid M={M} N={N} K={K} {w}")
+    GatedCase(M, N, K, w, g, act="silu" if N % 2 else "gelu_tanh", seed=M).check()
+
+
+def test_input_gradient_on_wide_low_tiles():
+    """33 rows against so many positions that 32 x 256 tiles take dA."""
+    M, N, K = 33, 40, 19500
+    c = GatedCase(M, N, K, "f16", seed=6, bias=False)
+    pre = c.plan.new_preact()
+    c.run(preact=pre)
+    C, gg, uu, e = c.reference()
+    dC = (synth.draw_fp16_activations(M, N, seed=7) * np.float16(0.1)).astype(np.float16)
+    out = c.plan.backward(c.Ad, c.packed, pre, host_to_device(dC))
+    ref = oracle.gated_grads_ref(c.A, *c.W, gg, uu, dC, c.act)
+    bound = oracle.gated_grads_bound(c.A, *c.W, gg, uu, dC, c.act, *e, False)
+    for name in ("dA", "dw_gate", "dw_up"):
+        assert_near(out[name].cpu().numpy().astype(np.float64), ref[name], bound[name] + 2.0**-11 * np.abs(ref[name]) + 2.0**-25, name)
+
+
+@pytest.mark.parametrize("w,g,M,N", [("f16", 0, 70, 60), ("i4", 128, 70, 4200), ("f16", 0, 3000, 100)])
+def test_training_step_in_a_graph(w, g, M, N):
+    """Forward and backward captured once and replayed on other inputs, ordinary and past fp16's range in turn."""
+    K = 256 if M < 3000 else 3300
+    c = GatedCase(M, N, K, w, g, seed=30, bias=False)
+    A, dC = c.Ad.clone(), host_to_device((synth.draw_fp16_activations(M, N, seed=8) * np.float16(0.1)).astype(np.float16))
+    pre, learns, dC0 = c.plan.new_preact(), w == "f16", dC.clone()
+
+    def step():
+        C = c.plan.run(A, c.packed, preact=pre)
+        return [C] + [t for t in c.plan.backward(A, c.packed, pre, dC, bias_grads=learns).values() if t is not None]
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        kept = step()
+    for shift, lift in ((0, 1.0), (3, 2.0**14), (5, 2.0**-12), (1, 1.0)):
+        A.copy_(c.Ad.roll(shift, 0))
+        dC.copy_((dC0.float() * lift).half())
+        for t in kept:
+            t.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        replayed = [t.clone() for t in kept]
+        for a, b in zip(replayed, step()):
+            assert torch.equal(a, b) or (torch.equal(a.isnan(), b.isnan()) and torch.equal(a.nan_to_num(), b.nan_to_num())), shift
+        torch.cuda.synchronize()
