@@ -11,8 +11,8 @@
 // would double the products), each sum's terms at a common scale where fp16's range asks for
 // one.  All of the passes read and write each value once and are
 // bound by HBM; the transposes go through LDS so that both sides are contiguous (N = 11008,
-// K = 4096: gradients of the pre-activations both ways at M = 2048 60 us for 318 MB and 5 us to
-// check their range, row by row at M = 1024 25 us for 113 MB and 5 us; the transposed int4
+// K = 4096: gradients of the pre-activations both ways at M = 2048 58 us for 318 MB and 5 us to
+// check their range, row by row at M = 1024 24 us for 113 MB and 5 us; the transposed int4
 // weights 48 us for 225 MB; X of 2048 rows 8 us).
 //
 // dA runs as one product over the inner columns of the gated plan (gate and up blocks of
@@ -154,7 +154,7 @@ __global__ __launch_bounds__(256) void gate_grad_kernel(GateGradArgs a) {
         }
 #pragma unroll
         for (int o = PER_ROW / 2; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor(most, o, 64));
-        if (i % PER_ROW == 0 && m < a.M) a.row_top[(size_t)m * gridDim.x + blockIdx.x] = most;
+        if (i % PER_ROW == 0 && m < a.M) a.row_top[(size_t)blockIdx.x * a.M + m] = most;
       }
       if (a.colwise) {
 #pragma unroll
@@ -212,7 +212,7 @@ __global__ __launch_bounds__(256) void gate_grad_range_kernel(GateGradArgs a, in
     const int lane = threadIdx.x & 63, m = blockIdx.x * 4 + (threadIdx.x >> 6);
     if (m >= a.M) return;
     float top = 0.f;
-    for (int i = lane; i < col_tiles; i += 64) top = fmaxf(top, a.row_top[(size_t)m * col_tiles + i]);
+    for (int i = lane; i < col_tiles; i += 64) top = fmaxf(top, a.row_top[(size_t)i * a.M + m]);
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
     const int e = range_shift(__uint_as_float(__float_as_uint(top) & 0xFFFF0000u));

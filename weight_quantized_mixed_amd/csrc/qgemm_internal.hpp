@@ -292,7 +292,7 @@ hipError_t launch_finalize_gate(const RunArgs& a, int acc_fp, hipStream_t st);
 // N columns, row by row (inner column order, rows of kd values, times 1 / row_scale) if
 // rowwise is given, and column by column (gate, then up: 2 N rows of mp values, times 1 /
 // col_scale) if colwise is, with the bias gradients (each may be null) if bias_part is.
-// row_top, col_top and bias_part are scratch: [M][gate_grad_col_tiles(N)],
+// row_top, col_top and bias_part are scratch: [gate_grad_col_tiles(N)][M],
 // [gate_grad_row_tiles(M)][N] and [gate_grad_row_tiles(M)][2 N].
 struct GateGradArgs {
   const _Float16 *preact, *dC;
