@@ -32,16 +32,17 @@
 // numbers of the block after next, so that no wait for a page number ever waits for the
 // data loads behind it.
 //
-// Measured (heads of 128): KEYS, 64 sequences of 512 own tokens, 8 key / value heads 24 us, 16
-// sequences of 8000 tokens 100 us (5.2 to 5.6 TB/s of keys and values); one sequence of 777
-// tokens, 32 heads 5.9 us and 4 us to join its 7 parts.  ROWS, 4096 tokens of 32 / 8 heads
-// 172-186 us (740-800 TFLOP/s), 2048 queries behind 16384 keys 860-950 TFLOP/s: a block of
+// Measured (heads of 128): KEYS, 64 sequences of 512 own tokens, 8 key / value heads 23 us
+// (5.7 TB/s of keys and values), 16 sequences of 8000 tokens 111 us (4.7 TB/s); one sequence of
+// 777 tokens, 32 heads 6.1 us and 4 us to join its 7 parts.  ROWS, 4096 tokens of 32 / 8 heads
+// 180-195 us (705-765 TFLOP/s), 2048 queries behind 16384 keys 690 us (846 TFLOP/s): a block of
 // 64 keys takes 128 rows 64 MFMAs (1024 cycles) and about 210 vector instructions (1220
 // cycles, 512 of them exponentials) a wave, two waves share a SIMD, and the two pipes
 // overlap only in part.
 //
 // Precision: scores, maxima and sums in fp32, exponentials as 2^(s c - m) with c = scale
-// log2 e; probabilities round to fp16 as operands.  The maximum used may lag the true one
+// log2 e; probabilities round to fp16 as operands (the matrix cores' full rate; error against 64
+// bits 2.6e-4 to 2.9e-4, 2.1e-4 of it the result's own rounding).  The maximum used may lag the true one
 // by up to 8 (probabilities up to 2^8, far inside fp16), which spares most of the
 // rescaling.
 //

@@ -304,7 +304,8 @@ __device__ __forceinline__ void store_superblocks(const _Float16 (&t)[TP][TPITCH
 
 // Transpose of a gated plan's blob into the fp16 blob of the dA product: its columns are
 // the K positions of the forward's weights, its reduction the inner columns.  A value is
-// (q - z) s in fp32, rounded once to fp16 (the operand type of the product).
+// (q - z) s in fp32, rounded once to fp16, the operand type of the product (a scale cannot leave
+// the sum here: it changes along the reduction).
 template <int FMT>
 __global__ __launch_bounds__(256) void transpose_blob_kernel(const uint4* __restrict__ W, const void* __restrict__ S,
                                                              int NB, int Npad, int nkb, int gate_n, int group_size,
@@ -359,7 +360,7 @@ __global__ __launch_bounds__(256) void transpose_blob_kernel(const uint4* __rest
 // (q - z) s of a packed int4 / uint4 blob, rounded once, as the fp16 blob of the same columns.
 // A thread takes a piece of 32 positions of a column (they share a group) to the four
 // pieces of 8 of one fp16 superblock; a wave's 16-byte stores fill whole superblocks.
-// Bound by HBM: 22016 columns, K = 4096 (208 MB) 37 us, 5.6 TB/s.
+// Bound by HBM: 22016 columns, K = 4096, groups of 64 (228 MB) 36 us, 6.3 TB/s.
 template <int FMT>
 __global__ __launch_bounds__(256) void expand_blob_kernel(const uint4* __restrict__ W, const void* __restrict__ S, int NB,
                                                           int Npad, int64_t pieces, int group_size, int zeros,

@@ -22,7 +22,7 @@ int choose_dl_tile(int fmt, int64_t M, int64_t N, int k_parts, int smode, bool g
   // Gated fp16 of 129 to 256 rows: the tile whose waves of 256 workgroups, each at the cost
   // measured for a wave of it, are soonest done.  (The rule below jumps from one wave of
   // large tiles that fill a little under 60 % of the CUs to three of the smallest: N = 6306,
-  // K = 2620, M = 186 67 us, so 35 us; N = 2900, K = 2560, M = 186 43 and 21 us.)
+  // K = 2624, M = 186 67 us, so 36 us; N = 2900, K = 2560, M = 186 43 and 21 us.)
   if (gated && fmt == FMT_F16 && M > 128 && M <= 256) {
     static const struct { int tile, cost; } waves_of[] = {{DL_128x256, 170}, {DL_64x256, 145}, {DL_64x128, 100},
                                                          {DL_32x128, 88},  {DL_32x64, 68}};
@@ -44,7 +44,7 @@ int choose_dl_tile(int fmt, int64_t M, int64_t N, int k_parts, int smode, bool g
   int pick = -1;
   for (int t : order) {
     // 128 x 128 only for int4 / int2 weights, whose upcast it shares over 128 rows
-    // (measured at M = 128, N = 32000: 58 -> 50 us for int4)
+    // (measured at M = 128, N = 32000: 58 -> 50 us for int4; not measured for int8 and fp16)
     if (t == DL_128x128 && !packed) continue;
     int bm, bn;
     dl_tile_dims(t, &bm, &bn);

@@ -190,7 +190,8 @@ __device__ __forceinline__ float gate_sigmoid(float c0, float c1, float x) {
 }
 __device__ __forceinline__ float gate_act(const RunArgs& a, float x) { return x * gate_sigmoid(a.act_c0, a.act_c1, x); }
 // stores output (row, c.col) from the two sums, in fp32 up to the one rounding of the
-// output (and one of each pre-activation, where they are kept for the backward pass)
+// output (and one of each pre-activation, where they are kept for the backward pass: half the
+// bytes to write and to read again; the output does not see it, the gradients start from it)
 __device__ __forceinline__ void gate_store(const RunArgs& a, int row, const GateCol& c, float g, float u) {
   if (a.row_scale) {
     const float rs = a.row_scale[row];
