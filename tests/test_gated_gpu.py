@@ -527,3 +527,32 @@ def test_training_step_in_a_graph(w, g, M, N):
         for a, b in zip(replayed, step()):
             assert torch.equal(a, b) or (torch.equal(a.isnan(), b.isnan()) and torch.equal(a.nan_to_num(), b.nan_to_num())), shift
         torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
+@pytest.mark.parametrize("M", [1, 3, 20, 70, 2000])
+def test_gates_past_any_square(M, act):
+    """Gates whose square leaves fp32 (an infinite bias, large scales of int8 sums): the activation
+    is the gate itself above and 0 below, as its formula gives."""
+    N, K = 2010 if M == 2000 else 40, 256
+    plan = QGated(M, N, K, "f16", act=act)
+    ones = torch.ones((N, K), dtype=torch.float16, device="cuda")
+    A = torch.full((M, K), 2.0**-8, dtype=torch.float16, device="cuda")
+    bias = torch.zeros(N, dtype=torch.float16, device="cuda")
+    bias[1::3] = float("inf")
+    up = ones.clone()
+    up[::2] = -1
+    C = plan.run(A, plan.pack(ones, up), bias_gate=bias)
+    sign = torch.ones(N, device="cuda")
+    sign[::2] = -1
+    assert torch.equal(C[:, 1::3].float(), (sign * float("inf"))[1::3].expand(M, -1))
+    keep = [i for i in range(N) if i % 3 != 1]
+    assert torch.isfinite(C[:, keep]).all()
+    plan = QGated(M, N, K, "i8", act=act)
+    w8 = torch.ones((N, K), dtype=torch.int8, device="cuda")
+    gate = w8.clone()
+    gate[1::2] = -1
+    A8 = torch.ones((M, K), dtype=torch.int8, device="cuda")
+    huge, cols = torch.full((M,), 1e15, device="cuda"), torch.full((N,), 1e3, device="cuda")  # g = +-2.56e20
+    C = plan.run_scaled(A8, plan.pack(gate, w8), huge, cols, cols * 1e-18)
+    assert torch.isposinf(C[:, ::2]).all() and (C[:, 1::2] == 0).all()

@@ -183,10 +183,12 @@ __device__ __forceinline__ GateCol gate_col(const RunArgs& a, int icol) {
 // x sigmoid(t), t = x (c0 + c1 x^2): silu with (1, 0); the tanh form of gelu with
 // (2 c, 2 c 0.044715), c = sqrt(2 / pi), since (1 + tanh y) / 2 = sigmoid(2 y).  The
 // hardware exponential and reciprocal are within a few ulp in fp32.
-// sigmoid(x (c0 + c1 x^2)), with the constants times -log2 e taken out of the exponent
+// sigmoid(x (c0 + c1 x^2)), with the constants times -log2 e taken out of the exponent; the
+// square stays finite, since silu's c1 of 0 times an infinite one (|x| from 1.8e19) would be NaN
 __device__ __forceinline__ float gate_sigmoid(float c0, float c1, float x) {
   constexpr float L = -1.4426950408889634f;
-  return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(x * (c0 * L + c1 * L * (x * x))));
+  const float xx = fminf(x * x, 3.4e38f);
+  return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(x * (c0 * L + c1 * L * xx)));
 }
 __device__ __forceinline__ float gate_act(const RunArgs& a, float x) { return x * gate_sigmoid(a.act_c0, a.act_c1, x); }
 // stores output (row, c.col) from the two sums, in fp32 up to the one rounding of the
