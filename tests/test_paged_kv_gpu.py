@@ -415,3 +415,28 @@ def test_attention_at_the_largest_scale():
     c = AttnCase(4, 2, 64, 16, [1, 3], [40, 7], 20, seed=16)
     c.q[:] = 0
     c.upload().check(scale=2.3e38)
+
+
+@pytest.mark.parametrize("D", [40, 64, 80, 96, 128, 192, 256])
+@pytest.mark.parametrize("qs,lens,prefix", [([1, 1], [90, 40], 70), ([30], [150], 0)])
+def test_infinite_keys_have_their_weight(D, qs, lens, prefix):
+    """A key that a query sees with a score of minus infinity weighs nothing, in every head dimension."""
+    c = AttnCase(4, 2, D, 16, qs, lens, prefix, seed=17)
+    c.q[..., 3] = np.abs(c.q[..., 3]) + np.float16(0.125)
+    c.upload()
+    at = [(c.tables[0, 1], 5, 21)] + ([(c.prefix_table[2], 1, 33)] if prefix else [])
+    for page, place, _ in at:
+        c.k[page, :, place, 3] = -np.inf
+    c.upload()
+    got, lse = c.run()
+    for b, (n, L) in enumerate(zip(qs, lens)):
+        seen = np.concatenate([np.ones((n, prefix), bool), np.arange(L)[None] <= (L - n + np.arange(n))[:, None]], axis=1)
+        seen[:, prefix + 21] &= b != 0
+        if prefix:
+            seen[:, 33] = False
+        r = slice(c.starts[b], c.starts[b + 1])
+        for h in range(4):
+            kt, vt = (np.concatenate([c.tokens[0][i][:, h // 2], c.tokens[b + 1][i][:, h // 2]]) for i in (0, 1))
+            ref, ref_lse, bound = oracle.attention_ref(c.q[r, h], kt, vt, seen, D ** -0.5)
+            assert_near(got[r, h], ref, bound, f"sequence {b} head {h}")
+            assert (np.abs(lse[r, h] - ref_lse) <= 1e-4 + 1e-5 * np.abs(ref_lse)).all()

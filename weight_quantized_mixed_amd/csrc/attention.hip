@@ -148,7 +148,14 @@ struct Item {
   const int32_t* own;    // pages of the keys from pre on
 };
 
-template <int DP, int KIND>
+// what keys hold past D: zeros, which add nothing to a score whatever the key's own values are
+// (another place of the key would: zero times its infinity is NaN)
+__device__ const uint4 PAST_D = {0, 0, 0, 0};
+
+// FULL: D is DP; else D is less, and the places past it are PAST_D in keys, the value's first ones
+// in values (whose products there go nowhere); an instance of its own, since branches on D cost the
+// full tiles 2 to 8 %
+template <int DP, int KIND, bool FULL>
 __device__ __forceinline__ void attend_tile(const AttnArgs& a, const AttnSplit& sp, const Item& it, uint8_t* lds) {
   using T = TileGeo<DP, KIND>;
   constexpr bool KEYS = T::KEYS;
@@ -231,7 +238,9 @@ __device__ __forceinline__ void attend_tile(const AttnArgs& a, const AttnSplit& 
     const int c_lane = lane % SL, r_lane = lane / SL;
     auto row_of_load = [&](int i) { return (KEYS ? i : i * 4 + wave) * RPI + r_lane; };
     int64_t off[LOADS];
+    uint32_t past = 0;  // loads whose place lies past D, a bit each
     auto find_rows = [&](int j) {
+      past = 0;
 #pragma unroll
       for (int i = 0; i < LOADS; ++i) {
         const int x = row_of_load(i);
@@ -240,14 +249,18 @@ __device__ __forceinline__ void attend_tile(const AttnArgs& a, const AttnSplit& 
         bool own;
         const int t = place(j, x, own);
         const int slot = slot_of<SL>(x, c_lane);
-        const uint32_t in_page = head_bytes + (uint32_t)(t & page_mask) * row_bytes + (slot * 8 < D ? slot * 16 : 0);
+        const uint32_t in_page = head_bytes + (uint32_t)(t & page_mask) * row_bytes + (FULL || slot * 8 < D ? slot * 16 : 0);
+        if (!FULL && slot * 8 >= D) past |= 1u << i;
         off[i] = (int64_t)((uint64_t)page * page_bytes + in_page);
       }
     };
-    auto load_block = [&](const _Float16* cache, uint32_t at) {
+    auto load_block = [&](const _Float16* cache, uint32_t at, auto KEY) {
 #pragma unroll
-      for (int i = 0; i < LOADS; ++i)
-        dma16v(reinterpret_cast<const uint8_t*>(cache) + off[i], at + (KEYS ? i : i * 4 + wave) * 1024);
+      for (int i = 0; i < LOADS; ++i) {
+        const uint8_t* from = reinterpret_cast<const uint8_t*>(cache) + off[i];
+        if (!FULL && KEY && (past >> i & 1)) from = reinterpret_cast<const uint8_t*>(&PAST_D);
+        dma16v(from, at + (KEYS ? i : i * 4 + wave) * 1024);
+      }
     };
 
     half8v p[NT][NK];
@@ -429,8 +442,8 @@ __device__ __forceinline__ void attend_tile(const AttnArgs& a, const AttnSplit& 
       find_rows(0);
       reads_done();
       load_pages(1);
-      load_block(a.k, kbuf_at);
-      load_block(a.v, kbuf_at + T::BLOCK);
+      load_block(a.k, kbuf_at, std::true_type{});
+      load_block(a.v, kbuf_at + T::BLOCK, std::false_type{});
       for (int j = 0; j < cnt; ++j) {
         const bool more = j + 1 < cnt;
         const int base = base_of(j);
@@ -442,7 +455,7 @@ __device__ __forceinline__ void attend_tile(const AttnArgs& a, const AttnSplit& 
         reads_done();
         if (more) {
           load_pages(j + 2);
-          load_block(a.k, kbuf_at);
+          load_block(a.k, kbuf_at, std::true_type{});
         }
         if (masked) hide(s, base);
         float top[NT];
@@ -454,7 +467,7 @@ __device__ __forceinline__ void attend_tile(const AttnArgs& a, const AttnSplit& 
         if (masked && !finite(kbuf + T::BLOCK)) set_apart(kbuf + T::BLOCK, base);
         product(kbuf + T::BLOCK);
         reads_done();
-        if (more) load_block(a.v, kbuf_at + T::BLOCK);
+        if (more) load_block(a.v, kbuf_at + T::BLOCK, std::false_type{});
       }
     } else {
       // Two blocks each of keys and values for the workgroup, of which a wave loads a
@@ -467,12 +480,12 @@ __device__ __forceinline__ void attend_tile(const AttnArgs& a, const AttnSplit& 
       load_pages(1);
       landed<0>();
       find_rows(0);
-      load_block(a.k, kbuf_at);
-      load_block(a.v, vbuf_at);
+      load_block(a.k, kbuf_at, std::true_type{});
+      load_block(a.v, vbuf_at, std::false_type{});
       find_rows(1);
       reads_done();
       load_pages(2);
-      if (cnt > 1) load_block(a.k, kbuf_at + T::BLOCK);
+      if (cnt > 1) load_block(a.k, kbuf_at + T::BLOCK, std::true_type{});
       // blocks that every row of the tile sees whole
       const int whole = (max(limit_of(it.row0), it.key0) - it.key0) / KT;
       Scores sa, sb;
@@ -488,12 +501,12 @@ __device__ __forceinline__ void attend_tile(const AttnArgs& a, const AttnSplit& 
         landed<0>();
         reads_done();
         asm volatile("s_barrier" ::: "memory");  // keys j + 1 and values j are whole; keys j, values j - 1 no longer read
-        if (j + 1 < cnt) load_block(a.v, vbuf_at + (odd ^ 1) * T::BLOCK);
+        if (j + 1 < cnt) load_block(a.v, vbuf_at + (odd ^ 1) * T::BLOCK, std::false_type{});
         if (j + 2 < cnt) {
           find_rows(j + 2);
           reads_done();
           load_pages(j + 3);
-          load_block(a.k, kbuf_at + odd * T::BLOCK);
+          load_block(a.k, kbuf_at + odd * T::BLOCK, std::true_type{});
         }
       };
       // A block that every row sees whole, in a fixed order of small steps (the fences keep
@@ -656,7 +669,7 @@ __device__ __forceinline__ int queries_of(const AttnArgs& a, int b, int& start, 
   return all;
 }
 
-template <int DP, int KIND_P, int KIND_S>
+template <int DP, int KIND_P, int KIND_S, bool FULL>
 __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void attend_kernel(AttnArgs a, AttnSplit sp) {
   extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
   const int G = a.q_heads / a.kv_heads;
@@ -686,7 +699,7 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void attend_kernel(AttnArgs
     it.lim0 = INT32_MIN / 2;
     it.slot = part;
     it.own = nullptr;
-    if constexpr (KIND_P != TILE_NONE) attend_tile<DP, KIND_P>(a, sp, it, lds);
+    if constexpr (KIND_P != TILE_NONE) attend_tile<DP, KIND_P, FULL>(a, sp, it, lds);
     return;
   }
   if (KIND_P != TILE_NONE) w -= sp.p_items;
@@ -720,7 +733,7 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void attend_kernel(AttnArgs
   it.key1 = min(it.pre + held, it.key0 + sp.s_chunk);
   it.slot = (sp.shared ? sp.p_splits : 0) + part;
   it.own = a.tables + (int64_t)b * a.table_width;
-  attend_tile<DP, KIND_S>(a, sp, it, lds);
+  attend_tile<DP, KIND_S, FULL>(a, sp, it, lds);
 }
 
 // Joins the partial results of every row, one wave a row: lane s weighs slot s, then the
@@ -820,7 +833,9 @@ hipError_t launch_kinds(const AttnArgs& a, const AttnSplit& p, hipStream_t st) {
   constexpr int lp = KIND_P == TILE_NONE ? 0 : TileGeo<DP, KIND_P == TILE_NONE ? KIND_S : KIND_P>::LDS;
   constexpr int lds = ls > lp ? ls : lp;
   static_assert(lds <= 160 * 1024, "LDS budget");
-  hipLaunchKernelGGL((attend_kernel<DP, KIND_P, KIND_S>), dim3((unsigned)(p.p_items + p.s_items)), dim3(256), lds, st, a, p);
+  const dim3 grid((unsigned)(p.p_items + p.s_items));
+  if (a.D == DP) hipLaunchKernelGGL((attend_kernel<DP, KIND_P, KIND_S, true>), grid, dim3(256), lds, st, a, p);
+  else hipLaunchKernelGGL((attend_kernel<DP, KIND_P, KIND_S, false>), grid, dim3(256), lds, st, a, p);
   return hipGetLastError();
 }
 
