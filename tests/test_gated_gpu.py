@@ -369,6 +369,7 @@ RANGES = [  # M, N, K, w: the products of every path that takes gradients as fp1
     (1, 1, 70, "f16"), (1, 40, 96, "f16"), (1, 40, 8300, "f16"), (5, 70, 200, "f16"), (20, 33, 136, "f16"), (40, 130, 129, "f16"),
     (100, 72, 200, "f16"), (200, 260, 520, "f16"), (700, 60, 1300, "f16"), (700, 60, 2000, "f16"), (1300, 60, 2100, "f16"),
     (1300, 100, 5000, "f16"), (3400, 100, 2900, "f16"), (2100, 4100, 2300, "f16"), (33, 100, 256, "i4"), (70, 4200, 256, "i4"),
+    (1300, 4200, 2048, "i4"),
 ]
 
 

@@ -380,8 +380,8 @@ size_t run_ws_bytes_for(const qgemm_plan* p, int64_t M, bool fold) {
 // writes the weights as an fp16 blob into the workspace and the fp16 tiles run on it, since
 // the direct-load tiles hold one scale per column and stage.  N = 11008, K = 4096, groups of
 // 64, int4 / uint4 with zero points on the LDS-staged tiles against so: M = 128 74 / 91 us
-// against 100, M = 192 177 / 228 against 113, M = 512 267 / 344 against 122 / 127, M = 2048
-// 626 / 689 against 318 / 322; N = 1506, K = 1536, M = 256 20.0 / 24.2 against 15.8 us.
+// against 100, M = 192 177 / 228 against 113, M = 512 267 / 344 against 125 / 123, M = 2048
+// 626 / 689 against 324 / 326; N = 1506, K = 1536, M = 256 20.0 / 24.2 against 15.8 us.
 #ifndef QG_EXPAND_MIN_M
 #define QG_EXPAND_MIN_M 129
 #endif

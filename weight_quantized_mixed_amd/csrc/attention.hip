@@ -35,7 +35,7 @@
 // Measured (heads of 128): KEYS, 64 sequences of 512 own tokens, 8 key / value heads 23 us
 // (5.7 TB/s of keys and values), 16 sequences of 8000 tokens 111 us (4.7 TB/s); one sequence of
 // 777 tokens, 32 heads 6.1 us and 4 us to join its 7 parts.  ROWS, 4096 tokens of 32 / 8 heads
-// 180-195 us (705-765 TFLOP/s), 2048 queries behind 16384 keys 690 us (846 TFLOP/s): a block of
+// 178-189 us (727-772 TFLOP/s), 2048 queries behind 16384 keys 677 us (863 TFLOP/s): a block of
 // 64 keys takes 128 rows 64 MFMAs (1024 cycles) and about 210 vector instructions (1220
 // cycles, 512 of them exponentials) a wave, two waves share a SIMD, and the two pipes
 // overlap only in part.

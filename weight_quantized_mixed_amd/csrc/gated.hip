@@ -11,9 +11,9 @@
 // would double the products), each sum's terms at a common scale where fp16's range asks for
 // one.  All of the passes read and write each value once and are
 // bound by HBM; the transposes go through LDS so that both sides are contiguous (N = 11008,
-// K = 4096: gradients of the pre-activations both ways at M = 2048 58 us for 318 MB and 5 us to
-// check their range, row by row at M = 1024 24 us for 113 MB and 5 us; the transposed int4
-// weights 48 us for 225 MB; X of 2048 rows 8 us).
+// K = 4096: gradients of the pre-activations both ways at M = 2048 58 us for 319 MB and 5 us to
+// check their range, row by row at M = 1024 23 us for 114 MB and 5 us; the transposed int4
+// weights 47 us for 225 MB; X of 2048 rows 8 us).
 //
 // dA runs as one product over the inner columns of the gated plan (gate and up blocks of
 // 16 alternate), so its weight operand is the transpose of the forward's blob, whatever
