@@ -440,3 +440,16 @@ def test_infinite_keys_have_their_weight(D, qs, lens, prefix):
             ref, ref_lse, bound = oracle.attention_ref(c.q[r, h], kt, vt, seen, D ** -0.5)
             assert_near(got[r, h], ref, bound, f"sequence {b} head {h}")
             assert (np.abs(lse[r, h] - ref_lse) <= 1e-4 + 1e-5 * np.abs(ref_lse)).all()
+
+
+@pytest.mark.parametrize("hq,hkv,D,qs,lens,prefix", [
+    (2, 1, 64, [1, 1], [1, 2398], 0), (1, 1, 8, [1], [700], 0), (2, 1, 40, [1], [1500], 0), (4, 1, 64, [2, 1], [3000, 2500], 4000),
+    (2, 1, 128, [1, 1], [4100, 3000], 4500), (2, 2, 80, [1, 2], [4100, 100], 4500), (1, 1, 256, [1, 1], [4100, 300], 4500),
+    (2, 1, 96, [1], [9000], 0), (8, 1, 64, [9, 9], [2000, 1500], 3000)])
+def test_many_parts_of_the_keys(hq, hkv, D, qs, lens, prefix):
+    """More parts than a row has 16-byte pieces of fp32, up to 32 of the prefix and 32 of the own tokens: all of them count."""
+    say(f"case parts hq={hq} hkv={hkv} D={D} q={qs} lens={lens} prefix={prefix}")
+    c = AttnCase(hq, hkv, D, 64, qs, lens, prefix, seed=19).upload()
+    c.check()
+    need = q.qgemm_attention_workspace(c.cache.desc, sum(qs), hq, len(qs), max(qs), max(lens), prefix)
+    assert need // (sum(qs) * hq * (D * 4 + 8)) > 5

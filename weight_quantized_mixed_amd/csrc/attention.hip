@@ -759,23 +759,24 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttnArgs a, AttnSplit 
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o, 64);
   const bool none = top == -INFINITY && sum == 0.f;
-  const int d0 = lane * 4;
-  if (d0 < a.D) {
-    const float* po = sp.part_o + th * a.D + d0;
-    float4v v = {0.f, 0.f, 0.f, 0.f};
-    for (int s0 = 0; s0 < sp.slots; s0 += 8) {
-      float4v p[8];
+  // lanes past D read its last values again: each lane holds a slot's weight, so all stay in
+  const int d0 = min(lane * 4, a.D - 4);
+  const float* po = sp.part_o + th * a.D + d0;
+  float4v v = {0.f, 0.f, 0.f, 0.f};
+  for (int s0 = 0; s0 < sp.slots; s0 += 8) {
+    float4v p[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int s = min(s0 + i, sp.slots - 1);
-        p[i] = *reinterpret_cast<const float4v*>(po + s * step * a.D);
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float ws = __shfl(w, s0 + i, 64);  // 0 past the last slot
-        if (ws != 0.f) v += ws * p[i];
-      }
+    for (int i = 0; i < 8; ++i) {
+      const int s = min(s0 + i, sp.slots - 1);
+      p[i] = *reinterpret_cast<const float4v*>(po + s * step * a.D);
     }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float ws = __shfl(w, s0 + i, 64);  // 0 past the last slot
+      if (ws != 0.f) v += ws * p[i];
+    }
+  }
+  if (lane * 4 < a.D) {
     half4v h;
 #pragma unroll
     for (int i = 0; i < 4; ++i) h[i] = (_Float16)(none ? 0.f : v[i] / sum);
