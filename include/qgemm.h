@@ -423,6 +423,112 @@ qgemm_status qgemm_kv_append(const qgemm_kv_cache* cache, int64_t T, int32_t q_h
                              void* stream);
 
 /*
+ * qgemm_kv_append of normed heads: every query and key head is first divided by its root mean
+ * square and multiplied by a weight,
+ *   x -> x w / sqrt(mean(x^2) + eps),
+ * then rotated (fp32 throughout, one rounding); the values are stored as they are.
+ *   q_weight, k_weight  device, fp16 [head_dim], each may be NULL (1 everywhere).
+ *   eps          finite and above 0, else QGEMM_ERR_INVALID_ARG.
+ * All else as in qgemm_kv_append; weights of 16-byte alignment take the widest accesses.
+ */
+qgemm_status qgemm_kv_append_norm(const qgemm_kv_cache* cache, int64_t T, int32_t q_heads, const void* q,
+                                  int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                                  int64_t v_stride, const void* q_weight, const void* k_weight, float eps,
+                                  const float* cos, const float* sin, int64_t n_positions, int32_t rot_dim,
+                                  int32_t interleaved, const int32_t* positions, const int64_t* slots,
+                                  void* q_out, void* stream);
+
+/*
+ * The same without a cache, for training: normed and rotated queries and keys as dense arrays.
+ *   head_dim     a multiple of 8 up to 256, else QGEMM_ERR_UNSUPPORTED; q_heads and kv_heads
+ *                need not divide each other.
+ *   k_out        device, fp16 [T, kv_heads, head_dim]; q_out and k_out may be q and k
+ *                themselves where those rows follow each other without gaps.
+ * A token whose position is outside [0, n_positions) gets NaN in both.  The other arguments as
+ * in qgemm_kv_append_norm.
+ */
+qgemm_status qgemm_norm_rotate(int64_t T, int32_t q_heads, int32_t kv_heads, int32_t head_dim, const void* q,
+                               int64_t q_stride, const void* k, int64_t k_stride, const void* q_weight,
+                               const void* k_weight, float eps, const float* cos, const float* sin,
+                               int64_t n_positions, int32_t rot_dim, int32_t interleaved,
+                               const int32_t* positions, void* q_out, void* k_out, void* stream);
+
+/*
+ * Workspace of qgemm_norm_rotate_backward (0 without weight gradients).  More than 2^31 - 1 heads
+ * of all tokens return QGEMM_ERR_UNSUPPORTED.
+ */
+qgemm_status qgemm_norm_rotate_backward_workspace(int64_t T, int32_t q_heads, int32_t kv_heads,
+                                                  int32_t head_dim, int32_t weight_grads,
+                                                  size_t* workspace_bytes);
+
+/*
+ * Gradients of qgemm_norm_rotate from those of its outputs.  For a head x with r = 1 / sqrt(mean(x^2)
+ * + eps) and g the output's gradient rotated back,
+ *   dx = r (g w) - x r^3 mean(x g w),   dw = sum of x r g over all tokens and heads.
+ *   q, k, weights, eps, cos, sin, positions: the forward's.
+ *   dq_out, dk_out  device, fp16 [T, q_heads, head_dim] and [T, kv_heads, head_dim].
+ *   dq, dk       device, fp16, rows dq_stride and dk_stride values apart (slices of one
+ *                array's rows are allowed); may lie where dq_out and dk_out do, row by row.
+ *   dq_weight, dk_weight  device, fp32 [head_dim], each may be NULL.  Sums in fp32 in a fixed
+ *                order: bitwise reproducible for the same sizes.
+ * A token whose position is outside the table gets zeros and adds nothing to the weights'
+ * gradients.  With T = 0 the weights' gradients are zeros.
+ */
+qgemm_status qgemm_norm_rotate_backward(int64_t T, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+                                        const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                                        const void* q_weight, const void* k_weight, float eps,
+                                        const float* cos, const float* sin, int64_t n_positions,
+                                        int32_t rot_dim, int32_t interleaved, const int32_t* positions,
+                                        const void* dq_out, const void* dk_out, void* dq, int64_t dq_stride,
+                                        void* dk, int64_t dk_stride, float* dq_weight, float* dk_weight,
+                                        void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Workspace of qgemm_kv_extend (0 for a decode batch).
+ */
+qgemm_status qgemm_kv_extend_workspace(int64_t B, int64_t T, size_t* workspace_bytes);
+
+/*
+ * Makes room in the cache for the new tokens of up to B sequences: block tables, slots, positions
+ * and lengths from the requests' lengths alone, all on the device.  Pages come from a pool, a
+ * ring of which ring_state says where its first free page is and how many follow:
+ *   ring_state   device, int32 [2]: {head, free}; free pages are ring[(head + i) mod ring_size].
+ *   ring         device, int32 [ring_size]; ring_size is at least the number of pages in the pool.
+ *   new_tokens   device, int32 [B]: tokens that sequence b gets, none (0), or -1: it ends.
+ *   lens         device, int32 [B]: its own tokens in the cache so far.
+ *   gone         device, int32 [B]: its first page that no window gave back, see below (0 at first).
+ *   tables       device, int32 [B, table_width]: the pages of its tokens.  Entries of new pages are
+ *                written; no others are touched.
+ *   page_size    as the cache's; prefix_len tokens of a shared prefix come before the own ones
+ *                (they count in positions and windows, their pages are not the pool's).
+ *   q_starts     device, int32 [B + 1]: the new tokens are rows q_starts[b] .. q_starts[b + 1] - 1
+ *                of the batch, in the order of the sequences (at most T).
+ *   lens_out, gone_out, ring_state_out: the same after the call; may be the arrays themselves.
+ *   positions    device, int32 [T], and slots int64 [T]: of each row of the batch, for the append.
+ *                Rows behind the last new token have position 0 and slot -1 (not stored).
+ *   refused      device, int32 [B]: 1 where a sequence's new tokens are not taken: they would pass
+ *                the table's width, T, or position 2^31 - 1; or they need pages and those together
+ *                with the pages that the sequences before need (the ones refused for want of pages
+ *                among them) are more than the pool has free.  Its length stays and its rows have
+ *                position -1 and slot -1, of which the append makes NaN queries and stores nothing.
+ * Pages of a sequence that ends go back to the ring's end.  With a window > 0 so do pages of
+ * tokens that no query from this call's on will see (those before the last window - 1 of lens,
+ * and not among the first `sinks` tokens, the prefix's included), and gone_out says up to which page;
+ * prefix_len, window and sinks are the same in every call on a pool then.  Pages given back can be
+ * taken by the next call.
+ * Pages are taken and given back in the order of the sequences and of their tokens: results are
+ * the same in every run.  Calls on one pool follow one another.  page_size is a power of two up to
+ * 65536, B at most 65535, else QGEMM_ERR_UNSUPPORTED.
+ */
+qgemm_status qgemm_kv_extend(int64_t B, int64_t T, int32_t page_size, const int32_t* new_tokens,
+                             const int32_t* lens, const int32_t* gone, const int32_t* ring_state,
+                             int32_t* ring, int64_t ring_size, int32_t* tables, int64_t table_width,
+                             int64_t prefix_len, int64_t window, int64_t sinks, int32_t* q_starts,
+                             int32_t* lens_out, int32_t* gone_out, int32_t* ring_state_out,
+                             int32_t* positions, int64_t* slots, int32_t* refused, void* workspace,
+                             size_t workspace_bytes, void* stream);
+
+/*
  * Workspace of qgemm_attention for these sizes (0 where no work is split).
  */
 qgemm_status qgemm_attention_workspace(const qgemm_kv_cache* cache, int64_t T, int32_t q_heads,
@@ -470,6 +576,29 @@ qgemm_status qgemm_attention(const qgemm_kv_cache* cache, int64_t T, int32_t q_h
                              const int32_t* prefix_table, int64_t prefix_len, int64_t max_q,
                              int64_t max_len, float scale, void* out, float* lse, void* workspace,
                              size_t workspace_bytes, void* stream);
+
+/*
+ * Workspace of qgemm_attention_window for these sizes (0 where no work is split).
+ */
+qgemm_status qgemm_attention_window_workspace(const qgemm_kv_cache* cache, int64_t T, int32_t q_heads,
+                                              int64_t B, int64_t max_q, int64_t max_len, int64_t prefix_len,
+                                              int64_t window, int64_t sinks, size_t* workspace_bytes);
+
+/*
+ * qgemm_attention with a sliding window and a few first tokens that stay visible: of the
+ *   c = prefix_len + max(0, kv_lens[b] - n + i + 1)
+ * keys that query i of a sequence sees causally (the prefix's first), it sees the last `window`
+ * and the first `sinks`.
+ *   window       at least 1 (the query's own token), sinks at least 0, each below 2^31.
+ * Pages that hold none of the keys seen are not read (their entries in the table may be anything).
+ * Each sequence reads what it sees of the prefix by itself.  All else as in qgemm_attention.
+ */
+qgemm_status qgemm_attention_window(const qgemm_kv_cache* cache, int64_t T, int32_t q_heads, const void* q,
+                                    int64_t q_stride, int64_t B, const int32_t* q_starts,
+                                    const int32_t* kv_lens, const int32_t* tables, int64_t table_width,
+                                    const int32_t* prefix_table, int64_t prefix_len, int64_t max_q,
+                                    int64_t max_len, int64_t window, int64_t sinks, float scale, void* out,
+                                    float* lse, void* workspace, size_t workspace_bytes, void* stream);
 
 /* Release a plan; NULL is a no-op.  Device buffers are the caller's. */
 void qgemm_destroy(qgemm_plan* plan);

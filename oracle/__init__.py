@@ -11,4 +11,5 @@ from .core import (  # noqa: F401
 )
 from .layer import (  # noqa: F401
     activation, gated_ref, gated_bound, gated_grads_ref, gated_grads_bound, sum_bound, rotate_ref, attention_ref,
+    window_visible, norm_rotate_ref, norm_rotate_grads_ref, extend_ref,
 )

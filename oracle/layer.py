@@ -6,7 +6,10 @@ TEST INFRASTRUCTURE ONLY, as oracle.core.  Definitions:
   dU = dC act(g), dG = dC u act'(g), dA = dG . Wg^T + dU . Wu^T, dW = d^T . A,
   db = column sums;
 * append: the pairs (a, b) of a head turn to (a c - b s, b c + a s);
-* attention: softmax over the prefix and the own tokens j <= len - n + i of query i.
+* attention: softmax over the prefix and the own tokens j <= len - n + i of query i, or of
+  these the last `window` and the first `sinks`;
+* normed heads: y = R(p) (x r w) with r = 1 / sqrt(mean(x^2) + eps), and its gradients;
+* extend: pages, slots and positions of new tokens, one page after the other.
 
 The error bounds next to them state what each rounding of the library can do (half-ulp
 2**-11 of an fp16 value; fp32 sums and elementary functions at 2**-20 of the sum of
@@ -128,3 +131,102 @@ def attention_ref(q, k, v, visible, scale):
     vmax = np.abs(v).max(initial=0)
     bound = (U16 + 2 * es) * (weighted + np.abs(out)) + visible.sum(1)[:, None] * TINY16 * vmax / safe + U16 * np.abs(out) + TINY16
     return out, lse, bound
+
+
+def window_visible(n, held, length, prefix, window, sinks):
+    """[n, prefix + held]: which keys each of n queries sees, of a sequence of `length` own tokens of which `held` are read."""
+    end = prefix + np.maximum(0, length - n + np.arange(n) + 1)[:, None]
+    key = np.arange(prefix + held)[None]
+    return (key < end) & ((key >= end - window) | (key < sinks))
+
+
+def norm_rotate_ref(x, w, eps, cos, sin, interleaved):
+    """x [T, H, D] normed, weighted (w None: 1) and turned, in float64, and the error bound of the library's result.
+
+    The norm of a head is a sum of at most 256 squares in fp32, 16 of them one after the other, a root and two products:
+    below 2**-20 relative in all; the rotation adds two fp32 roundings of its terms.
+    """
+    x = np.asarray(x, dtype=np.float64)
+    n = x / np.sqrt((x * x).mean(-1, keepdims=True) + eps) * (1.0 if w is None else np.asarray(w, dtype=np.float64))
+    y, _ = rotate_ref(n, cos, sin, interleaved)
+    return y, 2 * F32 * abs_turned(n, cos, sin, interleaved) + U16 * np.abs(y) + TINY16
+
+
+def abs_turned(x, cos, sin, interleaved):
+    """The sums of magnitudes of a rotation's terms."""
+    x = np.abs(np.asarray(x, dtype=np.float64))
+    y, _ = rotate_ref(x, np.abs(cos), -np.abs(sin), interleaved)  # a |c| + b |s| in the first places
+    z, _ = rotate_ref(x, np.abs(cos), np.abs(sin), interleaved)   # b |c| + a |s| in the second ones
+    return np.maximum(y, z)
+
+
+def norm_rotate_grads_ref(x, w, eps, cos, sin, interleaved, dy):
+    """(dx, dw, bound of dx, bound of dw) of norm_rotate_ref from dy, in float64; dw [D] sums over tokens and heads.
+
+    The bounds: below 2**-19 of the sums of magnitudes for dx (two sums over a head, as above, and products); a
+    weight's sum in fp32 has no longer chain of additions than 128, so 2**-17 of the sum of magnitudes.
+    """
+    x, dy = np.asarray(x, dtype=np.float64), np.asarray(dy, dtype=np.float64)
+    w = np.ones(x.shape[-1]) if w is None else np.asarray(w, dtype=np.float64)
+    r = 1 / np.sqrt((x * x).mean(-1, keepdims=True) + eps)
+    g, _ = rotate_ref(dy, cos, -np.asarray(sin, dtype=np.float64), interleaved)
+    u, h = x * r, g * w
+    dx = r * (h - u * (u * h).mean(-1, keepdims=True))
+    gm = abs_turned(dy, cos, sin, interleaved)
+    hm = gm * np.abs(w)
+    ex = 2 * F32 * r * (hm + np.abs(u) * (np.abs(u) * hm).mean(-1, keepdims=True)) + U16 * np.abs(dx) + TINY16
+    return dx, (u * g).sum((0, 1)), ex, 2.0**-17 * (np.abs(u) * gm).sum((0, 1)) + 1e-30
+
+
+def extend_ref(new_tokens, lens, gone, head, free, ring, tables, page, T, prefix=0, window=0, sinks=0):
+    """{"q_starts", "kv_lens", "gone", "head", "free", "positions", "slots", "refused", "ring", "tables"}."""
+    tables, ring = np.array(tables, dtype=np.int64), [int(p) for p in ring]
+    width, R, most = tables.shape[1], len(ring), 2**31 - 1
+    head, free = (head if 0 <= head < R else 0), min(max(free, 0), R)
+    pages = lambda tokens: -(-tokens // page)  # noqa: E731
+    first = pages(max(0, sinks - prefix))
+    out = {"q_starts": [0], "kv_lens": [], "gone": [], "positions": np.zeros(T, np.int64), "slots": np.full(T, -1, np.int64),
+           "refused": []}
+    back, wanted, used, row = [], 0, 0, 0
+    for b in range(len(lens)):
+        L, n, g = max(int(lens[b]), 0), int(new_tokens[b]), max(int(gone[b]), 0) if window else 0
+        has = min(pages(L), width)
+        absent = range(first, g)                                    # pages that a window gave back before
+        if n < 0:
+            back += [tables[b, p] for p in range(has) if p not in absent]
+            out["kv_lens"].append(0)
+            out["gone"].append(0)
+            out["refused"].append(0)
+            out["q_starts"].append(min(row, T))
+            continue
+        if window:
+            unseen = max(0, L - (window - 1))                       # the next query is token L
+            last = unseen // page
+            back += [tables[b, p] for p in range(first, min(last, has)) if p not in absent]
+            if last > first:
+                g = max(g, last)
+        out["gone"].append(g)
+        need = pages(L + n) - pages(L)
+        fits = pages(L + n) <= width and prefix + L + n <= most and row + n <= T
+        if fits:
+            wanted += need
+        ok = n == 0 or (fits and (need == 0 or wanted <= free))
+        out["refused"].append(int(not ok))
+        out["kv_lens"].append(L + n if ok else L)
+        for i in range(min(n, max(0, T - row))):
+            at, tok = row + i, L + i
+            if not ok:
+                out["positions"][at] = -1
+                continue
+            if tok // page >= pages(L) and tok % page == 0:
+                tables[b, tok // page] = ring[(head + used) % R]
+                used += 1
+            out["positions"][at] = prefix + tok
+            out["slots"][at] = tables[b, tok // page] * page + tok % page
+        row += n
+        out["q_starts"].append(min(row, T))
+    for i, p in enumerate(back):
+        if free + i < R:
+            ring[(head + free + i) % R] = int(p)
+    return {**{k: np.asarray(v) for k, v in out.items()}, "ring": np.asarray(ring), "tables": tables, "head": (head + used) % R,
+            "free": min(free + len(back), R) - used}

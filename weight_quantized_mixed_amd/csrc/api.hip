@@ -698,16 +698,142 @@ qgemm_status check_cache(const qgemm_kv_cache* c, int64_t T, int32_t q_heads) {
 
 // the sizes of an attention call, checked
 qgemm_status attention_shape(const qgemm_kv_cache* c, int64_t T, int32_t q_heads, int64_t B, int64_t max_q,
-                             int64_t max_len, int64_t prefix_len, AttnShape* s) {
+                             int64_t max_len, int64_t prefix_len, int64_t window, int64_t sinks, AttnShape* s) {
   const qgemm_status st = check_cache(c, T, q_heads);
   if (st != QGEMM_OK) return st;
   const int64_t least = T > 0 ? 1 : 0;  // a batch without queries may be without sequences too
   if (B < least || max_q < least || max_len < 0 || prefix_len < 0) return QGEMM_ERR_INVALID_ARG;
   if (B > 65535 || max_q > INT32_MAX || max_len > INT32_MAX || prefix_len > INT32_MAX) return QGEMM_ERR_UNSUPPORTED;
   if (max_len + prefix_len > INT32_MAX - 65536) return QGEMM_ERR_UNSUPPORTED;  // key positions are 32 bits wide
-  *s = {T, B, max_q < T ? max_q : T, max_len, prefix_len, q_heads, c->kv_heads, c->head_dim};
+  if (window < 0 || sinks < 0) return QGEMM_ERR_INVALID_ARG;
+  if (window > INT32_MAX || sinks > INT32_MAX) return QGEMM_ERR_UNSUPPORTED;
+  *s = {T, B, max_q < T ? max_q : T, max_len, prefix_len, q_heads, c->kv_heads, c->head_dim, window, sinks};
   if (T > 0 && !attention_grid_fits(*s)) return QGEMM_ERR_UNSUPPORTED;
   return QGEMM_OK;
+}
+
+// every address a multiple of mask + 1
+template <typename... P>
+bool aligned(uintptr_t mask, P... p) {
+  return (((reinterpret_cast<uintptr_t>(p)) | ...) & mask) == 0;
+}
+
+// the arguments of an append, checked and filled in (not where T is 0)
+qgemm_status append_args(const qgemm_kv_cache* cache, int64_t T, int32_t q_heads, const void* q, int64_t q_stride,
+                         const void* k, int64_t k_stride, const void* v, int64_t v_stride, const float* cos,
+                         const float* sin, int64_t n_positions, int32_t rot_dim, int32_t interleaved,
+                         const int32_t* positions, const int64_t* slots, void* q_out, AppendArgs* out) {
+  const qgemm_status s = check_cache(cache, T, q_heads);
+  if (s != QGEMM_OK) return s;
+  const int64_t kv_row = (int64_t)cache->kv_heads * cache->head_dim;
+  if (rot_dim < 0 || rot_dim % 2 != 0 || rot_dim > cache->head_dim) return QGEMM_ERR_INVALID_ARG;
+  if (interleaved != 0 && interleaved != 1) return QGEMM_ERR_INVALID_ARG;
+  if (q_stride < (int64_t)q_heads * cache->head_dim || k_stride < kv_row || v_stride < kv_row)
+    return QGEMM_ERR_INVALID_ARG;
+  // a token's pairs fit the grid's second dimension, one a thread
+  if (((int64_t)q_heads + 2 * cache->kv_heads) * cache->head_dim / 2 > (int64_t)65535 * 256) return QGEMM_ERR_UNSUPPORTED;
+  if (T == 0) return QGEMM_OK;
+  if (!q || !k || !v || !slots || !q_out) return QGEMM_ERR_INVALID_ARG;
+  if (rot_dim && (!cos || !sin || !positions || n_positions < 1)) return QGEMM_ERR_INVALID_ARG;
+  if (!aligned(1, q, k, v, q_out) || !aligned(3, cos, sin, positions) || !aligned(7, slots)) return QGEMM_ERR_INVALID_ARG;
+  AppendArgs& a = *out;
+  a.q = static_cast<const _Float16*>(q);
+  a.k = static_cast<const _Float16*>(k);
+  a.v = static_cast<const _Float16*>(v);
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.cos = cos;
+  a.sin = sin;
+  a.positions = positions;
+  a.slots = slots;
+  a.q_out = static_cast<_Float16*>(q_out);
+  a.k_cache = static_cast<_Float16*>(cache->k);
+  a.v_cache = static_cast<_Float16*>(cache->v);
+  a.n_positions = n_positions;
+  a.n_pages = cache->n_pages;
+  a.page = cache->page_size;
+  a.q_heads = q_heads;
+  a.kv_heads = cache->kv_heads;
+  a.D = cache->head_dim;
+  a.rot = rot_dim;
+  a.interleaved = interleaved;
+  return QGEMM_OK;
+}
+
+// (0 would make NaN of a head of zeros)
+bool norm_eps_ok(float eps) { return eps > 0.f && eps <= 3.402823466e38f; }
+
+// the sizes of normed and rotated rows without a cache
+qgemm_status check_norm(int64_t T, int32_t q_heads, int32_t kv_heads, int32_t D, int64_t q_stride, int64_t k_stride,
+                        float eps, int32_t rot_dim, int32_t interleaved) {
+  if (T < 0 || q_heads < 1 || kv_heads < 1 || D < 1 || !norm_eps_ok(eps)) return QGEMM_ERR_INVALID_ARG;
+  if (D % 8 != 0 || D > 256 || T > INT32_MAX || q_heads > 65535 || kv_heads > 65535) return QGEMM_ERR_UNSUPPORTED;
+  if (rot_dim < 0 || rot_dim % 2 != 0 || rot_dim > D) return QGEMM_ERR_INVALID_ARG;
+  if (interleaved != 0 && interleaved != 1) return QGEMM_ERR_INVALID_ARG;
+  if (q_stride < (int64_t)q_heads * D || k_stride < (int64_t)kv_heads * D) return QGEMM_ERR_INVALID_ARG;
+  return QGEMM_OK;
+}
+
+// ... and of their gradients: heads of all tokens are counted in 31 bits
+qgemm_status check_norm_grad(int64_t T, int32_t q_heads, int32_t kv_heads, int32_t D) {
+  if (T < 0 || q_heads < 1 || kv_heads < 1 || D < 1) return QGEMM_ERR_INVALID_ARG;
+  if (D % 8 != 0 || D > 256 || q_heads > 65535 || kv_heads > 65535) return QGEMM_ERR_UNSUPPORTED;
+  if (T > INT32_MAX / (q_heads > kv_heads ? q_heads : kv_heads)) return QGEMM_ERR_UNSUPPORTED;
+  return QGEMM_OK;
+}
+
+// an attention call (window 0: none)
+qgemm_status attention_impl(const qgemm_kv_cache* cache, int64_t T, int32_t q_heads, const void* q, int64_t q_stride,
+                            int64_t B, const int32_t* q_starts, const int32_t* kv_lens, const int32_t* tables,
+                            int64_t table_width, const int32_t* prefix_table, int64_t prefix_len, int64_t max_q,
+                            int64_t max_len, int64_t window, int64_t sinks, float scale, void* out, float* lse,
+                            void* workspace, size_t workspace_bytes, void* stream) {
+  AttnShape s;
+  const qgemm_status st = attention_shape(cache, T, q_heads, B, max_q, max_len, prefix_len, window, sinks, &s);
+  if (st != QGEMM_OK) return st;
+  if (table_width < 0 || q_stride < (int64_t)q_heads * cache->head_dim) return QGEMM_ERR_INVALID_ARG;
+  if (T == 0) return QGEMM_OK;
+  // scores are scaled by scale log2 e: an infinite one would make NaN of a score of 0
+  if (!(scale > 0.f) || !(scale * 1.4426950408889634f <= 3.402823466e38f)) return QGEMM_ERR_INVALID_ARG;
+  if (!q || !q_starts || !kv_lens || !out || (table_width && !tables) || (prefix_len && !prefix_table))
+    return QGEMM_ERR_INVALID_ARG;
+  if (q_stride % 8 != 0 || ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out)) & 15))
+    return QGEMM_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(q_starts) | reinterpret_cast<uintptr_t>(kv_lens) |
+       reinterpret_cast<uintptr_t>(tables) | reinterpret_cast<uintptr_t>(prefix_table) |
+       reinterpret_cast<uintptr_t>(lse)) & 3)
+    return QGEMM_ERR_INVALID_ARG;
+  const size_t need = attention_ws_bytes(s);
+  if (need && (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 15)))
+    return QGEMM_ERR_INVALID_ARG;
+  WindowArgs a;
+  a.q = static_cast<const _Float16*>(q);
+  a.k = static_cast<const _Float16*>(cache->k);
+  a.v = static_cast<const _Float16*>(cache->v);
+  a.out = static_cast<_Float16*>(out);
+  a.lse = lse;
+  a.q_starts = q_starts;
+  a.kv_lens = kv_lens;
+  a.tables = tables;
+  a.prefix_table = prefix_table;
+  a.q_stride = q_stride;
+  a.table_width = table_width;
+  a.prefix_len = prefix_len;
+  a.T = (int32_t)T;
+  a.q_heads = q_heads;
+  a.kv_heads = cache->kv_heads;
+  a.D = cache->head_dim;
+  a.n_pages = (int32_t)cache->n_pages;
+  a.page_shift = __builtin_ctz((unsigned)cache->page_size);
+  a.max_q = (int32_t)s.max_q;
+  a.max_len = (int32_t)max_len;
+  a.scale = scale;
+  a.window = (int32_t)s.window;
+  a.sinks = (int32_t)s.sinks;
+  (void)hipGetLastError();
+  hipError_t e = launch_attention(a, s, workspace, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? QGEMM_OK : QGEMM_ERR_DEVICE;
 }
 
 }  // namespace
@@ -909,48 +1035,183 @@ qgemm_status qgemm_kv_append(const qgemm_kv_cache* cache, int64_t T, int32_t q_h
                              const void* k, int64_t k_stride, const void* v, int64_t v_stride, const float* cos,
                              const float* sin, int64_t n_positions, int32_t rot_dim, int32_t interleaved,
                              const int32_t* positions, const int64_t* slots, void* q_out, void* stream) {
-  const qgemm_status s = check_cache(cache, T, q_heads);
-  if (s != QGEMM_OK) return s;
-  const int64_t kv_row = (int64_t)cache->kv_heads * cache->head_dim;
-  if (rot_dim < 0 || rot_dim % 2 != 0 || rot_dim > cache->head_dim) return QGEMM_ERR_INVALID_ARG;
-  if (interleaved != 0 && interleaved != 1) return QGEMM_ERR_INVALID_ARG;
-  if (q_stride < (int64_t)q_heads * cache->head_dim || k_stride < kv_row || v_stride < kv_row)
-    return QGEMM_ERR_INVALID_ARG;
-  // a token's pairs fit the grid's second dimension, one a thread
-  if (((int64_t)q_heads + 2 * cache->kv_heads) * cache->head_dim / 2 > (int64_t)65535 * 256) return QGEMM_ERR_UNSUPPORTED;
-  if (T == 0) return QGEMM_OK;
-  if (!q || !k || !v || !slots || !q_out) return QGEMM_ERR_INVALID_ARG;
-  if (rot_dim && (!cos || !sin || !positions || n_positions < 1)) return QGEMM_ERR_INVALID_ARG;
-  if (((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v) |
-        reinterpret_cast<uintptr_t>(q_out)) & 1) ||
-      ((reinterpret_cast<uintptr_t>(cos) | reinterpret_cast<uintptr_t>(sin) |
-        reinterpret_cast<uintptr_t>(positions)) & 3) ||
-      (reinterpret_cast<uintptr_t>(slots) & 7))
-    return QGEMM_ERR_INVALID_ARG;
   AppendArgs a;
+  const qgemm_status s = append_args(cache, T, q_heads, q, q_stride, k, k_stride, v, v_stride, cos, sin, n_positions,
+                                     rot_dim, interleaved, positions, slots, q_out, &a);
+  if (s != QGEMM_OK || T == 0) return s;
+  (void)hipGetLastError();
+  hipError_t e = launch_kv_append(a, T, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? QGEMM_OK : QGEMM_ERR_DEVICE;
+}
+
+qgemm_status qgemm_kv_append_norm(const qgemm_kv_cache* cache, int64_t T, int32_t q_heads, const void* q, int64_t q_stride,
+                                  const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                                  const void* q_weight, const void* k_weight, float eps, const float* cos,
+                                  const float* sin, int64_t n_positions, int32_t rot_dim, int32_t interleaved,
+                                  const int32_t* positions, const int64_t* slots, void* q_out, void* stream) {
+  NormArgs a;
+  const qgemm_status s = append_args(cache, T, q_heads, q, q_stride, k, k_stride, v, v_stride, cos, sin, n_positions,
+                                     rot_dim, interleaved, positions, slots, q_out, &a);
+  if (s != QGEMM_OK) return s;
+  if (!norm_eps_ok(eps) || !aligned(1, q_weight, k_weight)) return QGEMM_ERR_INVALID_ARG;
+  if (T == 0) return QGEMM_OK;
+  a.q_weight = static_cast<const _Float16*>(q_weight);
+  a.k_weight = static_cast<const _Float16*>(k_weight);
+  a.k_out = nullptr;
+  a.eps = eps;
+  (void)hipGetLastError();
+  hipError_t e = launch_norm_rotate(a, T, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? QGEMM_OK : QGEMM_ERR_DEVICE;
+}
+
+qgemm_status qgemm_norm_rotate(int64_t T, int32_t q_heads, int32_t kv_heads, int32_t head_dim, const void* q,
+                               int64_t q_stride, const void* k, int64_t k_stride, const void* q_weight,
+                               const void* k_weight, float eps, const float* cos, const float* sin,
+                               int64_t n_positions, int32_t rot_dim, int32_t interleaved, const int32_t* positions,
+                               void* q_out, void* k_out, void* stream) {
+  const qgemm_status s = check_norm(T, q_heads, kv_heads, head_dim, q_stride, k_stride, eps, rot_dim, interleaved);
+  if (s != QGEMM_OK || T == 0) return s;
+  if (!q || !k || !q_out || !k_out) return QGEMM_ERR_INVALID_ARG;
+  if (rot_dim && (!cos || !sin || !positions || n_positions < 1)) return QGEMM_ERR_INVALID_ARG;
+  if (!aligned(1, q, k, q_weight, k_weight, q_out, k_out) || !aligned(3, cos, sin, positions)) return QGEMM_ERR_INVALID_ARG;
+  NormArgs a = {};
   a.q = static_cast<const _Float16*>(q);
   a.k = static_cast<const _Float16*>(k);
-  a.v = static_cast<const _Float16*>(v);
   a.q_stride = q_stride;
   a.k_stride = k_stride;
-  a.v_stride = v_stride;
   a.cos = cos;
   a.sin = sin;
   a.positions = positions;
-  a.slots = slots;
   a.q_out = static_cast<_Float16*>(q_out);
-  a.k_cache = static_cast<_Float16*>(cache->k);
-  a.v_cache = static_cast<_Float16*>(cache->v);
+  a.k_out = static_cast<_Float16*>(k_out);
   a.n_positions = n_positions;
-  a.n_pages = cache->n_pages;
-  a.page = cache->page_size;
+  a.page = 1;
   a.q_heads = q_heads;
-  a.kv_heads = cache->kv_heads;
-  a.D = cache->head_dim;
+  a.kv_heads = kv_heads;
+  a.D = head_dim;
   a.rot = rot_dim;
   a.interleaved = interleaved;
+  a.q_weight = static_cast<const _Float16*>(q_weight);
+  a.k_weight = static_cast<const _Float16*>(k_weight);
+  a.eps = eps;
   (void)hipGetLastError();
-  hipError_t e = launch_kv_append(a, T, static_cast<hipStream_t>(stream));
+  hipError_t e = launch_norm_rotate(a, T, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? QGEMM_OK : QGEMM_ERR_DEVICE;
+}
+
+qgemm_status qgemm_norm_rotate_backward_workspace(int64_t T, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+                                                  int32_t weight_grads, size_t* workspace_bytes) {
+  if (!workspace_bytes) return QGEMM_ERR_INVALID_ARG;
+  const qgemm_status s = check_norm_grad(T, q_heads, kv_heads, head_dim);
+  if (s == QGEMM_OK) *workspace_bytes = weight_grads ? norm_grad_ws_bytes(T, q_heads, kv_heads, head_dim) : 0;
+  return s;
+}
+
+qgemm_status qgemm_norm_rotate_backward(int64_t T, int32_t q_heads, int32_t kv_heads, int32_t head_dim, const void* q,
+                                        int64_t q_stride, const void* k, int64_t k_stride, const void* q_weight,
+                                        const void* k_weight, float eps, const float* cos, const float* sin,
+                                        int64_t n_positions, int32_t rot_dim, int32_t interleaved,
+                                        const int32_t* positions, const void* dq_out, const void* dk_out, void* dq,
+                                        int64_t dq_stride, void* dk, int64_t dk_stride, float* dq_weight,
+                                        float* dk_weight, void* workspace, size_t workspace_bytes, void* stream) {
+  qgemm_status s = check_norm(T, q_heads, kv_heads, head_dim, q_stride, k_stride, eps, rot_dim, interleaved);
+  if (s == QGEMM_OK) s = check_norm_grad(T, q_heads, kv_heads, head_dim);
+  if (s != QGEMM_OK) return s;
+  if (dq_stride < (int64_t)q_heads * head_dim || dk_stride < (int64_t)kv_heads * head_dim) return QGEMM_ERR_INVALID_ARG;
+  const bool weights = dq_weight || dk_weight;
+  if (T == 0 && !weights) return QGEMM_OK;
+  if (T && (!q || !k || !dq_out || !dk_out || !dq || !dk)) return QGEMM_ERR_INVALID_ARG;
+  if (T && rot_dim && (!cos || !sin || !positions || n_positions < 1)) return QGEMM_ERR_INVALID_ARG;
+  if (!aligned(1, q, k, q_weight, k_weight, dq_out, dk_out, dq, dk) ||
+      !aligned(3, cos, sin, positions, dq_weight, dk_weight))
+    return QGEMM_ERR_INVALID_ARG;
+  if (weights && (!workspace || workspace_bytes < norm_grad_ws_bytes(T, q_heads, kv_heads, head_dim) || !aligned(15, workspace)))
+    return QGEMM_ERR_INVALID_ARG;
+  NormGradArgs a;
+  a.q = static_cast<const _Float16*>(q);
+  a.k = static_cast<const _Float16*>(k);
+  a.dq_out = static_cast<const _Float16*>(dq_out);
+  a.dk_out = static_cast<const _Float16*>(dk_out);
+  a.q_weight = static_cast<const _Float16*>(q_weight);
+  a.k_weight = static_cast<const _Float16*>(k_weight);
+  a.dq = static_cast<_Float16*>(dq);
+  a.dk = static_cast<_Float16*>(dk);
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.dq_stride = dq_stride;
+  a.dk_stride = dk_stride;
+  a.n_positions = n_positions;
+  a.cos = cos;
+  a.sin = sin;
+  a.positions = positions;
+  a.dq_weight = dq_weight;
+  a.dk_weight = dk_weight;
+  a.part = static_cast<float*>(workspace);
+  a.T = (int32_t)T;
+  a.q_heads = q_heads;
+  a.kv_heads = kv_heads;
+  a.D = head_dim;
+  a.rot = rot_dim;
+  a.interleaved = interleaved;
+  a.eps = eps;
+  (void)hipGetLastError();
+  hipError_t e = launch_norm_rotate_grad(a, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? QGEMM_OK : QGEMM_ERR_DEVICE;
+}
+
+qgemm_status qgemm_kv_extend_workspace(int64_t B, int64_t T, size_t* workspace_bytes) {
+  if (!workspace_bytes || B < 0 || T < 0) return QGEMM_ERR_INVALID_ARG;
+  if (B > 65535 || T > INT32_MAX) return QGEMM_ERR_UNSUPPORTED;
+  *workspace_bytes = extend_ws_bytes(B, T);
+  return QGEMM_OK;
+}
+
+qgemm_status qgemm_kv_extend(int64_t B, int64_t T, int32_t page_size, const int32_t* new_tokens, const int32_t* lens,
+                             const int32_t* gone, const int32_t* ring_state, int32_t* ring, int64_t ring_size,
+                             int32_t* tables, int64_t table_width, int64_t prefix_len, int64_t window, int64_t sinks,
+                             int32_t* q_starts, int32_t* lens_out, int32_t* gone_out, int32_t* ring_state_out,
+                             int32_t* positions, int64_t* slots, int32_t* refused, void* workspace,
+                             size_t workspace_bytes, void* stream) {
+  if (B < 0 || T < 0 || ring_size < 1 || table_width < 0 || prefix_len < 0 || window < 0 || sinks < 0 || page_size < 1)
+    return QGEMM_ERR_INVALID_ARG;
+  if ((page_size & (page_size - 1)) != 0 || page_size > 65536) return QGEMM_ERR_UNSUPPORTED;
+  if (B > 65535 || T > INT32_MAX || ring_size > INT32_MAX || table_width > INT32_MAX || prefix_len > INT32_MAX ||
+      window > INT32_MAX || sinks > INT32_MAX)
+    return QGEMM_ERR_UNSUPPORTED;
+  if (!ring_state || !ring || !q_starts || !ring_state_out) return QGEMM_ERR_INVALID_ARG;
+  if (B && (!new_tokens || !lens || !gone || !lens_out || !gone_out || !refused || (table_width && !tables)))
+    return QGEMM_ERR_INVALID_ARG;
+  if (T && (!positions || !slots)) return QGEMM_ERR_INVALID_ARG;
+  if (!aligned(3, new_tokens, lens, gone, ring_state, ring, tables, q_starts, lens_out, gone_out, ring_state_out, positions,
+               refused) || !aligned(7, slots))
+    return QGEMM_ERR_INVALID_ARG;
+  const size_t need = extend_ws_bytes(B, T);
+  if (need && (!workspace || workspace_bytes < need || !aligned(15, workspace))) return QGEMM_ERR_INVALID_ARG;
+  ExtendArgs a;
+  a.new_tokens = new_tokens;
+  a.lens = lens;
+  a.gone = gone;
+  a.ring_state = ring_state;
+  a.ring = ring;
+  a.tables = tables;
+  a.q_starts = q_starts;
+  a.lens_out = lens_out;
+  a.gone_out = gone_out;
+  a.ring_state_out = ring_state_out;
+  a.refused = refused;
+  a.positions = positions;
+  a.slots = slots;
+  a.scratch = workspace;
+  a.table_width = table_width;
+  a.prefix_len = prefix_len;
+  a.window = window;
+  a.B = (int32_t)B;
+  a.T = (int32_t)T;
+  a.ring_size = (int32_t)ring_size;
+  a.page_shift = __builtin_ctz((unsigned)page_size);
+  a.first_page = sinks > prefix_len ? (int32_t)((sinks - prefix_len + page_size - 1) / page_size) : 0;
+  (void)hipGetLastError();
+  hipError_t e = launch_kv_extend(a, static_cast<hipStream_t>(stream));
   return e == hipSuccess ? QGEMM_OK : QGEMM_ERR_DEVICE;
 }
 
@@ -958,7 +1219,17 @@ qgemm_status qgemm_attention_workspace(const qgemm_kv_cache* cache, int64_t T, i
                                        int64_t max_q, int64_t max_len, int64_t prefix_len, size_t* workspace_bytes) {
   if (!workspace_bytes) return QGEMM_ERR_INVALID_ARG;
   AttnShape s;
-  const qgemm_status st = attention_shape(cache, T, q_heads, B, max_q, max_len, prefix_len, &s);
+  const qgemm_status st = attention_shape(cache, T, q_heads, B, max_q, max_len, prefix_len, 0, 0, &s);
+  if (st == QGEMM_OK) *workspace_bytes = T == 0 ? 0 : attention_ws_bytes(s);
+  return st;
+}
+
+qgemm_status qgemm_attention_window_workspace(const qgemm_kv_cache* cache, int64_t T, int32_t q_heads, int64_t B,
+                                              int64_t max_q, int64_t max_len, int64_t prefix_len, int64_t window,
+                                              int64_t sinks, size_t* workspace_bytes) {
+  if (!workspace_bytes || window < 1) return QGEMM_ERR_INVALID_ARG;
+  AttnShape s;
+  const qgemm_status st = attention_shape(cache, T, q_heads, B, max_q, max_len, prefix_len, window, sinks, &s);
   if (st == QGEMM_OK) *workspace_bytes = T == 0 ? 0 : attention_ws_bytes(s);
   return st;
 }
@@ -968,49 +1239,19 @@ qgemm_status qgemm_attention(const qgemm_kv_cache* cache, int64_t T, int32_t q_h
                              int64_t table_width, const int32_t* prefix_table, int64_t prefix_len, int64_t max_q,
                              int64_t max_len, float scale, void* out, float* lse, void* workspace,
                              size_t workspace_bytes, void* stream) {
-  AttnShape s;
-  const qgemm_status st = attention_shape(cache, T, q_heads, B, max_q, max_len, prefix_len, &s);
-  if (st != QGEMM_OK) return st;
-  if (table_width < 0 || q_stride < (int64_t)q_heads * cache->head_dim) return QGEMM_ERR_INVALID_ARG;
-  if (T == 0) return QGEMM_OK;
-  // scores are scaled by scale log2 e: an infinite one would make NaN of a score of 0
-  if (!(scale > 0.f) || !(scale * 1.4426950408889634f <= 3.402823466e38f)) return QGEMM_ERR_INVALID_ARG;
-  if (!q || !q_starts || !kv_lens || !out || (table_width && !tables) || (prefix_len && !prefix_table))
-    return QGEMM_ERR_INVALID_ARG;
-  if (q_stride % 8 != 0 || ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out)) & 15))
-    return QGEMM_ERR_INVALID_ARG;
-  if ((reinterpret_cast<uintptr_t>(q_starts) | reinterpret_cast<uintptr_t>(kv_lens) |
-       reinterpret_cast<uintptr_t>(tables) | reinterpret_cast<uintptr_t>(prefix_table) |
-       reinterpret_cast<uintptr_t>(lse)) & 3)
-    return QGEMM_ERR_INVALID_ARG;
-  const size_t need = attention_ws_bytes(s);
-  if (need && (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 15)))
-    return QGEMM_ERR_INVALID_ARG;
-  AttnArgs a;
-  a.q = static_cast<const _Float16*>(q);
-  a.k = static_cast<const _Float16*>(cache->k);
-  a.v = static_cast<const _Float16*>(cache->v);
-  a.out = static_cast<_Float16*>(out);
-  a.lse = lse;
-  a.q_starts = q_starts;
-  a.kv_lens = kv_lens;
-  a.tables = tables;
-  a.prefix_table = prefix_table;
-  a.q_stride = q_stride;
-  a.table_width = table_width;
-  a.prefix_len = prefix_len;
-  a.T = (int32_t)T;
-  a.q_heads = q_heads;
-  a.kv_heads = cache->kv_heads;
-  a.D = cache->head_dim;
-  a.n_pages = (int32_t)cache->n_pages;
-  a.page_shift = __builtin_ctz((unsigned)cache->page_size);
-  a.max_q = (int32_t)s.max_q;
-  a.max_len = (int32_t)max_len;
-  a.scale = scale;
-  (void)hipGetLastError();
-  hipError_t e = launch_attention(a, s, workspace, static_cast<hipStream_t>(stream));
-  return e == hipSuccess ? QGEMM_OK : QGEMM_ERR_DEVICE;
+  return attention_impl(cache, T, q_heads, q, q_stride, B, q_starts, kv_lens, tables, table_width, prefix_table, prefix_len,
+                        max_q, max_len, 0, 0, scale, out, lse, workspace, workspace_bytes, stream);
+}
+
+qgemm_status qgemm_attention_window(const qgemm_kv_cache* cache, int64_t T, int32_t q_heads, const void* q,
+                                    int64_t q_stride, int64_t B, const int32_t* q_starts, const int32_t* kv_lens,
+                                    const int32_t* tables, int64_t table_width, const int32_t* prefix_table,
+                                    int64_t prefix_len, int64_t max_q, int64_t max_len, int64_t window, int64_t sinks,
+                                    float scale, void* out, float* lse, void* workspace, size_t workspace_bytes,
+                                    void* stream) {
+  if (window < 1) return QGEMM_ERR_INVALID_ARG;
+  return attention_impl(cache, T, q_heads, q, q_stride, B, q_starts, kv_lens, tables, table_width, prefix_table, prefix_len,
+                        max_q, max_len, window, sinks, scale, out, lse, workspace, workspace_bytes, stream);
 }
 
 qgemm_status qgemm_quantize_rows(const void* A, int64_t M, int64_t K, void* Q, float* scales, void* stream) {

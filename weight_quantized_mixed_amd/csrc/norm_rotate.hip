@@ -1,0 +1,366 @@
+// Norms of queries and keys for each head with the rotation of their positions in one pass,
+// and the gradients of both.
+//
+//   r = (mean x^2 + eps)^(-1/2),  n = x r w,  y = R(p) n
+//   g = R(-p) dy,  dw = sum x r g,  h = g w,  dx = r h - x r^3 mean(x h)
+// with R(p) the rotation of the pairs by the angles of position p, whose transpose is its
+// inverse for angles on the unit circle (for any others g takes the transpose, as a gradient
+// does).
+//
+// Every value is read once and written once, so the passes are bound by HBM (long prompts) or
+// by the launch (a decode batch).  A head belongs to LPH lanes (4, 8 or 16 for up to 64, 128 or
+// 256 values) of 16 values each, which are whole pairs: its sums are taken over those lanes by
+// DPP, its pairs turn in registers, and nothing passes through LDS.  A lane's values are 8 / V
+// pieces of V pairs, where V is what alignment, strides and sizes allow in one access each.
+//
+// The gradient of a norm's weight sums over tokens and heads: each lane adds up its own places
+// over the rows that its workgroup walks, the workgroup joins its lanes and leaves one row of
+// partial sums, and a second pass adds those in order (bitwise reproducible).
+#include <type_traits>
+
+#include "qgemm_internal.hpp"
+
+namespace qg {
+namespace {
+
+template <int V>
+struct Vec {
+  typedef _Float16 h __attribute__((ext_vector_type(V)));
+  typedef float f __attribute__((ext_vector_type(V)));
+};
+
+// sum over the LPH lanes of a head, in all of them
+template <int CTRL>
+__device__ __forceinline__ float add_dpp(float v) {
+  return v + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF, true));
+}
+template <int LPH>
+__device__ __forceinline__ float head_sum(float v) {
+  v = add_dpp<0xB1>(v);                             // lanes 1 0 3 2 of each four
+  v = add_dpp<0x4E>(v);                             // lanes 2 3 0 1
+  if constexpr (LPH >= 8) v = add_dpp<0x141>(v);    // the other four of each eight (mirrored)
+  if constexpr (LPH >= 16) v = add_dpp<0x140>(v);   // the other eight of each sixteen
+  return v;
+}
+
+// where a lane's piece c of a head lies: places of its two V-vectors, and whether they turn
+template <int V, bool INTERLEAVED>
+struct Piece {
+  int o0, o1, j;
+  bool live, turn;
+  __device__ __forceinline__ Piece(int c, int D, int half, bool turns) {
+    j = c * V;
+    live = j < D / 2;
+    turn = turns && j < half;
+    o0 = turn && !INTERLEAVED ? j : 2 * j;
+    o1 = turn && !INTERLEAVED ? j + half : 2 * j + V;
+  }
+};
+
+// places of pair e among the 2 V values of a turned piece
+template <int V, bool INTERLEAVED>
+__device__ __forceinline__ int first_of(int e) { return INTERLEAVED ? 2 * e : e; }
+template <int V, bool INTERLEAVED>
+__device__ __forceinline__ int second_of(int e) { return INTERLEAVED ? 2 * e + 1 : V + e; }
+
+template <int V>
+__device__ __forceinline__ void read(const _Float16* from, int o0, int o1, float* x) {
+  typedef typename Vec<V>::h hv;
+  const hv a = *reinterpret_cast<const hv*>(from + o0), b = *reinterpret_cast<const hv*>(from + o1);
+#pragma unroll
+  for (int e = 0; e < V; ++e) {
+    x[e] = (float)a[e];
+    x[V + e] = (float)b[e];
+  }
+}
+template <int V>
+__device__ __forceinline__ void write(_Float16* to, int o0, int o1, const float* x) {
+  typedef typename Vec<V>::h hv;
+  hv a, b;
+#pragma unroll
+  for (int e = 0; e < V; ++e) {
+    a[e] = (_Float16)x[e];
+    b[e] = (_Float16)x[V + e];
+  }
+  *reinterpret_cast<hv*>(to + o0) = a;
+  *reinterpret_cast<hv*>(to + o1) = b;
+}
+
+// turns the pairs of a piece by the angles of position pos, or back (BACK: the transpose)
+template <int V, bool INTERLEAVED, bool BACK>
+__device__ __forceinline__ void rotate(float* x, const float* cos, const float* sin, int64_t at) {
+  typedef typename Vec<V>::f fv;
+  const fv c = *reinterpret_cast<const fv*>(cos + at), s = *reinterpret_cast<const fv*>(sin + at);
+#pragma unroll
+  for (int e = 0; e < V; ++e) {
+    const int ia = first_of<V, INTERLEAVED>(e), ib = second_of<V, INTERLEAVED>(e);
+    const float p = x[ia], q = x[ib], t = BACK ? -s[e] : s[e];
+    x[ia] = p * c[e] - q * t;
+    x[ib] = q * c[e] + p * t;
+  }
+}
+
+// Forward.  Heads of a token in order: queries, keys, and with a cache the values (copied).
+template <int V, int LPH, bool INTERLEAVED>
+__global__ __launch_bounds__(256) void norm_rotate_kernel(NormArgs a, int tokens, int per_block) {
+  constexpr int PIECES = 8 / V;
+  const int sub = threadIdx.x % LPH, group = blockIdx.y * (256 / LPH) + threadIdx.x / LPH;
+  const int heads = a.q_heads + (a.k_out ? 1 : 2) * a.kv_heads;
+  const int dt = per_block > 1 ? group / heads : 0, h = group - dt * heads;
+  const int64_t t = (int64_t)blockIdx.x * per_block + dt;
+  if (h >= heads || dt >= per_block || t >= tokens) return;
+  const int half = a.rot / 2;
+  const bool is_q = h < a.q_heads, is_v = h >= a.q_heads + a.kv_heads;
+
+  const int64_t pos = a.rot ? a.positions[t] : 0;
+  const bool pos_ok = !a.rot || (pos >= 0 && pos < a.n_positions);
+  const int64_t slot = a.k_out ? 0 : a.slots[t];
+  if (!is_q && !a.k_out && !(pos_ok && slot >= 0 && slot < a.n_pages * a.page)) return;
+  const _Float16* src;
+  _Float16* dst;
+  if (is_q) {
+    src = a.q + t * a.q_stride + (int64_t)h * a.D;
+    dst = a.q_out + (t * a.q_heads + h) * a.D;
+  } else {
+    const int kh = is_v ? h - a.q_heads - a.kv_heads : h - a.q_heads;
+    src = (is_v ? a.v + t * a.v_stride : a.k + t * a.k_stride) + (int64_t)kh * a.D;
+    const int64_t page = slot / a.page, in_page = slot - page * a.page;
+    if (a.k_out) dst = a.k_out + (t * a.kv_heads + kh) * a.D;
+    else dst = (is_v ? a.v_cache : a.k_cache) + ((page * a.kv_heads + kh) * a.page + in_page) * a.D;
+  }
+
+  if (is_v) {  // as it is, bit by bit
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i) {
+      typedef typename Vec<V>::h hv;
+      const Piece<V, INTERLEAVED> p(i * LPH + sub, a.D, half, false);
+      if (!p.live) continue;
+      *reinterpret_cast<hv*>(dst + p.o0) = *reinterpret_cast<const hv*>(src + p.o0);
+      *reinterpret_cast<hv*>(dst + p.o1) = *reinterpret_cast<const hv*>(src + p.o1);
+    }
+    return;
+  }
+  float x[PIECES][2 * V], sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < PIECES; ++i) {
+    const Piece<V, INTERLEAVED> p(i * LPH + sub, a.D, half, true);
+    if (!p.live) continue;
+    read<V>(src, p.o0, p.o1, x[i]);
+#pragma unroll
+    for (int e = 0; e < 2 * V; ++e) sum = __builtin_fmaf(x[i][e], x[i][e], sum);
+  }
+  const float r = rsqrtf(head_sum<LPH>(sum) / (float)a.D + a.eps);
+  const _Float16* w = is_q ? a.q_weight : a.k_weight;
+#pragma unroll
+  for (int i = 0; i < PIECES; ++i) {
+    const Piece<V, INTERLEAVED> p(i * LPH + sub, a.D, half, true);
+    if (!p.live) continue;
+#pragma unroll
+    for (int e = 0; e < 2 * V; ++e) x[i][e] *= r;
+    if (w) {
+      float f[2 * V];
+      read<V>(w, p.o0, p.o1, f);
+#pragma unroll
+      for (int e = 0; e < 2 * V; ++e) x[i][e] *= f[e];
+    }
+    if (!pos_ok) {
+#pragma unroll
+      for (int e = 0; e < 2 * V; ++e) x[i][e] = __builtin_nanf("");
+    } else if (p.turn) {
+      rotate<V, INTERLEAVED, false>(x[i], a.cos, a.sin, pos * half + p.j);
+    }
+    write<V>(dst, p.o0, p.o1, x[i]);
+  }
+}
+
+// most workgroups of the gradients of queries, and of keys: each leaves a row of partial sums
+constexpr int GRAD_BLOCKS = 1024;
+
+// Gradients: blockIdx.y 0 walks the rows (token, head) of the queries, 1 those of the keys.
+template <int V, int LPH, bool INTERLEAVED>
+__global__ __launch_bounds__(256) void norm_rotate_grad_kernel(NormGradArgs a) {
+  constexpr int PIECES = 8 / V, GROUPS = 256 / LPH;
+  __shared__ float sums[4][256];
+  const bool is_k = blockIdx.y != 0;
+  const int sub = threadIdx.x % LPH, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int heads = is_k ? a.kv_heads : a.q_heads, half = a.rot / 2;
+  const _Float16* X = is_k ? a.k : a.q;
+  const _Float16* DY = is_k ? a.dk_out : a.dq_out;
+  _Float16* DX = is_k ? a.dk : a.dq;
+  const int64_t stride = is_k ? a.k_stride : a.q_stride, out_stride = is_k ? a.dk_stride : a.dq_stride;
+  const _Float16* w = is_k ? a.k_weight : a.q_weight;
+  float* dw = is_k ? a.dk_weight : a.dq_weight;
+  const uint32_t rows = (uint32_t)a.T * (uint32_t)heads;  // below 2^31 (checked)
+
+  float acc[PIECES][2 * V], wf[PIECES][2 * V];
+#pragma unroll
+  for (int i = 0; i < PIECES; ++i) {
+    const Piece<V, INTERLEAVED> p(i * LPH + sub, a.D, half, true);
+#pragma unroll
+    for (int e = 0; e < 2 * V; ++e) acc[i][e] = 0.f, wf[i][e] = 1.f;
+    if (w && p.live) read<V>(w, p.o0, p.o1, wf[i]);
+  }
+  for (uint32_t row = blockIdx.x * GROUPS + threadIdx.x / LPH; row < rows; row += gridDim.x * GROUPS) {
+    const uint32_t t = row / (uint32_t)heads, h = row - t * (uint32_t)heads;
+    const int64_t pos = a.rot ? a.positions[t] : 0;
+    const bool pos_ok = !a.rot || (pos >= 0 && pos < a.n_positions);
+    const _Float16* src = X + t * stride + (int64_t)h * a.D;
+    const _Float16* dsrc = DY + (int64_t)row * a.D;
+    _Float16* dst = DX + t * out_stride + (int64_t)h * a.D;
+    float x[PIECES][2 * V], g[PIECES][2 * V], xx = 0.f;
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i) {
+      const Piece<V, INTERLEAVED> p(i * LPH + sub, a.D, half, true);
+#pragma unroll
+      for (int e = 0; e < 2 * V; ++e) x[i][e] = g[i][e] = 0.f;
+      if (!p.live || !pos_ok) continue;
+      read<V>(src, p.o0, p.o1, x[i]);
+      read<V>(dsrc, p.o0, p.o1, g[i]);
+      if (p.turn) rotate<V, INTERLEAVED, true>(g[i], a.cos, a.sin, pos * half + p.j);
+#pragma unroll
+      for (int e = 0; e < 2 * V; ++e) xx = __builtin_fmaf(x[i][e], x[i][e], xx);
+    }
+    const float r = rsqrtf(head_sum<LPH>(xx) / (float)a.D + a.eps);
+    float xh = 0.f;
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i)
+#pragma unroll
+      for (int e = 0; e < 2 * V; ++e) {
+        x[i][e] *= r;
+        acc[i][e] = __builtin_fmaf(x[i][e], g[i][e], acc[i][e]);
+        g[i][e] *= wf[i][e];
+        xh = __builtin_fmaf(x[i][e], g[i][e], xh);
+      }
+    const float mean = head_sum<LPH>(xh) / (float)a.D;
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i) {
+      const Piece<V, INTERLEAVED> p(i * LPH + sub, a.D, half, true);
+      if (!p.live) continue;
+      float d[2 * V];
+#pragma unroll
+      for (int e = 0; e < 2 * V; ++e) d[e] = pos_ok ? r * (g[i][e] - x[i][e] * mean) : 0.f;
+      write<V>(dst, p.o0, p.o1, d);
+    }
+  }
+  if (!dw) return;
+  // this workgroup's sums, of the lanes with the same places
+#pragma unroll
+  for (int i = 0; i < PIECES; ++i) {
+    const Piece<V, INTERLEAVED> p(i * LPH + sub, a.D, half, true);
+#pragma unroll
+    for (int e = 0; e < 2 * V; ++e) {
+      float s = acc[i][e];
+#pragma unroll
+      for (int o = LPH; o < 64; o <<= 1) s += __shfl_xor(s, o, 64);
+      if (lane < LPH && p.live) sums[wave][e < V ? p.o0 + e : p.o1 + e - V] = s;
+    }
+  }
+  __syncthreads();
+  if ((int)threadIdx.x < a.D) {
+    const int d = threadIdx.x;
+    a.part[((int64_t)(is_k ? GRAD_BLOCKS : 0) + blockIdx.x) * a.D + d] = sums[0][d] + sums[1][d] + sums[2][d] + sums[3][d];
+  }
+}
+
+// The workgroups' partial sums added up in order: eight places of a weight a workgroup, 32 rows at a time.
+__global__ __launch_bounds__(256) void norm_weight_grad_kernel(NormGradArgs a, int q_blocks, int k_blocks) {
+  __shared__ float sums[32][8];
+  const bool is_k = blockIdx.y != 0;
+  float* out = is_k ? a.dk_weight : a.dq_weight;
+  if (!out) return;
+  const int n = is_k ? k_blocks : q_blocks, d = blockIdx.x * 8 + threadIdx.x % 8, r0 = threadIdx.x / 8;
+  const float* part = a.part + (int64_t)(is_k ? GRAD_BLOCKS : 0) * a.D + d;  // (D is a multiple of 8)
+  float s = 0.f;
+  for (int r = r0; r < n; r += 32) s += part[(int64_t)r * a.D];
+  sums[r0][threadIdx.x % 8] = s;
+  __syncthreads();
+  if (r0 == 0) {
+    s = 0.f;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) s += sums[i][threadIdx.x % 8];
+    out[d] = s;
+  }
+}
+
+// Calls f with the widest V that divides the pairs of the turned and of the copied part and every
+// row stride (`counts` has all of them ored), to which fp16 arrays (`halves`) and angles (`floats`)
+// are aligned, and with the lanes of a head.
+template <typename F>
+void dispatch(int D, bool interleaved, uintptr_t halves, uintptr_t floats, int64_t counts, F f) {
+  auto fits = [&](int v) {
+    return counts % v == 0 && (halves & (2 * v - 1)) == 0 && (floats & ((v > 4 ? 16 : 4 * v) - 1)) == 0;
+  };
+  auto lanes = [&](auto v, auto il) {
+    if (D <= 64) f(v, std::integral_constant<int, 4>{}, il);
+    else if (D <= 128) f(v, std::integral_constant<int, 8>{}, il);
+    else f(v, std::integral_constant<int, 16>{}, il);
+  };
+  auto order = [&](auto v) {
+    if (interleaved) lanes(v, std::true_type{});
+    else lanes(v, std::false_type{});
+  };
+  if (fits(8)) order(std::integral_constant<int, 8>{});
+  else if (fits(4)) order(std::integral_constant<int, 4>{});
+  else if (fits(2)) order(std::integral_constant<int, 2>{});
+  else order(std::integral_constant<int, 1>{});
+}
+
+template <typename... P>
+uintptr_t bits(P... p) {
+  return (reinterpret_cast<uintptr_t>(p) | ...);
+}
+
+int64_t grad_blocks(int64_t rows, int groups) {
+  const int64_t n = (rows + groups - 1) / groups;
+  return n < GRAD_BLOCKS ? n : GRAD_BLOCKS;
+}
+
+}  // namespace
+
+hipError_t launch_norm_rotate(const NormArgs& a, int64_t T, hipStream_t st) {
+  const uintptr_t halves = bits(a.q, a.k, a.v, a.q_out, a.k_out, a.k_cache, a.v_cache, a.q_weight, a.k_weight);
+  const int64_t counts = (int64_t)(a.rot / 2) | (a.D / 2) | a.D | a.q_stride | a.k_stride | a.v_stride;
+  dispatch(a.D, a.interleaved != 0, halves, bits(a.cos, a.sin), counts, [&](auto v, auto lph, auto il) {
+    constexpr int GROUPS = 256 / decltype(lph)::value;
+    const int heads = a.q_heads + (a.k_out ? 1 : 2) * a.kv_heads;
+    const int per_block = heads * 2 <= GROUPS ? GROUPS / heads : 1;  // tokens of a workgroup
+    // a launch holds fewer than 2^32 threads along its first dimension
+    const int64_t most = ((int64_t)1 << 23) * per_block;
+    for (int64_t t0 = 0; t0 < T; t0 += most) {
+      NormArgs b = a;
+      b.q += t0 * a.q_stride;
+      b.k += t0 * a.k_stride;
+      if (b.v) b.v += t0 * a.v_stride;
+      b.q_out += t0 * a.q_heads * a.D;
+      if (b.k_out) b.k_out += t0 * a.kv_heads * a.D;
+      if (b.positions) b.positions += t0;
+      if (b.slots) b.slots += t0;
+      const int64_t n = T - t0 < most ? T - t0 : most;
+      const dim3 grid((unsigned)((n + per_block - 1) / per_block), per_block > 1 ? 1u : (unsigned)((heads + GROUPS - 1) / GROUPS));
+      hipLaunchKernelGGL((norm_rotate_kernel<decltype(v)::value, decltype(lph)::value, decltype(il)::value>), grid, dim3(256),
+                         0, st, b, (int)n, per_block);
+    }
+  });
+  return hipGetLastError();
+}
+
+size_t norm_grad_ws_bytes(int64_t, int32_t, int32_t, int32_t D) { return (size_t)2 * GRAD_BLOCKS * D * sizeof(float); }
+
+hipError_t launch_norm_rotate_grad(const NormGradArgs& a, hipStream_t st) {
+  const uintptr_t halves = bits(a.q, a.k, a.dq_out, a.dk_out, a.dq, a.dk, a.q_weight, a.k_weight);
+  const int64_t counts = (int64_t)(a.rot / 2) | (a.D / 2) | a.D | a.q_stride | a.k_stride | a.dq_stride | a.dk_stride;
+  int64_t nq = 0, nk = 0;
+  dispatch(a.D, a.interleaved != 0, halves, bits(a.cos, a.sin), counts, [&](auto v, auto lph, auto il) {
+    constexpr int GROUPS = 256 / decltype(lph)::value;
+    nq = grad_blocks((int64_t)a.T * a.q_heads, GROUPS);
+    nk = grad_blocks((int64_t)a.T * a.kv_heads, GROUPS);
+    if (a.T > 0) hipLaunchKernelGGL((norm_rotate_grad_kernel<decltype(v)::value, decltype(lph)::value, decltype(il)::value>),
+                       dim3((unsigned)(nq > nk ? nq : nk), 2), dim3(256), 0, st, a);
+  });
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || (!a.dq_weight && !a.dk_weight)) return e;
+  hipLaunchKernelGGL(norm_weight_grad_kernel, dim3((unsigned)(a.D / 8), 2), dim3(256), 0, st, a, (int)nq, (int)nk);
+  return hipGetLastError();
+}
+
+}  // namespace qg

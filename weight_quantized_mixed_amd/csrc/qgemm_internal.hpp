@@ -329,6 +329,42 @@ struct AppendArgs {
 };
 hipError_t launch_kv_append(const AppendArgs& a, int64_t T, hipStream_t st);
 
+// the same of normed heads (norm_rotate.hip), into the cache, or into k_out where that is given;
+// q_weight and k_weight (each may be null) are fp16 [D]
+struct NormArgs : AppendArgs {
+  const _Float16 *q_weight, *k_weight;
+  _Float16* k_out;
+  float eps;
+};
+hipError_t launch_norm_rotate(const NormArgs& a, int64_t T, hipStream_t st);
+// gradients of that from those of the outputs: rows of dq and dk are dq_stride and dk_stride
+// values apart; dq_weight and dk_weight (fp32 [D], each may be null) sum over tokens and heads
+struct NormGradArgs {
+  const _Float16 *q, *k, *dq_out, *dk_out, *q_weight, *k_weight;
+  _Float16 *dq, *dk;
+  int64_t q_stride, k_stride, dq_stride, dk_stride, n_positions;
+  const float *cos, *sin;
+  const int32_t* positions;
+  float *dq_weight, *dk_weight, *part;
+  int32_t T, q_heads, kv_heads, D, rot, interleaved;
+  float eps;
+};
+size_t norm_grad_ws_bytes(int64_t T, int32_t q_heads, int32_t kv_heads, int32_t D);
+hipError_t launch_norm_rotate_grad(const NormGradArgs& a, hipStream_t st);
+
+// block tables, slots and positions of a batch's new tokens (kv_extend.hip)
+struct ExtendArgs {
+  const int32_t *new_tokens, *lens, *gone, *ring_state;
+  int32_t *ring, *tables;
+  int32_t *q_starts, *lens_out, *gone_out, *ring_state_out, *refused, *positions;
+  int64_t* slots;
+  void* scratch;
+  int64_t table_width, prefix_len, window;
+  int32_t B, T, ring_size, page_shift, first_page;  // first_page: the first one that holds no sink
+};
+size_t extend_ws_bytes(int64_t B, int64_t T);
+hipError_t launch_kv_extend(const ExtendArgs& a, hipStream_t st);
+
 // attention over the paged cache (attention.hip)
 struct AttnArgs {
   const _Float16 *q, *k, *v;
@@ -339,14 +375,21 @@ struct AttnArgs {
   int32_t T, q_heads, kv_heads, D, n_pages, page_shift, max_q, max_len;
   float scale;
 };
-// sizes that the host knows, which choose the split of the work
+// the same where a query sees the last `window` of the keys up to its own and the first `sinks`
+struct WindowArgs : AttnArgs {
+  int32_t window, sinks;
+};
+// sizes that the host knows, which choose the split of the work (window 0: none)
 struct AttnShape {
   int64_t T, B, max_q, max_len, prefix_len;
   int32_t q_heads, kv_heads, D;
+  int64_t window, sinks;
 };
 bool attention_grid_fits(const AttnShape& s);  // row numbers in 32 bits, work items in a launch
 size_t attention_ws_bytes(const AttnShape& s);
-hipError_t launch_attention(const AttnArgs& a, const AttnShape& s, void* ws, hipStream_t st);
+hipError_t launch_attention(const WindowArgs& a, const AttnShape& s, void* ws, hipStream_t st);
+struct AttnSplit;
+hipError_t launch_window_tiles(const WindowArgs& a, const AttnSplit& p, hipStream_t st);  // (attention_window.hip)
 
 // GEMV tuning: most waves per workgroup (they split the workgroup's K range)
 // and superblocks per register stage

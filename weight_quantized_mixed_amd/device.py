@@ -301,10 +301,27 @@ def _rows(t, name, T, width):
     return t.data_ptr(), step if T > 1 else width
 
 
-# the workspace of an attention call depends on its sizes alone
+def _on_device(stream, *tensors):
+    """The tensors lie on the device that the call's stream belongs to (None passes)."""
+    at = torch.cuda.current_device() if stream is None else stream.device.index
+    for t in tensors:
+        if t is not None and t.get_device() != at:
+            raise ValueError(f"qgemm takes tensors of the stream's device {at}, got one of {t.device}")
+
+
+def _angles(cos, sin):
+    """(rows, pairs) of the tables of angles."""
+    n_pos, half = cos.shape
+    _check(cos, "cos", (n_pos, half), torch.float32)
+    _check(sin, "sin", (n_pos, half), torch.float32)
+    return n_pos, half
+
+
+# the workspace of an attention call depends on its sizes alone (the last two: window and sinks, or none of them)
 _attention_workspace = functools.lru_cache(maxsize=256)(
-    lambda n_pages, page_size, kv_heads, head_dim, *sizes: _q.qgemm_attention_workspace(
-        _q.KVCacheDesc(4096, 4096, n_pages, page_size, kv_heads, head_dim), *sizes))
+    lambda n_pages, page_size, kv_heads, head_dim, *sizes: (
+        _q.qgemm_attention_workspace if len(sizes) == 6 else _q.qgemm_attention_window_workspace)(
+            _q.KVCacheDesc(4096, 4096, n_pages, page_size, kv_heads, head_dim), *sizes))
 
 
 class PagedKV:
@@ -323,31 +340,45 @@ class PagedKV:
         self.desc = _q.KVCacheDesc(_ptr(self.k), _ptr(self.v), self.n_pages, self.page_size, self.kv_heads, self.head_dim)
         self._workspace = _Workspace(self.k.device)
 
-    def append(self, q, k, v, cos, sin, positions, slots, q_out=None, interleaved=False, stream=None):
+    def append(self, q, k, v, cos, sin, positions, slots, q_out=None, interleaved=False, stream=None, norm_eps=None,
+               q_weight=None, k_weight=None):
         """Rotated queries [T, q_heads, head_dim]; the rotated keys and the values go to the cache's slots.
 
         q [T, q_heads * head_dim], k and v [T, kv_heads * head_dim]: rows may be slices of a wider array.
+        norm_eps: every query and key head is first divided by its root mean square (this added to the mean) and
+        multiplied by q_weight or k_weight (fp16 [head_dim], None: 1).
         """
         (T, width), D = q.shape, self.head_dim
         q_heads, kv_width = width // D, self.kv_heads * D
         qp, qs = _rows(q, "q", T, q_heads * D)
         kp, ks = _rows(k, "k", T, kv_width)
         vp, vs = _rows(v, "v", T, kv_width)
-        n_pos, half = cos.shape
-        _check(cos, "cos", (n_pos, half), torch.float32)
-        _check(sin, "sin", (n_pos, half), torch.float32)
+        n_pos, half = _angles(cos, sin)
         _check(positions, "positions", (T,), torch.int32)
         _check(slots, "slots", (T,), torch.int64)
         if q_out is None:
             q_out = _empty((T, q_heads, D), torch.float16, q.device, stream)
         _check(q_out, "q_out", (T, q_heads, D), torch.float16)
+        if norm_eps is not None:
+            _check(q_weight, "q_weight", (D,), torch.float16)
+            _check(k_weight, "k_weight", (D,), torch.float16)
+            _on_device(stream, self.k, q, k, v, cos, sin, positions, slots, q_out, q_weight, k_weight)
+            _q.qgemm_kv_append_norm(self.desc, T, q_heads, qp, qs, kp, ks, vp, vs, _ptr(q_weight), _ptr(k_weight), norm_eps,
+                                    _ptr(cos), _ptr(sin), n_pos, 2 * half, int(bool(interleaved)), _ptr(positions),
+                                    _ptr(slots), _ptr(q_out), _stream(stream))
+            return q_out
+        if q_weight is not None or k_weight is not None:
+            raise ValueError("q_weight and k_weight are those of norms: norm_eps is missing")
         _q.qgemm_kv_append(self.desc, T, q_heads, qp, qs, kp, ks, vp, vs, _ptr(cos), _ptr(sin), n_pos, 2 * half,
                            int(bool(interleaved)), _ptr(positions), _ptr(slots), _ptr(q_out), _stream(stream))
         return q_out
 
     def attend(self, q, q_starts, kv_lens, tables, max_q, max_len, prefix_table=None, prefix_len=0, scale=None,
-               out=None, lse=None, ws=None, stream=None):
-        """Causal attention of a ragged batch (q [T, q_heads, head_dim]) over its own pages and the shared prefix."""
+               out=None, lse=None, ws=None, stream=None, window=None, sinks=0):
+        """Causal attention of a ragged batch (q [T, q_heads, head_dim]) over its own pages and the shared prefix.
+
+        window: of the tokens up to its own (the prefix's among them) a query sees the last `window` and the first `sinks`.
+        """
         T, q_heads, D = q.shape
         step, per_head, one = q.stride()
         if (D != self.head_dim or q.dtype != torch.float16 or not q.is_cuda or (one != 1 and D > 1)
@@ -368,13 +399,140 @@ class PagedKV:
             out = _empty((T, q_heads, D), torch.float16, q.device, stream)
         _check(out, "out", (T, q_heads, D), torch.float16)
         _check(lse, "lse", (T, q_heads), torch.float32)
+        if window is None and sinks:
+            raise ValueError("sinks are those of a window: window is missing")
+        seen = () if window is None else (window, sinks)
         need = _attention_workspace(self.n_pages, self.page_size, self.kv_heads, D, T, q_heads, B, max_q, max_len,
-                                    prefix_len)
+                                    prefix_len, *seen)
         at = _stream(stream)
         if ws is None:
             ws = self._workspace.of(need, stream, at)
+        if seen:
+            _on_device(stream, self.k, q, q_starts, kv_lens, tables, out, lse, ws, prefix_table if prefix_len else None)
+            _q.qgemm_attention_window(self.desc, T, q_heads, qp, qs, B, _ptr(q_starts), _ptr(kv_lens), _ptr(tables), width,
+                                      _ptr(prefix_table) if prefix_len else 0, prefix_len, max_q, max_len, window, sinks,
+                                      D ** -0.5 if scale is None else scale, _ptr(out), _ptr(lse), _ptr(ws),
+                                      0 if ws is None else ws.numel(), at)
+            return out
         _q.qgemm_attention(self.desc, T, q_heads, qp, qs, B, _ptr(q_starts), _ptr(kv_lens), _ptr(tables), width,
                            _ptr(prefix_table) if prefix_len else 0, prefix_len, max_q, max_len,
                            D ** -0.5 if scale is None else scale, _ptr(out), _ptr(lse), _ptr(ws),
                            0 if ws is None else ws.numel(), at)
         return out
+
+
+class PagePool:
+    """Which pages of a cache are free, and which each of up to `sequences` sequences holds, all of it on the device.
+
+    ring: the pool's page numbers, int32 [n_pages] (0 .. n_pages - 1 if not given); tables: int32 [sequences, table_width].
+    prefix_len tokens of a shared prefix come before the sequences' own (in pages outside the pool); with a window, pages
+    of tokens that no query will see again are given back, but for those of the first `sinks` tokens.
+    state: int32 [2 * sequences + 2]: the sequences' lengths, their first pages that no window gave back, and of the ring
+    the first free page's place and how many are free.
+    """
+
+    def __init__(self, n_pages, page_size, sequences, table_width, prefix_len=0, window=None, sinks=0, device="cuda",
+                 ring=None, tables=None):
+        self.n_pages, self.page_size, self.B = int(n_pages), int(page_size), int(sequences)
+        self.table_width, self.prefix_len = int(table_width), int(prefix_len)
+        if window is not None and window < 1:
+            raise ValueError("window: at least 1 expected")
+        self.window, self.sinks = 0 if window is None else int(window), int(sinks)
+        i32 = torch.int32
+        if ring is None:
+            ring = torch.arange(self.n_pages, dtype=i32, device=device)
+        if tables is None:
+            tables = torch.full((self.B, self.table_width), -1, dtype=i32, device=device)
+        self.ring = _check(ring, "ring", (self.n_pages,), i32)
+        self.tables = _check(tables, "tables", (self.B, self.table_width), i32)
+        self.state = torch.zeros(2 * self.B + 2, dtype=i32, device=self.ring.device)
+        self.state[-1] = self.n_pages
+        self._workspace = _Workspace(self.ring.device)
+
+    @property
+    def lens(self):
+        """Own tokens of each sequence, int32 [sequences]."""
+        return self.state[:self.B]
+
+    def extend(self, new_tokens, T, state_out=None, ws=None, stream=None):
+        """Room for the batch's new tokens: how many each sequence gets (int32 [sequences]; -1: it ends), T rows in all.
+
+        {"q_starts", "kv_lens", "positions", "slots", "refused"} as append and attend take them; the tables, the ring and
+        the state are brought up to date.  Rows behind the last token have slot -1.  A sequence whose tokens find no room
+        is marked in refused (int32 [sequences]) and keeps its length; its rows have position and slot -1.
+        state_out: where the state after the call goes (by default the pool's own; else that stays as it was, and so the
+        same step may be taken again).  kv_lens is a part of it.
+        """
+        B, T, i32 = self.B, int(T), torch.int32
+        _check(new_tokens, "new_tokens", (B,), i32)
+        if state_out is None:
+            state_out = self.state
+        _check(state_out, "state_out", self.state.shape, i32)
+        _on_device(stream, self.state, self.ring, self.tables, new_tokens, state_out, ws)
+        q_starts, refused = _empty((B + 1,), i32, new_tokens.device, stream), _empty((B,), i32, new_tokens.device, stream)
+        positions, slots = _empty((T,), i32, new_tokens.device, stream), _empty((T,), torch.int64, new_tokens.device, stream)
+        at = _stream(stream)
+        if ws is None:
+            ws = self._workspace.of(_q.qgemm_kv_extend_workspace(B, T), stream, at)
+        old, new = _ptr(self.state), _ptr(state_out)
+        _q.qgemm_kv_extend(B, T, self.page_size, _ptr(new_tokens), old, old + 4 * B, old + 8 * B, _ptr(self.ring),
+                           self.n_pages, _ptr(self.tables), self.table_width, self.prefix_len, self.window, self.sinks,
+                           _ptr(q_starts), new, new + 4 * B, new + 8 * B, _ptr(positions), _ptr(slots), _ptr(refused),
+                           _ptr(ws), 0 if ws is None else ws.numel(), at)
+        return {"q_starts": q_starts, "kv_lens": state_out[:B], "positions": positions, "slots": slots, "refused": refused}
+
+
+def _norm_args(q, k, D, q_heads, kv_heads, cos, sin, positions, q_weight, k_weight, eps, interleaved):
+    """The arguments that normed and rotated heads and their gradients share, checked."""
+    T = q.shape[0]
+    n_pos, half = _angles(cos, sin)
+    _check(positions, "positions", (T,), torch.int32)
+    _check(q_weight, "q_weight", (D,), torch.float16)
+    _check(k_weight, "k_weight", (D,), torch.float16)
+    return (T, q_heads, kv_heads, D, *_rows(q, "q", T, q_heads * D), *_rows(k, "k", T, kv_heads * D), _ptr(q_weight),
+            _ptr(k_weight), eps, _ptr(cos), _ptr(sin), n_pos, 2 * half, int(bool(interleaved)), _ptr(positions))
+
+
+def norm_rotate(q, k, head_dim, cos, sin, positions, q_weight=None, k_weight=None, eps=1e-6, interleaved=False, q_out=None,
+                k_out=None, stream=None):
+    """(queries [T, q_heads, head_dim], keys [T, kv_heads, head_dim]): each head divided by its root mean square (eps added
+    to the mean), multiplied by its weight (fp16 [head_dim], None: 1) and rotated by its token's angles.
+
+    q [T, q_heads * head_dim], k [T, kv_heads * head_dim]: rows may be slices of a wider array.
+    """
+    D, T = int(head_dim), q.shape[0]
+    q_heads, kv_heads = q.shape[1] // D, k.shape[1] // D
+    args = _norm_args(q, k, D, q_heads, kv_heads, cos, sin, positions, q_weight, k_weight, eps, interleaved)
+    q_out = _empty((T, q_heads, D), torch.float16, q.device, stream) if q_out is None else q_out
+    k_out = _empty((T, kv_heads, D), torch.float16, q.device, stream) if k_out is None else k_out
+    _check(q_out, "q_out", (T, q_heads, D), torch.float16)
+    _check(k_out, "k_out", (T, kv_heads, D), torch.float16)
+    _on_device(stream, q, k, cos, sin, positions, q_weight, k_weight, q_out, k_out)
+    _q.qgemm_norm_rotate(*args, _ptr(q_out), _ptr(k_out), _stream(stream))
+    return q_out, k_out
+
+
+def norm_rotate_backward(q, k, dq_out, dk_out, cos, sin, positions, q_weight=None, k_weight=None, eps=1e-6,
+                         interleaved=False, weight_grads=True, dq=None, dk=None, ws=None, stream=None):
+    """{"dq", "dk", "dq_weight", "dk_weight"} of norm_rotate from the gradients of its outputs (the weights' in fp32; None
+    for a weight that is None, or where not asked for).
+
+    dq, dk: where the gradients go, shaped like q and k; rows may be slices of a wider array.
+    """
+    T, q_heads, D = dq_out.shape
+    kv_heads = dk_out.shape[1]
+    args = _norm_args(q, k, D, q_heads, kv_heads, cos, sin, positions, q_weight, k_weight, eps, interleaved)
+    _check(dq_out, "dq_out", (q.shape[0], q_heads, D), torch.float16)
+    _check(dk_out, "dk_out", (q.shape[0], kv_heads, D), torch.float16)
+    dq = _empty((T, q_heads * D), torch.float16, q.device, stream) if dq is None else dq
+    dk = _empty((T, kv_heads * D), torch.float16, q.device, stream) if dk is None else dk
+    new = lambda w: _empty((D,), torch.float32, q.device, stream) if weight_grads and w is not None else None  # noqa: E731
+    dqw, dkw = new(q_weight), new(k_weight)
+    need = _q.qgemm_norm_rotate_backward_workspace(T, q_heads, kv_heads, D, dqw is not None or dkw is not None)
+    if ws is None and need:
+        ws = _empty((need,), torch.uint8, q.device, stream)
+    _on_device(stream, q, k, dq_out, dk_out, cos, sin, positions, q_weight, k_weight, dq, dk, ws)
+    _q.qgemm_norm_rotate_backward(*args, _ptr(dq_out), _ptr(dk_out), *_rows(dq, "dq", T, q_heads * D),
+                                  *_rows(dk, "dk", T, kv_heads * D), _ptr(dqw), _ptr(dkw), _ptr(ws),
+                                  0 if ws is None else ws.numel(), _stream(stream))
+    return {"dq": dq, "dk": dk, "dq_weight": dqw, "dk_weight": dkw}

@@ -27,7 +27,9 @@ EXPORTED = ("qgemm_create", "qgemm_pack_weights", "qgemm_run", "qgemm_run_ex", "
             "qgemm_run_scaled", "qgemm_quantize_rows", "qgemm_destroy", "qgemm_plan_path",
             "qgemm_status_string", "qgemm_create_gated", "qgemm_pack_gated", "qgemm_run_gated",
             "qgemm_gated_backward_workspace", "qgemm_gated_backward", "qgemm_kv_append",
-            "qgemm_attention_workspace", "qgemm_attention")
+            "qgemm_attention_workspace", "qgemm_attention", "qgemm_kv_append_norm", "qgemm_norm_rotate",
+            "qgemm_norm_rotate_backward_workspace", "qgemm_norm_rotate_backward", "qgemm_kv_extend_workspace",
+            "qgemm_kv_extend", "qgemm_attention_window_workspace", "qgemm_attention_window")
 NOALLOC_MAX_SCRATCH = 32 << 20
 
 
@@ -98,8 +100,19 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.qgemm_attention_workspace.argtypes = [p_kv, c_i64, c_i32, c_i64, c_i64, c_i64, c_i64, p_sz]
     lib.qgemm_attention.argtypes = [p_kv, c_i64, c_i32, c_p, c_i64, c_i64, c_p, c_p, c_p, c_i64, c_p, c_i64, c_i64,
                                     c_i64, c_f, c_p, c_p, c_p, c_sz, c_p]
-    for name in ("qgemm_create_gated", "qgemm_pack_gated", "qgemm_run_gated", "qgemm_gated_backward_workspace",
-                 "qgemm_gated_backward", "qgemm_kv_append", "qgemm_attention_workspace", "qgemm_attention"):
+    norm = [c_p, c_p, c_f, c_p, c_p, c_i64, c_i32, c_i32]  # weights, eps, cos, sin, positions of the table, rot_dim, order
+    lib.qgemm_kv_append_norm.argtypes = [p_kv, c_i64, c_i32, c_p, c_i64, c_p, c_i64, c_p, c_i64] + norm + [c_p] * 4
+    lib.qgemm_norm_rotate.argtypes = [c_i64, c_i32, c_i32, c_i32, c_p, c_i64, c_p, c_i64] + norm + [c_p] * 4
+    lib.qgemm_norm_rotate_backward_workspace.argtypes = [c_i64, c_i32, c_i32, c_i32, c_i32, p_sz]
+    lib.qgemm_norm_rotate_backward.argtypes = ([c_i64, c_i32, c_i32, c_i32, c_p, c_i64, c_p, c_i64] + norm +
+                                               [c_p, c_p, c_p, c_p, c_i64, c_p, c_i64, c_p, c_p, c_p, c_sz, c_p])
+    lib.qgemm_kv_extend_workspace.argtypes = [c_i64, c_i64, p_sz]
+    lib.qgemm_kv_extend.argtypes = ([c_i64, c_i64, c_i32] + [c_p] * 5 + [c_i64, c_p] + [c_i64] * 4 + [c_p] * 8 +
+                                    [c_sz, c_p])
+    lib.qgemm_attention_window_workspace.argtypes = [p_kv, c_i64, c_i32] + [c_i64] * 6 + [p_sz]
+    lib.qgemm_attention_window.argtypes = [p_kv, c_i64, c_i32, c_p, c_i64, c_i64, c_p, c_p, c_p, c_i64, c_p, c_i64, c_i64,
+                                           c_i64, c_i64, c_i64, c_f, c_p, c_p, c_p, c_sz, c_p]
+    for name in EXPORTED[EXPORTED.index("qgemm_create_gated"):]:
         getattr(lib, name).restype = c_i32
     _lib = lib
     return lib
@@ -240,6 +253,91 @@ def qgemm_attention(cache, T, q_heads, q, q_stride, B, q_starts, kv_lens, tables
                                 stream or None)
     if st != QGEMM_OK:
         raise QGemmError(st, "qgemm_attention")
+
+
+def qgemm_kv_append_norm(cache, T, q_heads, q, q_stride, k, k_stride, v, v_stride, q_weight, k_weight, eps, cos, sin,
+                         n_positions, rot_dim, interleaved, positions, slots, q_out, stream=0):
+    st = load().qgemm_kv_append_norm(None if cache is None else ctypes.byref(cache), int(T), int(q_heads), q or None,
+                                     int(q_stride), k or None, int(k_stride), v or None, int(v_stride), q_weight or None,
+                                     k_weight or None, float(eps), cos or None, sin or None, int(n_positions),
+                                     int(rot_dim), int(interleaved), positions or None, slots or None, q_out or None,
+                                     stream or None)
+    if st != QGEMM_OK:
+        raise QGemmError(st, "qgemm_kv_append_norm")
+
+
+def qgemm_norm_rotate(T, q_heads, kv_heads, head_dim, q, q_stride, k, k_stride, q_weight, k_weight, eps, cos, sin,
+                      n_positions, rot_dim, interleaved, positions, q_out, k_out, stream=0):
+    st = load().qgemm_norm_rotate(int(T), int(q_heads), int(kv_heads), int(head_dim), q or None, int(q_stride), k or None,
+                                  int(k_stride), q_weight or None, k_weight or None, float(eps), cos or None, sin or None,
+                                  int(n_positions), int(rot_dim), int(interleaved), positions or None, q_out or None,
+                                  k_out or None, stream or None)
+    if st != QGEMM_OK:
+        raise QGemmError(st, "qgemm_norm_rotate")
+
+
+def qgemm_norm_rotate_backward_workspace(T, q_heads, kv_heads, head_dim, weight_grads) -> int:
+    n = ctypes.c_size_t()
+    st = load().qgemm_norm_rotate_backward_workspace(int(T), int(q_heads), int(kv_heads), int(head_dim),
+                                                     int(bool(weight_grads)), ctypes.byref(n))
+    if st != QGEMM_OK:
+        raise QGemmError(st, "qgemm_norm_rotate_backward_workspace")
+    return n.value
+
+
+def qgemm_norm_rotate_backward(T, q_heads, kv_heads, head_dim, q, q_stride, k, k_stride, q_weight, k_weight, eps, cos,
+                               sin, n_positions, rot_dim, interleaved, positions, dq_out, dk_out, dq, dq_stride, dk,
+                               dk_stride, dq_weight, dk_weight, workspace, workspace_bytes, stream=0):
+    st = load().qgemm_norm_rotate_backward(int(T), int(q_heads), int(kv_heads), int(head_dim), q or None, int(q_stride),
+                                           k or None, int(k_stride), q_weight or None, k_weight or None, float(eps),
+                                           cos or None, sin or None, int(n_positions), int(rot_dim), int(interleaved),
+                                           positions or None, dq_out or None, dk_out or None, dq or None, int(dq_stride),
+                                           dk or None, int(dk_stride), dq_weight or None, dk_weight or None,
+                                           workspace or None, int(workspace_bytes), stream or None)
+    if st != QGEMM_OK:
+        raise QGemmError(st, "qgemm_norm_rotate_backward")
+
+
+def qgemm_kv_extend_workspace(B, T) -> int:
+    n = ctypes.c_size_t()
+    st = load().qgemm_kv_extend_workspace(int(B), int(T), ctypes.byref(n))
+    if st != QGEMM_OK:
+        raise QGemmError(st, "qgemm_kv_extend_workspace")
+    return n.value
+
+
+def qgemm_kv_extend(B, T, page_size, new_tokens, lens, gone, ring_state, ring, ring_size, tables, table_width, prefix_len,
+                    window, sinks, q_starts, lens_out, gone_out, ring_state_out, positions, slots, refused, workspace,
+                    workspace_bytes, stream=0):
+    st = load().qgemm_kv_extend(int(B), int(T), int(page_size), new_tokens or None, lens or None, gone or None,
+                                ring_state or None, ring or None, int(ring_size), tables or None, int(table_width),
+                                int(prefix_len), int(window), int(sinks), q_starts or None, lens_out or None,
+                                gone_out or None, ring_state_out or None, positions or None, slots or None,
+                                refused or None, workspace or None, int(workspace_bytes), stream or None)
+    if st != QGEMM_OK:
+        raise QGemmError(st, "qgemm_kv_extend")
+
+
+def qgemm_attention_window_workspace(cache, T, q_heads, B, max_q, max_len, prefix_len, window, sinks) -> int:
+    n = ctypes.c_size_t()
+    st = load().qgemm_attention_window_workspace(None if cache is None else ctypes.byref(cache), int(T), int(q_heads),
+                                                 int(B), int(max_q), int(max_len), int(prefix_len), int(window),
+                                                 int(sinks), ctypes.byref(n))
+    if st != QGEMM_OK:
+        raise QGemmError(st, "qgemm_attention_window_workspace")
+    return n.value
+
+
+def qgemm_attention_window(cache, T, q_heads, q, q_stride, B, q_starts, kv_lens, tables, table_width, prefix_table,
+                           prefix_len, max_q, max_len, window, sinks, scale, out, lse, workspace, workspace_bytes,
+                           stream=0):
+    st = load().qgemm_attention_window(None if cache is None else ctypes.byref(cache), int(T), int(q_heads), q or None,
+                                       int(q_stride), int(B), q_starts or None, kv_lens or None, tables or None,
+                                       int(table_width), prefix_table or None, int(prefix_len), int(max_q), int(max_len),
+                                       int(window), int(sinks), float(scale), out or None, lse or None,
+                                       workspace or None, int(workspace_bytes), stream or None)
+    if st != QGEMM_OK:
+        raise QGemmError(st, "qgemm_attention_window")
 
 
 def qgemm_destroy(plan):
