@@ -41,23 +41,32 @@ __device__ __forceinline__ uint32_t wave_scan(uint32_t v) {
   return add_from<0x143, 0xC>(v);  // row 1's last lane into rows 2 and 3
 }
 
-// sum of v over the threads before this one, behind `carry`, which grows by all threads' sum
-__device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t& carry, uint32_t* totals) {
+// Sums of N values over the threads before this one, each behind its `carry`, which grows by
+// all threads' sum.
+template <int N>
+__device__ __forceinline__ void block_scan(uint32_t (&v)[N], uint32_t (&carry)[N], uint32_t (*totals)[WAVES]) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const uint32_t upto = wave_scan(v);
-  uint32_t before = __shfl_up(upto, 1, 64);
-  if (lane == 0) before = 0;
-  if (lane == 63) totals[wave] = upto;
-  __syncthreads();
-  uint32_t all = carry, mine = carry;
+  uint32_t before[N];
 #pragma unroll
-  for (int w = 0; w < WAVES; ++w) {
-    if (w < wave) mine = add(mine, totals[w]);
-    all = add(all, totals[w]);
+  for (int i = 0; i < N; ++i) {
+    const uint32_t upto = wave_scan(v[i]);
+    before[i] = __shfl_up(upto, 1, 64);
+    if (lane == 0) before[i] = 0;
+    if (lane == 63) totals[i][wave] = upto;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    uint32_t all = carry[i], mine = carry[i];
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) {
+      if (w < wave) mine = add(mine, totals[i][w]);
+      all = add(all, totals[i][w]);
+    }
+    carry[i] = all;
+    v[i] = add(mine, before[i]);
   }
   __syncthreads();  // (the totals may be written again)
-  carry = all;
-  return add(mine, before);
 }
 
 // what a token asks of its sequence
@@ -92,9 +101,9 @@ __device__ __forceinline__ void place_token(const ExtendArgs& a, int t, int b, G
   a.slots[t] = slot;
 }
 
-// the last of n ascending starts that is at most t (n if there is none: n >= 1, start(0) is 0)
-template <typename F>
-__device__ __forceinline__ int sequence_of(int t, int n, F start) {
+// the last of n ascending starts that is at most t (n >= 1, start(0) is 0)
+template <typename T, typename F>
+__device__ __forceinline__ int sequence_of(T t, int n, F start) {
   int lo = 0, hi = n;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -104,32 +113,32 @@ __device__ __forceinline__ int sequence_of(int t, int n, F start) {
   return lo;
 }
 
+// the pages that a sequence gives back, as their places in its table: [0, to0), then from1 on
+struct Given {
+  uint32_t put;  // pages that the sequences before give back
+  int32_t to0, from1;
+};
+
 // ALL: the tokens too
 template <bool ALL>
 __global__ __launch_bounds__(THREADS) void extend_kernel(ExtendArgs a) {
-  __shared__ uint32_t totals[WAVES];
+  __shared__ uint32_t totals[2][WAVES];
+  __shared__ Given lists[THREADS];
   __shared__ Grown grown[ALL ? ONE_LAUNCH_SEQUENCES : 1];
-  const int lane = threadIdx.x & 63;
-  const int R = a.ring_size;
+  const int lane = threadIdx.x & 63, R = a.ring_size;
   int head = a.ring_state[0], free = a.ring_state[1];
   // (a state that no call left is brought into range, so that nothing is touched outside the pool)
   head = head < 0 || head >= R ? 0 : head;
   free = min(max(free, 0), R);
-  uint32_t rows = 0, wanted = 0, taken = 0, back = 0;
+  uint32_t sums[2] = {0, 0}, wanted[1] = {0}, taken = 0;  // rows and pages given back; pages asked for
   for (int b0 = 0; b0 < a.B; b0 += THREADS) {
     const int b = b0 + threadIdx.x;
     const bool in = b < a.B;
     const int asked = in ? a.new_tokens[b] : 0, n = max(asked, 0);
     const int len = in ? max(a.lens[b], 0) : 0, gone = in && a.window ? max(a.gone[b], 0) : 0;
     const int old = pages_of(len, a.page_shift), now = pages_of((int64_t)len + n, a.page_shift);
-    const uint32_t start = block_scan((uint32_t)n, rows, totals);
-    // what no other sequence can help
-    const bool fits = now <= a.table_width && a.prefix_len + len + n <= INT32_MAX && add(start, (uint32_t)n) <= (uint32_t)a.T;
-    const uint32_t need = fits ? now - old : 0;
-    const uint32_t before = block_scan(need, wanted, totals);
-    const bool refused = n > 0 && (!fits || (need > 0 && add(before, need) > (uint32_t)free));
-    // pages given back: [from0, to0) and [from1, to1), of those that the table has
-    const int held = min((int64_t)old, a.table_width);
+    // what goes back, of the pages that the table has
+    const int held = (int)min((int64_t)old, a.table_width);
     int to0 = 0, from1 = 0, to1 = 0, gone_now = 0;
     if (asked < 0) {
       to0 = gone > a.first_page ? min(a.first_page, held) : 0;
@@ -141,53 +150,56 @@ __global__ __launch_bounds__(THREADS) void extend_kernel(ExtendArgs a) {
       to1 = min(past, held);
       gone_now = past > a.first_page ? max(gone, past) : gone;
     }
-    const int n1 = max(to1 - from1, 0), given = to0 + n1;
-    const uint32_t put = block_scan((uint32_t)given, back, totals);
-    // the i-th page given back by a sequence; the pool never holds more than it has places
-    auto give = [&](int of, uint32_t at, int i, int to0, int from1) {
-      const int64_t place = (int64_t)free + at + i;
-      if (place >= R) return;
-      const int64_t x = head + place;
-      a.ring[x < R ? x : x - R] = a.tables[(int64_t)of * a.table_width + (i < to0 ? i : from1 + i - to0)];
-    };
-    // a sequence's few pages by its own thread, many by the wave
-    if (given > 0 && given <= 2)
-      for (int i = 0; i < given; ++i) give(b, put, i, to0, from1);
-    for (uint64_t many = __ballot(given > 2); many; many &= many - 1) {
-      const int from = __builtin_ctzll(many);
-      const int g = __shfl(given, from, 64), t0 = __shfl(to0, from, 64), f1 = __shfl(from1, from, 64);
-      const uint32_t at = __shfl(put, from, 64);
-      for (int i = lane; i < g; i += 64) give(b - lane + from, at, i, t0, f1);
-    }
+    const uint32_t back0 = sums[1];
+    uint32_t first[2] = {(uint32_t)n, (uint32_t)(to0 + max(to1 - from1, 0))};
+    block_scan(first, sums, totals);
+    // what no other sequence can help
+    const uint32_t start = first[0];
+    const bool fits = now <= a.table_width && a.prefix_len + len + n <= INT32_MAX && add(start, (uint32_t)n) <= (uint32_t)a.T;
+    const uint32_t need = fits ? now - old : 0;
+    lists[threadIdx.x] = {first[1] - back0, to0, from1};
+    uint32_t before[1] = {need};
+    block_scan(before, wanted, totals);
+    const bool refused = n > 0 && (!fits || (need > 0 && add(before[0], need) > (uint32_t)free));
     if (in) {
-      const int first = (int)min(start, (uint32_t)a.T);
-      a.q_starts[b] = first;
+      const int row = (int)min(start, (uint32_t)a.T);
+      a.q_starts[b] = row;
       a.refused[b] = refused;
       a.lens_out[b] = asked < 0 ? 0 : refused ? len : len + n;
       a.gone_out[b] = gone_now;
-      const Grown s = {first, len, refused ? -1 : (int)before};
+      const Grown s = {row, len, refused ? -1 : (int)before[0]};
       if constexpr (ALL) grown[b] = s;
       else reinterpret_cast<Grown*>(a.scratch)[b] = s;
     }
-    // the pages of those that were not refused, who come first
-    if (need > 0 && !refused) taken = max(taken, add(before, need));
+    // those that were not refused come first
+    if (need > 0 && !refused) taken = max(taken, add(before[0], need));
+    // the pages given back by these sequences, a thread each; the pool never holds more than it has places
+    const int64_t room = (int64_t)R - free - back0, back = min((int64_t)sums[1] - back0, room);
+    for (int64_t i = threadIdx.x; i < back; i += THREADS) {
+      const int of = sequence_of((uint32_t)i, THREADS, [&](int x) { return lists[x].put; });
+      const Given g = lists[of];
+      const int nth = (int)((uint32_t)i - g.put), page = nth < g.to0 ? nth : g.from1 + nth - g.to0;
+      const int64_t x = (int64_t)head + free + back0 + i;  // below 2 R
+      a.ring[x < R ? x : x - R] = a.tables[(int64_t)(b0 + of) * a.table_width + page];
+    }
+    if (b0 + THREADS < a.B) __syncthreads();  // (the lists are written again)
   }
   // over the workgroup: the largest of `taken`
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) taken = max(taken, (uint32_t)__shfl_xor(taken, o, 64));
-  if (lane == 0) totals[threadIdx.x >> 6] = taken;
+  if (lane == 0) totals[0][threadIdx.x >> 6] = taken;
   __syncthreads();
+  const int end = (int)min(sums[0], (uint32_t)a.T);
   if (threadIdx.x == 0) {
 #pragma unroll
-    for (int w = 1; w < WAVES; ++w) taken = max(taken, totals[w]);
+    for (int w = 1; w < WAVES; ++w) taken = max(taken, totals[0][w]);
     const int64_t next = (int64_t)head + taken;
-    a.q_starts[a.B] = (int)min(rows, (uint32_t)a.T);
+    a.q_starts[a.B] = end;
     a.ring_state_out[0] = (int)(next < R ? next : next - R);
-    a.ring_state_out[1] = (int)(min((int64_t)free + back, (int64_t)R) - taken);
-    if constexpr (!ALL) reinterpret_cast<Grown*>(a.scratch)[a.B] = {(int)min(rows, (uint32_t)a.T), head, 0};
+    a.ring_state_out[1] = (int)(min((int64_t)free + sums[1], (int64_t)R) - taken);
+    if constexpr (!ALL) reinterpret_cast<Grown*>(a.scratch)[a.B] = {end, head, 0};
   }
   if constexpr (ALL) {
-    const int end = (int)min(rows, (uint32_t)a.T);
     for (int t = threadIdx.x; t < a.T; t += THREADS) {
       int b = a.B;
       if (t < end) b = sequence_of(t, a.B, [&](int i) { return grown[i].start; });

@@ -262,22 +262,29 @@ __global__ __launch_bounds__(256) void norm_rotate_grad_kernel(NormGradArgs a) {
   }
 }
 
-// The workgroups' partial sums added up in order: eight places of a weight a workgroup, 32 rows at a time.
-__global__ __launch_bounds__(256) void norm_weight_grad_kernel(NormGradArgs a, int q_blocks, int k_blocks) {
-  __shared__ float sums[32][8];
+// The workgroups' partial sums added up in order: 16 places of a weight a workgroup (64 bytes of a
+// row), 64 rows at a time, all loads of a thread in flight together.
+__global__ __launch_bounds__(1024) void norm_weight_grad_kernel(NormGradArgs a, int q_blocks, int k_blocks) {
+  __shared__ float sums[16][16];
   const bool is_k = blockIdx.y != 0;
   float* out = is_k ? a.dk_weight : a.dq_weight;
   if (!out) return;
-  const int n = is_k ? k_blocks : q_blocks, d = blockIdx.x * 8 + threadIdx.x % 8, r0 = threadIdx.x / 8;
-  const float* part = a.part + (int64_t)(is_k ? GRAD_BLOCKS : 0) * a.D + d;  // (D is a multiple of 8)
+  const int n = is_k ? k_blocks : q_blocks, col = threadIdx.x % 16, r0 = threadIdx.x / 16, d = blockIdx.x * 16 + col;
+  const float* part = a.part + (int64_t)(is_k ? GRAD_BLOCKS : 0) * a.D + min(d, a.D - 1);
+  float v[GRAD_BLOCKS / 64];
+#pragma unroll
+  for (int i = 0; i < GRAD_BLOCKS / 64; ++i) v[i] = r0 + 64 * i < n ? part[(int64_t)(r0 + 64 * i) * a.D] : 0.f;
   float s = 0.f;
-  for (int r = r0; r < n; r += 32) s += part[(int64_t)r * a.D];
-  sums[r0][threadIdx.x % 8] = s;
+#pragma unroll
+  for (int i = 0; i < GRAD_BLOCKS / 64; ++i) s += v[i];
+  s += __shfl_xor(s, 16, 64);
+  s += __shfl_xor(s, 32, 64);
+  if ((threadIdx.x & 63) < 16) sums[threadIdx.x >> 6][col] = s;
   __syncthreads();
-  if (r0 == 0) {
+  if (threadIdx.x < 16 && d < a.D) {
     s = 0.f;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) s += sums[i][threadIdx.x % 8];
+    for (int i = 0; i < 16; ++i) s += sums[i][col];
     out[d] = s;
   }
 }
@@ -359,7 +366,7 @@ hipError_t launch_norm_rotate_grad(const NormGradArgs& a, hipStream_t st) {
   });
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || (!a.dq_weight && !a.dk_weight)) return e;
-  hipLaunchKernelGGL(norm_weight_grad_kernel, dim3((unsigned)(a.D / 8), 2), dim3(256), 0, st, a, (int)nq, (int)nk);
+  hipLaunchKernelGGL(norm_weight_grad_kernel, dim3((unsigned)((a.D + 15) / 16), 2), dim3(1024), 0, st, a, (int)nq, (int)nk);
   return hipGetLastError();
 }
 

@@ -301,20 +301,24 @@ def _rows(t, name, T, width):
     return t.data_ptr(), step if T > 1 else width
 
 
-def _on_device(stream, *tensors):
-    """The tensors lie on the device that the call's stream belongs to (None passes)."""
-    at = torch.cuda.current_device() if stream is None else stream.device.index
-    for t in tensors:
-        if t is not None and t.get_device() != at:
-            raise ValueError(f"qgemm takes tensors of the stream's device {at}, got one of {t.device}")
+def _arg(t, name, shape, dtype, at):
+    """Address of a contiguous tensor argument of this shape and type on device `at` (None: no address)."""
+    if t is None:
+        return 0
+    if t.dtype != dtype or t.shape != shape:
+        raise ValueError(f"{name}: {dtype} {tuple(shape)} expected, got {t.dtype} {tuple(t.shape)}")
+    if t.get_device() != at or not t.is_contiguous():
+        raise ValueError(f"{name}: a contiguous tensor on device {at} expected, got one on {t.device}")
+    return t.data_ptr()
 
 
-def _angles(cos, sin):
-    """(rows, pairs) of the tables of angles."""
-    n_pos, half = cos.shape
-    _check(cos, "cos", (n_pos, half), torch.float32)
-    _check(sin, "sin", (n_pos, half), torch.float32)
-    return n_pos, half
+def _launch_stream(at, stream):
+    """Handle of the stream for a call whose tensors lie on device `at`: a kernel runs on the device of its stream."""
+    if at < 0:
+        raise ValueError("qgemm takes device tensors only")
+    if at != (torch.cuda.current_device() if stream is None else stream.device.index):
+        raise ValueError(f"the tensors lie on device {at}, which is not that of the stream")
+    return _stream(stream)
 
 
 # the workspace of an attention call depends on its sizes alone (the last two: window and sinks, or none of them)
@@ -353,22 +357,28 @@ class PagedKV:
         qp, qs = _rows(q, "q", T, q_heads * D)
         kp, ks = _rows(k, "k", T, kv_width)
         vp, vs = _rows(v, "v", T, kv_width)
-        n_pos, half = _angles(cos, sin)
-        _check(positions, "positions", (T,), torch.int32)
-        _check(slots, "slots", (T,), torch.int64)
+        n_pos, half = cos.shape
         if q_out is None:
             q_out = _empty((T, q_heads, D), torch.float16, q.device, stream)
-        _check(q_out, "q_out", (T, q_heads, D), torch.float16)
         if norm_eps is not None:
-            _check(q_weight, "q_weight", (D,), torch.float16)
-            _check(k_weight, "k_weight", (D,), torch.float16)
-            _on_device(stream, self.k, q, k, v, cos, sin, positions, slots, q_out, q_weight, k_weight)
-            _q.qgemm_kv_append_norm(self.desc, T, q_heads, qp, qs, kp, ks, vp, vs, _ptr(q_weight), _ptr(k_weight), norm_eps,
-                                    _ptr(cos), _ptr(sin), n_pos, 2 * half, int(bool(interleaved)), _ptr(positions),
-                                    _ptr(slots), _ptr(q_out), _stream(stream))
+            at, i32, f32, f16 = self.k.get_device(), torch.int32, torch.float32, torch.float16
+            for t in (q, k, v):
+                if t.get_device() != at:
+                    raise ValueError(f"the cache lies on device {at}, got a tensor on {t.device}")
+            _q.qgemm_kv_append_norm(
+                self.desc, T, q_heads, qp, qs, kp, ks, vp, vs, _arg(q_weight, "q_weight", (D,), f16, at),
+                _arg(k_weight, "k_weight", (D,), f16, at), norm_eps, _arg(cos, "cos", (n_pos, half), f32, at),
+                _arg(sin, "sin", (n_pos, half), f32, at), n_pos, 2 * half, 1 if interleaved else 0,
+                _arg(positions, "positions", (T,), i32, at), _arg(slots, "slots", (T,), torch.int64, at),
+                _arg(q_out, "q_out", (T, q_heads, D), f16, at), _launch_stream(at, stream))
             return q_out
         if q_weight is not None or k_weight is not None:
             raise ValueError("q_weight and k_weight are those of norms: norm_eps is missing")
+        _check(cos, "cos", (n_pos, half), torch.float32)
+        _check(sin, "sin", (n_pos, half), torch.float32)
+        _check(positions, "positions", (T,), torch.int32)
+        _check(slots, "slots", (T,), torch.int64)
+        _check(q_out, "q_out", (T, q_heads, D), torch.float16)
         _q.qgemm_kv_append(self.desc, T, q_heads, qp, qs, kp, ks, vp, vs, _ptr(cos), _ptr(sin), n_pos, 2 * half,
                            int(bool(interleaved)), _ptr(positions), _ptr(slots), _ptr(q_out), _stream(stream))
         return q_out
@@ -408,7 +418,10 @@ class PagedKV:
         if ws is None:
             ws = self._workspace.of(need, stream, at)
         if seen:
-            _on_device(stream, self.k, q, q_starts, kv_lens, tables, out, lse, ws, prefix_table if prefix_len else None)
+            for t in (self.k, q_starts, kv_lens, tables, out):
+                if t.get_device() != q.get_device():
+                    raise ValueError(f"the tensors lie on devices {q.device} and {t.device}")
+            _launch_stream(q.get_device(), stream)
             _q.qgemm_attention_window(self.desc, T, q_heads, qp, qs, B, _ptr(q_starts), _ptr(kv_lens), _ptr(tables), width,
                                       _ptr(prefix_table) if prefix_len else 0, prefix_len, max_q, max_len, window, sinks,
                                       D ** -0.5 if scale is None else scale, _ptr(out), _ptr(lse), _ptr(ws),
@@ -447,7 +460,7 @@ class PagePool:
         self.tables = _check(tables, "tables", (self.B, self.table_width), i32)
         self.state = torch.zeros(2 * self.B + 2, dtype=i32, device=self.ring.device)
         self.state[-1] = self.n_pages
-        self._workspace = _Workspace(self.ring.device)
+        self._workspace, self._sizes, self._need = _Workspace(self.ring.device), None, 0
 
     @property
     def lens(self):
@@ -463,34 +476,38 @@ class PagePool:
         state_out: where the state after the call goes (by default the pool's own; else that stays as it was, and so the
         same step may be taken again).  kv_lens is a part of it.
         """
-        B, T, i32 = self.B, int(T), torch.int32
-        _check(new_tokens, "new_tokens", (B,), i32)
+        B, T, i32, at = self.B, int(T), torch.int32, self.ring.get_device()
         if state_out is None:
             state_out = self.state
-        _check(state_out, "state_out", self.state.shape, i32)
-        _on_device(stream, self.state, self.ring, self.tables, new_tokens, state_out, ws)
-        q_starts, refused = _empty((B + 1,), i32, new_tokens.device, stream), _empty((B,), i32, new_tokens.device, stream)
-        positions, slots = _empty((T,), i32, new_tokens.device, stream), _empty((T,), torch.int64, new_tokens.device, stream)
-        at = _stream(stream)
+        n = 2 * B + 2
+        asked, old = _arg(new_tokens, "new_tokens", (B,), i32, at), _arg(self.state, "state", (n,), i32, at)
+        new, ring = _arg(state_out, "state_out", (n,), i32, at), _arg(self.ring, "ring", (self.n_pages,), i32, at)
+        tables = _arg(self.tables, "tables", (B, self.table_width), i32, at)
+        handle = _launch_stream(at, stream)
+        if (B, T) != self._sizes:
+            self._sizes, self._need = (B, T), _q.qgemm_kv_extend_workspace(B, T)
         if ws is None:
-            ws = self._workspace.of(_q.qgemm_kv_extend_workspace(B, T), stream, at)
-        old, new = _ptr(self.state), _ptr(state_out)
-        _q.qgemm_kv_extend(B, T, self.page_size, _ptr(new_tokens), old, old + 4 * B, old + 8 * B, _ptr(self.ring),
-                           self.n_pages, _ptr(self.tables), self.table_width, self.prefix_len, self.window, self.sinks,
-                           _ptr(q_starts), new, new + 4 * B, new + 8 * B, _ptr(positions), _ptr(slots), _ptr(refused),
-                           _ptr(ws), 0 if ws is None else ws.numel(), at)
+            ws = self._workspace.of(self._need, stream, handle)
+        # one allocation for the three int32 arrays
+        q_starts, refused, positions = _empty((2 * B + 1 + T,), i32, self.ring.device, stream).split((B + 1, B, T))
+        slots = _empty((T,), torch.int64, self.ring.device, stream)
+        first = q_starts.data_ptr()
+        _q.qgemm_kv_extend(B, T, self.page_size, asked, old, old + 4 * B, old + 8 * B, ring, self.n_pages, tables,
+                           self.table_width, self.prefix_len, self.window, self.sinks, first, new, new + 4 * B, new + 8 * B,
+                           first + 4 * (2 * B + 1), slots.data_ptr(), first + 4 * (B + 1), _ptr(ws),
+                           0 if ws is None else ws.numel(), handle)
         return {"q_starts": q_starts, "kv_lens": state_out[:B], "positions": positions, "slots": slots, "refused": refused}
 
 
-def _norm_args(q, k, D, q_heads, kv_heads, cos, sin, positions, q_weight, k_weight, eps, interleaved):
+def _norm_args(q, k, D, q_heads, kv_heads, cos, sin, positions, q_weight, k_weight, eps, interleaved, at):
     """The arguments that normed and rotated heads and their gradients share, checked."""
-    T = q.shape[0]
-    n_pos, half = _angles(cos, sin)
-    _check(positions, "positions", (T,), torch.int32)
-    _check(q_weight, "q_weight", (D,), torch.float16)
-    _check(k_weight, "k_weight", (D,), torch.float16)
-    return (T, q_heads, kv_heads, D, *_rows(q, "q", T, q_heads * D), *_rows(k, "k", T, kv_heads * D), _ptr(q_weight),
-            _ptr(k_weight), eps, _ptr(cos), _ptr(sin), n_pos, 2 * half, int(bool(interleaved)), _ptr(positions))
+    T, (n_pos, half), f16, f32 = q.shape[0], cos.shape, torch.float16, torch.float32
+    table = (_arg(q_weight, "q_weight", (D,), f16, at), _arg(k_weight, "k_weight", (D,), f16, at), eps,
+             _arg(cos, "cos", (n_pos, half), f32, at), _arg(sin, "sin", (n_pos, half), f32, at), n_pos, 2 * half,
+             1 if interleaved else 0, _arg(positions, "positions", (T,), torch.int32, at))
+    if k.get_device() != at:
+        raise ValueError(f"q and k lie on devices {q.device} and {k.device}")
+    return (T, q_heads, kv_heads, D, *_rows(q, "q", T, q_heads * D), *_rows(k, "k", T, kv_heads * D), *table)
 
 
 def norm_rotate(q, k, head_dim, cos, sin, positions, q_weight=None, k_weight=None, eps=1e-6, interleaved=False, q_out=None,
@@ -500,16 +517,21 @@ def norm_rotate(q, k, head_dim, cos, sin, positions, q_weight=None, k_weight=Non
 
     q [T, q_heads * head_dim], k [T, kv_heads * head_dim]: rows may be slices of a wider array.
     """
-    D, T = int(head_dim), q.shape[0]
-    q_heads, kv_heads = q.shape[1] // D, k.shape[1] // D
-    args = _norm_args(q, k, D, q_heads, kv_heads, cos, sin, positions, q_weight, k_weight, eps, interleaved)
-    q_out = _empty((T, q_heads, D), torch.float16, q.device, stream) if q_out is None else q_out
-    k_out = _empty((T, kv_heads, D), torch.float16, q.device, stream) if k_out is None else k_out
-    _check(q_out, "q_out", (T, q_heads, D), torch.float16)
-    _check(k_out, "k_out", (T, kv_heads, D), torch.float16)
-    _on_device(stream, q, k, cos, sin, positions, q_weight, k_weight, q_out, k_out)
-    _q.qgemm_norm_rotate(*args, _ptr(q_out), _ptr(k_out), _stream(stream))
+    D, (T, q_width), at, f16 = int(head_dim), q.shape, q.get_device(), torch.float16
+    q_heads, kv_heads = q_width // D, k.shape[1] // D
+    args = _norm_args(q, k, D, q_heads, kv_heads, cos, sin, positions, q_weight, k_weight, eps, interleaved, at)
+    handle = _launch_stream(at, stream)
+    if q_out is None:
+        q_out = _empty((T, q_heads, D), f16, q.device, stream)
+    if k_out is None:
+        k_out = _empty((T, kv_heads, D), f16, q.device, stream)
+    _q.qgemm_norm_rotate(*args, _arg(q_out, "q_out", (T, q_heads, D), f16, at), _arg(k_out, "k_out", (T, kv_heads, D), f16, at),
+                         handle)
     return q_out, k_out
+
+
+# the workspace of gradients depends on their sizes alone
+_norm_workspace = functools.lru_cache(maxsize=256)(_q.qgemm_norm_rotate_backward_workspace)
 
 
 def norm_rotate_backward(q, k, dq_out, dk_out, cos, sin, positions, q_weight=None, k_weight=None, eps=1e-6,
@@ -519,20 +541,22 @@ def norm_rotate_backward(q, k, dq_out, dk_out, cos, sin, positions, q_weight=Non
 
     dq, dk: where the gradients go, shaped like q and k; rows may be slices of a wider array.
     """
-    T, q_heads, D = dq_out.shape
-    kv_heads = dk_out.shape[1]
-    args = _norm_args(q, k, D, q_heads, kv_heads, cos, sin, positions, q_weight, k_weight, eps, interleaved)
-    _check(dq_out, "dq_out", (q.shape[0], q_heads, D), torch.float16)
-    _check(dk_out, "dk_out", (q.shape[0], kv_heads, D), torch.float16)
-    dq = _empty((T, q_heads * D), torch.float16, q.device, stream) if dq is None else dq
-    dk = _empty((T, kv_heads * D), torch.float16, q.device, stream) if dk is None else dk
-    new = lambda w: _empty((D,), torch.float32, q.device, stream) if weight_grads and w is not None else None  # noqa: E731
-    dqw, dkw = new(q_weight), new(k_weight)
-    need = _q.qgemm_norm_rotate_backward_workspace(T, q_heads, kv_heads, D, dqw is not None or dkw is not None)
-    if ws is None and need:
-        ws = _empty((need,), torch.uint8, q.device, stream)
-    _on_device(stream, q, k, dq_out, dk_out, cos, sin, positions, q_weight, k_weight, dq, dk, ws)
-    _q.qgemm_norm_rotate_backward(*args, _ptr(dq_out), _ptr(dk_out), *_rows(dq, "dq", T, q_heads * D),
-                                  *_rows(dk, "dk", T, kv_heads * D), _ptr(dqw), _ptr(dkw), _ptr(ws),
-                                  0 if ws is None else ws.numel(), _stream(stream))
+    (T, q_heads, D), kv_heads, at, f16 = dq_out.shape, dk_out.shape[1], q.get_device(), torch.float16
+    args = _norm_args(q, k, D, q_heads, kv_heads, cos, sin, positions, q_weight, k_weight, eps, interleaved, at)
+    grads = _arg(dq_out, "dq_out", (q.shape[0], q_heads, D), f16, at), _arg(dk_out, "dk_out", (q.shape[0], kv_heads, D), f16, at)
+    handle = _launch_stream(at, stream)
+    if dq is None:
+        dq = _empty((T, q_heads * D), f16, q.device, stream)
+    if dk is None:
+        dk = _empty((T, kv_heads * D), f16, q.device, stream)
+    if dq.get_device() != at or dk.get_device() != at:
+        raise ValueError(f"dq and dk lie on devices {dq.device} and {dk.device}")
+    dqw = dkw = None
+    if weight_grads and (q_weight is not None or k_weight is not None):
+        dqw, dkw = _empty((2, D), torch.float32, q.device, stream).unbind()
+        dqw, dkw = None if q_weight is None else dqw, None if k_weight is None else dkw
+        if ws is None:
+            ws = _empty((_norm_workspace(T, q_heads, kv_heads, D, True),), torch.uint8, q.device, stream)
+    _q.qgemm_norm_rotate_backward(*args, *grads, *_rows(dq, "dq", T, q_heads * D), *_rows(dk, "dk", T, kv_heads * D), _ptr(dqw),
+                                  _ptr(dkw), _ptr(ws), 0 if ws is None else ws.numel(), handle)
     return {"dq": dq, "dk": dk, "dq_weight": dqw, "dk_weight": dkw}

@@ -257,21 +257,21 @@ def qgemm_attention(cache, T, q_heads, q, q_stride, B, q_starts, kv_lens, tables
 
 def qgemm_kv_append_norm(cache, T, q_heads, q, q_stride, k, k_stride, v, v_stride, q_weight, k_weight, eps, cos, sin,
                          n_positions, rot_dim, interleaved, positions, slots, q_out, stream=0):
-    st = load().qgemm_kv_append_norm(None if cache is None else ctypes.byref(cache), int(T), int(q_heads), q or None,
-                                     int(q_stride), k or None, int(k_stride), v or None, int(v_stride), q_weight or None,
-                                     k_weight or None, float(eps), cos or None, sin or None, int(n_positions),
-                                     int(rot_dim), int(interleaved), positions or None, slots or None, q_out or None,
-                                     stream or None)
+    st = load().qgemm_kv_append_norm(None if cache is None else ctypes.byref(cache), int(T), int(q_heads), q,
+                                     int(q_stride), k, int(k_stride), v, int(v_stride), q_weight,
+                                     k_weight, float(eps), cos, sin, int(n_positions),
+                                     int(rot_dim), int(interleaved), positions, slots, q_out,
+                                     stream)
     if st != QGEMM_OK:
         raise QGemmError(st, "qgemm_kv_append_norm")
 
 
 def qgemm_norm_rotate(T, q_heads, kv_heads, head_dim, q, q_stride, k, k_stride, q_weight, k_weight, eps, cos, sin,
                       n_positions, rot_dim, interleaved, positions, q_out, k_out, stream=0):
-    st = load().qgemm_norm_rotate(int(T), int(q_heads), int(kv_heads), int(head_dim), q or None, int(q_stride), k or None,
-                                  int(k_stride), q_weight or None, k_weight or None, float(eps), cos or None, sin or None,
-                                  int(n_positions), int(rot_dim), int(interleaved), positions or None, q_out or None,
-                                  k_out or None, stream or None)
+    st = load().qgemm_norm_rotate(int(T), int(q_heads), int(kv_heads), int(head_dim), q, int(q_stride), k,
+                                  int(k_stride), q_weight, k_weight, float(eps), cos, sin,
+                                  int(n_positions), int(rot_dim), int(interleaved), positions, q_out,
+                                  k_out, stream)
     if st != QGEMM_OK:
         raise QGemmError(st, "qgemm_norm_rotate")
 
@@ -288,12 +288,12 @@ def qgemm_norm_rotate_backward_workspace(T, q_heads, kv_heads, head_dim, weight_
 def qgemm_norm_rotate_backward(T, q_heads, kv_heads, head_dim, q, q_stride, k, k_stride, q_weight, k_weight, eps, cos,
                                sin, n_positions, rot_dim, interleaved, positions, dq_out, dk_out, dq, dq_stride, dk,
                                dk_stride, dq_weight, dk_weight, workspace, workspace_bytes, stream=0):
-    st = load().qgemm_norm_rotate_backward(int(T), int(q_heads), int(kv_heads), int(head_dim), q or None, int(q_stride),
-                                           k or None, int(k_stride), q_weight or None, k_weight or None, float(eps),
-                                           cos or None, sin or None, int(n_positions), int(rot_dim), int(interleaved),
-                                           positions or None, dq_out or None, dk_out or None, dq or None, int(dq_stride),
-                                           dk or None, int(dk_stride), dq_weight or None, dk_weight or None,
-                                           workspace or None, int(workspace_bytes), stream or None)
+    st = load().qgemm_norm_rotate_backward(int(T), int(q_heads), int(kv_heads), int(head_dim), q, int(q_stride),
+                                           k, int(k_stride), q_weight, k_weight, float(eps),
+                                           cos, sin, int(n_positions), int(rot_dim), int(interleaved),
+                                           positions, dq_out, dk_out, dq, int(dq_stride),
+                                           dk, int(dk_stride), dq_weight, dk_weight,
+                                           workspace, int(workspace_bytes), stream)
     if st != QGEMM_OK:
         raise QGemmError(st, "qgemm_norm_rotate_backward")
 
@@ -309,11 +309,11 @@ def qgemm_kv_extend_workspace(B, T) -> int:
 def qgemm_kv_extend(B, T, page_size, new_tokens, lens, gone, ring_state, ring, ring_size, tables, table_width, prefix_len,
                     window, sinks, q_starts, lens_out, gone_out, ring_state_out, positions, slots, refused, workspace,
                     workspace_bytes, stream=0):
-    st = load().qgemm_kv_extend(int(B), int(T), int(page_size), new_tokens or None, lens or None, gone or None,
-                                ring_state or None, ring or None, int(ring_size), tables or None, int(table_width),
-                                int(prefix_len), int(window), int(sinks), q_starts or None, lens_out or None,
-                                gone_out or None, ring_state_out or None, positions or None, slots or None,
-                                refused or None, workspace or None, int(workspace_bytes), stream or None)
+    st = load().qgemm_kv_extend(int(B), int(T), int(page_size), new_tokens, lens, gone,
+                                ring_state, ring, int(ring_size), tables, int(table_width),
+                                int(prefix_len), int(window), int(sinks), q_starts, lens_out,
+                                gone_out, ring_state_out, positions, slots,
+                                refused, workspace, int(workspace_bytes), stream)
     if st != QGEMM_OK:
         raise QGemmError(st, "qgemm_kv_extend")
 
@@ -331,11 +331,11 @@ def qgemm_attention_window_workspace(cache, T, q_heads, B, max_q, max_len, prefi
 def qgemm_attention_window(cache, T, q_heads, q, q_stride, B, q_starts, kv_lens, tables, table_width, prefix_table,
                            prefix_len, max_q, max_len, window, sinks, scale, out, lse, workspace, workspace_bytes,
                            stream=0):
-    st = load().qgemm_attention_window(None if cache is None else ctypes.byref(cache), int(T), int(q_heads), q or None,
-                                       int(q_stride), int(B), q_starts or None, kv_lens or None, tables or None,
-                                       int(table_width), prefix_table or None, int(prefix_len), int(max_q), int(max_len),
-                                       int(window), int(sinks), float(scale), out or None, lse or None,
-                                       workspace or None, int(workspace_bytes), stream or None)
+    st = load().qgemm_attention_window(None if cache is None else ctypes.byref(cache), int(T), int(q_heads), q,
+                                       int(q_stride), int(B), q_starts, kv_lens, tables,
+                                       int(table_width), prefix_table, int(prefix_len), int(max_q), int(max_len),
+                                       int(window), int(sinks), float(scale), out, lse,
+                                       workspace, int(workspace_bytes), stream)
     if st != QGEMM_OK:
         raise QGemmError(st, "qgemm_attention_window")
 
