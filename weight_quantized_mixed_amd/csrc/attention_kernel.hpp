@@ -167,6 +167,34 @@ __device__ __forceinline__ int end_at(const Item& it, int i) {
   return it.pre_lim + min(INT32_MAX - it.pre_lim, max(0, it.lim0 + i));
 }
 
+// the key at place x of an item's list
+__device__ __forceinline__ int key_at(const Item& it, int x) {
+  const int before = it.n_late + it.n_early;
+  return x + (x < it.n_late ? it.late : x < before ? it.early - it.n_late : -before);
+}
+
+// places of an item's list that a row sees: those below late, n_early of them from early on,
+// and n_first from the first keys' place on
+struct Seen {
+  int late, early, first;
+  uint32_t n_early, n_first;
+  // (written without branches: the row differs from lane to lane)
+  __device__ __forceinline__ bool operator()(int x) const {
+    return (x < late) | ((uint32_t)(x - early) < n_early) | ((uint32_t)(x - first) < n_first);
+  }
+};
+// ... of a row that ends at key `end`, below place `stop`
+__device__ __forceinline__ Seen seen_by(const Item& it, int end, int window, int stop) {
+  auto length = [](int from, int to) { return (uint32_t)max(to - from, 0); };
+  Seen s;
+  s.late = min(stop, min(max(min(end, it.held) - it.late, 0), it.n_late));
+  s.early = it.n_late + max(end - window - it.early, 0);
+  s.n_early = length(s.early, min(stop, it.n_late + min(max(end - it.early, 0), it.n_early)));
+  s.first = it.n_late + it.n_early;
+  s.n_first = length(s.first, min(stop, s.first + min(end, it.list - s.first)));
+  return s;
+}
+
 // what keys hold past D: zeros, which add nothing to a score whatever the key's own values are
 // (another place of the key would: zero times its infinity is NaN)
 __device__ const uint4 PAST_D = {0, 0, 0, 0};
@@ -197,9 +225,9 @@ __device__ __forceinline__ void attend_tile(const Args& a, const AttnSplit& sp, 
     if constexpr (WIN) return min(it.key1, max(0, min(end_of(r), it.held) - it.late));
     else return it.pre_lim + min(cap, max(0, it.lim0 + min(r, it.rows - 1) / G));
   };
-  int lim[NT];  // (with a window the end in the sequence)
+  int lim[NT];
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) lim[nt] = WIN ? end_of(wrow0 + nt * 16 + l16) : limit_of(wrow0 + nt * 16 + l16);
+  for (int nt = 0; nt < NT; ++nt) lim[nt] = limit_of(wrow0 + nt * 16 + l16);
   // over the tile's last row (the limits grow with the row), this wave's first and last
   const int kend = __builtin_amdgcn_readfirstlane(WIN ? it.key1 : limit_of(it.row0 + T::BM - 1));
   const int wave_lo = __builtin_amdgcn_readfirstlane(limit_of(wrow0));
@@ -210,17 +238,15 @@ __device__ __forceinline__ void attend_tile(const Args& a, const AttnSplit& sp, 
   const int j0 = KEYS ? wave : 0, jstep = KEYS ? 4 : 1;
   const int cnt = nblk > j0 ? (nblk - j0 + jstep - 1) / jstep : 0;
   auto base_of = [&](int j) { return it.key0 + (j0 + j * jstep) * KT; };
-  // key at place x of the item's order, and whether row block nt sees what is there
-  auto key_at = [&](int x) {
-    if constexpr (!WIN) return x;
-    else return x < it.n_late ? it.late + x : x < it.n_late + it.n_early ? it.early + (x - it.n_late) : x - it.n_late - it.n_early;
-  };
+  // whether row block nt sees what is at place x of the item's order
+  Seen seen[WIN ? NT : 1];
+  if constexpr (WIN) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) seen[nt] = seen_by(it, end_of(wrow0 + nt * 16 + l16), a.window, kend);
+  }
   auto sees = [&](int nt, int x) {
-    if constexpr (!WIN) return x < lim[nt];
-    else {
-      const int key = key_at(x);
-      return x < kend && key < lim[nt] && (key >= lim[nt] - a.window || key < a.sinks);
-    }
+    if constexpr (WIN) return seen[nt](x);
+    else return x < lim[nt];
   };
   // whether any row of this wave may see keys of the block from base on
   auto busy = [&](int base) {
@@ -265,7 +291,8 @@ __device__ __forceinline__ void attend_tile(const Args& a, const AttnSplit& sp, 
     const uint32_t head_bytes = (uint32_t)it.kvh * row_bytes << a.page_shift;
     // token of place x of block j, as its place in the prefix's or the sequence's own pages
     auto place = [&](int j, int x, bool& own) {
-      const int t = key_at(min(base_of(j) + x, kend - 1));
+      int t = min(base_of(j) + x, kend - 1);
+      if constexpr (WIN) t = key_at(it, t);
       own = t >= it.pre;
       return own ? t - it.pre : t;
     };
@@ -711,40 +738,10 @@ __device__ __forceinline__ int queries_of(const AttnArgs& a, int b, int& start, 
   return all;
 }
 
-template <int DP, int KIND_P, int KIND_S, bool FULL, typename Args>
-__global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void attend_kernel(Args a, AttnSplit sp) {
-  extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
+// The w-th item of the sequences; false where it has no rows.
+template <int KIND, typename Args>
+__device__ __forceinline__ bool sequence_item(const Args& a, const AttnSplit& sp, int w, Item& it) {
   const int G = a.q_heads / a.kv_heads;
-  int w = blockIdx.x;
-  Item it;
-  if (KIND_P != TILE_NONE && w < sp.p_items) {
-    // workgroups go to the 8 XCDs in turn: the tiles of one part and head (the same keys)
-    // follow each other in one of them
-    const int groups = a.kv_heads * sp.p_splits;
-    int group, tile;
-    if ((groups & 7) == 0) {
-      group = (w >> 3) / sp.p_tiles * 8 + (w & 7);
-      tile = (w >> 3) % sp.p_tiles;
-    } else {
-      group = w / sp.p_tiles;
-      tile = w % sp.p_tiles;
-    }
-    const int part = group % sp.p_splits;
-    it.kvh = group / sp.p_splits;
-    it.row0 = tile * tile_rows(KIND_P);
-    it.rows = a.T * G;
-    it.tok0 = 0;
-    it.last_tok = a.T - 1;
-    it.key0 = part * sp.p_chunk;
-    it.key1 = min((int)a.prefix_len, it.key0 + sp.p_chunk);
-    it.pre = it.pre_lim = (int)a.prefix_len;
-    it.lim0 = INT32_MIN / 2;
-    it.slot = part;
-    it.own = nullptr;
-    if constexpr (KIND_P != TILE_NONE) attend_tile<DP, KIND_P, FULL>(a, sp, it, lds);
-    return;
-  }
-  if (KIND_P != TILE_NONE) w -= sp.p_items;
   // The last tiles of the sequences see the most keys: they start first, of all sequences.
   // A group (sequence, part, head: the same keys) stays in one XCD where the groups divide
   // evenly, and the heads of a sequence, which cost the same, go to different ones (with a
@@ -763,9 +760,9 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void attend_kernel(Args a, 
   const int b = group / a.kv_heads / sp.s_splits;
   int n;
   const int all = queries_of(a, b, it.tok0, n);
-  it.row0 = tile * tile_rows(KIND_S);
+  it.row0 = tile * tile_rows(KIND);
   it.rows = n * G;
-  if (it.row0 >= it.rows) return;
+  if (it.row0 >= it.rows) return false;
   it.last_tok = it.tok0 + n - 1;
   const int64_t room = a.table_width << a.page_shift;
   const int len = max(a.kv_lens[b], 0), held = (int)min((int64_t)min(len, a.max_len), room);
@@ -777,7 +774,7 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void attend_kernel(Args a, 
   it.own = a.tables + (int64_t)b * a.table_width;
   if constexpr (std::is_same_v<Args, WindowArgs>) {
     // the ends of the tile's first and last row, and where their windows begin
-    const int end0 = end_at(it, it.row0 / G), end1 = end_at(it, (min(it.row0 + tile_rows(KIND_S), it.rows) - 1) / G);
+    const int end0 = end_at(it, it.row0 / G), end1 = end_at(it, (min(it.row0 + tile_rows(KIND), it.rows) - 1) / G);
     const int begin1 = end1 - a.window;
     it.held = it.pre + held;
     it.late = it.early = it.n_early = 0;
@@ -792,7 +789,43 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void attend_kernel(Args a, 
     it.list = it.n_late + it.n_early + n_first;
     it.key1 = min(it.list, it.key0 + sp.s_chunk);
   }
-  attend_tile<DP, KIND_S, FULL>(a, sp, it, lds);
+  return true;
+}
+
+template <int DP, int KIND_P, int KIND_S, bool FULL, typename Args>
+__global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void attend_kernel(Args a, AttnSplit sp) {
+  extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
+  int w = blockIdx.x;
+  Item it;
+  if (KIND_P != TILE_NONE && w < sp.p_items) {
+    // workgroups go to the 8 XCDs in turn: the tiles of one part and head (the same keys)
+    // follow each other in one of them
+    const int groups = a.kv_heads * sp.p_splits;
+    int group, tile;
+    if ((groups & 7) == 0) {
+      group = (w >> 3) / sp.p_tiles * 8 + (w & 7);
+      tile = (w >> 3) % sp.p_tiles;
+    } else {
+      group = w / sp.p_tiles;
+      tile = w % sp.p_tiles;
+    }
+    const int part = group % sp.p_splits;
+    it.kvh = group / sp.p_splits;
+    it.row0 = tile * tile_rows(KIND_P);
+    it.rows = a.T * (a.q_heads / a.kv_heads);
+    it.tok0 = 0;
+    it.last_tok = a.T - 1;
+    it.key0 = part * sp.p_chunk;
+    it.key1 = min((int)a.prefix_len, it.key0 + sp.p_chunk);
+    it.pre = it.pre_lim = (int)a.prefix_len;
+    it.lim0 = INT32_MIN / 2;
+    it.slot = part;
+    it.own = nullptr;
+    if constexpr (KIND_P != TILE_NONE) attend_tile<DP, KIND_P, FULL>(a, sp, it, lds);
+    return;
+  }
+  if (KIND_P != TILE_NONE) w -= sp.p_items;
+  if (sequence_item<KIND_S>(a, sp, w, it)) attend_tile<DP, KIND_S, FULL>(a, sp, it, lds);
 }
 
 template <int DP, int KIND_P, int KIND_S, typename Args>
