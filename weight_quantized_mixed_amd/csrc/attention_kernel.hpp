@@ -738,14 +738,12 @@ __device__ __forceinline__ int queries_of(const AttnArgs& a, int b, int& start, 
   return all;
 }
 
-// The w-th item of the sequences; false where it has no rows.
-template <int KIND, typename Args>
-__device__ __forceinline__ bool sequence_item(const Args& a, const AttnSplit& sp, int w, Item& it) {
+// The w-th item of a call with a window; false where it has no rows.  (Placed as in attend_kernel
+// below, whose items are written out there: through a function of their own its tiles of 128 rows
+// took other registers and 4 % longer.)
+template <int KIND>
+__device__ __forceinline__ bool window_item(const WindowArgs& a, const AttnSplit& sp, int w, Item& it) {
   const int G = a.q_heads / a.kv_heads;
-  // The last tiles of the sequences see the most keys: they start first, of all sequences.
-  // A group (sequence, part, head: the same keys) stays in one XCD where the groups divide
-  // evenly, and the heads of a sequence, which cost the same, go to different ones (with a
-  // sequence in one XCD, four prompts of 700 to 1024 tokens took 165 us).
   const int groups = sp.s_items / sp.s_tiles;
   int tile, group;
   if ((groups & 7) == 0) {
@@ -766,35 +764,33 @@ __device__ __forceinline__ bool sequence_item(const Args& a, const AttnSplit& sp
   it.last_tok = it.tok0 + n - 1;
   const int64_t room = a.table_width << a.page_shift;
   const int len = max(a.kv_lens[b], 0), held = (int)min((int64_t)min(len, a.max_len), room);
-  it.pre = it.pre_lim = sp.shared ? 0 : (int)a.prefix_len;
-  it.lim0 = len - all + 1;  // from the true lengths, also where rows or tokens past the call's bounds are left out
+  it.pre = it.pre_lim = (int)a.prefix_len;
+  it.lim0 = len - all + 1;
   it.key0 = part * sp.s_chunk;
-  it.key1 = min(it.pre + held, it.key0 + sp.s_chunk);
-  it.slot = (sp.shared ? sp.p_splits : 0) + part;
+  it.slot = part;
   it.own = a.tables + (int64_t)b * a.table_width;
-  if constexpr (std::is_same_v<Args, WindowArgs>) {
-    // the ends of the tile's first and last row, and where their windows begin
-    const int end0 = end_at(it, it.row0 / G), end1 = end_at(it, (min(it.row0 + tile_rows(KIND), it.rows) - 1) / G);
-    const int begin1 = end1 - a.window;
-    it.held = it.pre + held;
-    it.late = it.early = it.n_early = 0;
-    int n_first = 0;
-    if (begin1 > a.sinks) {  // (else no row has a key between its first ones and its window)
-      it.late = begin1;
-      it.early = max(a.sinks, end0 - a.window);
-      it.n_early = max(0, min(it.late, it.held) - it.early);
-      n_first = min(a.sinks, it.held);
-    }
-    it.n_late = max(0, min(end1, it.held) - it.late);
-    it.list = it.n_late + it.n_early + n_first;
-    it.key1 = min(it.list, it.key0 + sp.s_chunk);
+  // the ends of the tile's first and last row, and where their windows begin
+  const int end0 = end_at(it, it.row0 / G), end1 = end_at(it, (min(it.row0 + tile_rows(KIND), it.rows) - 1) / G);
+  const int begin1 = end1 - a.window;
+  it.held = it.pre + held;
+  it.late = it.early = it.n_early = 0;
+  int n_first = 0;
+  if (begin1 > a.sinks) {  // (else no row has a key between its first ones and its window)
+    it.late = begin1;
+    it.early = max(a.sinks, end0 - a.window);
+    it.n_early = max(0, min(it.late, it.held) - it.early);
+    n_first = min(a.sinks, it.held);
   }
+  it.n_late = max(0, min(end1, it.held) - it.late);
+  it.list = it.n_late + it.n_early + n_first;
+  it.key1 = min(it.list, it.key0 + sp.s_chunk);
   return true;
 }
 
 template <int DP, int KIND_P, int KIND_S, bool FULL, typename Args>
 __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void attend_kernel(Args a, AttnSplit sp) {
   extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
+  const int G = a.q_heads / a.kv_heads;
   int w = blockIdx.x;
   Item it;
   if (KIND_P != TILE_NONE && w < sp.p_items) {
@@ -812,7 +808,7 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void attend_kernel(Args a, 
     const int part = group % sp.p_splits;
     it.kvh = group / sp.p_splits;
     it.row0 = tile * tile_rows(KIND_P);
-    it.rows = a.T * (a.q_heads / a.kv_heads);
+    it.rows = a.T * G;
     it.tok0 = 0;
     it.last_tok = a.T - 1;
     it.key0 = part * sp.p_chunk;
@@ -825,7 +821,41 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void attend_kernel(Args a, 
     return;
   }
   if (KIND_P != TILE_NONE) w -= sp.p_items;
-  if (sequence_item<KIND_S>(a, sp, w, it)) attend_tile<DP, KIND_S, FULL>(a, sp, it, lds);
+  if constexpr (std::is_same_v<Args, WindowArgs>) {
+    if (window_item<KIND_S>(a, sp, w, it)) attend_tile<DP, KIND_S, FULL>(a, sp, it, lds);
+    return;
+  }
+  // The last tiles of the sequences see the most keys: they start first, of all sequences.
+  // A group (sequence, part, head: the same keys) stays in one XCD where the groups divide
+  // evenly, and the heads of a sequence, which cost the same, go to different ones (with a
+  // sequence in one XCD, four prompts of 700 to 1024 tokens took 165 us).
+  const int groups = sp.s_items / sp.s_tiles;
+  int tile, group;
+  if ((groups & 7) == 0) {
+    tile = sp.s_tiles - 1 - (w >> 3) / (groups >> 3);
+    group = (w >> 3) % (groups >> 3) * 8 + (w & 7);
+  } else {
+    tile = sp.s_tiles - 1 - w / groups;
+    group = w % groups;
+  }
+  it.kvh = group % a.kv_heads;
+  const int part = group / a.kv_heads % sp.s_splits;
+  const int b = group / a.kv_heads / sp.s_splits;
+  int n;
+  const int all = queries_of(a, b, it.tok0, n);
+  it.row0 = tile * tile_rows(KIND_S);
+  it.rows = n * G;
+  if (it.row0 >= it.rows) return;
+  it.last_tok = it.tok0 + n - 1;
+  const int64_t room = a.table_width << a.page_shift;
+  const int len = max(a.kv_lens[b], 0), held = (int)min((int64_t)min(len, a.max_len), room);
+  it.pre = it.pre_lim = sp.shared ? 0 : (int)a.prefix_len;
+  it.lim0 = len - all + 1;  // from the true lengths, also where rows or tokens past the call's bounds are left out
+  it.key0 = part * sp.s_chunk;
+  it.key1 = min(it.pre + held, it.key0 + sp.s_chunk);
+  it.slot = (sp.shared ? sp.p_splits : 0) + part;
+  it.own = a.tables + (int64_t)b * a.table_width;
+  attend_tile<DP, KIND_S, FULL>(a, sp, it, lds);
 }
 
 template <int DP, int KIND_P, int KIND_S, typename Args>

@@ -69,7 +69,7 @@ __global__ __launch_bounds__(256, 2) void window_rows_kernel(WindowArgs a, AttnS
   constexpr int SL = T::SL, LOADS = T::LOADS, NQ = T::NQ, ND = T::ND;
   extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
   Item it;
-  if (!sequence_item<TILE_ROWS128>(a, sp, blockIdx.x, it)) return;
+  if (!window_item<TILE_ROWS128>(a, sp, blockIdx.x, it)) return;
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
