@@ -1,4 +1,4 @@
-"""Build libqgemm.so in-tree with hipcc for gfx950.
+"""Build libqgemm.so (hipcc, gfx950) and the module _binding.so (the host compiler) in-tree.
 
     python -m weight_quantized_mixed_amd.build
 """
@@ -7,6 +7,7 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -14,9 +15,11 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libqgemm.so")
+BINDING = os.path.join(PKG, "_binding.so")
 SOURCES = ["api.hip", "pack.hip", "gemv.hip", "gemv16.hip", "mfma.hip", "mfma_dl.hip", "mfma_dl_gated.hip", "mfma_dl_rows.hip", "mfma_big.hip", "reduce.hip", "quant.hip", "gemv_mfma.hip", "gemv_mfma4.hip", "gated.hip",
            "kv_append.hip", "attention.hip", "attention_window.hip", "norm_rotate.hip", "kv_extend.hip"]
 
+CXX = os.environ.get("CXX", "g++")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 # packed fp32 vector ops are disabled for every device pass
 DEVICE_FLAGS = ["-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]
@@ -33,6 +36,20 @@ def _run(cmd):
     return out
 
 
+def build_binding() -> str:
+    """The Python module that takes tensors to the C ABI (csrc/binding.cpp), against the installed PyTorch."""
+    import torch
+    from torch.utils.cpp_extension import include_paths
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    include = [os.path.join(ROOT, "include"), *include_paths(), sysconfig.get_paths()["include"]]
+    out = _run([CXX, "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall", "-Wno-unused-variable",
+                f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *(f"-I{d}" for d in include[:1]),
+                *(x for d in include[1:] for x in ("-isystem", d)), os.path.join(CSRC, "binding.cpp"), "-o", BINDING + ".tmp",
+                f"-L{lib}", f"-Wl,-rpath,{lib}", "-lc10", "-ltorch_cpu", "-ltorch_python"])
+    os.replace(BINDING + ".tmp", BINDING)
+    return out
+
+
 def build(verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     objs = [os.path.join(BUILD, s.replace(".hip", ".o")) for s in SOURCES]
@@ -42,7 +59,9 @@ def build(verbose: bool = False) -> str:
         return _run([HIPCC, *COMMON, *DEVICE_FLAGS, "-c", src, "-o", objs[i]])
 
     with ThreadPoolExecutor(max_workers=min(len(SOURCES), os.cpu_count() or 4)) as ex:
+        binding = ex.submit(build_binding)
         outs = list(ex.map(compile_one, range(len(SOURCES))))
+        outs.append(binding.result())
     tmp = LIB + ".tmp"
     outs.append(_run([HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp, *objs]))
     os.replace(tmp, LIB)

@@ -9,6 +9,7 @@ until the call's work is done.
 """
 from __future__ import annotations
 
+import ctypes
 import functools
 
 import numpy as np
@@ -301,24 +302,16 @@ def _rows(t, name, T, width):
     return t.data_ptr(), step if T > 1 else width
 
 
-def _arg(t, name, shape, dtype, at):
-    """Address of a contiguous tensor argument of this shape and type on device `at` (None: no address)."""
-    if t is None:
-        return 0
-    if t.dtype != dtype or t.shape != shape:
-        raise ValueError(f"{name}: {dtype} {tuple(shape)} expected, got {t.dtype} {tuple(t.shape)}")
-    if t.get_device() != at or not t.is_contiguous():
-        raise ValueError(f"{name}: a contiguous tensor on device {at} expected, got one on {t.device}")
-    return t.data_ptr()
-
-
-def _launch_stream(at, stream):
-    """Handle of the stream for a call whose tensors lie on device `at`: a kernel runs on the device of its stream."""
+def _place(t, stream):
+    """(device of a tensor, handle of the stream for a call on it): a kernel runs on the device of its stream."""
+    at = t.get_device()
     if at < 0:
-        raise ValueError("qgemm takes device tensors only")
+        return at, 0  # (refused by the call, behind its other checks)
     if at != (torch.cuda.current_device() if stream is None else stream.device.index):
         raise ValueError(f"the tensors lie on device {at}, which is not that of the stream")
-    return _stream(stream)
+    if stream is not None:
+        return at, stream.cuda_stream
+    return at, _stream(None) if _raw_stream is None else _raw_stream(at)
 
 
 # the workspace of an attention call depends on its sizes alone (the last two: window and sinks, or none of them)
@@ -342,6 +335,7 @@ class PagedKV:
         self.k = _check(new() if k is None else k, "k", shape, torch.float16)
         self.v = _check(new() if v is None else v, "v", shape, torch.float16)
         self.desc = _q.KVCacheDesc(_ptr(self.k), _ptr(self.v), self.n_pages, self.page_size, self.kv_heads, self.head_dim)
+        self.address = ctypes.addressof(self.desc)
         self._workspace = _Workspace(self.k.device)
 
     def append(self, q, k, v, cos, sin, positions, slots, q_out=None, interleaved=False, stream=None, norm_eps=None,
@@ -352,32 +346,26 @@ class PagedKV:
         norm_eps: every query and key head is first divided by its root mean square (this added to the mean) and
         multiplied by q_weight or k_weight (fp16 [head_dim], None: 1).
         """
+        if norm_eps is not None:
+            at, handle = _place(self.k, stream)
+            if stream is not None and q_out is None:
+                q_out = _empty((q.shape[0], q.shape[1] // self.head_dim, self.head_dim), torch.float16, q.device, stream)
+            return _q.binding().append_norm(at, handle, self.address, self.kv_heads, self.head_dim, q, k, v, cos, sin, positions,
+                                            q_weight, k_weight, norm_eps, interleaved, slots, q_out)
+        if q_weight is not None or k_weight is not None:
+            raise ValueError("q_weight and k_weight are those of norms: norm_eps is missing")
         (T, width), D = q.shape, self.head_dim
         q_heads, kv_width = width // D, self.kv_heads * D
         qp, qs = _rows(q, "q", T, q_heads * D)
         kp, ks = _rows(k, "k", T, kv_width)
         vp, vs = _rows(v, "v", T, kv_width)
         n_pos, half = cos.shape
-        if q_out is None:
-            q_out = _empty((T, q_heads, D), torch.float16, q.device, stream)
-        if norm_eps is not None:
-            at, i32, f32, f16 = self.k.get_device(), torch.int32, torch.float32, torch.float16
-            for t in (q, k, v):
-                if t.get_device() != at:
-                    raise ValueError(f"the cache lies on device {at}, got a tensor on {t.device}")
-            _q.qgemm_kv_append_norm(
-                self.desc, T, q_heads, qp, qs, kp, ks, vp, vs, _arg(q_weight, "q_weight", (D,), f16, at),
-                _arg(k_weight, "k_weight", (D,), f16, at), norm_eps, _arg(cos, "cos", (n_pos, half), f32, at),
-                _arg(sin, "sin", (n_pos, half), f32, at), n_pos, 2 * half, 1 if interleaved else 0,
-                _arg(positions, "positions", (T,), i32, at), _arg(slots, "slots", (T,), torch.int64, at),
-                _arg(q_out, "q_out", (T, q_heads, D), f16, at), _launch_stream(at, stream))
-            return q_out
-        if q_weight is not None or k_weight is not None:
-            raise ValueError("q_weight and k_weight are those of norms: norm_eps is missing")
         _check(cos, "cos", (n_pos, half), torch.float32)
         _check(sin, "sin", (n_pos, half), torch.float32)
         _check(positions, "positions", (T,), torch.int32)
         _check(slots, "slots", (T,), torch.int64)
+        if q_out is None:
+            q_out = _empty((T, q_heads, D), torch.float16, q.device, stream)
         _check(q_out, "q_out", (T, q_heads, D), torch.float16)
         _q.qgemm_kv_append(self.desc, T, q_heads, qp, qs, kp, ks, vp, vs, _ptr(cos), _ptr(sin), n_pos, 2 * half,
                            int(bool(interleaved)), _ptr(positions), _ptr(slots), _ptr(q_out), _stream(stream))
@@ -390,6 +378,18 @@ class PagedKV:
         window: of the tokens up to its own (the prefix's among them) a query sees the last `window` and the first `sinks`.
         """
         T, q_heads, D = q.shape
+        if window is not None:
+            at, handle = _place(self.k, stream)
+            need = _attention_workspace(self.n_pages, self.page_size, self.kv_heads, self.head_dim, T, q_heads, tables.shape[0],
+                                        max_q, max_len, prefix_len, window, sinks)
+            if ws is None:
+                ws = self._workspace.of(need, stream, handle)
+            if stream is not None and out is None:
+                out = _empty((T, q_heads, D), torch.float16, q.device, stream)
+            return _q.binding().attend_window(at, handle, self.address, self.head_dim, q, q_starts, kv_lens, tables, max_q, max_len,
+                                              prefix_table, prefix_len, scale, window, sinks, out, lse, ws)
+        if sinks:
+            raise ValueError("sinks are those of a window: window is missing")
         step, per_head, one = q.stride()
         if (D != self.head_dim or q.dtype != torch.float16 or not q.is_cuda or (one != 1 and D > 1)
                 or (per_head != D and q_heads > 1) or (step < q_heads * D and T > 1)):
@@ -409,24 +409,11 @@ class PagedKV:
             out = _empty((T, q_heads, D), torch.float16, q.device, stream)
         _check(out, "out", (T, q_heads, D), torch.float16)
         _check(lse, "lse", (T, q_heads), torch.float32)
-        if window is None and sinks:
-            raise ValueError("sinks are those of a window: window is missing")
-        seen = () if window is None else (window, sinks)
         need = _attention_workspace(self.n_pages, self.page_size, self.kv_heads, D, T, q_heads, B, max_q, max_len,
-                                    prefix_len, *seen)
+                                    prefix_len)
         at = _stream(stream)
         if ws is None:
             ws = self._workspace.of(need, stream, at)
-        if seen:
-            for t in (self.k, q_starts, kv_lens, tables, out):
-                if t.get_device() != q.get_device():
-                    raise ValueError(f"the tensors lie on devices {q.device} and {t.device}")
-            _launch_stream(q.get_device(), stream)
-            _q.qgemm_attention_window(self.desc, T, q_heads, qp, qs, B, _ptr(q_starts), _ptr(kv_lens), _ptr(tables), width,
-                                      _ptr(prefix_table) if prefix_len else 0, prefix_len, max_q, max_len, window, sinks,
-                                      D ** -0.5 if scale is None else scale, _ptr(out), _ptr(lse), _ptr(ws),
-                                      0 if ws is None else ws.numel(), at)
-            return out
         _q.qgemm_attention(self.desc, T, q_heads, qp, qs, B, _ptr(q_starts), _ptr(kv_lens), _ptr(tables), width,
                            _ptr(prefix_table) if prefix_len else 0, prefix_len, max_q, max_len,
                            D ** -0.5 if scale is None else scale, _ptr(out), _ptr(lse), _ptr(ws),
@@ -460,7 +447,6 @@ class PagePool:
         self.tables = _check(tables, "tables", (self.B, self.table_width), i32)
         self.state = torch.zeros(2 * self.B + 2, dtype=i32, device=self.ring.device)
         self.state[-1] = self.n_pages
-        self._workspace, self._sizes, self._need = _Workspace(self.ring.device), None, 0
 
     @property
     def lens(self):
@@ -476,38 +462,18 @@ class PagePool:
         state_out: where the state after the call goes (by default the pool's own; else that stays as it was, and so the
         same step may be taken again).  kv_lens is a part of it.
         """
-        B, T, i32, at = self.B, int(T), torch.int32, self.ring.get_device()
-        if state_out is None:
-            state_out = self.state
-        n = 2 * B + 2
-        asked, old = _arg(new_tokens, "new_tokens", (B,), i32, at), _arg(self.state, "state", (n,), i32, at)
-        new, ring = _arg(state_out, "state_out", (n,), i32, at), _arg(self.ring, "ring", (self.n_pages,), i32, at)
-        tables = _arg(self.tables, "tables", (B, self.table_width), i32, at)
-        handle = _launch_stream(at, stream)
-        if (B, T) != self._sizes:
-            self._sizes, self._need = (B, T), _q.qgemm_kv_extend_workspace(B, T)
-        if ws is None:
-            ws = self._workspace.of(self._need, stream, handle)
-        # one allocation for the three int32 arrays
-        q_starts, refused, positions = _empty((2 * B + 1 + T,), i32, self.ring.device, stream).split((B + 1, B, T))
-        slots = _empty((T,), torch.int64, self.ring.device, stream)
-        first = q_starts.data_ptr()
-        _q.qgemm_kv_extend(B, T, self.page_size, asked, old, old + 4 * B, old + 8 * B, ring, self.n_pages, tables,
-                           self.table_width, self.prefix_len, self.window, self.sinks, first, new, new + 4 * B, new + 8 * B,
-                           first + 4 * (2 * B + 1), slots.data_ptr(), first + 4 * (B + 1), _ptr(ws),
-                           0 if ws is None else ws.numel(), handle)
-        return {"q_starts": q_starts, "kv_lens": state_out[:B], "positions": positions, "slots": slots, "refused": refused}
-
-
-def _norm_args(q, k, D, q_heads, kv_heads, cos, sin, positions, q_weight, k_weight, eps, interleaved, at):
-    """The arguments that normed and rotated heads and their gradients share, checked."""
-    T, (n_pos, half), f16, f32 = q.shape[0], cos.shape, torch.float16, torch.float32
-    table = (_arg(q_weight, "q_weight", (D,), f16, at), _arg(k_weight, "k_weight", (D,), f16, at), eps,
-             _arg(cos, "cos", (n_pos, half), f32, at), _arg(sin, "sin", (n_pos, half), f32, at), n_pos, 2 * half,
-             1 if interleaved else 0, _arg(positions, "positions", (T,), torch.int32, at))
-    if k.get_device() != at:
-        raise ValueError(f"q and k lie on devices {q.device} and {k.device}")
-    return (T, q_heads, kv_heads, D, *_rows(q, "q", T, q_heads * D), *_rows(k, "k", T, kv_heads * D), *table)
+        at, handle = _place(self.ring, stream)
+        made = slots = None
+        if stream is not None:  # results come from the stream's memory
+            B, T = self.B, int(T)
+            made = _empty((2 * B + 1 + T,), torch.int32, self.ring.device, stream)
+            slots = _empty((T,), torch.int64, self.ring.device, stream)
+            if ws is None:
+                ws = _empty((_q.qgemm_kv_extend_workspace(B, T),), torch.uint8, self.ring.device, stream)
+        q_starts, kv_lens, positions, slots, refused = _q.binding().extend(
+            at, handle, self.page_size, self.prefix_len, self.window, self.sinks, T, new_tokens, self.state, self.ring, self.tables,
+            state_out, ws, made, slots)
+        return {"q_starts": q_starts, "kv_lens": kv_lens, "positions": positions, "slots": slots, "refused": refused}
 
 
 def norm_rotate(q, k, head_dim, cos, sin, positions, q_weight=None, k_weight=None, eps=1e-6, interleaved=False, q_out=None,
@@ -517,21 +483,11 @@ def norm_rotate(q, k, head_dim, cos, sin, positions, q_weight=None, k_weight=Non
 
     q [T, q_heads * head_dim], k [T, kv_heads * head_dim]: rows may be slices of a wider array.
     """
-    D, (T, q_width), at, f16 = int(head_dim), q.shape, q.get_device(), torch.float16
-    q_heads, kv_heads = q_width // D, k.shape[1] // D
-    args = _norm_args(q, k, D, q_heads, kv_heads, cos, sin, positions, q_weight, k_weight, eps, interleaved, at)
-    handle = _launch_stream(at, stream)
-    if q_out is None:
-        q_out = _empty((T, q_heads, D), f16, q.device, stream)
-    if k_out is None:
-        k_out = _empty((T, kv_heads, D), f16, q.device, stream)
-    _q.qgemm_norm_rotate(*args, _arg(q_out, "q_out", (T, q_heads, D), f16, at), _arg(k_out, "k_out", (T, kv_heads, D), f16, at),
-                         handle)
-    return q_out, k_out
-
-
-# the workspace of gradients depends on their sizes alone
-_norm_workspace = functools.lru_cache(maxsize=256)(_q.qgemm_norm_rotate_backward_workspace)
+    at, handle = _place(q, stream)
+    if stream is not None:
+        new = lambda x: _empty((x.shape[0], x.shape[1] // head_dim, head_dim), torch.float16, x.device, stream)  # noqa: E731
+        q_out, k_out = new(q) if q_out is None else q_out, new(k) if k_out is None else k_out
+    return _q.binding().norm_rotate(at, handle, head_dim, q, k, cos, sin, positions, q_weight, k_weight, eps, interleaved, q_out, k_out)
 
 
 def norm_rotate_backward(q, k, dq_out, dk_out, cos, sin, positions, q_weight=None, k_weight=None, eps=1e-6,
@@ -541,22 +497,15 @@ def norm_rotate_backward(q, k, dq_out, dk_out, cos, sin, positions, q_weight=Non
 
     dq, dk: where the gradients go, shaped like q and k; rows may be slices of a wider array.
     """
-    (T, q_heads, D), kv_heads, at, f16 = dq_out.shape, dk_out.shape[1], q.get_device(), torch.float16
-    args = _norm_args(q, k, D, q_heads, kv_heads, cos, sin, positions, q_weight, k_weight, eps, interleaved, at)
-    grads = _arg(dq_out, "dq_out", (q.shape[0], q_heads, D), f16, at), _arg(dk_out, "dk_out", (q.shape[0], kv_heads, D), f16, at)
-    handle = _launch_stream(at, stream)
-    if dq is None:
-        dq = _empty((T, q_heads * D), f16, q.device, stream)
-    if dk is None:
-        dk = _empty((T, kv_heads * D), f16, q.device, stream)
-    if dq.get_device() != at or dk.get_device() != at:
-        raise ValueError(f"dq and dk lie on devices {dq.device} and {dk.device}")
-    dqw = dkw = None
-    if weight_grads and (q_weight is not None or k_weight is not None):
-        dqw, dkw = _empty((2, D), torch.float32, q.device, stream).unbind()
-        dqw, dkw = None if q_weight is None else dqw, None if k_weight is None else dkw
-        if ws is None:
-            ws = _empty((_norm_workspace(T, q_heads, kv_heads, D, True),), torch.uint8, q.device, stream)
-    _q.qgemm_norm_rotate_backward(*args, *grads, *_rows(dq, "dq", T, q_heads * D), *_rows(dk, "dk", T, kv_heads * D), _ptr(dqw),
-                                  _ptr(dkw), _ptr(ws), 0 if ws is None else ws.numel(), handle)
+    at, handle = _place(q, stream)
+    dw = None
+    if stream is not None:
+        new = lambda shape, dtype: _empty(shape, dtype, q.device, stream)  # noqa: E731
+        dq, dk = new(q.shape, torch.float16) if dq is None else dq, new(k.shape, torch.float16) if dk is None else dk
+        if weight_grads:
+            T, q_heads, D = dq_out.shape
+            dw = new((2, D), torch.float32)
+            ws = new((_q.qgemm_norm_rotate_backward_workspace(T, q_heads, dk_out.shape[1], D, True),), torch.uint8) if ws is None else ws
+    dq, dk, dqw, dkw = _q.binding().norm_rotate_backward(at, handle, q, k, dq_out, dk_out, cos, sin, positions, q_weight, k_weight, eps,
+                                                         interleaved, weight_grads, dq, dk, dw, ws)
     return {"dq": dq, "dk": dk, "dq_weight": dqw, "dk_weight": dkw}

@@ -118,6 +118,24 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     return lib
 
 
+_binding = None
+
+
+def binding():
+    """The module that takes tensors to the C ABI (csrc/binding.cpp), on the library that load() gave."""
+    global _binding
+    if _binding is None:
+        lib = load()
+        try:
+            from . import _binding as module
+        except ImportError as e:
+            raise FileNotFoundError("_binding.so is missing or does not fit this PyTorch: build it with "
+                                    "`python -m weight_quantized_mixed_amd.build`") from e
+        module.bind({name: ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in EXPORTED}, QGemmError)
+        _binding = module
+    return _binding
+
+
 def _dt(x) -> int:
     return DTYPES[x] if isinstance(x, str) else int(x)
 
