@@ -8,11 +8,12 @@
 // back by a call is taken by a later call.
 //
 // One workgroup takes the sums, 1024 sequences at a time (DPP scans of a wave, the waves'
-// totals through LDS), writes what there is one of per sequence, and gives pages back.  Then
-// a token finds its sequence by bisection of the rows' starts, its page in the table (the
-// last page held, which it may fill up) or in the ring, and the first token of a new page
-// writes the table's entry.  Up to ONE_LAUNCH tokens the same workgroup does that, from LDS;
-// more go to a second launch of many workgroups, which reads the sequences from the workspace.
+// totals through LDS), and writes what there is one of per sequence.  Then a token finds its
+// sequence by bisection of the rows' starts, its page in the table (the last page held, which
+// it may fill up) or in the ring, and the first token of a new page writes the table's entry;
+// a page given back finds its sequence and its place in the table the same way, a thread each.
+// Up to ONE_LAUNCH tokens the same workgroup does that, from LDS; more go to a second launch of
+// many workgroups, which reads the sequences from the workspace.
 //
 // Sums saturate at 2^32 - 1 instead of wrapping, which is past every limit they are held
 // against (tokens of the batch, pages of the pool), and saturated sums can be joined in any order.
@@ -69,28 +70,48 @@ __device__ __forceinline__ void block_scan(uint32_t (&v)[N], uint32_t (&carry)[N
   __syncthreads();  // (the totals may be written again)
 }
 
-// what a token asks of its sequence
-struct Grown {
-  int32_t start;  // first row
+// What the second part asks of a sequence: where its rows and the pages that it gives back
+// begin among all, and the rest.
+struct Rest {
   int32_t len;    // tokens held before
   int32_t taken;  // pages that the sequences before take from the pool, or -1: refused
+  // pages given back, as their places in its table: [0, to0), then from1 on
+  int32_t to0, from1;
+};
+struct Steps {
+  Rest* rest;
+  uint32_t *starts, *puts;
+};
+// totals of a call, and the ring as it was found
+struct Totals {
+  int32_t rows, back, head, free;
 };
 
 __device__ __forceinline__ int pages_of(int64_t tokens, int shift) { return (int)((tokens + (1 << shift) - 1) >> shift); }
 
-// token t of the batch, in sequence b (or in none)
-__device__ __forceinline__ void place_token(const ExtendArgs& a, int t, int b, Grown s, int head) {
-  int pos = 0;
+// the last of n ascending starts that is at most x (n >= 1, start(0) is 0)
+__device__ __forceinline__ int sequence_of(uint32_t x, int n, const uint32_t* starts) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (starts[mid] <= x) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+// token t of the batch, of sequence b (s) that begins in row start
+__device__ __forceinline__ void place_token(const ExtendArgs& a, int t, int b, int start, const Rest& s, int head) {
+  int pos = -1;
   int64_t slot = -1;
-  if (b < a.B && s.taken < 0) pos = -1;
-  if (b < a.B && s.taken >= 0) {
-    const int j = s.len + (t - s.start), p = j >> a.page_shift, in_page = j & ((1 << a.page_shift) - 1);
+  if (s.taken >= 0) {
+    const int j = s.len + (t - start), p = j >> a.page_shift, in_page = j & ((1 << a.page_shift) - 1);
     const int old = pages_of(s.len, a.page_shift);
     int32_t* entry = a.tables + (int64_t)b * a.table_width + p;
     int32_t page;
     if (p < old) page = *entry;
     else {
-      int64_t at = (int64_t)head + s.taken + (p - old);
+      const int64_t at = (int64_t)head + s.taken + (p - old);
       page = a.ring[at < a.ring_size ? at : at - a.ring_size];
       if (in_page == 0) *entry = page;
     }
@@ -101,30 +122,22 @@ __device__ __forceinline__ void place_token(const ExtendArgs& a, int t, int b, G
   a.slots[t] = slot;
 }
 
-// the last of n ascending starts that is at most t (n >= 1, start(0) is 0)
-template <typename T, typename F>
-__device__ __forceinline__ int sequence_of(T t, int n, F start) {
-  int lo = 0, hi = n;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (start(mid) <= t) lo = mid;
-    else hi = mid;
-  }
-  return lo;
+// the i-th page given back, the nth of sequence b; the pool never holds more than it has places
+__device__ __forceinline__ void give_back(const ExtendArgs& a, uint32_t i, int b, uint32_t nth, const Rest& s, const Totals& t) {
+  const int64_t place = (int64_t)t.free + i, x = (int64_t)t.head + place;
+  if (place < a.ring_size)
+    a.ring[x < a.ring_size ? x : x - a.ring_size] =
+        a.tables[(int64_t)b * a.table_width + ((int)nth < s.to0 ? nth : s.from1 + (int)nth - s.to0)];
 }
 
-// the pages that a sequence gives back, as their places in its table: [0, to0), then from1 on
-struct Given {
-  uint32_t put;  // pages that the sequences before give back
-  int32_t to0, from1;
-};
-
-// ALL: the tokens too
+// The sums, and what there is one of per sequence.  ALL: tokens and pages given back too.
 template <bool ALL>
-__global__ __launch_bounds__(THREADS) void extend_kernel(ExtendArgs a) {
+__global__ __launch_bounds__(THREADS) void extend_kernel(ExtendArgs a, Steps steps, Totals* end) {
+  constexpr int HELD = ALL ? ONE_LAUNCH_SEQUENCES : 1;
   __shared__ uint32_t totals[2][WAVES];
-  __shared__ Given lists[THREADS];
-  __shared__ Grown grown[ALL ? ONE_LAUNCH_SEQUENCES : 1];
+  __shared__ Rest held_rest[HELD];
+  __shared__ uint32_t held_starts[HELD], held_puts[HELD];
+  if constexpr (ALL) steps = {held_rest, held_starts, held_puts};
   const int lane = threadIdx.x & 63, R = a.ring_size;
   int head = a.ring_state[0], free = a.ring_state[1];
   // (a state that no call left is brought into range, so that nothing is touched outside the pool)
@@ -150,72 +163,87 @@ __global__ __launch_bounds__(THREADS) void extend_kernel(ExtendArgs a) {
       to1 = min(past, held);
       gone_now = past > a.first_page ? max(gone, past) : gone;
     }
-    const uint32_t back0 = sums[1];
     uint32_t first[2] = {(uint32_t)n, (uint32_t)(to0 + max(to1 - from1, 0))};
     block_scan(first, sums, totals);
     // what no other sequence can help
     const uint32_t start = first[0];
     const bool fits = now <= a.table_width && a.prefix_len + len + n <= INT32_MAX && add(start, (uint32_t)n) <= (uint32_t)a.T;
     const uint32_t need = fits ? now - old : 0;
-    lists[threadIdx.x] = {first[1] - back0, to0, from1};
     uint32_t before[1] = {need};
     block_scan(before, wanted, totals);
     const bool refused = n > 0 && (!fits || (need > 0 && add(before[0], need) > (uint32_t)free));
     if (in) {
-      const int row = (int)min(start, (uint32_t)a.T);
-      a.q_starts[b] = row;
+      const uint32_t row = min(start, (uint32_t)a.T);
+      a.q_starts[b] = (int)row;
       a.refused[b] = refused;
       a.lens_out[b] = asked < 0 ? 0 : refused ? len : len + n;
       a.gone_out[b] = gone_now;
-      const Grown s = {row, len, refused ? -1 : (int)before[0]};
-      if constexpr (ALL) grown[b] = s;
-      else reinterpret_cast<Grown*>(a.scratch)[b] = s;
+      steps.starts[b] = row;
+      steps.puts[b] = first[1];
+      steps.rest[b] = {len, refused ? -1 : (int)before[0], to0, from1};
     }
     // those that were not refused come first
     if (need > 0 && !refused) taken = max(taken, add(before[0], need));
-    // the pages given back by these sequences, a thread each; the pool never holds more than it has places
-    const int64_t room = (int64_t)R - free - back0, back = min((int64_t)sums[1] - back0, room);
-    for (int64_t i = threadIdx.x; i < back; i += THREADS) {
-      const int of = sequence_of((uint32_t)i, THREADS, [&](int x) { return lists[x].put; });
-      const Given g = lists[of];
-      const int nth = (int)((uint32_t)i - g.put), page = nth < g.to0 ? nth : g.from1 + nth - g.to0;
-      const int64_t x = (int64_t)head + free + back0 + i;  // below 2 R
-      a.ring[x < R ? x : x - R] = a.tables[(int64_t)(b0 + of) * a.table_width + page];
-    }
-    if (b0 + THREADS < a.B) __syncthreads();  // (the lists are written again)
   }
   // over the workgroup: the largest of `taken`
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) taken = max(taken, (uint32_t)__shfl_xor(taken, o, 64));
   if (lane == 0) totals[0][threadIdx.x >> 6] = taken;
   __syncthreads();
-  const int end = (int)min(sums[0], (uint32_t)a.T);
+  const Totals t = {(int)min(sums[0], (uint32_t)a.T), (int)min(sums[1], (uint32_t)R), head, free};
   if (threadIdx.x == 0) {
 #pragma unroll
     for (int w = 1; w < WAVES; ++w) taken = max(taken, totals[0][w]);
     const int64_t next = (int64_t)head + taken;
-    a.q_starts[a.B] = end;
+    a.q_starts[a.B] = t.rows;
     a.ring_state_out[0] = (int)(next < R ? next : next - R);
-    a.ring_state_out[1] = (int)(min((int64_t)free + sums[1], (int64_t)R) - taken);
-    if constexpr (!ALL) reinterpret_cast<Grown*>(a.scratch)[a.B] = {end, head, 0};
+    a.ring_state_out[1] = (int)(min((int64_t)free + t.back, (int64_t)R) - taken);
+    if constexpr (!ALL) *end = t;
   }
   if constexpr (ALL) {
-    for (int t = threadIdx.x; t < a.T; t += THREADS) {
-      int b = a.B;
-      if (t < end) b = sequence_of(t, a.B, [&](int i) { return grown[i].start; });
-      place_token(a, t, b, b < a.B ? grown[b] : Grown{0, 0, 0}, head);
+    for (int i = threadIdx.x; i < a.T; i += THREADS) {
+      if (i < t.rows) {
+        const int b = sequence_of(i, a.B, held_starts);
+        place_token(a, i, b, held_starts[b], held_rest[b], head);
+      } else {
+        a.positions[i] = 0;
+        a.slots[i] = -1;
+      }
+    }
+    for (int i = threadIdx.x; i < t.back; i += THREADS) {
+      const int b = sequence_of(i, a.B, held_puts);
+      give_back(a, i, b, i - held_puts[b], held_rest[b], t);
     }
   }
 }
 
-__global__ __launch_bounds__(256) void place_tokens_kernel(ExtendArgs a) {
-  const Grown* grown = reinterpret_cast<const Grown*>(a.scratch);
-  const int end = grown[a.B].start, head = grown[a.B].len;
-  const int t = (int)(blockIdx.x * 256 + threadIdx.x);
-  if (t >= a.T) return;
-  int b = a.B;
-  if (t < end) b = sequence_of(t, a.B, [&](int i) { return grown[i].start; });
-  place_token(a, t, b, b < a.B ? grown[b] : Grown{0, 0, 0}, head);
+// Tokens, and pages given back, of many: the first GIVING workgroups take the pages, the others
+// a token a thread.  Up to STAGED sequences their starts are bisected in LDS (1500 sequences:
+// with 11 reads from the L2 one behind the other the tokens alone took 5.2 us).
+constexpr int GIVING = 32, STAGED = 4096;
+__global__ __launch_bounds__(256) void place_kernel(ExtendArgs a, Steps steps, const Totals* end) {
+  __shared__ uint32_t held[STAGED];
+  const Totals t = *end;
+  const bool giving = blockIdx.x < GIVING;
+  const uint32_t* starts = giving ? steps.puts : steps.starts;
+  const int64_t i0 = (int64_t)(giving ? blockIdx.x : blockIdx.x - GIVING) * 256, i = i0 + threadIdx.x;
+  if (a.B <= STAGED && i0 < (giving ? t.back : t.rows)) {
+    for (int b = threadIdx.x; b < a.B; b += 256) held[b] = starts[b];
+    __syncthreads();
+    starts = held;
+  }
+  if (giving) {
+    for (int64_t k = i; k < t.back; k += GIVING * 256) {
+      const int b = sequence_of((uint32_t)k, a.B, starts);
+      give_back(a, (uint32_t)k, b, (uint32_t)k - starts[b], steps.rest[b], t);
+    }
+  } else if (i < t.rows) {
+    const int b = sequence_of((uint32_t)i, a.B, starts);
+    place_token(a, (int)i, b, starts[b], steps.rest[b], t.head);
+  } else if (i < a.T) {
+    a.positions[i] = 0;
+    a.slots[i] = -1;
+  }
 }
 
 bool one_launch(int64_t B, int64_t T) { return T <= ONE_LAUNCH && B <= ONE_LAUNCH_SEQUENCES; }
@@ -223,18 +251,23 @@ bool one_launch(int64_t B, int64_t T) { return T <= ONE_LAUNCH && B <= ONE_LAUNC
 }  // namespace
 
 size_t extend_ws_bytes(int64_t B, int64_t T) {
-  return one_launch(B, T) ? 0 : (size_t)(B + 1) * sizeof(Grown);
+  return one_launch(B, T) ? 0 : sizeof(Totals) + (size_t)B * (sizeof(Rest) + 2 * sizeof(uint32_t));
 }
 
 hipError_t launch_kv_extend(const ExtendArgs& a, hipStream_t st) {
   if (one_launch(a.B, a.T)) {
-    hipLaunchKernelGGL(extend_kernel<true>, dim3(1), dim3(THREADS), 0, st, a);
+    hipLaunchKernelGGL(extend_kernel<true>, dim3(1), dim3(THREADS), 0, st, a, Steps{}, nullptr);
     return hipGetLastError();
   }
-  hipLaunchKernelGGL(extend_kernel<false>, dim3(1), dim3(THREADS), 0, st, a);
+  Totals* end = static_cast<Totals*>(a.scratch);
+  Steps steps;
+  steps.rest = reinterpret_cast<Rest*>(end + 1);
+  steps.starts = reinterpret_cast<uint32_t*>(steps.rest + a.B);
+  steps.puts = steps.starts + a.B;
+  hipLaunchKernelGGL(extend_kernel<false>, dim3(1), dim3(THREADS), 0, st, a, steps, end);
   const hipError_t e = hipGetLastError();
-  if (e != hipSuccess || a.T == 0) return e;
-  hipLaunchKernelGGL(place_tokens_kernel, dim3((unsigned)(((int64_t)a.T + 255) / 256)), dim3(256), 0, st, a);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(place_kernel, dim3((unsigned)(GIVING + ((int64_t)a.T + 255) / 256)), dim3(256), 0, st, a, steps, end);
   return hipGetLastError();
 }
 
