@@ -216,14 +216,17 @@ def test_norms_in_place_and_empty():
 
 
 def test_norms_of_more_tokens_than_one_launch_holds():
-    """2^23 + 5 rows of 33 heads: the last ones are normed too, and row offsets pass 2^31 values."""
-    T, hq, D = 2**23 + 5, 32, 8
+    """2^24 + 5 rows of 33 heads of 4 lanes (a launch takes 2^31 lanes): those of the second launch are normed too, and row
+    offsets pass 2^32 values."""
+    T, hq, D = 2**24 + 5, 32, 8
+    most = 2**31 // (33 * 4)
+    assert most < T
     gen = torch.Generator(device="cuda").manual_seed(1)
     x = torch.randint(-500, 500, (T, hq * D), generator=gen, device="cuda", dtype=torch.int16).half()
     cos, sin = torch.tensor([[1.0], [0.0]], device="cuda"), torch.tensor([[0.0], [1.0]], device="cuda")
     pos = torch.arange(T, device="cuda", dtype=I32) & 1
     qo, ko = norm_rotate(x, x[:, :D], D, cos, sin, pos, eps=1e-5, interleaved=True)
-    at = torch.tensor([0, 1, 2**23 - 1, 2**23, 2**23 + 1, T - 1], device="cuda")
+    at = torch.tensor([0, 1, most - 1, most, most + 1, T - 1], device="cuda")
     heads = x[at].view(-1, hq, D).cpu().numpy()
     c, s = cos.cpu().numpy()[pos[at].cpu()], sin.cpu().numpy()[pos[at].cpu()]
     y, e = oracle.norm_rotate_ref(heads, None, 1e-5, c, s, True)
