@@ -658,3 +658,124 @@ def test_serving_with_a_window(hq, hkv, D, rot, window, sinks, prefix):
                 ks, vs = (p[:, h // (hq // hkv)] for p in past[b])
                 ref, _, bound = oracle.attention_ref(qh[r0:r0 + n, h], ks, vs, seen, D ** -0.5)
                 assert_near(out[r0:r0 + n, h], ref, bound, f"step {step} sequence {b} head {h}")
+
+
+def test_windowed_example_runs(capsys, monkeypatch):
+    import os
+    import sys
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+    import windowed_decoder_layer as ex
+    monkeypatch.setattr(sys, "argv", ["windowed_decoder_layer.py", "--steps", "11"])
+    ex.main()
+    out = capsys.readouterr().out
+    assert out.count("finite: True") == 3 and "refused: 0" in out
+
+
+# ---- other calls that the documentation allows
+
+def test_windowed_cache_offsets_past_32_bits():
+    """Pages whose byte and value offsets pass 2**32, for single tokens and for tiles of 128 rows."""
+    hkv, D, page = 8, 128, 256
+    n_pages = (2**32 + 2**27) // (hkv * D * page)
+    k, v = (torch.empty((n_pages, hkv, page, D), dtype=torch.float16, device="cuda") for _ in range(2))
+    cache = PagedKV(n_pages, page, hkv, D, k=k, v=v)
+    rng = np.random.default_rng(2)
+    T, window, sinks = 300, 100, 7
+    rows = dev(halves(rng, T, 3 * hkv * D))
+    qt, kt, vt = rows.split([hkv * D] * 3, dim=1)
+    pages = np.array([n_pages - 1, n_pages - 3], np.int32)
+    t = np.arange(T)
+    slots = pages[t // page].astype(np.int64) * page + t % page
+    none = torch.empty((1, 0), device="cuda")
+    qo = cache.append(qt, kt, vt, none, none, torch.zeros(T, dtype=I32, device="cuda"), dev(slots), norm_eps=1e-5)
+    assert torch.equal(v[n_pages - 3, :, : T - page].transpose(0, 1), vt[page:].view(-1, hkv, D))
+    kn = k[n_pages - 1].transpose(0, 1), k[n_pages - 3, :, : T - page].transpose(0, 1)
+    kh, vh, qh = torch.cat(kn).cpu().numpy(), vt.reshape(T, hkv, D).cpu().numpy(), qo.cpu().numpy()
+    for n in (1, 200):
+        got = f64(cache.attend(qo[T - n:], ints([0, n]), ints([T]), ints(pages[None]), n, T, window=window, sinks=sinks))
+        seen = oracle.window_visible(n, T, T, 0, window, sinks)
+        for h in range(hkv):
+            ref, _, bound = oracle.attention_ref(qh[T - n:, h], kh[:, h], vh[:, h], seen, D ** -0.5)
+            assert_near(got[:, h], ref, bound, f"{n} queries, head {h}")
+
+
+def random_window_case(seed):
+    rng = np.random.default_rng(1000 + seed)
+    hkv = int(rng.choice([1, 2, 3]))
+    G = int(rng.choice([1, 2, 5, 8]))
+    B = int(rng.integers(1, 5))
+    qs = [int(rng.choice([0, 1, 3, rng.integers(1, 200)])) for _ in range(B)]
+    qs[0] = max(qs[0], 1)
+    lens = [int(rng.integers(0, 400)) if rng.random() < 0.3 else n + int(rng.integers(0, 500)) for n in qs]
+    return (hkv * G, hkv, int(rng.choice([8, 40, 64, 88, 128, 136])), int(rng.choice([1, 4, 16, 128])), qs, lens,
+            int(rng.choice([0, rng.integers(1, 300)])), int(rng.choice([1, 2, 63, 64, 65, rng.integers(1, 600)])), int(rng.choice([0, 1, 64, rng.integers(0, 400)])))
+
+
+@pytest.mark.parametrize("seed", range(40))
+def test_windowed_attention_at_random(seed):
+    """Mixed queries, lengths shorter than the queries among them, sinks past the windows, every page size."""
+    a = random_window_case(seed)
+    say("case window", a)
+    WindowCase(*a, seed=seed).upload().check()
+
+
+def test_calls_refuse_what_they_cannot_take():
+    c = NormCase(6, 4, 2, 64, 64, False, True, seed=4)
+    qt, kt, vt = c.split()
+    cos, sin, pos = c.tables()
+    slots = torch.arange(6, device="cuda")
+    cache = PagedKV(2, 8, 2, 64)
+    for eps in (0.0, -1.0, float("nan"), 1e-60):
+        for f in (lambda: cache.append(qt, kt, vt, cos, sin, pos, slots, norm_eps=eps),
+                  lambda: norm_rotate(qt, kt, 64, cos, sin, pos, eps=eps)):
+            with pytest.raises(q.QGemmError) as e:
+                f()
+            assert e.value.status == q.QGEMM_ERR_INVALID_ARG
+    d3 = torch.zeros((6, 4, 64), dtype=torch.float16, device="cuda")
+    for what, f in (("positions:", lambda: norm_rotate(qt, kt, 64, cos, sin, pos.cpu())),
+                    ("k:", lambda: cache.append(qt, kt.float(), vt, cos, sin, pos, slots, norm_eps=1e-5)),
+                    ("v:", lambda: cache.append(qt, kt, vt[:, :64], cos, sin, pos, slots, norm_eps=1e-5)),
+                    ("slots:", lambda: cache.append(qt, kt, vt, cos, sin, pos, slots.int(), norm_eps=1e-5)),
+                    ("q_out:", lambda: cache.append(qt, kt, vt, cos, sin, pos, slots, norm_eps=1e-5, q_out=d3.transpose(0, 1))),
+                    ("dk_out:", lambda: norm_rotate_backward(qt, kt, d3, d3[:, :2], cos, sin, pos)),
+                    ("dq:", lambda: norm_rotate_backward(qt, kt, d3, d3[:, :2].contiguous(), cos, sin, pos, dq=d3[0])),
+                    ("k:", lambda: norm_rotate(qt, kt[:5], 64, cos, sin, pos)), ("q:", lambda: norm_rotate(qt[0], kt, 64, cos, sin, pos))):
+        with pytest.raises(ValueError, match=what):
+            f()
+    with pytest.raises(TypeError):
+        q.binding().extend(0, 0)
+    w = WindowCase(4, 2, 64, 16, [1], [40], 20, 30, 2, seed=3).upload()
+    for kw, error in ((dict(window=0), q.QGemmError), (dict(window=-3), q.QGemmError), (dict(sinks=-1), q.QGemmError), (dict(prefix_table=None), ValueError),
+                      (dict(tables=w.dtables.long()), ValueError), (dict(q_starts=w.dstarts[:1]), ValueError), (dict(q=w.dq.float()), ValueError),
+                      (dict(q=w.dq[:, :, :32]), ValueError), (dict(lse=torch.zeros((1, 4), dtype=torch.float64, device="cuda")), ValueError)):
+        args = dict(q=w.dq, q_starts=w.dstarts, kv_lens=w.dlens, tables=w.dtables, max_q=1, max_len=40, prefix_table=w.dprefix, prefix_len=20, window=30,
+                    sinks=2)
+        with pytest.raises(error):
+            w.cache.attend(**{**args, **kw})
+    pool = PagePool(6, 16, 3, 4)
+    with pytest.raises(ValueError, match="new_tokens:"):
+        pool.extend(torch.zeros(3, dtype=I32), 4)
+    for page in (0, 24):
+        with pytest.raises(q.QGemmError):
+            PagePool(6, page, 3, 4).extend(torch.zeros(3, dtype=I32, device="cuda"), 4)
+    with pytest.raises(ValueError):
+        pool.extend(torch.zeros(3, dtype=I32, device="cuda"), -1)
+
+
+def test_results_do_not_depend_on_what_memory_held():
+    """Workspaces and results of every call begin as NaN or junk: the results are the same."""
+    c = NormCase(700, 8, 2, 96, 64, True, True, seed=7)
+    qt, kt, _ = c.split()
+    dq, dk = dev(halves(c.rng, 700, 8, 96)), dev(halves(c.rng, 700, 2, 96))
+    p = PoolCase(50, 16, 40, 900, np.arange(50) * 7, window=64, sinks=4)
+    new = ints(np.where(np.arange(50) % 7 == 6, -1, 100))
+    results = []
+    for fill in (0xFF, 0x00, 0x7B):
+        torch.cuda.empty_cache()
+        junk = [torch.full((1 << 22,), fill, dtype=torch.uint8, device="cuda") for _ in range(24)]
+        del junk
+        r = norm_rotate_backward(qt, kt, dq, dk, *c.tables(), eps=c.eps, interleaved=True, **c.weights())
+        pool = p.pool()
+        e = pool.extend(new, 5200)
+        results.append([*r.values(), *(t.clone() for t in e.values()), pool.tables.clone(), pool.ring.clone(), pool.state.clone()])
+    assert all(torch.equal(a, b) for other in results[1:] for a, b in zip(results[0], other))
