@@ -182,7 +182,21 @@ struct Seen {
   __device__ __forceinline__ bool operator()(int x) const {
     return (x < late) | ((uint32_t)(x - early) < n_early) | ((uint32_t)(x - first) < n_first);
   }
+  // the same of the 64 places from x on, a bit each
+  __device__ __forceinline__ uint64_t from(int x) const {
+    auto below = [&](int to) {
+      const int n = min(max(to - x, 0), 64);
+      return n < 64 ? ((uint64_t)1 << n) - 1 : ~(uint64_t)0;
+    };
+    return below(late) | (below(early + (int)n_early) & ~below(early)) | (below(first + (int)n_first) & ~below(first));
+  }
 };
+// score s where bit `at` of the places seen is set, else -inf: two instructions, where the three
+// intervals took ten for each score
+__device__ __forceinline__ float where_seen(uint64_t bits, int at, float s) {
+  const uint32_t keep = (uint32_t)__builtin_amdgcn_sbfe((int)(uint32_t)(bits >> (at & 32)), at & 31, 1);
+  return __uint_as_float((__float_as_uint(s) & keep) | (0xFF800000u & ~keep));
+}
 // ... of a row that ends at key `end`, below place `stop`
 __device__ __forceinline__ Seen seen_by(const Item& it, int end, int window, int stop) {
   auto length = [](int from, int to) { return (uint32_t)max(to - from, 0); };
@@ -356,10 +370,15 @@ __device__ __forceinline__ void attend_tile(const Args& a, const AttnSplit& sp, 
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         const int n = lim[nt] - base - 4 * g;
+        uint64_t bits = 0;
+        if constexpr (WIN) bits = seen[nt].from(base + 4 * g);
 #pragma unroll
         for (int u = 0; u < NSUB; ++u)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) s[nt][u][i] = (WIN ? sees(nt, base + 4 * g + u * 16 + i) : u * 16 + i < n) ? s[nt][u][i] : -INFINITY;
+          for (int i = 0; i < 4; ++i) {
+            if constexpr (WIN) s[nt][u][i] = where_seen(bits, u * 16 + i, s[nt][u][i]);
+            else s[nt][u][i] = u * 16 + i < n ? s[nt][u][i] : -INFINITY;
+          }
       }
     };
     // the largest score of each row of a block (log2 units)

@@ -1,5 +1,5 @@
-// Attention with a window: tiles of 128 rows on 32 x 32 x 16 MFMAs (few rows take the tiles of
-// attention_kernel.hpp).
+// Attention with a window: tiles of 128 rows on 32 x 32 x 16 MFMAs (few rows, and heads past 128
+// places, take the tiles of attention_kernel.hpp: here those would spill).
 //
 // A wave has 32 rows.  S^T = K Q^T takes 32 keys at a time and 16 places of the head, O^T = V^T P^T
 // 32 places of the head and 16 keys.  Lane l holds row l % 32; of a product's 32 results per row
@@ -206,10 +206,11 @@ __global__ __launch_bounds__(256, 2) void window_rows_kernel(WindowArgs a, AttnS
       s[u] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf, qf[t], s[u], 0, 0, 0);
     };
     auto hide = [&](Scores& s, int base) {
+      const uint64_t bits = seen.from(base + 4 * half);
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) s[u][i] = seen(base + 4 * half + 32 * u + 8 * (i / 4) + i % 4) ? s[u][i] : -INFINITY;
+        for (int i = 0; i < 16; ++i) s[u][i] = where_seen(bits, 32 * u + 8 * (i / 4) + i % 4, s[u][i]);
     };
     // over the two lanes of a row
     auto both = [&](float v, auto f) {
@@ -349,7 +350,7 @@ __global__ __launch_bounds__(256, 2) void window_rows_kernel(WindowArgs a, AttnS
         else f[x % AHEAD] = v_operand(odd, (x + AHEAD - NS) % ND, (x + AHEAD - NS) / ND);
 #pragma unroll
         for (int y = x * PS / NS; y < (x + 1) * PS / NS; ++y) exp_pair(now, y);
-        });
+      });
       float part = -INFINITY;
       static_for(std::make_integer_sequence<int, NP>{}, [&](auto X) {
         constexpr int x = decltype(X)::value, PX = 3 * ND;  // the last pairs before the keys that need them
@@ -362,7 +363,7 @@ __global__ __launch_bounds__(256, 2) void window_rows_kernel(WindowArgs a, AttnS
 #pragma unroll
         for (int y = x * 32 / NP; y < (x + 1) * 32 / NP; ++y) part = fmaxf(part, next[y / 16][y % 16]);
         stay(part);
-        });
+      });
       float top;
       if (j + 1 < whole) top = both(part, larger) * c;
       else {

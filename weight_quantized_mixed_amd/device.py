@@ -428,7 +428,8 @@ class PagePool:
     prefix_len tokens of a shared prefix come before the sequences' own (in pages outside the pool); with a window, pages
     of tokens that no query will see again are given back, but for those of the first `sinks` tokens.
     state: int32 [2 * sequences + 2]: the sequences' lengths, their first pages that no window gave back, and of the ring
-    the first free page's place and how many are free.
+    the first free page's place and how many are free.  Each call takes the state that the one before left: calls on one
+    pool follow one another, on one stream or with the caller's waits between streams.
     """
 
     def __init__(self, n_pages, page_size, sequences, table_width, prefix_len=0, window=None, sinks=0, device="cuda",
@@ -447,6 +448,7 @@ class PagePool:
         self.tables = _check(tables, "tables", (self.B, self.table_width), i32)
         self.state = torch.zeros(2 * self.B + 2, dtype=i32, device=self.ring.device)
         self.state[-1] = self.n_pages
+        self._streams = set()
 
     @property
     def lens(self):
@@ -463,6 +465,11 @@ class PagePool:
         same step may be taken again).  kv_lens is a part of it.
         """
         at, handle = _place(self.ring, stream)
+        if handle not in self._streams:  # freed with the pool, its arrays wait for every stream that used them
+            for t in (self.state, self.ring, self.tables):
+                if at >= 0:
+                    t.record_stream(torch.cuda.current_stream() if stream is None else stream)
+            self._streams.add(handle)
         made = slots = None
         if stream is not None:  # results come from the stream's memory
             B, T = self.B, int(T)
