@@ -113,6 +113,13 @@ __device__ __forceinline__ void landed() {
   asm volatile("" ::: "memory");
 }
 
+// query heads of a key / value head, and the query of an item's row; with a window without a division
+// (a tile of a small one takes about 10 us, of which those at its start were 1)
+__device__ __forceinline__ int heads_per_kv(const AttnArgs& a) { return a.q_heads / a.kv_heads; }
+__device__ __forceinline__ int heads_per_kv(const WindowArgs& a) { return a.per_head; }
+__device__ __forceinline__ int query_of(const AttnArgs&, int row, int per_head) { return row / per_head; }
+__device__ __forceinline__ int query_of(const WindowArgs& a, int row, int) { return a.by_per_head(row); }
+
 // Geometry of a tile kind for head dimensions up to DP.
 template <int DP, int KIND>
 struct TileGeo {
@@ -226,14 +233,14 @@ __device__ __forceinline__ void attend_tile(const Args& a, const AttnSplit& sp, 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int g = lane >> 4, l16 = lane & 15;
-  const int G = a.q_heads / a.kv_heads, D = a.D;
+  const int G = heads_per_kv(a), D = a.D;
 
   // ---- rows of this wave, and the keys that they see (the smaller of the two bounds before
   // pre_lim is added: the lengths that a call holds may pass the ones it states)
   const int wrow0 = it.row0 + (KEYS ? 0 : wave * NT * 16);
   const int cap = it.key1 - it.pre_lim;
   // keys up to row r's own, the prefix's among them
-  auto end_of = [&](int r) { return end_at(it, min(r, it.rows - 1) / G); };
+  auto end_of = [&](int r) { return end_at(it, query_of(a, min(r, it.rows - 1), G)); };
   // ... and in the order of the item: the keys below this are seen, and (without a window) no others
   auto limit_of = [&](int r) {
     if constexpr (WIN) return min(it.key1, max(0, min(end_of(r), it.held) - it.late));
@@ -284,7 +291,15 @@ __device__ __forceinline__ void attend_tile(const Args& a, const AttnSplit& sp, 
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int r = min(wrow0 + nt * 16 + l16, it.rows - 1);
-      const int tok = min(it.tok0 + r / G, it.last_tok), head = it.kvh * G + r % G;
+      int tok, head;
+      if constexpr (WIN) {
+        const int i = query_of(a, r, G);
+        tok = min(it.tok0 + i, it.last_tok);
+        head = it.kvh * G + (r - i * G);
+      } else {
+        tok = min(it.tok0 + r / G, it.last_tok);
+        head = it.kvh * G + r % G;
+      }
       const _Float16* q = a.q + (int64_t)tok * a.q_stride + (int64_t)head * D;
 #pragma unroll
       for (int t = 0; t < NQ; ++t) {
@@ -692,7 +707,7 @@ __device__ __forceinline__ void attend_tile(const Args& a, const AttnSplit& sp, 
   for (int nt = 0; nt < NT; ++nt) l[nt] = across_rows(l[nt], [](float x, float y) { return x + y; });
   // number of row r among all (query, head) pairs
   auto pair_of = [&](int r) {
-    const int i = r / G;
+    const int i = query_of(a, r, G);
     return (int64_t)(it.tok0 + i) * a.q_heads + it.kvh * G + (r - i * G);
   };
   // (m, l, o) of a pair: into its partial slot, or divided into the output
@@ -762,23 +777,13 @@ __device__ __forceinline__ int queries_of(const AttnArgs& a, int b, int& start, 
 // took other registers and 4 % longer.)
 template <int KIND>
 __device__ __forceinline__ bool window_item(const WindowArgs& a, const AttnSplit& sp, int w, Item& it) {
-  const int G = a.q_heads / a.kv_heads;
-  const int groups = sp.s_items / sp.s_tiles;
-  int tile, group;
-  if ((groups & 7) == 0) {
-    tile = sp.s_tiles - 1 - (w >> 3) / (groups >> 3);
-    group = (w >> 3) % (groups >> 3) * 8 + (w & 7);
-  } else {
-    tile = sp.s_tiles - 1 - w / groups;
-    group = w % groups;
-  }
-  it.kvh = group % a.kv_heads;
-  const int part = group / a.kv_heads % sp.s_splits;
-  const int b = group / a.kv_heads / sp.s_splits;
+  const int above = a.by_groups(w), tile = sp.s_tiles - 1 - above, group = w - above * a.groups;
+  const int pair = a.by_kv_heads(group), b = a.by_splits(pair), part = pair - b * sp.s_splits;
+  it.kvh = group - pair * a.kv_heads;
   int n;
   const int all = queries_of(a, b, it.tok0, n);
   it.row0 = tile * tile_rows(KIND);
-  it.rows = n * G;
+  it.rows = n * a.per_head;
   if (it.row0 >= it.rows) return false;
   it.last_tok = it.tok0 + n - 1;
   const int64_t room = a.table_width << a.page_shift;
@@ -789,7 +794,8 @@ __device__ __forceinline__ bool window_item(const WindowArgs& a, const AttnSplit
   it.slot = part;
   it.own = a.tables + (int64_t)b * a.table_width;
   // the ends of the tile's first and last row, and where their windows begin
-  const int end0 = end_at(it, it.row0 / G), end1 = end_at(it, (min(it.row0 + tile_rows(KIND), it.rows) - 1) / G);
+  const int end0 = end_at(it, a.by_per_head(it.row0));
+  const int end1 = end_at(it, a.by_per_head(min(it.row0 + tile_rows(KIND), it.rows) - 1));
   const int begin1 = end1 - a.window;
   it.held = it.pre + held;
   it.late = it.early = it.n_early = 0;
@@ -809,9 +815,13 @@ __device__ __forceinline__ bool window_item(const WindowArgs& a, const AttnSplit
 template <int DP, int KIND_P, int KIND_S, bool FULL, typename Args>
 __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void attend_kernel(Args a, AttnSplit sp) {
   extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
-  const int G = a.q_heads / a.kv_heads;
   int w = blockIdx.x;
   Item it;
+  if constexpr (std::is_same_v<Args, WindowArgs>) {
+    if (window_item<KIND_S>(a, sp, w, it)) attend_tile<DP, KIND_S, FULL>(a, sp, it, lds);
+    return;
+  }
+  const int G = a.q_heads / a.kv_heads;
   if (KIND_P != TILE_NONE && w < sp.p_items) {
     // workgroups go to the 8 XCDs in turn: the tiles of one part and head (the same keys)
     // follow each other in one of them
@@ -840,10 +850,6 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void attend_kernel(Args a, 
     return;
   }
   if (KIND_P != TILE_NONE) w -= sp.p_items;
-  if constexpr (std::is_same_v<Args, WindowArgs>) {
-    if (window_item<KIND_S>(a, sp, w, it)) attend_tile<DP, KIND_S, FULL>(a, sp, it, lds);
-    return;
-  }
   // The last tiles of the sequences see the most keys: they start first, of all sequences.
   // A group (sequence, part, head: the same keys) stays in one XCD where the groups divide
   // evenly, and the heads of a sequence, which cost the same, go to different ones (with a

@@ -64,7 +64,7 @@ typedef float float16v __attribute__((ext_vector_type(16)));
 __device__ __forceinline__ void stay(float& v) { asm volatile("" : "+v"(v)); }
 
 template <int DP, bool FULL>
-__global__ __launch_bounds__(256, 2) void window_rows_kernel(WindowArgs a, AttnSplit sp) {
+__global__ __launch_bounds__(256, DP == 64 ? 3 : 2) void window_rows_kernel(WindowArgs a, AttnSplit sp) {
   using T = RowsGeo<DP>;
   constexpr int SL = T::SL, LOADS = T::LOADS, NQ = T::NQ, ND = T::ND;
   extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
@@ -74,16 +74,16 @@ __global__ __launch_bounds__(256, 2) void window_rows_kernel(WindowArgs a, AttnS
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int half = lane >> 5, l32 = lane & 31, l16 = lane & 15;
-  const int G = a.q_heads / a.kv_heads, D = a.D;
+  const int G = a.per_head, D = a.D;
   const int kend = __builtin_amdgcn_readfirstlane(it.key1);
   const int cnt = kend > it.key0 ? (kend - it.key0 + KT - 1) / KT : 0;
   auto base_of = [&](int j) { return it.key0 + j * KT; };
 
   // this lane's row, its place among the tokens and what it sees
-  const int row = min(it.row0 + wave * 32 + l32, it.rows - 1), query = row / G;
+  const int row = min(it.row0 + wave * 32 + l32, it.rows - 1), query = a.by_per_head(row);
   const Seen seen = seen_by(it, end_at(it, query), a.window, kend);
   // blocks that every row of the tile sees whole
-  const int first_end = end_at(it, it.row0 / G);
+  const int first_end = end_at(it, a.by_per_head(it.row0));
   const int whole = (max(min(kend, min(max(min(first_end, it.held) - it.late, 0), it.n_late)), it.key0) - it.key0) / KT;
 
   float16v o[ND];
@@ -333,7 +333,9 @@ __global__ __launch_bounds__(256, 2) void window_rows_kernel(WindowArgs a, AttnS
       publish(j + 3, next_rows);
       next_rows = find(j + 4);
     };
-    constexpr int AHEAD = 4, NS = 2 * NQ, NP = 4 * ND, PS = 12;  // (PS pairs of the 16 beside the scores)
+    // (three workgroups a CU with heads of 64, which leaves registers for two operands ahead: window 64
+    // 32 -> 28 us, 1024 101 -> 98 us; PS pairs of the 16 beside the scores)
+    constexpr int AHEAD = DP == 64 ? 2 : 4, NS = 2 * NQ, NP = 4 * ND, PS = 12;
     static_assert(NS % AHEAD == 0 && NP >= AHEAD, "operand ring");
     // a block that is not the last one: its probabilities and product, and the scores of the next
     auto block = [&](int j, auto ODD, Scores& now, Scores& next) {
@@ -472,7 +474,14 @@ hipError_t launch_dim(const WindowArgs& a, const AttnSplit& p, hipStream_t st) {
 
 }  // namespace
 
-hipError_t launch_window_tiles(const WindowArgs& a, const AttnSplit& p, hipStream_t st) {
+hipError_t launch_window_tiles(const WindowArgs& args, const AttnSplit& p, hipStream_t st) {
+  WindowArgs a = args;
+  a.per_head = a.q_heads / a.kv_heads;
+  a.groups = p.s_items / p.s_tiles;
+  a.by_per_head = Divide::by(a.per_head);
+  a.by_groups = Divide::by(a.groups);
+  a.by_kv_heads = Divide::by(a.kv_heads);
+  a.by_splits = Divide::by(p.s_splits);
   return a.D <= 64 ? launch_dim<64>(a, p, st) : a.D <= 128 ? launch_dim<128>(a, p, st) : launch_dim<256>(a, p, st);
 }
 

@@ -365,6 +365,21 @@ struct ExtendArgs {
 size_t extend_ws_bytes(int64_t B, int64_t T);
 hipError_t launch_kv_extend(const ExtendArgs& a, hipStream_t st);
 
+// Division of 32-bit numbers by one that the host knows, as a product (Granlund and Montgomery,
+// 1994): n / d = (t + ((n - t) >> s1)) >> s2 with t the high half of n mul.
+struct Divide {
+  uint32_t mul, s1, s2;
+  static Divide by(uint32_t d) {
+    uint32_t l = 0;
+    while (((uint64_t)1 << l) < d) ++l;
+    return {(uint32_t)(((((uint64_t)1 << l) - d) << 32) / d + 1), l < 1 ? l : 1, l < 1 ? 0 : l - 1};
+  }
+  __device__ __forceinline__ int operator()(int n) const {
+    const uint32_t t = __umulhi(mul, (uint32_t)n);
+    return (int)((t + (((uint32_t)n - t) >> s1)) >> s2);
+  }
+};
+
 // attention over the paged cache (attention.hip)
 struct AttnArgs {
   const _Float16 *q, *k, *v;
@@ -378,6 +393,10 @@ struct AttnArgs {
 // the same where a query sees the last `window` of the keys up to its own and the first `sinks`
 struct WindowArgs : AttnArgs {
   int32_t window, sinks;
+  // set by launch_window_tiles: query heads of a key / value head, (sequence, part, head) groups of
+  // items, and divisions by these and by the other sizes
+  int32_t per_head, groups;
+  Divide by_per_head, by_groups, by_kv_heads, by_splits;
 };
 // sizes that the host knows, which choose the split of the work (window 0: none)
 struct AttnShape {
