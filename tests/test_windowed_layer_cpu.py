@@ -194,3 +194,11 @@ def test_wrong_tensors_are_refused_before_any_address():
             norm_rotate_backward(x, x, x.view(4, 2, 32), x.view(4, 2, 32), **{"cos": t, "sin": t, "positions": pos, **kw})
     with pytest.raises(ValueError, match="device tensors only"):
         norm_rotate(x, x, 32, t, t, pos)
+
+
+def test_sizes_past_32_bits_are_refused_by_name():
+    torch = pytest.importorskip("torch")
+    from weight_quantized_mixed_amd.device import PagePool
+    pool = PagePool(4, 2**32 + 16, 2, 4, device="cpu")
+    with pytest.raises(ValueError, match="page_size"):
+        pool.extend(torch.zeros(2, dtype=torch.int32), 0)

@@ -779,3 +779,35 @@ def test_results_do_not_depend_on_what_memory_held():
         e = pool.extend(new, 5200)
         results.append([*r.values(), *(t.clone() for t in e.values()), pool.tables.clone(), pool.ring.clone(), pool.state.clone()])
     assert all(torch.equal(a, b) for other in results[1:] for a, b in zip(results[0], other))
+
+
+def test_workspaces_have_to_be_whole():
+    """A workspace that is large by its shape alone is refused, and so is a small one."""
+    byte = torch.zeros(1, dtype=torch.uint8, device="cuda")
+    c = NormCase(6, 4, 2, 64, 64, False, True, seed=4)
+    qt, kt, _ = c.split()
+    d = [torch.zeros((6, h, 64), dtype=torch.float16, device="cuda") for h in (4, 2)]
+    w = WindowCase(4, 2, 64, 16, [1], [2000], 0, 1500, 2, seed=3).upload()
+    pool = PagePool(6, 16, 3, 4)
+    for ws, error in ((byte.expand(1 << 24), ValueError), (byte, q.QGemmError)):
+        for f in (lambda: norm_rotate_backward(qt, kt, *d, *c.tables(), **c.weights(), ws=ws),
+                  lambda: w.cache.attend(w.dq, w.dstarts, w.dlens, w.dtables, max_q=1, max_len=2000, window=1500, sinks=2, ws=ws),
+                  lambda: pool.extend(torch.zeros(3, dtype=I32, device="cuda"), 5000, ws=ws)):
+            with pytest.raises(error):
+                f()
+
+
+def test_windows_in_parts_do_not_depend_on_what_memory_held():
+    w = WindowCase(8, 2, 128, 16, [1, 3, 40, 0], [3000, 5, 900, 60], 70, 1500, 40, seed=3).upload()
+    need = q.qgemm_attention_window_workspace(w.cache.desc, 44, 8, 4, 40, 3000, 70, 1500, 40)
+    assert need > 0
+    results = []
+    for fill in (0xFF, 0x00, 0x7B):
+        ws = torch.full((need,), fill, dtype=torch.uint8, device="cuda")
+        out = torch.full((44, 8, 128), float("nan"), dtype=torch.float16, device="cuda")
+        lse = torch.full((44, 8), float("nan"), device="cuda")
+        w.cache.attend(w.dq, w.dstarts, w.dlens, w.dtables, max_q=40, max_len=3000, prefix_table=w.dprefix, prefix_len=70, window=1500, sinks=40,
+                       ws=ws, out=out, lse=lse)
+        results.append((out, lse))
+    assert not torch.isnan(results[0][0]).any()
+    assert all(torch.equal(a, b) for other in results[1:] for a, b in zip(results[0], other))

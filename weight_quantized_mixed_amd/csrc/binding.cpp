@@ -131,6 +131,24 @@ Rows rows(const at::Tensor* t, const char* name, int64_t T, int64_t width, int64
   return {t->data_ptr(), T > 1 ? t->stride(0) : width};
 }
 
+// a number that the library takes in 32 bits
+int32_t narrow(int64_t v, const char* name) {
+  if (v != (int32_t)v) throw std::invalid_argument(std::string(name) + ": " + std::to_string(v) + " is too large");
+  return (int32_t)v;
+}
+
+// address and bytes of a workspace (null for null)
+struct Scratch {
+  void* at;
+  size_t bytes;
+};
+Scratch scratch(const at::Tensor* t, int64_t device) {
+  if (!t) return {nullptr, 0};
+  on_device(*t, "ws", device);
+  if (!t->is_contiguous()) throw std::invalid_argument("ws: a contiguous tensor expected");
+  return {t->data_ptr(), (size_t)t->nbytes()};
+}
+
 void two(const at::Tensor* t, const char* name) {
   if (t->dim() != 2) throw std::invalid_argument(std::string(name) + ": two dimensions expected, got " + shape_of(t->sizes()));
 }
@@ -172,7 +190,7 @@ Norm norm_args(Args& a, int64_t T, int64_t D) {
   n.interleaved = a.truth();
   n.n_positions = cos->size(0);
   const int64_t half = cos->size(1);
-  n.rot = (int32_t)(2 * half);
+  n.rot = narrow(2 * half, "rot_dim");
   n.cos = (float*)whole(cos, "cos", {n.n_positions, half}, at::kFloat, a.device);
   n.sin = (float*)whole(sin, "sin", {n.n_positions, half}, at::kFloat, a.device);
   n.positions = (int32_t*)whole(pos, "positions", {T}, at::kInt, a.device);
@@ -203,7 +221,7 @@ PyObject* append_norm(PyObject*, PyObject* const* args, Py_ssize_t) {
     at::Tensor made;
     if (!out) out = &(made = empty({T, heads, D}, at::kHalf, a.device));
     void* to = whole(out, "q_out", {T, heads, D}, at::kHalf, a.device);
-    check(lib.append_norm(cache, T, (int32_t)heads, rq.at, rq.step, rk.at, rk.step, rv.at, rv.step, n.q_weight, n.k_weight, n.eps,
+    check(lib.append_norm(cache, T, narrow(heads, "q_heads"), rq.at, rq.step, rk.at, rk.step, rv.at, rv.step, n.q_weight, n.k_weight, n.eps,
                           n.cos, n.sin, n.n_positions, n.rot, n.interleaved, n.positions, slots, to, stream),
           "qgemm_kv_append_norm");
     return result(given, made);
@@ -223,6 +241,7 @@ PyObject* norm_rotate(PyObject*, PyObject* const* args, Py_ssize_t) {
     two(k, "k");
     if (D < 1) throw std::invalid_argument("head_dim: at least 1 expected");
     const int64_t T = q->size(0), hq = q->size(1) / D, hk = k->size(1) / D;
+    const int32_t nq = narrow(hq, "q_heads"), nk = narrow(hk, "kv_heads");
     const Norm n = norm_args(a, T, D);
     const Rows rq = rows(q, "q", T, hq * D, a.device), rk = rows(k, "k", T, hk * D, a.device);
     PyObject *gq = a.next[0], *gk = a.next[1];
@@ -232,7 +251,7 @@ PyObject* norm_rotate(PyObject*, PyObject* const* args, Py_ssize_t) {
     if (!qo) qo = &(mq = empty({T, hq, D}, at::kHalf, a.device));
     if (!ko) ko = &(mk = empty({T, hk, D}, at::kHalf, a.device));
     void *to_q = whole(qo, "q_out", {T, hq, D}, at::kHalf, a.device), *to_k = whole(ko, "k_out", {T, hk, D}, at::kHalf, a.device);
-    check(lib.norm_rotate(T, (int32_t)hq, (int32_t)hk, (int32_t)D, rq.at, rq.step, rk.at, rk.step, n.q_weight, n.k_weight, n.eps, n.cos,
+    check(lib.norm_rotate(T, nq, nk, narrow(D, "head_dim"), rq.at, rq.step, rk.at, rk.step, n.q_weight, n.k_weight, n.eps, n.cos,
                           n.sin, n.n_positions, n.rot, n.interleaved, n.positions, to_q, to_k, stream),
           "qgemm_norm_rotate");
     PyObject *a0 = result(gq, mq), *a1 = result(gk, mk);
@@ -250,6 +269,7 @@ PyObject* norm_rotate_backward(PyObject*, PyObject* const* args, Py_ssize_t) {
     const at::Tensor *q = a.tensor("q"), *k = a.tensor("k"), *dqo = a.tensor("dq_out"), *dko = a.tensor("dk_out");
     if (dqo->dim() != 3 || dko->dim() != 3) throw std::invalid_argument("dq_out, dk_out: three dimensions expected");
     const int64_t T = dqo->size(0), hq = dqo->size(1), hk = dko->size(1), D = dqo->size(2);
+    const int32_t nq = narrow(hq, "q_heads"), nk = narrow(hk, "kv_heads");
     const Norm n = norm_args(a, T, D);
     const Rows rq = rows(q, "q", T, hq * D, a.device), rk = rows(k, "k", T, hk * D, a.device);
     const void *gq = whole(dqo, "dq_out", {T, hq, D}, at::kHalf, a.device), *gk = whole(dko, "dk_out", {T, hk, D}, at::kHalf, a.device);
@@ -262,20 +282,20 @@ PyObject* norm_rotate_backward(PyObject*, PyObject* const* args, Py_ssize_t) {
     if (!dk) dk = &(mk = empty({T, hk * D}, at::kHalf, a.device));
     const Rows to_q = rows(dq, "dq", T, hq * D, a.device), to_k = rows(dk, "dk", T, hk * D, a.device);
     float *wq = nullptr, *wk = nullptr;
-    size_t bytes = 0;
+    Scratch held{nullptr, 0};
     if (weights) {
-      check(lib.norm_rotate_backward_workspace(T, (int32_t)hq, (int32_t)hk, (int32_t)D, 1, &bytes), "qgemm_norm_rotate_backward_workspace");
+      size_t bytes = 0;
+      check(lib.norm_rotate_backward_workspace(T, nq, nk, narrow(D, "head_dim"), 1, &bytes), "qgemm_norm_rotate_backward_workspace");
       if (!dw) dw = &(mw = empty({2, D}, at::kFloat, a.device));
       if (!ws) ws = &(ms = empty({(int64_t)bytes}, at::kByte, a.device));
       float* w = (float*)whole(dw, "weights", {2, D}, at::kFloat, a.device);
       wq = n.q_weight ? w : nullptr;
       wk = n.k_weight ? w + D : nullptr;
-      bytes = (size_t)ws->nbytes();
-      on_device(*ws, "ws", a.device);
+      held = scratch(ws, a.device);
     }
-    check(lib.norm_rotate_backward(T, (int32_t)hq, (int32_t)hk, (int32_t)D, rq.at, rq.step, rk.at, rk.step, n.q_weight, n.k_weight, n.eps,
+    check(lib.norm_rotate_backward(T, nq, nk, narrow(D, "head_dim"), rq.at, rq.step, rk.at, rk.step, n.q_weight, n.k_weight, n.eps,
                                    n.cos, n.sin, n.n_positions, n.rot, n.interleaved, n.positions, gq, gk, to_q.at, to_q.step, to_k.at,
-                                   to_k.step, wq, wk, weights ? ws->data_ptr() : nullptr, bytes, stream),
+                                   to_k.step, wq, wk, held.at, held.bytes, stream),
           "qgemm_norm_rotate_backward");
     auto weight = [&](float* w, int64_t i) {
       if (w) return THPVariable_Wrap(dw->select(0, i));
@@ -295,7 +315,8 @@ PyObject* extend(PyObject*, PyObject* const* args, Py_ssize_t) {
     Args a{args, -1};
     a.device = a.integer();
     void* stream = (void*)a.integer();
-    const int64_t page = a.integer(), prefix = a.integer(), window = a.integer(), sinks = a.integer(), T = a.integer();
+    const int32_t page = narrow(a.integer(), "page_size");
+    const int64_t prefix = a.integer(), window = a.integer(), sinks = a.integer(), T = a.integer();
     const at::Tensor *news = a.tensor("new_tokens"), *state = a.tensor("state"), *ring = a.tensor("ring"), *tables = a.tensor("tables");
     const at::Tensor *out = a.tensor("state_out", true), *ws = a.tensor("ws", true), *res = a.tensor("results", true);
     PyObject* given = *a.next;
@@ -314,15 +335,14 @@ PyObject* extend(PyObject*, PyObject* const* args, Py_ssize_t) {
     size_t bytes = 0;
     check(lib.extend_workspace(B, T, &bytes), "qgemm_kv_extend_workspace");
     if (bytes && !ws) ws = &(mw = empty({(int64_t)bytes}, at::kByte, a.device));
-    if (ws) on_device(*ws, "ws", a.device);
+    const Scratch held = scratch(ws, a.device);
     // one allocation for the three int32 arrays: q_starts, refused, positions
     if (!res) res = &(mr = empty({2 * B + 1 + T}, at::kInt, a.device));
     if (!slots) slots = &(ms = empty({T}, at::kLong, a.device));
     int32_t* to = (int32_t*)whole(res, "results", {2 * B + 1 + T}, at::kInt, a.device);
     int64_t* to_slots = (int64_t*)whole(slots, "slots", {T}, at::kLong, a.device);
-    check(lib.extend(B, T, (int32_t)page, asked, before, before + B, before + 2 * B, pages, R, table, width, prefix, window, sinks, to, after,
-                     after + B, after + 2 * B, to + 2 * B + 1, to_slots, to + B + 1, ws ? ws->data_ptr() : nullptr,
-                     ws ? (size_t)ws->nbytes() : 0, stream),
+    check(lib.extend(B, T, page, asked, before, before + B, before + 2 * B, pages, R, table, width, prefix, window, sinks, to, after,
+                     after + B, after + 2 * B, to + 2 * B + 1, to_slots, to + B + 1, held.at, held.bytes, stream),
           "qgemm_kv_extend");
     auto part = [](const at::Tensor& t, int64_t from, int64_t count) { return THPVariable_Wrap(t.narrow(0, from, count)); };
     PyObject *a0 = part(*res, 0, B + 1), *a1 = part(*out, 0, B), *a2 = part(*res, 2 * B + 1, T), *a3 = result(given, ms),
@@ -372,9 +392,9 @@ PyObject* attend_window(PyObject*, PyObject* const* args, Py_ssize_t) {
     if (!out) out = &(made = empty({T, heads, D}, at::kHalf, a.device));
     void* to = whole(out, "out", {T, heads, D}, at::kHalf, a.device);
     float* sums = (float*)whole(lse, "lse", {T, heads}, at::kFloat, a.device);
-    if (ws) on_device(*ws, "ws", a.device);
-    check(lib.attention_window(cache, T, (int32_t)heads, q->data_ptr(), step, B, s, l, t, width, p, prefix_len, max_q, max_len, window, sinks,
-                               (float)scale, to, sums, ws ? ws->data_ptr() : nullptr, ws ? (size_t)ws->nbytes() : 0, stream),
+    const Scratch held = scratch(ws, a.device);
+    check(lib.attention_window(cache, T, narrow(heads, "q_heads"), q->data_ptr(), step, B, s, l, t, width, p, prefix_len, max_q, max_len, window, sinks,
+                               (float)scale, to, sums, held.at, held.bytes, stream),
           "qgemm_attention_window");
     return result(given, made);
   });
