@@ -16,11 +16,16 @@
 // (the compiler may move things between the steps: fences kept them apart for nothing, but sums and
 // maxima that it gathered behind the loop cost 2 %).
 //
-// Measured (8192 tokens of one prompt, 32 / 8 heads of 128): window 64 54 us, 256 79 us, 1024
-// 169 us (770 TFLOP/s), 4096 435 us (950); on 16 x 16 x 32 tiles 78, 111, 200 and 466 us.  A block of
-// two workgroups takes a CU about 3850 cycles (4650 on the 16 x 16 tiles) at 1.84 GHz (2.04):
-// the clock gives way to the matrix cores, so fewer stalls buy less time than cycles, and neither
-// deeper operand rings, other orders of the steps nor wave priorities moved it by 1 %.
+// Measured (8192 tokens of one prompt, 32 / 8 heads of 128): window 64 46 us, 256 72 us, 1024
+// 162 us (807 TFLOP/s), 4096 426 us (970); 32 / 4 heads of 64: 27, 40, 96 and 261 us.  The 16 x 16 x
+// 32 tiles took 78, 111, 200 and 466 us with heads of 128, these 54, 79, 169 and 435 as they were
+// first; then scores hidden by bits instead of intervals (window 64 54 -> 49 us) and items placed
+// without divisions (49 -> 46).  A block of two workgroups takes a CU about 3850 cycles (4650 on the
+// 16 x 16 tiles) at 1.84 GHz (2.04): the clock gives way to the matrix cores, so fewer stalls buy
+// less time than cycles, and neither deeper operand rings, other orders of the steps nor wave
+// priorities moved it by 1 %.  The LDS gives each wave the whole block, 32 KiB of keys and values for
+// heads of 128, 1024 cycles for the four waves and as many as their products; 64 rows a wave would
+// halve that, but left one wave to a SIMD and took no less time.
 //
 // Where a key's row lies in the cache one lane of each wave finds out, two blocks ahead of its
 // loads, and leaves it in LDS for the lanes that load (found by every lane for itself it took about

@@ -15,6 +15,11 @@
 // Up to ONE_LAUNCH tokens the same workgroup does that, from LDS; more go to a second launch of
 // many workgroups, which reads the sequences from the workspace.
 //
+// Measured: 1 sequence 3.9 us, 48 sequences of up to 8000 tokens 5.2 us (a launch with nothing in it
+// about 2.5); 24 sequences of 8400 tokens 3.8 + 3.5 us, 1500 of 30000 tokens 5.8 + 5.5 us.  Nothing but
+// latency bounds it: the sums wait for two barriers a thousand sequences, a token for the reads of
+// its bisection, which lie one behind the other.
+//
 // Sums saturate at 2^32 - 1 instead of wrapping, which is past every limit they are held
 // against (tokens of the batch, pages of the pool), and saturated sums can be joined in any order.
 #include "qgemm_internal.hpp"
