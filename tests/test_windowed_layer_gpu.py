@@ -811,3 +811,35 @@ def test_windows_in_parts_do_not_depend_on_what_memory_held():
         results.append((out, lse))
     assert not torch.isnan(results[0][0]).any()
     assert all(torch.equal(a, b) for other in results[1:] for a, b in zip(results[0], other))
+
+
+@pytest.mark.parametrize("D", [136, 192, 256])
+def test_windows_of_wide_heads_over_many_rows(D):
+    """Enough tiles that those of 128 rows are taken for heads past 128 too (20 of 64 rows a sequence's heads, 256 CUs)."""
+    say("case wide heads", D)
+    WindowCase(16, 16, D, 16, [300, 301, 299, 250], [300, 500, 290, 600], 20, 100, 30, seed=D).upload().check()
+    WindowCase(32, 16, D, 64, [150, 1, 170], [150, 900, 400], 0, 260, 0, seed=D + 1).upload().check()
+
+
+@pytest.mark.parametrize("hq,hkv,D,qs,lens", [(4, 2, 64, [40, 150], [50, 150]), (4, 2, 128, [40, 150], [50, 150]), (16, 16, 256, [300, 301, 299, 250], [310, 500, 299, 600]),
+                                              (16, 16, 136, [300, 301, 299, 250], [310, 500, 299, 600])])
+def test_infinities_at_any_place_reach_the_rows_that_see_them(hq, hkv, D, qs, lens):
+    c = WindowCase(hq, hkv, D, 16, qs, lens, 70, 90, 33, seed=D)
+    rng = np.random.default_rng(D)
+    bad = []  # (sequence, token, kv head, place, value)
+    for b, n in enumerate(lens):
+        for t in rng.choice(n, 12, replace=False):
+            if c.visible(b)[:, 70 + t].any():
+                bad.append((b, int(t), int(rng.integers(hkv)), int(rng.integers(D)), float(rng.choice([np.inf, -np.inf, np.nan]))))
+    say(f"case infinities {hq}/{hkv} heads of {D}: {len(bad)}")
+    plain, _ = c.upload().run()
+    want = plain.copy()
+    for b, t, h, e, value in bad:
+        c.v[c.tables[b, t // 16], h, t % 16, e] = value
+        rows = np.flatnonzero(c.visible(b)[:, 70 + t]) + c.starts[b]
+        heads = range(h * (hq // hkv), (h + 1) * (hq // hkv))
+        with np.errstate(invalid="ignore"):
+            want[np.ix_(rows, heads, [e])] += np.asarray(value, want.dtype)
+    got, _ = c.upload().run()
+    finite = np.isfinite(want)
+    assert not finite.all() and np.array_equal(got[finite], plain[finite]) and np.array_equal(got[~finite], want[~finite], equal_nan=True)

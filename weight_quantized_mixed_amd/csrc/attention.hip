@@ -70,25 +70,43 @@ void split_keys(int64_t keys, int64_t items, int64_t want, int64_t min_chunk, in
 // The same for a window, whose few keys make a join dear (300 queries with a window of 100, 32 / 8
 // heads of 128, three sequences: 11 us whole and 28 us in two parts): the number of parts whose sum of
 // three terms is least, each as measured, in us.  A block of 64 keys (KEYS: 128, by four waves) takes a CU
-// 0.65, 1.0 and 1.7 (KEYS: a quarter more) with heads of 64, 128 and 256; an item's beginning and end as
+// 0.65, 1.0 and 1.7 (128 rows: 2.4; KEYS: a quarter more) with heads of 64, 128 and 256; an item's beginning and end as
 // long as about two and a half of them; items run a CU each, then the next.  A join is 4 and the partial
 // results at 4.85 TB/s both ways.  Over 120 batches of 20 to 1000 queries and windows of 100 to 6000 this
 // takes 0.78 of the time that as many parts as make 512 items take (geometric mean; 0.37 to 1.06), over 114
 // of one or two queries 0.96 (0.70 to 1.04).
-void split_window(const AttnShape& s, int64_t keys, AttnSplit* p) {
-  const int64_t G = s.q_heads / s.kv_heads, rows = tile_rows(p->kind_s), step = p->kind_s == TILE_KEYS ? 128 : 64;
-  // (the tiles that have rows, as many as there may be)
-  const int64_t tiles = s.B + s.T * G / rows, most = s.B * p->s_tiles, items = (tiles < most ? tiles : most) * s.kv_heads;
-  const double width = s.D <= 64 ? 0.65 : s.D <= 128 ? 1.0 : 1.7, block = p->kind_s == TILE_KEYS ? 1.25 * width : width;
+// With heads past 128 the tiles of 64 rows, which one workgroup is soonest done with, are weighed against
+// those of 128 (8 / 2 heads of 256, window 100: 300 queries 11 and 17 us, 3000 queries 24 and 20).
+void split_window(const AttnShape& s, AttnSplit* p) {
+  const int64_t G = s.q_heads / s.kv_heads, max_rows = s.max_q * G;
   const double part = 2.0 * s.T * s.q_heads * (s.D + 2) * sizeof(float) / 4.85e6;
-  if (keys < 1) keys = 1;
-  double best = 0;
-  for (int n = 1; n <= JOIN_SLOTS / 2; ++n) {
-    const int64_t chunk = div_up(div_up(keys, n), step) * step, parts = div_up(keys, chunk);
-    if (parts < n) continue;  // (these parts have been looked at)
-    const double us = div_up(items * parts, 256) * (chunk / step + 2.5) * block + (parts > 1 ? 4 + parts * part : 0);
-    if (n == 1 || us < best) best = us, p->s_chunk = (int)chunk, p->s_splits = (int)parts;
-  }
+  double best = INFINITY;
+  auto weigh = [&](int kind, double block) {
+    const int64_t rows = tile_rows(kind), step = kind == TILE_KEYS ? 128 : 64;
+    // the window of a tile's last query, what its earlier ones see before that, and the first keys
+    const int64_t queries = (rows - 1) / G + 2, all = s.max_len + s.prefix_len;
+    const int64_t list = s.window + (queries < s.max_q ? queries : s.max_q) + s.sinks;
+    const int64_t keys = all < 1 ? 1 : list < all ? list : all;
+    // (the tiles that have rows, as many as there may be)
+    const int64_t of_rows = s.B + s.T * G / rows, most = s.B * div_up(max_rows, rows);
+    const int64_t items = (of_rows < most ? of_rows : most) * s.kv_heads;
+    for (int n = 1; n <= JOIN_SLOTS / 2; ++n) {
+      const int64_t chunk = div_up(div_up(keys, n), step) * step, parts = div_up(keys, chunk);
+      if (parts < n) continue;  // (these parts have been looked at)
+      const double us = div_up(items * parts, 256) * (chunk / step + 2.5) * block + (parts > 1 ? 4 + parts * part : 0);
+      if (us >= best) continue;
+      best = us;
+      p->kind_s = kind;
+      p->s_tiles = (int)div_up(max_rows, rows);
+      p->s_chunk = (int)chunk;
+      p->s_splits = (int)parts;
+    }
+  };
+  const double width = s.D <= 64 ? 0.65 : s.D <= 128 ? 1.0 : 1.7;
+  if (max_rows <= 16) weigh(TILE_KEYS, 1.25 * width);
+  else if (max_rows <= 64) weigh(TILE_ROWS64, width);
+  else if (s.D <= 128) weigh(TILE_ROWS128, width);
+  else weigh(TILE_ROWS64, width), weigh(TILE_ROWS128, 2.4);
 }
 
 // (head dimensions past 128 keep 64 rows: with 128 the accumulators of a wave spilled)
@@ -98,12 +116,17 @@ int kind_for(int64_t rows, int D) {
 
 AttnSplit choose_split(const AttnShape& s) {
   AttnSplit p = {};
+  p.kind_p = TILE_NONE;
+  if (s.window) {  // (each sequence reads what it sees of the prefix by itself)
+    split_window(s, &p);
+    p.s_items = (int)(s.B * s.kv_heads * p.s_tiles * p.s_splits);
+    p.slots = p.s_splits > 1 ? p.s_splits : 0;
+    return p;
+  }
   const int64_t G = s.q_heads / s.kv_heads, rows = s.max_q * G;
   int64_t keys = s.max_len + s.prefix_len;  // of one item
   p.kind_s = kind_for(rows, s.D);
-  p.kind_p = TILE_NONE;
-  // (with a window each sequence reads what it sees of the prefix by itself)
-  p.shared = s.prefix_len > 0 && s.B > 1 && rows <= 64 && !s.window;
+  p.shared = s.prefix_len > 0 && s.B > 1 && rows <= 64;
   p.s_tiles = (int)div_up(rows, tile_rows(p.kind_s));
   const int64_t s_base = s.B * s.kv_heads * p.s_tiles;
   if (p.shared) {
@@ -111,15 +134,9 @@ AttnSplit choose_split(const AttnShape& s) {
     p.p_tiles = (int)div_up(s.T * G, tile_rows(p.kind_p));
     split_keys(s.prefix_len, (int64_t)p.p_tiles * s.kv_heads, 256, 128, &p.p_chunk, &p.p_splits);
     p.p_items = p.p_tiles * p.p_splits * s.kv_heads;
+    keys = s.max_len;
   }
-  if (p.shared) keys = s.max_len;
-  if (s.window) {  // the window of a tile's last query, what its earlier ones see before that, and the first keys
-    const int64_t queries = (tile_rows(p.kind_s) - 1) / G + 2;
-    const int64_t list = s.window + (queries < s.max_q ? queries : s.max_q) + s.sinks;
-    split_window(s, list < keys ? list : keys, &p);
-  } else {
-    split_keys(keys, s_base, 512, 128, &p.s_chunk, &p.s_splits);
-  }
+  split_keys(keys, s_base, 512, 128, &p.s_chunk, &p.s_splits);
   p.s_items = (int)(s_base * p.s_splits);
   p.slots = (p.shared ? p.p_splits : 0) + p.s_splits;
   if (p.slots == 1) p.slots = 0;

@@ -1,5 +1,5 @@
-// Attention with a window: tiles of 128 rows on 32 x 32 x 16 MFMAs (few rows, and heads past 128
-// places, take the tiles of attention_kernel.hpp: here those would spill).
+// Attention with a window: tiles of 128 rows on 32 x 32 x 16 MFMAs (up to 64 rows a sequence take the
+// tiles of attention_kernel.hpp).
 //
 // A wave has 32 rows.  S^T = K Q^T takes 32 keys at a time and 16 places of the head, O^T = V^T P^T
 // 32 places of the head and 16 keys.  Lane l holds row l % 32; of a product's 32 results per row
@@ -20,12 +20,15 @@
 // 162 us (807 TFLOP/s), 4096 426 us (970); 32 / 4 heads of 64: 27, 40, 96 and 261 us.  The 16 x 16 x
 // 32 tiles took 78, 111, 200 and 466 us with heads of 128, these 54, 79, 169 and 435 as they were
 // first; then scores hidden by bits instead of intervals (window 64 54 -> 49 us) and items placed
-// without divisions (49 -> 46).  A block of two workgroups takes a CU about 3850 cycles (4650 on the
-// 16 x 16 tiles) at 1.84 GHz (2.04): the clock gives way to the matrix cores, so fewer stalls buy
-// less time than cycles, and neither deeper operand rings, other orders of the steps nor wave
-// priorities moved it by 1 %.  The LDS gives each wave the whole block, 32 KiB of keys and values for
-// heads of 128, 1024 cycles for the four waves and as many as their products; 64 rows a wave would
-// halve that, but left one wave to a SIMD and took no less time.
+// without divisions (49 -> 46).  16 / 4 heads of 256 (one workgroup a CU, sums in the accumulation
+// registers): 67, 95, 199 and 482 us, on 16 x 16 x 32 tiles of 64 rows 94, 146, 325 and 816.
+//
+// With heads of 128 a block of two workgroups takes a CU about 3850 cycles (4650 on the 16 x 16 tiles)
+// at 1.84 GHz (2.04): the clock gives way to the matrix cores, so fewer stalls buy less time than
+// cycles, and neither deeper operand rings, other orders of the steps nor wave priorities moved it by
+// 1 %.  The LDS gives each wave the whole block, 32 KiB of keys and values: 1024 cycles for the four
+// waves, as many as their products; 64 rows a wave would halve that, but left one wave to a SIMD and
+// took no less time.
 //
 // Where a key's row lies in the cache one lane of each wave finds out, two blocks ahead of its
 // loads, and leaves it in LDS for the lanes that load (found by every lane for itself it took about
@@ -69,7 +72,7 @@ typedef float float16v __attribute__((ext_vector_type(16)));
 __device__ __forceinline__ void stay(float& v) { asm volatile("" : "+v"(v)); }
 
 template <int DP, bool FULL>
-__global__ __launch_bounds__(256, DP == 64 ? 3 : 2) void window_rows_kernel(WindowArgs a, AttnSplit sp) {
+__global__ __launch_bounds__(256, DP == 64 ? 3 : DP == 128 ? 2 : 1) void window_rows_kernel(WindowArgs a, AttnSplit sp) {
   using T = RowsGeo<DP>;
   constexpr int SL = T::SL, LOADS = T::LOADS, NQ = T::NQ, ND = T::ND;
   extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
@@ -174,24 +177,21 @@ __global__ __launch_bounds__(256, DP == 64 ? 3 : 2) void window_rows_kernel(Wind
       }
     }
     // ... values 16 t + 8 half .. + 7 of key 32 u + l % 32
-    uint32_t key_read[NQ];
-#pragma unroll
-    for (int t = 0; t < NQ; ++t) key_read[t] = l32 * T::ROWB + (((2 * t + half) ^ key_swizzle<SL>(l32)) * 16);
+    const uint32_t key_read = l32 * T::ROWB + ((half ^ key_swizzle<SL>(l32)) * 16);
     auto k_operand = [&](int odd, int u, int t) {
-      return *reinterpret_cast<const half8v*>(lds + odd * T::BLOCK + u * 32 * T::ROWB + key_read[t]);
+      return *reinterpret_cast<const half8v*>(lds + odd * T::BLOCK + u * 32 * T::ROWB + (key_read ^ (t * 32)));
     };
     // ... value 32 d + l % 32 of keys 16 k + 4 half + (0..3) and + 8
-    uint32_t value_read[ND];
+    uint32_t value_read;
     {
       const int r = 4 * half + (l16 >> 2), lo = 2 * ((lane >> 4) & 1) + ((l16 >> 1) & 1);
-#pragma unroll
-      for (int d = 0; d < ND; ++d) value_read[d] = r * T::ROWB + (((4 * d) ^ value_swizzle<SL>(r)) + lo) * 16 + (l16 & 1) * 8;
+      value_read = r * T::ROWB + (value_swizzle<SL>(r) + lo) * 16 + (l16 & 1) * 8;
     }
     auto v_operand = [&](int odd, int d, int k) {
       half8v v;
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
-        const uint8_t* at = lds + VALUES + odd * T::BLOCK + (16 * k + 8 * hf) * T::ROWB + value_read[d];
+        const uint8_t* at = lds + VALUES + odd * T::BLOCK + (16 * k + 8 * hf) * T::ROWB + (value_read ^ (d * 64));
         const short4v x = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
             (__attribute__((address_space(3))) short4v*)(__attribute__((address_space(3))) void*)at);
         const half4v y = __builtin_bit_cast(half4v, x);
@@ -240,7 +240,11 @@ __global__ __launch_bounds__(256, DP == 64 ? 3 : 2) void window_rows_kernel(Wind
         m = to;
         l *= keep;
 #pragma unroll
-        for (int d = 0; d < ND; ++d) o[d] *= keep;
+        for (int d = 0; d < ND; ++d) {
+          // (in accumulation registers with heads of 256: read here, and not on the way to the branch, 213 -> 199 us)
+          if constexpr (DP == 256) asm volatile("" : "+a"(o[d]));
+          o[d] *= keep;
+        }
       }
       ref = m == -INFINITY ? 0.f : m;
     };
@@ -257,12 +261,12 @@ __global__ __launch_bounds__(256, DP == 64 ? 3 : 2) void window_rows_kernel(Wind
     };
     auto product_step = [&](const half8v& v, int d, int k) { o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, p[k], o[d], 0, 0, 0); };
 
-    // Takes the infinities and NaN out of a block of values that some rows do not see whole
-    // (0 times one would be NaN): first each is added to the rows that see its key, then it
-    // becomes 0 in LDS.  A quarter of the block is looked at by each wave; what follows is rare,
-    // and small rather than fast: one element at a time.
+    // Takes the infinities and NaN out of a block of values that some rows do not see whole (0 times
+    // one would be NaN): they become 0 in LDS, and are added behind the last block.  A quarter of the
+    // block is looked at by each wave; the rest is rare.
     uint32_t* const flag = reinterpret_cast<uint32_t*>(lds + 4 * T::BLOCK + 4 * T::RING);
-    auto clean = [&](int odd, int base) {
+    bool cleaned = false;
+    auto clean = [&](int odd) {
       int lane = threadIdx.x & 63;
       asm volatile("" : "+v"(lane));  // (addresses made here, rather than kept through the loop and spilled)
       uint8_t* const vb = lds + VALUES + odd * T::BLOCK;
@@ -278,33 +282,8 @@ __global__ __launch_bounds__(256, DP == 64 ? 3 : 2) void window_rows_kernel(Wind
       reads_done();
       asm volatile("s_barrier" ::: "memory");
       const uint4 f = *reinterpret_cast<const uint4*>(flag);
-      const bool bad_any = __builtin_amdgcn_readfirstlane(f.x | f.y | f.z | f.w) != 0;
-      if (bad_any) {
-        constexpr int PER = DP / 64;  // values of a key that a lane looks at
-#pragma unroll 1
-        for (int x = 0; x < KT; ++x) {
-#pragma unroll 1
-          for (int h = 0; h < PER; ++h) {
-            const int e = lane * PER + h;
-            const uint32_t bits = *reinterpret_cast<const uint16_t*>(vb + x * T::ROWB + (e / 8 ^ value_swizzle<SL>(x)) * 16 + e % 8 * 2);
-            uint64_t bad = __ballot((bits & 0x7C00u) == 0x7C00u);
-            while (bad) {
-              const int from = __builtin_ctzll(bad);
-              bad &= bad - 1;
-              const uint32_t b16 = (uint32_t)__builtin_amdgcn_readlane((int)bits, from);
-              const float val = (float)__builtin_bit_cast(_Float16, (uint16_t)b16);
-              const int at = from * PER + h;  // place of the value: o[at / 32][4 (at / 8 % 4) + at % 4] of lanes with half at / 4 % 2
-              const float add = half == (at >> 2 & 1) && seen(base + x) ? val : 0.f;
-#pragma unroll
-              for (int d = 0; d < ND; ++d)
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                  if (d == at >> 5 && i == (at >> 3 & 3) * 4 + (at & 3)) o[d][i] += add;
-            }
-          }
-        }
-        reads_done();
-        asm volatile("s_barrier" ::: "memory");  // (no wave cleans what another still looks at)
+      if (__builtin_amdgcn_readfirstlane(f.x | f.y | f.z | f.w) != 0) {
+        cleaned = true;
 #pragma unroll 1
         for (int i = wave; i < T::BLOCK / 1024; i += 4) {
           uint4* at = reinterpret_cast<uint4*>(vb + i * 1024 + lane * 16);
@@ -323,6 +302,38 @@ __global__ __launch_bounds__(256, DP == 64 ? 3 : 2) void window_rows_kernel(Wind
         asm volatile("s_barrier" ::: "memory");
       }
     };
+    // ... and adds each to the rows that see its key: the blocks' values read again from the cache, one
+    // value of a key at a time (in the loop, with heads of 256, it drove the sums into memory).
+    auto add_cleaned = [&] {
+      constexpr int PER = DP / 64;  // values of a key that a lane looks at
+#pragma unroll 1
+      for (int x = base_of(whole); x < kend; ++x) {
+        const int key = key_at(it, x);
+        const bool own = key >= it.pre;
+        const int t = own ? key - it.pre : key;
+        uint32_t page = (uint32_t)(own ? it.own : a.prefix_table)[t >> a.page_shift];
+        if (page >= (uint32_t)a.n_pages) page = 0;
+        const _Float16* const row = a.v + ((uint64_t)page * page_bytes + head_bytes + ((uint32_t)t & page_mask) * row_bytes) / 2;
+#pragma unroll 1
+        for (int h = 0; h < PER; ++h) {
+          const int e = lane * PER + h;
+          const uint32_t bits = FULL || e < D ? __builtin_bit_cast(uint16_t, row[e]) : 0;
+          uint64_t bad = __ballot((bits & 0x7C00u) == 0x7C00u);
+          while (bad) {
+            const int from = __builtin_ctzll(bad);
+            bad &= bad - 1;
+            const float val = (float)__builtin_bit_cast(_Float16, (uint16_t)__builtin_amdgcn_readlane((int)bits, from));
+            const int at = from * PER + h;  // place of the value: o[at / 32][4 (at / 8 % 4) + at % 4] of lanes with half at / 4 % 2
+            const float add = half == (at >> 2 & 1) && seen(x) ? val : 0.f;
+#pragma unroll
+            for (int d = 0; d < ND; ++d)
+#pragma unroll
+              for (int i = 0; i < 16; ++i)
+                o[d][i] += d == at >> 5 && i == (at >> 3 & 3) * 4 + (at & 3) ? add : 0.f;
+          }
+        }
+      }
+    };
 
     // Keys j + 1 and values j are whole, keys j and values j - 1 no longer read: their successors load.
     auto stage = [&](int j) {
@@ -339,14 +350,15 @@ __global__ __launch_bounds__(256, DP == 64 ? 3 : 2) void window_rows_kernel(Wind
       next_rows = find(j + 4);
     };
     // (three workgroups a CU with heads of 64, which leaves registers for two operands ahead: window 64
-    // 32 -> 28 us, 1024 101 -> 98 us; PS pairs of the 16 beside the scores)
+    // 32 -> 28 us, 1024 101 -> 98 us; eight ahead with heads of 256 were level; PS pairs of the 16 beside
+    // the scores)
     constexpr int AHEAD = DP == 64 ? 2 : 4, NS = 2 * NQ, NP = 4 * ND, PS = 12;
     static_assert(NS % AHEAD == 0 && NP >= AHEAD, "operand ring");
     // a block that is not the last one: its probabilities and product, and the scores of the next
     auto block = [&](int j, auto ODD, Scores& now, Scores& next) {
       constexpr int odd = decltype(ODD)::value;
       stage(j);
-      if (j >= whole) clean(odd, base_of(j));
+      if (j >= whole) clean(odd);
       half8v f[AHEAD];
 #pragma unroll
       for (int x = 0; x < AHEAD; ++x) f[x] = k_operand(odd ^ 1, x % 2, x / 2);
@@ -408,13 +420,14 @@ __global__ __launch_bounds__(256, DP == 64 ? 3 : 2) void window_rows_kernel(Wind
     reads_done();
     asm volatile("s_barrier" ::: "memory");
     const int odd = j & 1;
-    if (j >= whole) clean(odd, base_of(j));
+    if (j >= whole) clean(odd);
 #pragma unroll
     for (int x = 0; x < 16; ++x) exp_pair(sa, x);
 #pragma unroll
     for (int k = 0; k < 4; ++k)
 #pragma unroll
       for (int d = 0; d < ND; ++d) product_step(v_operand(odd, d, k), d, k);
+    if (cleaned) add_cleaned();
     l = both(l, [](float x, float y) { return x + y; });
   }
 
@@ -473,8 +486,7 @@ template <int DP>
 hipError_t launch_dim(const WindowArgs& a, const AttnSplit& p, hipStream_t st) {
   if (p.kind_s == TILE_KEYS) return launch_kinds<DP, TILE_NONE, TILE_KEYS>(a, p, st);
   if (p.kind_s == TILE_ROWS64) return launch_kinds<DP, TILE_NONE, TILE_ROWS64>(a, p, st);
-  if constexpr (DP <= 128) return launch_rows<DP>(a, p, st);
-  return hipErrorInvalidValue;
+  return launch_rows<DP>(a, p, st);
 }
 
 }  // namespace
