@@ -14,7 +14,7 @@
 // pieces of V pairs, where V is what alignment, strides and sizes allow in one access each.
 //
 // Measured: 48 tokens 3.7 us; 8190 tokens of 32 + 8 + 8 heads of 128 (201 MB) 35 to 44 us, the sizes
-// that the cache partly holds; gradients of 4096 tokens of 32 + 8 heads (126 MB) 25 us, 5.0 TB/s (a
+// that the cache partly holds; gradients of 4096 tokens of 32 + 8 heads (126 MB) 24.5 us, 5.1 TB/s (a
 // 2 GiB copy reaches 4.85), the weights' second pass 3.9 us.
 //
 // The gradient of a norm's weight sums over tokens and heads: each lane adds up its own places
@@ -179,8 +179,10 @@ __global__ __launch_bounds__(256) void norm_rotate_kernel(NormArgs a, int tokens
   }
 }
 
-// most workgroups of the gradients of queries, and of keys: each leaves a row of partial sums
-constexpr int GRAD_BLOCKS = 1024;
+// most workgroups of the gradients of queries, and of keys: each leaves a row of partial sums (a step of
+// 2870 tokens of 16 + 8 heads of 80 took 25.9 us with 1024, of which some walked one row and some two, 22.7
+// with 512; of 4096 tokens of 32 + 8 heads of 128 44.9 and 43.7)
+constexpr int GRAD_BLOCKS = 512;
 
 // Gradients: blockIdx.y 0 walks the rows (token, head) of the queries, 1 those of the keys.
 template <int V, int LPH, bool INTERLEAVED>
