@@ -17,7 +17,7 @@
 // maxima that it gathered behind the loop cost 2 %).
 //
 // Measured (8192 tokens of one prompt, 32 / 8 heads of 128): window 64 46 us, 256 72 us, 1024
-// 162 us (807 TFLOP/s), 4096 426 us (970); 32 / 4 heads of 64: 27, 40, 96 and 261 us.  The 16 x 16 x
+// 162 us (807 TFLOP/s), 4096 426 us (970); 32 / 4 heads of 64: 26, 40, 96 and 261 us.  The 16 x 16 x
 // 32 tiles took 78, 111, 200 and 466 us with heads of 128, these 54, 79, 169 and 435 as they were
 // first; then scores hidden by bits instead of intervals (window 64 54 -> 49 us) and items placed
 // without divisions (49 -> 46).  16 / 4 heads of 256 (one workgroup a CU, sums in the accumulation

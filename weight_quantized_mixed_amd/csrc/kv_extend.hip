@@ -15,8 +15,8 @@
 // Up to ONE_LAUNCH tokens the same workgroup does that, from LDS; more go to a second launch of
 // many workgroups, which reads the sequences from the workspace.
 //
-// Measured: 1 sequence 3.9 us, 48 sequences of up to 8000 tokens 5.2 us (a launch with nothing in it
-// about 2.5); 24 sequences of 8400 tokens 3.8 + 3.5 us, 1500 of 30000 tokens 5.8 + 5.5 us.  Nothing but
+// Measured: 1 sequence 3.7 us, 48 sequences of up to 8000 tokens 4.8 us (a launch with nothing in it
+// about 2.5); 24 sequences of 8400 tokens 3.7 + 3.4 us, 1500 of 30000 tokens 5.8 + 5.1 us.  Nothing but
 // latency bounds it: the sums wait for two barriers a thousand sequences, a token for the reads of
 // its bisection, which lie one behind the other.
 //
