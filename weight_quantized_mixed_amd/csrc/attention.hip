@@ -92,7 +92,10 @@ void split_window(const AttnShape& s, AttnSplit* p) {
     const int64_t items = (of_rows < most ? of_rows : most) * s.kv_heads;
     for (int n = 1; n <= JOIN_SLOTS / 2; ++n) {
       const int64_t chunk = div_up(div_up(keys, n), step) * step, parts = div_up(keys, chunk);
-      if (parts < n) continue;  // (these parts have been looked at)
+      if (parts < n) {  // (these parts have been looked at)
+        if (chunk == step) break;
+        continue;
+      }
       const double us = div_up(items * parts, 256) * (chunk / step + 2.5) * block + (parts > 1 ? 4 + parts * part : 0);
       if (us >= best) continue;
       best = us;

@@ -13,8 +13,8 @@
 // DPP, its pairs turn in registers, and nothing passes through LDS.  A lane's values are 8 / V
 // pieces of V pairs, where V is what alignment, strides and sizes allow in one access each.
 //
-// Measured: 48 tokens 3.7 us; 8190 tokens of 32 + 8 + 8 heads of 128 (201 MB) 35 to 44 us, the sizes
-// that the cache partly holds; gradients of 4096 tokens of 32 + 8 heads (126 MB) 24.5 us, 5.1 TB/s (a
+// Measured: 48 tokens 3.7 us; 8190 tokens of 32 + 8 + 8 heads of 128 (201 MB) 35 to 39 us, as the
+// caches have it; gradients of 4096 tokens of 32 + 8 heads (126 MB) 24.5 us, 5.1 TB/s (a
 // 2 GiB copy reaches 4.85), the weights' second pass 3.9 us.
 //
 // The gradient of a norm's weight sums over tokens and heads: each lane adds up its own places
@@ -106,7 +106,7 @@ __device__ __forceinline__ void rotate(float* x, const float* cos, const float* 
 
 // Forward.  Heads of a token in order: queries, keys, and with a cache the values (copied); the
 // heads of all tokens one after the other, LPH lanes each (a token to a row of workgroups left lanes
-// idle where its heads do not fill them: 8000 tokens of 96 heads of 128, 393 MB, 84 us; so 76 us, 5.2 TB/s).
+// idle where its heads do not fill them: 8000 tokens of 96 heads of 128, 393 MB, 84 us; so 75 us, 5.2 TB/s).
 template <int V, int LPH, bool INTERLEAVED>
 __global__ __launch_bounds__(256) void norm_rotate_kernel(NormArgs a, int tokens) {
   constexpr int PIECES = 8 / V;
@@ -118,31 +118,39 @@ __global__ __launch_bounds__(256) void norm_rotate_kernel(NormArgs a, int tokens
   const int half = a.rot / 2;
   const bool is_q = h < a.q_heads, is_v = h >= a.q_heads + a.kv_heads;
 
+  // the head is read before its position and slot are known: one wait for memory
+  // less (8190 tokens of 32 + 8 + 8 heads, three inputs in turn, 42.8 -> 39.0 us)
+  typedef typename Vec<V>::h hv;
+  const int kh = is_v ? h - a.q_heads - a.kv_heads : h - a.q_heads;
+  const _Float16* src = is_q ? a.q + t * a.q_stride + (int64_t)h * a.D
+                             : (is_v ? a.v + t * a.v_stride : a.k + t * a.k_stride) + (int64_t)kh * a.D;
+  hv first[PIECES], second[PIECES];
+#pragma unroll
+  for (int i = 0; i < PIECES; ++i) {
+    const Piece<V, INTERLEAVED> p(i * LPH + sub, a.D, half, !is_v);
+    if (!p.live) continue;
+    first[i] = *reinterpret_cast<const hv*>(src + p.o0);
+    second[i] = *reinterpret_cast<const hv*>(src + p.o1);
+  }
   const int64_t pos = a.rot ? a.positions[t] : 0;
   const bool pos_ok = !a.rot || (pos >= 0 && pos < a.n_positions);
   const int64_t slot = a.k_out ? 0 : a.slots[t];
   if (!is_q && !a.k_out && !(pos_ok && slot >= 0 && slot < a.n_pages * a.page)) return;
-  const _Float16* src;
   _Float16* dst;
-  if (is_q) {
-    src = a.q + t * a.q_stride + (int64_t)h * a.D;
-    dst = a.q_out + (t * a.q_heads + h) * a.D;
-  } else {
-    const int kh = is_v ? h - a.q_heads - a.kv_heads : h - a.q_heads;
-    src = (is_v ? a.v + t * a.v_stride : a.k + t * a.k_stride) + (int64_t)kh * a.D;
+  if (is_q) dst = a.q_out + (t * a.q_heads + h) * a.D;
+  else if (a.k_out) dst = a.k_out + (t * a.kv_heads + kh) * a.D;
+  else {
     const int64_t page = slot / a.page, in_page = slot - page * a.page;
-    if (a.k_out) dst = a.k_out + (t * a.kv_heads + kh) * a.D;
-    else dst = (is_v ? a.v_cache : a.k_cache) + ((page * a.kv_heads + kh) * a.page + in_page) * a.D;
+    dst = (is_v ? a.v_cache : a.k_cache) + ((page * a.kv_heads + kh) * a.page + in_page) * a.D;
   }
 
   if (is_v) {  // as it is, bit by bit
 #pragma unroll
     for (int i = 0; i < PIECES; ++i) {
-      typedef typename Vec<V>::h hv;
       const Piece<V, INTERLEAVED> p(i * LPH + sub, a.D, half, false);
       if (!p.live) continue;
-      *reinterpret_cast<hv*>(dst + p.o0) = *reinterpret_cast<const hv*>(src + p.o0);
-      *reinterpret_cast<hv*>(dst + p.o1) = *reinterpret_cast<const hv*>(src + p.o1);
+      *reinterpret_cast<hv*>(dst + p.o0) = first[i];
+      *reinterpret_cast<hv*>(dst + p.o1) = second[i];
     }
     return;
   }
@@ -151,7 +159,11 @@ __global__ __launch_bounds__(256) void norm_rotate_kernel(NormArgs a, int tokens
   for (int i = 0; i < PIECES; ++i) {
     const Piece<V, INTERLEAVED> p(i * LPH + sub, a.D, half, true);
     if (!p.live) continue;
-    read<V>(src, p.o0, p.o1, x[i]);
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      x[i][e] = (float)first[i][e];
+      x[i][V + e] = (float)second[i][e];
+    }
 #pragma unroll
     for (int e = 0; e < 2 * V; ++e) sum = __builtin_fmaf(x[i][e], x[i][e], sum);
   }
