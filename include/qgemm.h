@@ -484,7 +484,7 @@ qgemm_status qgemm_norm_rotate_backward(int64_t T, int32_t q_heads, int32_t kv_h
                                         void* workspace, size_t workspace_bytes, void* stream);
 
 /*
- * Workspace of qgemm_kv_extend (0 for a decode batch).
+ * Workspace of qgemm_kv_extend (0 for few tokens).
  */
 qgemm_status qgemm_kv_extend_workspace(int64_t B, int64_t T, size_t* workspace_bytes);
 

@@ -308,7 +308,7 @@ EXTEND = [  # B, page, lens up to, new up to, prefix, window, sinks, ends, spare
     (64, 16, 900, 1, 100, 256, 4, 0.1, 64, 0), (64, 16, 900, 1, 0, 256, 40, 0.1, 10, 9), (65, 4, 300, 30, 0, 50, 0, 0.1, 100, 1),
     (130, 64, 2000, 90, 17, 500, 100, 0.05, 40, 700), (1024, 16, 60, 3, 0, 20, 2, 0.2, 300, 0), (1025, 1, 20, 3, 0, 4, 1, 0.2, 2000, 0),
     (2048, 16, 60, 2, 0, 0, 0, 0.2, 3000, 2), (2049, 2, 60, 1, 5, 16, 9, 0.2, 3000, 2), (5000, 16, 300, 2, 0, 64, 0, 0.1, 1000, 100),
-    (3, 65536, 200000, 9000, 1, 70000, 3, 0.0, 3, 0), (3, 16, 5000, 9000, 0, 700, 20, 0.0, 2000, 0), (20, 256, 9000, 1, 0, 1, 0, 0.5, 9, 44),
+    (3, 65536, 200000, 9000, 1, 70000, 3, 0.0, 3, 0), (3, 16, 5000, 9000, 0, 700, 20, 0.0, 2000, 0), (20, 256, 9000, 1, 0, 1, 0, 0.5, 9, 44), (8, 16, 3000, 1500, 0, 500, 4, 0.1, 1500, 60), (8, 1, 300, 2500, 0, 0, 0, 0.0, 1000, 3),
 ]
 
 
@@ -358,6 +358,7 @@ def test_extend_of_nothing():
     none.check([], 0)
     none.check([], 7)
     none.check([], 5000)
+    none.check([], 20000)
 
 
 def test_extend_with_states_that_no_call_left():
@@ -389,7 +390,7 @@ def test_extend_step_by_step_in_a_graph():
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         got = pool.extend(new, T)
-        wide = big.extend(new, 5000)  # the form of two launches
+        wide = big.extend(new, 20000)  # the form of two launches
     side = torch.cuda.Stream()
     for step in range(25):
         n = np.where(rng.random(B) < 0.1, -1, rng.integers(0, 8, B))
@@ -398,7 +399,7 @@ def test_extend_step_by_step_in_a_graph():
         if step % 5 == 4:  # an eager one between the replays
             side.wait_stream(torch.cuda.current_stream())
             eager = pool.extend(new, T, stream=side)
-            big.extend(new, 5000, stream=side)
+            big.extend(new, 20000, stream=side)
             torch.cuda.current_stream().wait_stream(side)
             outs = eager
         else:
@@ -776,7 +777,7 @@ def test_results_do_not_depend_on_what_memory_held():
         del junk
         r = norm_rotate_backward(qt, kt, dq, dk, *c.tables(), eps=c.eps, interleaved=True, **c.weights())
         pool = p.pool()
-        e = pool.extend(new, 5200)
+        e = pool.extend(new, 7000)
         results.append([*r.values(), *(t.clone() for t in e.values()), pool.tables.clone(), pool.ring.clone(), pool.state.clone()])
     assert all(torch.equal(a, b) for other in results[1:] for a, b in zip(results[0], other))
 
@@ -792,7 +793,7 @@ def test_workspaces_have_to_be_whole():
     for ws, error in ((byte.expand(1 << 24), ValueError), (byte, q.QGemmError)):
         for f in (lambda: norm_rotate_backward(qt, kt, *d, *c.tables(), **c.weights(), ws=ws),
                   lambda: w.cache.attend(w.dq, w.dstarts, w.dlens, w.dtables, max_q=1, max_len=2000, window=1500, sinks=2, ws=ws),
-                  lambda: pool.extend(torch.zeros(3, dtype=I32, device="cuda"), 5000, ws=ws)):
+                  lambda: pool.extend(torch.zeros(3, dtype=I32, device="cuda"), 50000, ws=ws)):
             with pytest.raises(error):
                 f()
 

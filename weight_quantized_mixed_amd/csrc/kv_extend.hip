@@ -12,7 +12,7 @@
 // sequence by bisection of the rows' starts, its page in the table (the last page held, which
 // it may fill up) or in the ring, and the first token of a new page writes the table's entry;
 // a page given back finds its sequence and its place in the table the same way, a thread each.
-// Up to ONE_LAUNCH tokens the same workgroup does that, from LDS; more go to a second launch of
+// For few tokens the same workgroup does that, from LDS (one_launch); more go to a second launch of
 // many workgroups, which reads the sequences from the workspace.
 //
 // Measured: 1 sequence 3.7 us, 48 sequences of up to 8000 tokens 4.8 us (a launch with nothing in it
@@ -28,7 +28,7 @@ namespace qg {
 namespace {
 
 constexpr int THREADS = 1024, WAVES = THREADS / 64;
-constexpr int ONE_LAUNCH = 4096, ONE_LAUNCH_SEQUENCES = 2048;
+constexpr int ONE_LAUNCH_SEQUENCES = 2048;
 
 __device__ __forceinline__ uint32_t add(uint32_t a, uint32_t b) { return __builtin_elementwise_add_sat(a, b); }
 
@@ -251,7 +251,14 @@ __global__ __launch_bounds__(256) void place_kernel(ExtendArgs a, Steps steps, c
   }
 }
 
-bool one_launch(int64_t B, int64_t T) { return T <= ONE_LAUNCH && B <= ONE_LAUNCH_SEQUENCES; }
+// One workgroup takes 0.24 us for a thousand tokens and 0.08 more for each step of the bisection, a second
+// launch 4.5 in all: 24 sequences of 4800 tokens 7.9 us as one and 10.4 as two, of 19200 16.8 and 10.7;
+// 300 sequences of 9300 tokens 14.9 and 10.7.
+bool one_launch(int64_t B, int64_t T) {
+  int steps = 0;
+  while (((int64_t)1 << steps) < B) ++steps;
+  return B <= ONE_LAUNCH_SEQUENCES && T * (3 + steps) <= 57600;
+}
 
 }  // namespace
 
