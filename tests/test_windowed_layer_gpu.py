@@ -308,7 +308,8 @@ EXTEND = [  # B, page, lens up to, new up to, prefix, window, sinks, ends, spare
     (64, 16, 900, 1, 100, 256, 4, 0.1, 64, 0), (64, 16, 900, 1, 0, 256, 40, 0.1, 10, 9), (65, 4, 300, 30, 0, 50, 0, 0.1, 100, 1),
     (130, 64, 2000, 90, 17, 500, 100, 0.05, 40, 700), (1024, 16, 60, 3, 0, 20, 2, 0.2, 300, 0), (1025, 1, 20, 3, 0, 4, 1, 0.2, 2000, 0),
     (2048, 16, 60, 2, 0, 0, 0, 0.2, 3000, 2), (2049, 2, 60, 1, 5, 16, 9, 0.2, 3000, 2), (5000, 16, 300, 2, 0, 64, 0, 0.1, 1000, 100),
-    (3, 65536, 200000, 9000, 1, 70000, 3, 0.0, 3, 0), (3, 16, 5000, 9000, 0, 700, 20, 0.0, 2000, 0), (20, 256, 9000, 1, 0, 1, 0, 0.5, 9, 44), (8, 16, 3000, 1500, 0, 500, 4, 0.1, 1500, 60), (8, 1, 300, 2500, 0, 0, 0, 0.0, 1000, 3),
+    (3, 65536, 200000, 9000, 1, 70000, 3, 0.0, 3, 0), (3, 16, 5000, 9000, 0, 700, 20, 0.0, 2000, 0), (20, 256, 9000, 1, 0, 1, 0, 0.5, 9, 44),
+    (8, 16, 3000, 1500, 0, 500, 4, 0.1, 1500, 60), (8, 1, 300, 2500, 0, 0, 0, 0.0, 1000, 3),
 ]
 
 
