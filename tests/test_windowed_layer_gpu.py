@@ -845,3 +845,12 @@ def test_infinities_at_any_place_reach_the_rows_that_see_them(hq, hkv, D, qs, le
     got, _ = c.upload().run()
     finite = np.isfinite(want)
     assert not finite.all() and np.array_equal(got[finite], plain[finite]) and np.array_equal(got[~finite], want[~finite], equal_nan=True)
+
+
+@pytest.mark.parametrize("hq,hkv,D,qs,lens,prefix,window,sinks", [
+    (4, 2, 128, [200], [700], 0, 64, 300), (4, 2, 64, [200, 333], [250, 333], 150, 20, 257), (8, 1, 128, [90], [2000], 0, 900, 1000),
+    (16, 16, 256, [300, 301, 299, 250], [310, 500, 299, 600], 20, 50, 250)])
+def test_many_first_keys(hq, hkv, D, qs, lens, prefix, window, sinks):
+    """Blocks of first keys that every row of a tile sees, behind ones of the window that some do not; keys split or not."""
+    say(f"case first keys hq={hq} hkv={hkv} D={D} q={qs} lens={lens} prefix={prefix} window={window} sinks={sinks}")
+    WindowCase(hq, hkv, D, 16, qs, lens, prefix, window, sinks, seed=sinks).upload().check()

@@ -94,6 +94,11 @@ __global__ __launch_bounds__(256, DP == 64 ? 3 : DP == 128 ? 2 : 1) void window_
   const int first_end = end_at(it, a.by_per_head(it.row0));
   const int whole = (max(min(kend, min(max(min(first_end, it.held) - it.late, 0), it.n_late)), it.key0) - it.key0) / KT;
 
+  // ... the leading ones, and among the first keys (of which later rows see what the tile's first does:
+  // 8192 tokens of 32 / 8 heads of 128, window 1024 and 512 first ones 228 -> 218 us)
+  const int first_at = it.n_late + it.n_early, first_to = min(kend, first_at + min(first_end, it.list - first_at));
+  auto masked = [&](int j) { return j >= whole && !(base_of(j) >= first_at && base_of(j) + KT <= first_to); };
+
   float16v o[ND];
   float m = -INFINITY, l = 0.f;
 #pragma unroll
@@ -358,7 +363,7 @@ __global__ __launch_bounds__(256, DP == 64 ? 3 : DP == 128 ? 2 : 1) void window_
     auto block = [&](int j, auto ODD, Scores& now, Scores& next) {
       constexpr int odd = decltype(ODD)::value;
       stage(j);
-      if (j >= whole) clean(odd);
+      if (masked(j)) clean(odd);
       half8v f[AHEAD];
 #pragma unroll
       for (int x = 0; x < AHEAD; ++x) f[x] = k_operand(odd ^ 1, x % 2, x / 2);
@@ -384,7 +389,7 @@ __global__ __launch_bounds__(256, DP == 64 ? 3 : DP == 128 ? 2 : 1) void window_
         stay(part);
       });
       float top;
-      if (j + 1 < whole) top = both(part, larger) * c;
+      if (!masked(j + 1)) top = both(part, larger) * c;
       else {
         hide(next, base_of(j + 1));
         top = largest(next);
@@ -402,7 +407,7 @@ __global__ __launch_bounds__(256, DP == 64 ? 3 : DP == 128 ? 2 : 1) void window_
     for (int t = 0; t < NQ; ++t)
 #pragma unroll
       for (int u = 0; u < 2; ++u) score_step(k_operand(0, u, t), sa, u, t);
-    if (whole < 1) hide(sa, it.key0);
+    if (masked(0)) hide(sa, it.key0);
     raise(largest(sa));
     int j = 0;
     for (; j + 2 < cnt; j += 2) {
@@ -420,7 +425,7 @@ __global__ __launch_bounds__(256, DP == 64 ? 3 : DP == 128 ? 2 : 1) void window_
     reads_done();
     asm volatile("s_barrier" ::: "memory");
     const int odd = j & 1;
-    if (j >= whole) clean(odd);
+    if (masked(j)) clean(odd);
 #pragma unroll
     for (int x = 0; x < 16; ++x) exp_pair(sa, x);
 #pragma unroll
