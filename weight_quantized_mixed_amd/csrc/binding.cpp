@@ -139,6 +139,12 @@ int32_t narrow(int64_t v, const char* name) {
   return (int32_t)v;
 }
 
+// the places of a head, by which widths are divided
+int64_t head_dim(int64_t D) {
+  if (D < 1) throw std::invalid_argument("head_dim: at least 1 expected");
+  return D;
+}
+
 // address and bytes of a workspace (null for null)
 struct Scratch {
   void* at;
@@ -216,7 +222,7 @@ PyObject* append_norm(PyObject*, PyObject* const* args, Py_ssize_t) {
     a.device = a.integer();
     void* stream = (void*)a.integer();
     const qgemm_kv_cache* cache = (const qgemm_kv_cache*)a.integer();
-    const int64_t kv_heads = a.integer(), D = a.integer();
+    const int64_t kv_heads = a.integer(), D = head_dim(a.integer());
     const at::Tensor *q = a.tensor("q"), *k = a.tensor("k"), *v = a.tensor("v");
     two(q, "q");
     const int64_t T = q->size(0), heads = q->size(1) / D;
@@ -244,11 +250,10 @@ PyObject* norm_rotate(PyObject*, PyObject* const* args, Py_ssize_t) {
     Args a{args, -1};
     a.device = a.integer();
     void* stream = (void*)a.integer();
-    const int64_t D = a.integer();
+    const int64_t D = head_dim(a.integer());
     const at::Tensor *q = a.tensor("q"), *k = a.tensor("k");
     two(q, "q");
     two(k, "k");
-    if (D < 1) throw std::invalid_argument("head_dim: at least 1 expected");
     const int64_t T = q->size(0), hq = q->size(1) / D, hk = k->size(1) / D;
     const int32_t nq = narrow(hq, "q_heads"), nk = narrow(hk, "kv_heads");
     const Norm n = norm_args(a, T, D);
