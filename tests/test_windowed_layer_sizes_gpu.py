@@ -1,0 +1,53 @@
+"""Normed heads, block tables and windowed attention at sizes and over memory that their other GPU tests leave out: sums over
+millions of heads, many pages that come back at once, tiles of wide heads, workspaces that begin as junk."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from gpu_helpers import say
+from test_paged_kv_gpu import assert_near, dev, halves
+from weight_quantized_mixed_amd import qgemm as q
+from weight_quantized_mixed_amd.device import norm_rotate_backward
+
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():  # pragma: no cover - CPU containers
+    pytest.skip("needs a GPU", allow_module_level=True)
+
+
+def f64(t):
+    return t.cpu().numpy().astype(np.float64)
+
+
+@pytest.mark.parametrize("T,hq,hkv,D,kinds,one_sign", [(2**21, 32, 1, 8, 1, True), (40001, 32, 3, 128, 97, False), (70001, 3, 16, 200, 89, False)])
+def test_weight_gradients_over_millions_of_heads(T, hq, hkv, D, kinds, one_sign):
+    """Token t is that of t mod kinds, so the sums are known; terms of one sign lose most where a sum in fp32 is long."""
+    say(f"case weight gradients T={T} hq={hq} hkv={hkv} D={D}")
+    rng = np.random.default_rng(D)
+    draw = (lambda *s: rng.uniform(0.5, 2, s).astype(np.float16)) if one_sign else (lambda *s: halves(rng, *s))
+    xq, xk, dyq, dyk = draw(kinds, hq, D), draw(kinds, hkv, D), draw(kinds, hq, D), draw(kinds, hkv, D)
+    if one_sign:  # one head for all, so that every sum has one term over and over
+        xq, dyq = np.repeat(xq[:, :1], hq, 1), np.repeat(dyq[:, :1], hq, 1)
+    qw, kw = draw(D), draw(D)
+    times = np.bincount(np.arange(T) % kinds, minlength=kinds)[:, None, None]
+    at = torch.arange(T, device="cuda") % kinds
+    spread = lambda x: dev(x)[at]  # noqa: E731
+    none, pos = torch.zeros((1, 0), device="cuda"), torch.zeros(T, dtype=torch.int32, device="cuda")
+    args = (spread(xq).view(T, -1), spread(xk).view(T, -1), spread(dyq), spread(dyk), none, none, pos)
+    r = norm_rotate_backward(*args, q_weight=dev(qw), k_weight=dev(kw), eps=1e-5)
+    t = np.zeros((kinds, 0))
+    for name, x, w, dy in (("q", xq, qw, dyq), ("k", xk, kw, dyk)):
+        dx, _, ex, _ = oracle.norm_rotate_grads_ref(x, w, 1e-5, t, t, False, dy)
+        unit = x / np.sqrt((x.astype(np.float64) ** 2).mean(-1, keepdims=True) + 1e-5)
+        terms = times * unit * dy
+        # the reference's bound: 2**-17 of the sum of magnitudes
+        assert_near(f64(r[f"d{name}_weight"]), terms.sum((0, 1)), 2.0**-17 * np.abs(terms).sum((0, 1)), f"d{name}_weight")
+        assert_near(f64(r[f"d{name}"][:kinds]).reshape(dx.shape), dx, ex, f"d{name}")
+        assert torch.equal(r[f"d{name}"], r[f"d{name}"][at])
+    again = norm_rotate_backward(*args, q_weight=dev(qw), k_weight=dev(kw), eps=1e-5)
+    assert all(torch.equal(r[n], again[n]) for n in r)
+    need = q.qgemm_norm_rotate_backward_workspace(T, hq, hkv, D, True)
+    ws = torch.full((need,), 0xFF, dtype=torch.uint8, device="cuda")
+    again = norm_rotate_backward(*args, q_weight=dev(qw), k_weight=dev(kw), eps=1e-5, ws=ws)
+    assert all(torch.equal(r[n], again[n]) for n in r)

@@ -18,8 +18,8 @@
 // 2 GiB copy reaches 4.85), the weights' second pass 3.9 us.
 //
 // The gradient of a norm's weight sums over tokens and heads: each lane adds up its own places
-// over the rows that its workgroup walks, the workgroup joins its lanes and leaves one row of
-// partial sums, and a second pass adds those in order (bitwise reproducible).
+// over the rows that its workgroup walks (at most CHAIN), the workgroup joins its lanes and
+// leaves one row of partial sums, and a second pass adds those in order (bitwise reproducible).
 #include <type_traits>
 
 #include "qgemm_internal.hpp"
@@ -191,10 +191,12 @@ __global__ __launch_bounds__(256) void norm_rotate_kernel(NormArgs a, int tokens
   }
 }
 
-// most workgroups of the gradients of queries, and of keys: each leaves a row of partial sums (a step of
-// 2870 tokens of 16 + 8 heads of 80 took 25.9 us with 1024, of which some walked one row and some two, 22.7
-// with 512; of 4096 tokens of 32 + 8 heads of 128 44.9 and 43.7)
-constexpr int GRAD_BLOCKS = 512;
+// Workgroups of the gradients of queries, and of keys: each leaves a row of partial sums.  512 up to CHAIN rows
+// a lane (a step of 2870 tokens of 16 + 8 heads of 80 took 25.9 us with 1024, of which some walked one row and some
+// two, 22.7 with 512; of 4096 tokens of 32 + 8 heads of 128 44.9 and 43.7), beyond as many as keep it at that: no
+// value passes more than CHAIN additions in fp32 here and 33 behind them, however many the rows (67 million rows of
+// heads of 8 by 512 workgroups are 2048 a lane, whose sum in fp32 was off by 2^-15).
+constexpr int GRAD_BLOCKS = 512, CHAIN = 64;
 
 // Gradients: blockIdx.y 0 walks the rows (token, head) of the queries, 1 those of the keys.
 template <int V, int LPH, bool INTERLEAVED>
@@ -278,25 +280,33 @@ __global__ __launch_bounds__(256) void norm_rotate_grad_kernel(NormGradArgs a) {
   __syncthreads();
   if ((int)threadIdx.x < a.D) {
     const int d = threadIdx.x;
-    a.part[((int64_t)(is_k ? GRAD_BLOCKS : 0) + blockIdx.x) * a.D + d] = sums[0][d] + sums[1][d] + sums[2][d] + sums[3][d];
+    a.part[((int64_t)(is_k ? gridDim.x : 0) + blockIdx.x) * a.D + d] = sums[0][d] + sums[1][d] + sums[2][d] + sums[3][d];
   }
 }
 
 // The workgroups' partial sums added up in order: 16 places of a weight a workgroup (64 bytes of a
-// row), 64 rows at a time, all loads of a thread in flight together.
-__global__ __launch_bounds__(1024) void norm_weight_grad_kernel(NormGradArgs a, int q_blocks, int k_blocks) {
+// row), 64 rows at a time, the loads of GRAD_BLOCKS rows in flight together, and the sums of these in 64 bits.
+__global__ __launch_bounds__(1024) void norm_weight_grad_kernel(NormGradArgs a, int blocks, int q_blocks, int k_blocks) {
   __shared__ float sums[16][16];
   const bool is_k = blockIdx.y != 0;
   float* out = is_k ? a.dk_weight : a.dq_weight;
   if (!out) return;
   const int n = is_k ? k_blocks : q_blocks, col = threadIdx.x % 16, r0 = threadIdx.x / 16, d = blockIdx.x * 16 + col;
-  const float* part = a.part + (int64_t)(is_k ? GRAD_BLOCKS : 0) * a.D + min(d, a.D - 1);
-  float v[GRAD_BLOCKS / 64];
+  const float* part = a.part + (int64_t)(is_k ? blocks : 0) * a.D + min(d, a.D - 1);
+  double total = 0.;
+  for (int n0 = 0; n0 < n; n0 += GRAD_BLOCKS) {
+    float v[GRAD_BLOCKS / 64];
 #pragma unroll
-  for (int i = 0; i < GRAD_BLOCKS / 64; ++i) v[i] = r0 + 64 * i < n ? part[(int64_t)(r0 + 64 * i) * a.D] : 0.f;
-  float s = 0.f;
+    for (int i = 0; i < GRAD_BLOCKS / 64; ++i) {
+      const int r = n0 + r0 + 64 * i;
+      v[i] = r < n ? part[(int64_t)r * a.D] : 0.f;
+    }
+    float s = 0.f;
 #pragma unroll
-  for (int i = 0; i < GRAD_BLOCKS / 64; ++i) s += v[i];
+    for (int i = 0; i < GRAD_BLOCKS / 64; ++i) s += v[i];
+    total += s;
+  }
+  float s = (float)total;
   s += __shfl_xor(s, 16, 64);
   s += __shfl_xor(s, 32, 64);
   if ((threadIdx.x & 63) < 16) sums[threadIdx.x >> 6][col] = s;
@@ -338,8 +348,8 @@ uintptr_t bits(P... p) {
 }
 
 int64_t grad_blocks(int64_t rows, int groups) {
-  const int64_t n = (rows + groups - 1) / groups;
-  return n < GRAD_BLOCKS ? n : GRAD_BLOCKS;
+  const int64_t n = (rows + groups - 1) / groups, least = (n + CHAIN - 1) / CHAIN;
+  return least > GRAD_BLOCKS ? least : n < GRAD_BLOCKS ? n : GRAD_BLOCKS;
 }
 
 }  // namespace
@@ -369,22 +379,32 @@ hipError_t launch_norm_rotate(const NormArgs& a, int64_t T, hipStream_t st) {
   return hipGetLastError();
 }
 
-size_t norm_grad_ws_bytes(int64_t, int32_t, int32_t, int32_t D) { return (size_t)2 * GRAD_BLOCKS * D * sizeof(float); }
+size_t norm_grad_ws_bytes(int64_t T, int32_t q_heads, int32_t kv_heads, int32_t D) {
+  const int groups = D <= 64 ? 64 : D <= 128 ? 32 : 16;  // heads of a workgroup, as in dispatch
+  const int64_t n = grad_blocks(T * (q_heads > kv_heads ? q_heads : kv_heads), groups);
+  return (size_t)2 * (n > GRAD_BLOCKS ? n : GRAD_BLOCKS) * D * sizeof(float);
+}
 
 hipError_t launch_norm_rotate_grad(const NormGradArgs& a, hipStream_t st) {
   const uintptr_t halves = bits(a.q, a.k, a.dq_out, a.dk_out, a.dq, a.dk, a.q_weight, a.k_weight);
   const int64_t counts = (int64_t)(a.rot / 2) | (a.D / 2) | a.D | a.q_stride | a.k_stride | a.dq_stride | a.dk_stride;
-  int64_t nq = 0, nk = 0;
+  int64_t blocks = 0, nq = 0, nk = 0;  // of the launch, and those that have rows of queries and of keys
   dispatch(a.D, a.interleaved != 0, halves, bits(a.cos, a.sin), counts, [&](auto v, auto lph, auto il) {
     constexpr int GROUPS = 256 / decltype(lph)::value;
-    nq = grad_blocks((int64_t)a.T * a.q_heads, GROUPS);
-    nk = grad_blocks((int64_t)a.T * a.kv_heads, GROUPS);
+    const int64_t rows_q = (int64_t)a.T * a.q_heads, rows_k = (int64_t)a.T * a.kv_heads;
+    blocks = grad_blocks(rows_q > rows_k ? rows_q : rows_k, GROUPS);
+    auto with_rows = [&](int64_t rows) {
+      const int64_t n = (rows + GROUPS - 1) / GROUPS;
+      return n < blocks ? n : blocks;
+    };
+    nq = with_rows(rows_q);
+    nk = with_rows(rows_k);
     if (a.T > 0) hipLaunchKernelGGL((norm_rotate_grad_kernel<decltype(v)::value, decltype(lph)::value, decltype(il)::value>),
-                       dim3((unsigned)(nq > nk ? nq : nk), 2), dim3(256), 0, st, a);
+                       dim3((unsigned)blocks, 2), dim3(256), 0, st, a);
   });
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || (!a.dq_weight && !a.dk_weight)) return e;
-  hipLaunchKernelGGL(norm_weight_grad_kernel, dim3((unsigned)((a.D + 15) / 16), 2), dim3(1024), 0, st, a, (int)nq, (int)nk);
+  hipLaunchKernelGGL(norm_weight_grad_kernel, dim3((unsigned)((a.D + 15) / 16), 2), dim3(1024), 0, st, a, (int)blocks, (int)nq, (int)nk);
   return hipGetLastError();
 }
 
