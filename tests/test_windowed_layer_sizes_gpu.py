@@ -7,6 +7,7 @@ import torch
 import oracle
 from gpu_helpers import say
 from test_paged_kv_gpu import assert_near, dev, halves
+from test_windowed_layer_gpu import WindowCase
 from weight_quantized_mixed_amd import qgemm as q
 from weight_quantized_mixed_amd.device import norm_rotate_backward
 
@@ -51,3 +52,45 @@ def test_weight_gradients_over_millions_of_heads(T, hq, hkv, D, kinds, one_sign)
     ws = torch.full((need,), 0xFF, dtype=torch.uint8, device="cuda")
     again = norm_rotate_backward(*args, q_weight=dev(qw), k_weight=dev(kw), eps=1e-5, ws=ws)
     assert all(torch.equal(r[n], again[n]) for n in r)
+
+
+def kernels_of(call):
+    """Names of the kernels that a call runs."""
+    call()
+    torch.cuda.synchronize()
+    with torch.profiler.profile(activities=[torch.profiler.ProfilerActivity.CUDA]) as p:
+        call()
+        torch.cuda.synchronize()
+    return [e.name for e in p.events()]
+
+
+def assert_tiles(c, D, parts):
+    """The tiles of 128 rows for heads past 128, and the keys in so many parts: where a rule of the split moves a case away from
+    them, the case has to move too."""
+    names = kernels_of(c.run)
+    want = f"window_rows_kernel<256, {'true' if D == 256 else 'false'}>"
+    assert any(want in n for n in names), names
+    assert any("attend_join_kernel" in n for n in names) == (parts > 1), names
+    T = sum(c.qs)
+    need = q.qgemm_attention_window_workspace(c.cache.desc, T, c.hq, len(c.qs), max(c.qs), max(c.lens), c.prefix, c.window, c.sinks)
+    assert need == (parts * T * c.hq * (D + 2) * 4 if parts > 1 else 0)
+
+
+WIDE = [  # q_heads, kv_heads, D, page, queries, own tokens, prefix, window, sinks, parts
+    (6, 2, 136, 16, [500, 499, 480, 500, 470, 500], [500, 499, 700, 510, 470, 500], 5, 64, 9, 1),
+    (8, 2, 256, 64, [500, 499, 480, 500, 470, 500], [500, 499, 700, 510, 470, 500], 5, 64, 9, 1),
+    (10, 2, 192, 16, [700, 650, 700], [900, 650, 701], 30, 300, 40, 1), (14, 2, 256, 1, [400, 390, 400, 399], [800, 390, 400, 700], 0, 100, 0, 1),
+    (16, 4, 256, 16, [300, 301, 299, 250], [300, 500, 290, 600], 20, 100, 30, 1), (4, 2, 256, 16, [520], [9000], 0, 8000, 100, 13),
+    (4, 2, 136, 32, [1000], [4000], 0, 3000, 50, 7), (6, 2, 256, 16, [520], [6000], 100, 5000, 100, 9),
+    (6, 2, 248, 64, [1, 520], [30, 6000], 100, 5000, 100, 9), (8, 2, 256, 128, [1000], [4000], 0, 3000, 50, 4),
+    (3, 1, 256, 16, [1000, 900], [2000, 3000], 0, 2000, 50, 5),
+]
+
+
+@pytest.mark.parametrize("hq,hkv,D,page,qs,lens,prefix,window,sinks,parts", WIDE)
+def test_wide_heads_that_share_keys(hq, hkv, D, page, qs, lens, prefix, window, sinks, parts):
+    """Several query heads of a key head, two to seven, in tiles that begin between a token's heads; keys whole and in parts."""
+    say(f"case wide heads hq={hq} hkv={hkv} D={D} page={page} q={qs} lens={lens} prefix={prefix} window={window} sinks={sinks}")
+    c = WindowCase(hq, hkv, D, page, qs, lens, prefix, window, sinks, seed=D + hq).upload()
+    assert_tiles(c, D, parts)
+    c.check()
