@@ -555,7 +555,9 @@ qgemm_status qgemm_attention_workspace(const qgemm_kv_cache* cache, int64_t T, i
  *   prefix_len   tokens of the prefix, >= 0; every query sees all of them.
  * Query i of a sequence sees own token j iff j <= kv_lens[b] - n + i.  A query that sees
  * nothing gets zeros (and lse -inf).  Keys and values that a query does not see never
- * enter its result, whatever they hold (NaN and infinities included).
+ * enter its result, whatever they hold (NaN and infinities included).  An infinite or NaN value
+ * of a key that it does see makes its result infinite or NaN; where that key's probability rounds
+ * to 0, the result may be infinite, NaN, or what a value of 0 gives.
  *   max_q, max_len  bounds of n and kv_lens (host values, so that a captured call can be
  *                replayed with other lengths); rows past max_q are not written, tokens past
  *                max_len or the table not read.  A page number outside the cache reads

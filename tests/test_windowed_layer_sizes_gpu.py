@@ -94,3 +94,60 @@ def test_wide_heads_that_share_keys(hq, hkv, D, page, qs, lens, prefix, window, 
     c = WindowCase(hq, hkv, D, page, qs, lens, prefix, window, sinks, seed=D + hq).upload()
     assert_tiles(c, D, parts)
     c.check()
+
+
+# ---- infinite values
+
+@pytest.mark.parametrize("hq,hkv,D,qs,lens,prefix,window,sinks", [
+    (4, 2, 128, [200], [700], 0, 64, 300), (4, 2, 64, [150], [600], 70, 40, 257), (8, 2, 256, [500, 499, 480, 500, 470, 500], [900, 499, 700, 510, 470, 500], 5, 64, 209),
+    (8, 1, 128, [90], [2000], 0, 900, 1000), (8, 2, 128, [5], [400], 0, 90, 200)])
+def test_infinite_values_behind_vanishing_probabilities(hq, hkv, D, qs, lens, prefix, window, sinks):
+    """One key that every row scores far below the others, among first keys that whole tiles see, at the window's edge, and both: its
+    infinite value reaches no other place and no row that does not see it."""
+    say(f"case vanishing hq={hq} hkv={hkv} D={D} q={qs} window={window} sinks={sinks}")
+    c = WindowCase(hq, hkv, D, 16, qs, lens, prefix, window, sinks, seed=D)
+    c.q[:] = 1  # (scores of about 1, and of -30 sqrt(D) for keys of -30: e^-240 and less, which is 0 in fp32)
+    seen = c.visible(0)
+    partly = np.flatnonzero(seen.any(0) & ~seen.all(0))
+    partly = partly[partly >= prefix]
+    first, edge = prefix + 10, partly[len(partly) // 2]
+    assert seen[:, first].all()
+    for at in ([first], [edge], [first, edge]):
+        k, v = c.k.copy(), c.v.copy()
+        for t in at:
+            page, i = c.tables[0, (t - prefix) // 16], (t - prefix) % 16
+            c.k[page, :, i] = -30
+        plain, _ = c.upload().run()
+        for t in at:
+            c.v[c.tables[0, (t - prefix) // 16], :, (t - prefix) % 16, 7] = np.inf
+        got, _ = c.upload().run()
+        hit = np.zeros(plain.shape, bool)
+        hit[:qs[0], :, 7] = seen[:, at].any(1)[:, None]
+        assert np.array_equal(got[~hit], plain[~hit])
+        assert (np.isposinf(got[hit]) | np.isnan(got[hit]) | (got[hit] == plain[hit])).all()
+        c.k, c.v = k, v
+
+
+@pytest.mark.parametrize("hq,hkv,D,qs,lens,prefix,window,sinks", [
+    (8, 2, 256, [500, 499, 480, 500, 470, 500], [900, 499, 700, 510, 470, 500], 5, 64, 209), (6, 2, 136, [1000], [4000], 0, 3000, 500),
+    (4, 2, 128, [200], [700], 0, 64, 300), (8, 1, 128, [90], [2000], 0, 900, 1000)])
+def test_infinities_among_first_keys_and_at_the_edges(hq, hkv, D, qs, lens, prefix, window, sinks):
+    """Infinities in blocks of first keys that whole tiles see, beside ones that some rows do not; keys whole and in parts."""
+    c = WindowCase(hq, hkv, D, 16, qs, lens, prefix, window, sinks, seed=D + 1)
+    rng = np.random.default_rng(D)
+    say(f"case infinities {hq}/{hkv} heads of {D}")
+    plain, _ = c.upload().run()
+    want = plain.copy()
+    for b, n in enumerate(lens):
+        seen = c.visible(b)
+        edge = [t for t in np.flatnonzero(seen.any(0) & ~seen.all(0)) if t >= prefix]
+        tokens = {prefix + int(t) for t in rng.integers(0, min(sinks, n), 3)} | {int(t) for t in rng.choice(edge, 5, replace=False)}
+        for t in sorted(tokens):
+            h, e, value = int(rng.integers(hkv)), int(rng.integers(D)), float(rng.choice([np.inf, -np.inf, np.nan]))
+            c.v[c.tables[b, (t - prefix) // 16], h, (t - prefix) % 16, e] = value
+            rows, heads = np.flatnonzero(seen[:, t]) + c.starts[b], range(h * (hq // hkv), (h + 1) * (hq // hkv))
+            with np.errstate(invalid="ignore"):
+                want[np.ix_(rows, heads, [e])] += np.asarray(value, want.dtype)
+    got, _ = c.upload().run()
+    finite = np.isfinite(want)
+    assert not finite.all() and np.array_equal(got[finite], plain[finite]) and np.array_equal(got[~finite], want[~finite], equal_nan=True)

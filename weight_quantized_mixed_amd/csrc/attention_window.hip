@@ -270,8 +270,8 @@ __global__ __launch_bounds__(256, DP == 64 ? 3 : DP == 128 ? 2 : 1) void window_
     // one would be NaN): they become 0 in LDS, and are added behind the last block.  A quarter of the
     // block is looked at by each wave; the rest is rare.
     uint32_t* const flag = reinterpret_cast<uint32_t*>(lds + 4 * T::BLOCK + 4 * T::RING);
-    bool cleaned = false;
-    auto clean = [&](int odd) {
+    int cleaned_from = cnt, cleaned_to = 0;  // all blocks that were changed are among these
+    auto clean = [&](int j, int odd) {
       int lane = threadIdx.x & 63;
       asm volatile("" : "+v"(lane));  // (addresses made here, rather than kept through the loop and spilled)
       uint8_t* const vb = lds + VALUES + odd * T::BLOCK;
@@ -288,7 +288,8 @@ __global__ __launch_bounds__(256, DP == 64 ? 3 : DP == 128 ? 2 : 1) void window_
       asm volatile("s_barrier" ::: "memory");
       const uint4 f = *reinterpret_cast<const uint4*>(flag);
       if (__builtin_amdgcn_readfirstlane(f.x | f.y | f.z | f.w) != 0) {
-        cleaned = true;
+        cleaned_from = min(cleaned_from, j);
+        cleaned_to = j + 1;
 #pragma unroll 1
         for (int i = wave; i < T::BLOCK / 1024; i += 4) {
           uint4* at = reinterpret_cast<uint4*>(vb + i * 1024 + lane * 16);
@@ -307,12 +308,14 @@ __global__ __launch_bounds__(256, DP == 64 ? 3 : DP == 128 ? 2 : 1) void window_
         asm volatile("s_barrier" ::: "memory");
       }
     };
-    // ... and adds each to the rows that see its key: the blocks' values read again from the cache, one
-    // value of a key at a time (in the loop, with heads of 256, it drove the sums into memory).
+    // ... and adds each to the rows that see its key: the values of those blocks read again from the cache, one
+    // value of a key at a time (in the loop, with heads of 256, it drove the sums into memory).  Blocks of first
+    // keys that all rows see were not cleaned and may lie between them.
     auto add_cleaned = [&] {
       constexpr int PER = DP / 64;  // values of a key that a lane looks at
 #pragma unroll 1
-      for (int x = base_of(whole); x < kend; ++x) {
+      for (int x = base_of(cleaned_from); x < min(base_of(cleaned_to), kend); ++x) {
+        if (!masked((x - it.key0) / KT)) continue;
         const int key = key_at(it, x);
         const bool own = key >= it.pre;
         const int t = own ? key - it.pre : key;
@@ -363,7 +366,7 @@ __global__ __launch_bounds__(256, DP == 64 ? 3 : DP == 128 ? 2 : 1) void window_
     auto block = [&](int j, auto ODD, Scores& now, Scores& next) {
       constexpr int odd = decltype(ODD)::value;
       stage(j);
-      if (masked(j)) clean(odd);
+      if (masked(j)) clean(j, odd);
       half8v f[AHEAD];
 #pragma unroll
       for (int x = 0; x < AHEAD; ++x) f[x] = k_operand(odd ^ 1, x % 2, x / 2);
@@ -425,14 +428,14 @@ __global__ __launch_bounds__(256, DP == 64 ? 3 : DP == 128 ? 2 : 1) void window_
     reads_done();
     asm volatile("s_barrier" ::: "memory");
     const int odd = j & 1;
-    if (masked(j)) clean(odd);
+    if (masked(j)) clean(j, odd);
 #pragma unroll
     for (int x = 0; x < 16; ++x) exp_pair(sa, x);
 #pragma unroll
     for (int k = 0; k < 4; ++k)
 #pragma unroll
       for (int d = 0; d < ND; ++d) product_step(v_operand(odd, d, k), d, k);
-    if (cleaned) add_cleaned();
+    if (cleaned_to) add_cleaned();
     l = both(l, [](float x, float y) { return x + y; });
   }
 
