@@ -7,7 +7,7 @@ import torch
 import oracle
 from gpu_helpers import say
 from test_paged_kv_gpu import assert_near, dev, halves
-from test_windowed_layer_gpu import WindowCase
+from test_windowed_layer_gpu import PoolCase, WindowCase
 from weight_quantized_mixed_amd import qgemm as q
 from weight_quantized_mixed_amd.device import norm_rotate_backward
 
@@ -151,3 +151,63 @@ def test_infinities_among_first_keys_and_at_the_edges(hq, hkv, D, qs, lens, pref
     got, _ = c.upload().run()
     finite = np.isfinite(want)
     assert not finite.all() and np.array_equal(got[finite], plain[finite]) and np.array_equal(got[~finite], want[~finite], equal_nan=True)
+
+
+# ---- many pages given back
+
+@pytest.mark.parametrize("B,page,most,prefix,window,sinks,ends", [
+    (1, 1, 30000, 0, 0, 0, 1.0), (1, 1, 8193, 0, 0, 0, 1.0), (1, 1, 8192, 0, 0, 0, 1.0), (3, 1, 30000, 5, 40, 90, 0.4), (48, 1, 2500, 0, 0, 0, 0.5), (300, 4, 900, 10, 64, 30, 0.3),
+    (1500, 1, 200, 0, 20, 7, 0.1), (2048, 1, 60, 0, 0, 0, 0.6), (2048, 1, 9, 0, 0, 0, 1.0), (40, 1, 5000, 0, 4000, 600, 0.5)])
+def test_many_pages_come_back(B, page, most, prefix, window, sinks, ends):
+    """Steps of few tokens in which long sequences end or their windows first move on: thousands of pages, of sequences of mixed
+    lengths, some of which hold none."""
+    say(f"case pages back B={B} page={page} lens={most} window={window} sinks={sinks}")
+    rng = np.random.default_rng(B + most)
+    lens = rng.integers(0, most + 1, B)
+    lens[rng.random(B) < 0.2] = 0
+    lens[0] = most
+    new = np.where(rng.random(B) < ends, -1, rng.integers(0, 2, B))
+    c = PoolCase(B, page, -(-(most + 1) // page), int((-(-lens // page)).sum()) + 40, lens, prefix, window, sinks, seed=B, gone=False)
+    got, want, pool = c.check(new, int(np.maximum(new, 0).sum()) + 3)
+    assert want["free"] - c.free > 5000 and q.qgemm_kv_extend_workspace(B, int(np.maximum(new, 0).sum()) + 3) == 0
+    c.check(new, int(np.maximum(new, 0).sum()), None, torch.full_like(pool.state, -5))
+
+
+# ---- memory
+
+@pytest.mark.parametrize("T", [700, 7000])
+def test_results_and_workspaces_may_begin_as_anything(T):
+    """Every array that the calls write, their workspaces among them, begins as NaN, zeros or junk; one launch and two."""
+    rng = np.random.default_rng(T)
+    rows, hq, hkv, D, rot = 300, 8, 2, 96, 64
+    x, dyq, dyk = dev(halves(rng, rows, (hq + hkv) * D)), dev(halves(rng, rows, hq, D)), dev(halves(rng, rows, hkv, D))
+    qw, kw, cos, sin = dev(halves(rng, D)), dev(halves(rng, D)), *(dev(rng.standard_normal((9, rot // 2)).astype(np.float32)) for _ in range(2))
+    pos = dev(rng.integers(-1, 9, rows).astype(np.int32))
+    B, page, width = 50, 16, 40
+    c = PoolCase(B, page, width, 900, np.arange(B) * 7, window=64, sinks=4)
+    new = dev(np.where(np.arange(B) % 7 == 6, -1, T // 60).astype(np.int32))
+    norm_ws, extend_ws = q.qgemm_norm_rotate_backward_workspace(rows, hq, hkv, D, True), q.qgemm_kv_extend_workspace(B, T)
+    assert norm_ws > 0 and (extend_ws > 0) == (T == 7000)
+    results = []
+    for fill in (0xFF, 0x00, 0x7B):
+        def junk(*shape, dtype=torch.float16):
+            return torch.full((int(np.prod(shape)) * dtype.itemsize,), fill, dtype=torch.uint8, device="cuda").view(dtype).view(shape)
+
+        turn = (qw.data_ptr(), kw.data_ptr(), 1e-5, cos.data_ptr(), sin.data_ptr(), 9, rot, 1, pos.data_ptr())
+        src = (x.data_ptr(), (hq + hkv) * D, x.data_ptr() + 2 * hq * D, (hq + hkv) * D)
+        qo, ko, dq, dk = junk(rows, hq, D), junk(rows, hkv, D), junk(rows, hq * D), junk(rows, hkv * D)
+        dw, ws = junk(2, D, dtype=torch.float32), junk(norm_ws, dtype=torch.uint8)
+        q.qgemm_norm_rotate(rows, hq, hkv, D, *src, *turn, qo.data_ptr(), ko.data_ptr())
+        q.qgemm_norm_rotate_backward(rows, hq, hkv, D, *src, *turn, dyq.data_ptr(), dyk.data_ptr(), dq.data_ptr(), hq * D, dk.data_ptr(), hkv * D,
+                                     dw.data_ptr(), dw.data_ptr() + 4 * D, ws.data_ptr(), norm_ws)
+        pool, i32 = c.pool(), torch.int32
+        starts, after, where, slots, refused = junk(B + 1, dtype=i32), junk(2 * B + 2, dtype=i32), junk(T, dtype=i32), junk(T, dtype=torch.int64), junk(B, dtype=i32)
+        ws = junk(max(extend_ws, 16), dtype=torch.uint8)
+        at, to = pool.state.data_ptr(), after.data_ptr()
+        q.qgemm_kv_extend(B, T, page, new.data_ptr(), at, at + 4 * B, at + 8 * B, pool.ring.data_ptr(), len(c.ring), pool.tables.data_ptr(), width, 0, 64, 4,
+                          starts.data_ptr(), to, to + 4 * B, to + 8 * B, where.data_ptr(), slots.data_ptr(), refused.data_ptr(), ws.data_ptr(), extend_ws)
+        results.append([t.view(torch.uint8) for t in (qo, ko, dq, dk, dw, starts, after, where, slots, refused, pool.ring, pool.tables)])
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for other in results[1:] for a, b in zip(results[0], other))
+    want = oracle.extend_ref(new.cpu().numpy(), c.lens, c.gone, c.head, c.free, c.ring, c.tables, page, T, 0, 64, 4)
+    assert np.array_equal(slots.cpu().numpy(), want["slots"]) and np.array_equal(refused.cpu().numpy(), want["refused"])

@@ -254,6 +254,11 @@ __global__ __launch_bounds__(256) void place_kernel(ExtendArgs a, Steps steps, c
 // One workgroup takes 0.24 us for a thousand tokens and 0.08 more for each step of the bisection, a second
 // launch 4.5 in all: 24 sequences of 4800 tokens 7.9 us as one and 10.4 as two, of 19200 16.8 and 10.7;
 // 300 sequences of 9300 tokens 14.9 and 10.7.
+// The rule leaves out what comes back, which the host does not know: that takes one workgroup as long as as many tokens,
+// and the second launch 0.14 us a thousand pages.  In the long run as many come back as are taken, one a sequence in
+// page_size steps, for which the launch does not pay (2048 sequences of 8000 tokens, one more each: 8.8 us as one, 2049 of
+// them 13.0 as two); in a step in which very many end it would (pages of 16, one of fifty ending: 29.5 and 15.1 us, one of
+// two, 512000 pages: 570 and 84).
 bool one_launch(int64_t B, int64_t T) {
   int steps = 0;
   while (((int64_t)1 << steps) < B) ++steps;
