@@ -469,8 +469,9 @@ qgemm_status qgemm_norm_rotate_backward_workspace(int64_t T, int32_t q_heads, in
  *   dq_out, dk_out  device, fp16 [T, q_heads, head_dim] and [T, kv_heads, head_dim].
  *   dq, dk       device, fp16, rows dq_stride and dk_stride values apart (slices of one
  *                array's rows are allowed); may lie where dq_out and dk_out do, row by row.
- *   dq_weight, dk_weight  device, fp32 [head_dim], each may be NULL.  Sums in fp32 in a fixed
- *                order: bitwise reproducible for the same sizes.
+ *   dq_weight, dk_weight  device, fp32 [head_dim], each may be NULL.  Sums in a fixed order, at
+ *                most 128 additions in fp32 one after the other: bitwise reproducible for the
+ *                same sizes.
  * A token whose position is outside the table gets zeros and adds nothing to the weights'
  * gradients.  With T = 0 the weights' gradients are zeros.
  */

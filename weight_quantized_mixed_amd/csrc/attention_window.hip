@@ -21,7 +21,9 @@
 // 32 tiles took 78, 111, 200 and 466 us with heads of 128, these 54, 79, 169 and 435 as they were
 // first; then scores hidden by bits instead of intervals (window 64 54 -> 49 us) and items placed
 // without divisions (49 -> 46).  16 / 4 heads of 256 (one workgroup a CU, sums in the accumulation
-// registers): 67, 95, 199 and 482 us, on 16 x 16 x 32 tiles of 64 rows 94, 146, 325 and 816.
+// registers): 67, 95, 199 and 482 us, on 16 x 16 x 32 tiles of 64 rows 94, 146, 325 and 816.  Heads of
+// 136 to 248, whose loads past the head are set apart, spill 11 registers (24 / 8 heads of 192, window
+// 1024 272 us).  Precision: as in attention_kernel.hpp, with the probabilities in fp16 as operands.
 //
 // With heads of 128 a block of two workgroups takes a CU about 3850 cycles (4650 on the 16 x 16 tiles)
 // at 1.84 GHz (2.04): the clock gives way to the matrix cores, so fewer stalls buy less time than
@@ -357,7 +359,7 @@ __global__ __launch_bounds__(256, DP == 64 ? 3 : DP == 128 ? 2 : 1) void window_
       publish(j + 3, next_rows);
       next_rows = find(j + 4);
     };
-    // (three workgroups a CU with heads of 64, which leaves registers for two operands ahead: window 64
+    // (three workgroups a CU with heads of 64, which leaves registers for two operands ahead and spills three: window 64
     // 32 -> 28 us, 1024 101 -> 98 us; eight ahead with heads of 256 were level; PS pairs of the 16 beside
     // the scores)
     constexpr int AHEAD = DP == 64 ? 2 : 4, NS = 2 * NQ, NP = 4 * ND, PS = 12;

@@ -15,7 +15,7 @@
 //
 // Measured: 48 tokens 3.7 us; 8190 tokens of 32 + 8 + 8 heads of 128 (201 MB) 35 to 39 us, as the
 // caches have it; gradients of 4096 tokens of 32 + 8 heads (126 MB) 24.5 us, 5.1 TB/s (a
-// 2 GiB copy reaches 4.85), the weights' second pass 3.9 us.
+// 2 GiB copy reaches 4.85), the weights' second pass 4.0 us.
 //
 // The gradient of a norm's weight sums over tokens and heads: each lane adds up its own places
 // over the rows that its workgroup walks (at most CHAIN), the workgroup joins its lanes and
