@@ -462,7 +462,8 @@ class PagePool:
         the state are brought up to date.  Rows behind the last token have slot -1.  A sequence whose tokens find no room
         is marked in refused (int32 [sequences]) and keeps its length; its rows have position and slot -1.
         state_out: where the state after the call goes (by default the pool's own; else that stays as it was, and so the
-        same step may be taken again).  kv_lens is a part of it.
+        same step may be taken again).  kv_lens is a part of it: the next call that writes there changes it, behind the work
+        that was put on the stream before.
         """
         at, handle = _place(self.ring, stream)
         if handle not in self._streams:  # freed with the pool, its arrays wait for every stream that used them
@@ -489,6 +490,7 @@ def norm_rotate(q, k, head_dim, cos, sin, positions, q_weight=None, k_weight=Non
     to the mean), multiplied by its weight (fp16 [head_dim], None: 1) and rotated by its token's angles.
 
     q [T, q_heads * head_dim], k [T, kv_heads * head_dim]: rows may be slices of a wider array.
+    The results carry no history, whatever the inputs: norm_rotate_backward gives the gradients.
     """
     at, handle = _place(q, stream)
     if stream is not None:
